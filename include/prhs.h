@@ -271,6 +271,144 @@ prhs_status prhs_decode_step(const prhs_kv* kv, const void* q, const void* gate,
 prhs_status prhs_append_kv(const prhs_kv* kv, const void* k_new, const void* v_new,
                            cudaStream_t stream);
 
+/* ------------------------------------------------------------------------- *
+ * Token batches: several new tokens per sequence in one step (prompt chunks,
+ * drafted tokens that one step verifies, plain decode with one token each).
+ *
+ * The tokens of all sequences are packed: sequence b owns tokens
+ * [cu_new[b], cu_new[b + 1]) of arrays with T token rows (T may exceed
+ * cu_new[B]: the tokens behind the last sequence are padding). seq_lens[b] is
+ * the length t_b of the cached prefix; the new tokens follow it. A step is
+ *   prhs_plan_tokens    pages, slots, positions and masks of the new tokens
+ *   prhs_rope_append    rotated q; k and v into the cache, or k kept packed
+ *   prhs_tree_attn      attention over the cache and the new tokens
+ *   prhs_commit_tokens  accepted tokens join the cache, lengths advance
+ * and stays on the device: it can be captured into a graph. Token strides are
+ * in elements, at least the row's, and multiples of 16 bytes. Arrays of rows
+ * are 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+#define PRHS_TREE_MAX 128                     /* drafted tokens of one sequence's tree */
+#define PRHS_TREE_WORDS (PRHS_TREE_MAX / 32)  /* 32-bit words of one token's mask */
+
+/* Pages, slots, positions and tree masks of T packed tokens, built on the
+ * device from the cached lengths t_b and n_b = n_new[b] new tokens each:
+ *   cu_new[b] = sum of n_new over the sequences before b       int32 [B + 1]
+ *   slots[i]  = the cache slot of token i = cu_new[b] + j, its position being
+ *               t_b + j: page * block_size + row of a paged cache, b * t_max +
+ *               position of a contiguous one                   int32 [T]
+ *   positions[i] = t_b + j, or with parents t_b + the token's depth int32 [T]
+ * parents (nullable, int32 [T], as packed) makes each sequence's tokens a tree:
+ * a token's parent is an earlier token's number j within its sequence, or -1
+ * for a root, which follows the cached prefix. tree_mask ([T][PRHS_TREE_WORDS]
+ * uint32, set exactly when parents is) gets bit j of token i for itself and
+ * its ancestors; a tree has at most PRHS_TREE_MAX tokens.
+ * Padding tokens get slot -1, position 0 and an empty mask.
+ * Paged caches: row b of kv->block_table holds n_pages[b] pages (int32 [B]).
+ * The pages that t_b + n_b positions need beyond those are taken from
+ * free_pages[free_head[0] .. n_free) in the order of the sequences, and
+ * written to kv->block_table; free_head_out[0] and n_pages_out[b] are the
+ * new counts (they may be the input arrays themselves). n_pages keeps counting
+ * the pages that rejected tokens left unused, so they are used next. All six
+ * page arguments are ignored for a contiguous cache.
+ * A sequence that cannot be placed takes no page and its slots are -1: more
+ * than t_max positions, tokens beyond T, or more pages than are free
+ * (PRHS_DEV_CAPACITY); a negative n_b, a tree above PRHS_TREE_MAX tokens
+ * (PRHS_DEV_BAD_LEN); a page outside the pool (PRHS_DEV_BAD_BLOCK). When pages
+ * run out at one sequence, later ones that need new pages get none either. A
+ * parent outside [-1, j) is flagged (PRHS_DEV_BAD_INDEX) and read as -1. */
+prhs_status prhs_plan_tokens(const prhs_kv* kv, const int32_t* n_new, int T,
+                             const int32_t* parents, const int32_t* free_pages, int n_free,
+                             const int32_t* free_head, const int32_t* n_pages, int32_t* cu_new,
+                             int32_t* positions, int32_t* slots, uint32_t* tree_mask,
+                             int32_t* free_head_out, int32_t* n_pages_out, cudaStream_t stream);
+
+/* Rotary positions. Pair i of the first rot_dim elements of a head is turned
+ * by the angle position * theta_i; the other elements are kept. The angle is
+ * kept in turns as a 64-bit binary fraction: turns[i] is theta_i / (2 pi)
+ * modulo 1, times 2^64, and position * turns[i] modulo 2^64 is the angle of any
+ * int32 position, as exact as theta_i was in float64. */
+typedef struct prhs_rope {
+  int rot_dim;            /* a multiple of 16, 16 .. d */
+  int interleaved;        /* 0: pair i is (x_i, x_{i + rot_dim / 2}); 1: (x_{2i}, x_{2i + 1}) */
+  const uint64_t* turns;  /* [rot_dim / 2], device */
+  float mscale;           /* factor on cos and sin (1 but for PRHS_ROPE_RAMP) */
+} prhs_rope;
+
+/* How theta_i = base^(-2i / rot_dim) is changed for contexts longer than the
+ * original one, by `factor`; t_i = original * theta_i / (2 pi) are the turns of
+ * pair i over the original context. */
+typedef enum {
+  PRHS_ROPE_PLAIN = 0,
+  PRHS_ROPE_LINEAR = 1,  /* theta_i / factor */
+  PRHS_ROPE_NTK = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  PRHS_ROPE_BANDS = 3,   /* theta_i where t_i >= high, theta_i / factor where t_i <= low,
+                            between them mixed linearly in t_i */
+  PRHS_ROPE_RAMP = 4     /* the same mixed linearly in i, from the pair with t_i = high (rounded
+                            down) to the one with t_i = low (rounded up); mscale =
+                            0.1 ln(factor) + 1 (arXiv 2309.00071) */
+} prhs_rope_kind;
+
+/* Fills turns[rot_dim / 2] and *mscale, both in HOST memory, in float64. Needs
+ * base > 1 and factor >= 1; PRHS_ROPE_BANDS and PRHS_ROPE_RAMP need original > 0
+ * and high > low > 0. Needs no device. */
+prhs_status prhs_rope_turns(prhs_rope_kind kind, int rot_dim, double base, double factor,
+                            double original, double low, double high, uint64_t* turns,
+                            float* mscale);
+
+/* Rotates q [T][Hq][d] and k [T][Hkv][d] of T tokens at positions [T] (int32)
+ * and puts them, with v [T][Hkv][d], where they are needed:
+ *   q_out [T][Hq][d]  rotated q (may be q itself when q_stride = Hq * d)
+ *   k_out [T][Hkv][d] rotated k (nullable; may be k itself when k_stride = Hkv * d)
+ *   the cache's rows slots[i] of every KV head: rotated k, and v (slots nullable: the
+ *   cache is not written and v is not read)
+ * q, k, v and the results have the cache's element type; sin, cos and products
+ * are fp32, rounded once. With slots, a token of slot -1 is padding: nothing
+ * of it is written. A slot outside the cache is flagged (PRHS_DEV_BAD_INDEX)
+ * and treated as padding. Slots must differ: of two tokens with one slot either
+ * may be left in each 16-byte piece of the row. */
+prhs_status prhs_rope_append(const prhs_kv* kv, const prhs_rope* rope, int T,
+                             const int32_t* positions, const int32_t* slots, const void* q,
+                             long long q_stride, const void* k, long long k_stride, const void* v,
+                             long long v_stride, void* q_out, void* k_out, cudaStream_t stream);
+
+/* Bytes of workspace prhs_tree_attn needs for this cache and at most max_new
+ * tokens a sequence (0 for an invalid descriptor). It needs no initialisation. */
+size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new);
+
+/* Attention of the new tokens: token j of sequence b attends the cached keys
+ * [0, t_b) and, of its sequence's new tokens (k_new, v_new: packed rows
+ * [T][Hkv][d], not read from the cache), those whose bit is set in its
+ * tree_mask row ([T][PRHS_TREE_WORDS] uint32; bits at or above n_b are ignored),
+ * or tokens 0 .. j where tree_mask is null (a causal chunk of any length):
+ *   lse = log sum exp(s),  out = sum exp(s - lse) v,  s = scale * <q, k>
+ * over the attended keys; out = 0 and lse = -inf where there are none.
+ * out [T][Hq][d] has the cache's element type (fp32 accumulation, rounded
+ * once), lse [T][Hq] is fp32. Rows of padding tokens are left as they are.
+ * max_new bounds the tokens of any sequence, at most PRHS_TREE_MAX with
+ * tree_mask; a sequence with more, or with cu_new not ascending within [0, T],
+ * is flagged (PRHS_DEV_BAD_LEN) and its rows are left as they are. Keys on a
+ * page outside the pool are flagged (PRHS_DEV_BAD_BLOCK) and not attended. Rows
+ * of the cache at or beyond t_b are not used, whatever they hold. */
+prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,
+                           const void* v_new, long long v_stride, float scale, int T,
+                           const int32_t* cu_new, int max_new, const uint32_t* tree_mask, void* out,
+                           float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Adds m_b = accept_n[b] tokens of each sequence to its cache: row t_b + i of
+ * every KV head gets the packed rows of token accept_idx[b][i] (int32
+ * [B][accept_cap], numbers within the sequence's new tokens; nullable: token i
+ * itself), and new_lens[b] = t_b + m_b (int32 [B]; may be kv->seq_lens itself).
+ * The positions must be mapped (prhs_plan_tokens). k_new and v_new nullable
+ * together: the rows are in the cache already (prhs_rope_append), only the
+ * lengths advance. A sequence with m_b outside [0, n_b] or above accept_cap,
+ * a number outside [0, n_b), no room or an unmapped page is flagged
+ * (PRHS_DEV_BAD_LEN, _BAD_INDEX, _CAPACITY, _BAD_BLOCK) and keeps its rows and
+ * its length. */
+prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,
+                               const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
+                               const void* k_new, long long k_stride, const void* v_new,
+                               long long v_stride, int32_t* new_lens, cudaStream_t stream);
+
 /* Self-test of the kernels' failure path (no counterpart in the paper): one
  * warp waits on a shared-memory mbarrier that nothing arrives on, through the
  * same bounded wait every TMA pipeline of the library uses, but giving up

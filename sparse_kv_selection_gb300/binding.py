@@ -24,9 +24,17 @@ EXPORTS = ["prhs_workspace_size", "prhs_workspace_init", "prhs_score_select", "p
            "prhs_score",
            "prhs_select", "prhs_cis_dilate",
            "prhs_sparse_attn", "prhs_sparse_attn_noalloc", "prhs_set_mass", "prhs_dense_attn",
-           "prhs_decode_step", "prhs_append_kv", "prhs_selftest_wait_timeout", "prhs_last_error",
+           "prhs_decode_step", "prhs_append_kv", "prhs_plan_tokens", "prhs_rope_turns",
+           "prhs_rope_append", "prhs_tree_workspace_size", "prhs_tree_attn",
+           "prhs_commit_tokens", "prhs_selftest_wait_timeout", "prhs_last_error",
            "prhs_device_error_bits", "prhs_status_str", "prhs_last_message", "prhs_num_sms",
            "prhs_launch_count"]
+
+
+# Drafted tokens of one sequence's tree, and the 32-bit words of a token's mask.
+TREE_MAX = 128
+TREE_WORDS = TREE_MAX // 32
+ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
 
 
 class PrhsError(RuntimeError):
@@ -43,6 +51,11 @@ class prhs_kv(ctypes.Structure):
                 ("max_blocks", ctypes.c_int), ("num_blocks", ctypes.c_int)]
 
 
+class prhs_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("turns", ctypes.c_void_p), ("mscale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -57,6 +70,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, I, F, D, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
     KV = ctypes.POINTER(prhs_kv)
+    ROPE, L = ctypes.POINTER(prhs_rope), ctypes.c_longlong
     sig = {
         "prhs_workspace_size": (Z, [KV, I]),
         "prhs_workspace_init": (I, [P, Z, P]),
@@ -72,6 +86,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "prhs_decode_step": (I, [KV, P, P, F, I, P, I, I, I, I, D, I, P, P, P, I, P, P, P, I, P, P, P, P,
                                  P, Z, P]),
         "prhs_append_kv": (I, [KV, P, P, P]),
+        "prhs_plan_tokens": (I, [KV, P, I, P, P, I, P, P, P, P, P, P, P, P, P]),
+        "prhs_rope_turns": (I, [I, I, D, D, D, D, D, P, ctypes.POINTER(F)]),
+        "prhs_rope_append": (I, [KV, ROPE, I, P, P, P, L, P, L, P, L, P, P, P]),
+        "prhs_tree_workspace_size": (Z, [KV, I]),
+        "prhs_tree_attn": (I, [KV, P, P, L, P, L, F, I, P, I, P, P, P, P, Z, P]),
+        "prhs_commit_tokens": (I, [KV, I, P, P, I, P, P, L, P, L, P, P]),
         "prhs_selftest_wait_timeout": (I, [ctypes.c_uint, P]),
         "prhs_last_error": (I, []),
         "prhs_device_error_bits": (ctypes.c_uint, []),
@@ -273,6 +293,192 @@ def append_kv(kv, k_new, v_new, stream=None) -> None:
     """Write one key and value row per (sequence, KV head) at each
     sequence's current length and advance kv.seq_lens (prhs_append_kv)."""
     _check(load().prhs_append_kv(kv.ref(), _ptr(k_new), _ptr(v_new), _stream(stream)), "append_kv")
+
+
+# --------------------------------------------------------------------------- #
+# token batches: several new tokens per sequence in one step
+# --------------------------------------------------------------------------- #
+def _array(t, name, shape, dtype, device, optional=False):
+    """Pointer of a packed array argument after checking what it is."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _rows(t, name, T, heads, d, dtype, device):
+    """Pointer and token stride of [T][heads][d] rows that may be a view of a
+    wider buffer (a fused projection's output): packed within a token."""
+    if t is None:
+        return None, heads * d
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (T, heads, d):
+        raise ValueError(f"{name} must have shape {(T, heads, d)}, got {tuple(t.shape)}")
+    if t.numel() and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+        raise ValueError(f"{name}: the rows of one token must be packed")
+    return t.data_ptr(), (t.stride(0) if T > 1 else heads * d)
+
+
+def _on(kv, stream):
+    """The cache's device made current, and the stream there to launch on."""
+    with torch.cuda.device(kv.k.device):
+        return torch.cuda.device(kv.k.device), _stream(stream)
+
+
+def rope_turns(rot_dim, base=10000.0, kind="plain", factor=1.0, original=0.0, low=0.0, high=0.0):
+    """The fixed-point turns a position of each rotated pair (a list of Python
+    integers below 2**64) and the factor on cos and sin (prhs_rope_turns)."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_KINDS)}, got {kind!r}")
+    out = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
+    mscale = ctypes.c_float()
+    _check(load().prhs_rope_turns(ROPE_KINDS[kind], int(rot_dim), float(base), float(factor),
+                                  float(original), float(low), float(high), out,
+                                  ctypes.byref(mscale)), "rope_turns")
+    return list(out), float(mscale.value)
+
+
+class RopeTable:
+    """Rotary frequencies on the device, for rope_append.
+
+    rot_dim elements of each head are rotated (a multiple of 16 up to d),
+    pairs (i, i + rot_dim / 2) or, interleaved, (2i, 2i + 1). scaling: None,
+    "linear", "ntk", "bands" or "ramp" with factor (and original, low, high
+    for the last two), as prhs_rope_kind defines them.
+    """
+
+    def __init__(self, rot_dim, base=10000.0, *, interleaved=False, scaling=None, factor=1.0,
+                 original=0.0, low=0.0, high=0.0, device="cuda"):
+        turns, mscale = rope_turns(rot_dim, base, scaling or "plain", factor, original, low, high)
+        signed = [x - (1 << 64) if x >= 1 << 63 else x for x in turns]
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+        self.mscale = mscale
+        self.desc = prhs_rope(int(rot_dim), int(bool(interleaved)), self.turns.data_ptr(), mscale)
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def plan_tokens(kv, n_new, cu_new, positions, slots, *, parents=None, tree_mask=None,
+                free_pages=None, free_head=None, n_pages=None, free_head_out=None,
+                n_pages_out=None, stream=None) -> None:
+    """Pages, slots, positions and tree masks of positions.numel() packed
+    tokens (prhs_plan_tokens). On a paged cache kv.block_table gets the new
+    pages; free_head and n_pages are updated in place unless their _out arrays
+    are given."""
+    dev, i32, T, B = kv.k.device, torch.int32, positions.numel(), kv.B
+    paged = kv.block_table is not None
+    if paged:
+        free_head_out = free_head if free_head_out is None else free_head_out
+        n_pages_out = n_pages if n_pages_out is None else n_pages_out
+        n_free = 0 if free_pages is None else free_pages.numel()
+        pages = [_array(free_pages, "free_pages", (n_free,), i32, dev, optional=True), n_free,
+                 _array(free_head, "free_head", (1,), i32, dev), _array(n_pages, "n_pages", (B,), i32, dev)]
+        pages_out = [_array(free_head_out, "free_head_out", (1,), i32, dev),
+                     _array(n_pages_out, "n_pages_out", (B,), i32, dev)]
+    else:
+        pages, pages_out = [None, 0, None, None], [None, None]
+    guard, st = _on(kv, stream)
+    with guard:
+        _check(load().prhs_plan_tokens(
+            kv.ref(), _array(n_new, "n_new", (B,), i32, dev), T,
+            _array(parents, "parents", (T,), i32, dev, optional=True), *pages,
+            _array(cu_new, "cu_new", (B + 1,), i32, dev), _array(positions, "positions", (T,), i32, dev),
+            _array(slots, "slots", (T,), i32, dev),
+            _array(tree_mask, "tree_mask", (T, TREE_WORDS), i32, dev, optional=True), *pages_out, st),
+            "plan_tokens")
+
+
+def rope_append(kv, rope, positions, q, k, v, q_out, *, slots=None, k_out=None, stream=None) -> None:
+    """Rotate q [T][Hq][d] and k [T][Hkv][d] at positions [T] into q_out and,
+    where given, k_out; with slots, rotated k and v go to those rows of the
+    cache (prhs_rope_append). q, k and v may be views with a token stride."""
+    dev, dt, T = kv.k.device, kv.k.dtype, positions.numel()
+    Hq, Hkv, d = kv.Hq, kv.desc.Hkv, kv.desc.d
+    if rope.turns.device != dev:
+        raise ValueError(f"rope is on {rope.turns.device}, the cache on {dev}")
+    if v is None and slots is not None:
+        raise ValueError("v is required with slots")
+    qp, qs = _rows(q, "q", T, Hq, d, dt, dev)
+    kp, ks = _rows(k, "k", T, Hkv, d, dt, dev)
+    vp, vs = _rows(v, "v", T, Hkv, d, dt, dev)
+    guard, st = _on(kv, stream)
+    with guard:
+        _check(load().prhs_rope_append(
+            kv.ref(), rope.ref(), T, _array(positions, "positions", (T,), torch.int32, dev),
+            _array(slots, "slots", (T,), torch.int32, dev, optional=True), qp, qs, kp, ks, vp, vs,
+            _array(q_out, "q_out", (T, Hq, d), dt, dev),
+            _array(k_out, "k_out", (T, Hkv, d), dt, dev, optional=True), st), "rope_append")
+
+
+def tree_workspace_size(kv: KVCache, max_new: int) -> int:
+    with torch.cuda.device(kv.k.device):
+        n = load().prhs_tree_workspace_size(kv.ref(), int(max_new))
+    if n == 0:
+        raise PrhsError(PRHS_EINVAL, "tree_workspace_size", load().prhs_last_message().decode())
+    return n
+
+
+def make_tree_workspace(kv: KVCache, max_new: int):
+    """Allocate (through torch) the workspace of tree_attn for this cache and
+    at most max_new tokens a sequence."""
+    return torch.empty(tree_workspace_size(kv, max_new), dtype=torch.uint8, device=kv.k.device)
+
+
+def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree_mask=None,
+              stream=None) -> None:
+    """Attention of packed new tokens over their caches and each other: by
+    tree_mask [T][4] int32, or causal (prhs_tree_attn). out [T][Hq][d] has the
+    cache's element type, lse [T][Hq] is float32."""
+    dev, dt, T = kv.k.device, kv.k.dtype, q.shape[0]
+    Hq, Hkv, d = kv.Hq, kv.desc.Hkv, kv.desc.d
+    kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
+    vp, vs = _rows(v_new, "v_new", T, Hkv, d, dt, dev)
+    if ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, the cache on {dev}")
+    guard, st = _on(kv, stream)
+    with guard:
+        _check(load().prhs_tree_attn(
+            kv.ref(), _array(q, "q", (T, Hq, d), dt, dev), kp, ks, vp, vs, float(scale), T,
+            _array(cu_new, "cu_new", (kv.B + 1,), torch.int32, dev), int(max_new),
+            _array(tree_mask, "tree_mask", (T, TREE_WORDS), torch.int32, dev, optional=True),
+            _array(out, "out", (T, Hq, d), dt, dev), _array(lse, "lse", (T, Hq), torch.float32, dev),
+            _ptr(ws), ws.numel() * ws.element_size(), st), "tree_attn")
+
+
+def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, accept_idx=None, k_new=None, v_new=None,
+                  T=None, stream=None) -> None:
+    """Write the accepted tokens' packed rows behind each cached prefix and
+    advance the lengths (prhs_commit_tokens), in place unless new_lens is
+    given. Without k_new and v_new only the lengths advance; T then bounds the
+    packed tokens (default: B * t_max)."""
+    dev, dt, i32, B = kv.k.device, kv.k.dtype, torch.int32, kv.B
+    Hkv, d = kv.desc.Hkv, kv.desc.d
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new must be both given or both left out")
+    if T is None:
+        T = k_new.shape[0] if k_new is not None else min(B * kv.t_max, ((1 << 31) - 1) // (kv.Hq + 2 * Hkv))
+    kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
+    vp, vs = _rows(v_new, "v_new", T, Hkv, d, dt, dev)
+    cap = 0 if accept_idx is None else accept_idx.shape[-1]
+    guard, st = _on(kv, stream)
+    with guard:
+        _check(load().prhs_commit_tokens(
+            kv.ref(), int(T), _array(cu_new, "cu_new", (B + 1,), i32, dev),
+            _array(accept_idx, "accept_idx", (B, cap), i32, dev, optional=True), cap,
+            _array(accept_n, "accept_n", (B,), i32, dev), kp, ks, vp, vs,
+            _array(kv.seq_lens if new_lens is None else new_lens, "new_lens", (B,), i32, dev), st),
+            "commit_tokens")
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:

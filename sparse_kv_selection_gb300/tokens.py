@@ -1,0 +1,80 @@
+"""Steps that feed several new tokens per sequence through one KV cache.
+
+``TokenBatch`` holds the device buffers of such a step and calls the four
+operators in order: ``plan`` (pages, slots, positions, tree masks), ``rotate``
+(rotary positions; k and v into the cache or kept packed), ``attend`` (over
+the cache and the new tokens) and ``commit`` (accepted tokens join the cache).
+It serves prompt chunks (``rotate(..., append=True)``, then ``commit`` of all
+tokens), the verification of drafted trees, and plain decode with one token a
+sequence. Nothing synchronises with the host, so a step can be captured into a
+graph; the same cache can be decoded by ``SparseDecoder`` between steps.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as _b
+
+
+class TokenBatch:
+    def __init__(self, kv: _b.KVCache, rope: _b.RopeTable, *, max_tokens: int, max_new: int,
+                 free_pages=None, n_pages=None, scale: float | None = None, stream=None):
+        """max_tokens packed tokens at most (padding included), max_new of one
+        sequence. A paged cache needs free_pages (int32, the pages that no
+        sequence holds) and n_pages (int32 [B], the pages each row of its block
+        table holds)."""
+        dev, B, d = kv.k.device, kv.B, kv.desc.d
+        self.kv, self.rope, self.stream = kv, rope, stream
+        self.max_new = int(max_new)
+        self.scale = scale if scale is not None else d ** -0.5
+        i32 = dict(device=dev, dtype=torch.int32)
+        T = int(max_tokens)
+        self.cu_new = torch.zeros(B + 1, **i32)
+        self.positions = torch.zeros(T, **i32)
+        self.slots = torch.full((T,), -1, **i32)
+        self._mask = torch.zeros(T, _b.TREE_WORDS, **i32)
+        self.tree_mask = None
+        self.pages = {}
+        if kv.block_table is not None:
+            if free_pages is None or n_pages is None:
+                raise ValueError("a paged cache needs free_pages and n_pages")
+            self.pages = dict(free_pages=free_pages, n_pages=n_pages,
+                              free_head=torch.zeros(1, **i32))
+        self.q = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
+        self.k = torch.zeros(T, kv.desc.Hkv, d, device=dev, dtype=kv.k.dtype)
+        self.v = None
+        self.out = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
+        self.lse = torch.zeros(T, kv.Hq, device=dev, dtype=torch.float32)
+        self.ws = _b.make_tree_workspace(kv, self.max_new)
+        self._in_cache = False
+
+    def plan(self, n_new: torch.Tensor, parents: torch.Tensor | None = None) -> None:
+        """Place n_new[b] tokens behind each sequence's cached prefix. parents
+        ([max_tokens] int32, packed) makes them trees; without, they are chunks."""
+        self.tree_mask = None if parents is None else self._mask
+        _b.plan_tokens(self.kv, n_new, self.cu_new, self.positions, self.slots, parents=parents,
+                       tree_mask=self.tree_mask, stream=self.stream, **self.pages)
+
+    def rotate(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, append: bool = False) -> None:
+        """Rotate q [max_tokens][Hq][d] and k [max_tokens][Hkv][d] at the planned
+        positions; append writes k and v into the cache at the planned slots
+        (chunks whose tokens will all be committed). v is kept for attend and
+        commit: it must not change before them."""
+        if append and self.tree_mask is not None:
+            raise ValueError("a tree's tokens join the cache when they are committed")
+        _b.rope_append(self.kv, self.rope, self.positions, q, k, v, self.q,
+                       slots=self.slots if append else None, k_out=self.k, stream=self.stream)
+        self.v, self._in_cache = v, append
+
+    def attend(self, out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> None:
+        """Attention of the new tokens into out and lse (the batch's own by default)."""
+        _b.tree_attn(self.kv, self.q, self.k, self.v, self.scale, self.cu_new, self.max_new,
+                     self.out if out is None else out, self.lse if lse is None else lse, self.ws,
+                     tree_mask=self.tree_mask, stream=self.stream)
+
+    def commit(self, accept_n: torch.Tensor, accept_idx: torch.Tensor | None = None) -> None:
+        """Add accept_n[b] tokens (numbers accept_idx[b], or the first ones) to
+        each sequence's cache and advance its length."""
+        rows = {} if self._in_cache and accept_idx is None else dict(k_new=self.k, v_new=self.v)
+        _b.commit_tokens(self.kv, self.cu_new, accept_n, accept_idx=accept_idx,
+                         T=self.positions.numel(), stream=self.stream, **rows)
