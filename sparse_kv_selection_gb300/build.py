@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libprhs.so")
 SOURCES = ["api.cu", "score.cu", "cis.cu", "attn.cu", "attn_cluster.cu", "select.cu", "retrieve.cu", "dense.cu",
-           "noalloc.cu", "mass.cu", "grow.cu", "plan.cu", "rope.cu", "tree.cu", "commit.cu", "tokens_api.cu"]
+           "noalloc.cu", "mass.cu", "grow.cu", "plan.cu", "rope.cu", "tree.cu", "tree_tc.cu", "commit.cu", "tokens_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,7 +10,7 @@
 #include <string>
 #include <vector>
 
-#include "kernels.h"
+#include "tokens.h"
 
 namespace prhs {
 
@@ -562,6 +562,24 @@ prhs_status abi_device(unsigned** err, int* sms) {
 prhs_status abi_fail(prhs_status s, const char* msg) { return fail(s, "%s", msg); }
 void abi_count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 KVView abi_view(const prhs_kv& kv, unsigned* err) { return view_of(kv, err); }
+prhs_status abi_encode_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides, const uint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return fail(PRHS_ECUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t d[5], st[5];
+  cuuint32_t bx[5], one[5];
+  for (int i = 0; i < rank; i++) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    one[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, bx, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PRHS_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return PRHS_OK;
+}
 int abi_attn_ctas(const prhs_kv& kv, bool sparse, int cap, int sms) {
   return attn_ctas(kv, sparse, cap, sms);
 }

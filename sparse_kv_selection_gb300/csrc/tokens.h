@@ -71,7 +71,16 @@ struct TreeLaunch {
   void* out;             // the cache's element type
   float* lse;
 };
-cudaError_t launch_tree(const TreeLaunch& a, cudaStream_t s);
+cudaError_t launch_tree(const TreeLaunch& a, cudaStream_t s);  // fp32
+// bf16: two launches, the first counted by the callee; *err is the launches'
+// result when the descriptors could be made. Workspace bytes of a call.
+prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
+size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
+
+// TMA descriptor of a bf16 tensor with the 128-byte swizzle (dims and box
+// innermost first, strides in bytes from dimension 1 on).
+prhs_status abi_encode_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides, const uint32_t* box);
 
 // Tokens [c0, c0 + n) of sequence b; none (flagged) when cu_new is not
 // ascending within [0, T] or the sequence has more than max_new.

@@ -27,6 +27,11 @@ prhs_status launched(cudaError_t e, const char* what) {
   return abi_fail(PRHS_ECUDA, cudaGetErrorString(e));
 }
 
+// fp32 caches need none; the size stays positive so that 0 means an error.
+size_t tree_ws_bytes(const KVView& kv, int max_new, int sms) {
+  return kv.dtype == PRHS_BF16 ? tree_tc_workspace(kv, max_new, sms) : 256;
+}
+
 // Checks shared by every entry point: descriptor, device, token count.
 prhs_status begin(const prhs_kv* kv, int T, KVView* view, int* sms) {
   prhs_status s = abi_check_kv(kv);
@@ -179,7 +184,10 @@ size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new) {
     abi_fail(PRHS_EINVAL, "tree: max_new must be positive");
     return 0;
   }
-  return 256;
+  unsigned* err = nullptr;
+  int sms = 0;
+  if (abi_device(&err, &sms) != PRHS_OK) return 0;
+  return tree_ws_bytes(abi_view(*kv, err), max_new, sms);
 }
 
 prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,
@@ -201,7 +209,12 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
     return s;
   if (T > 0 && max_new > T) max_new = T;
   if ((s = begin(kv, T, &a.kv, &sms)) != PRHS_OK) return s;
-  const size_t need = prhs_tree_workspace_size(kv, max_new);
+  // 32-bit tile counts: units (256 rows of tokens times group) times their tiles
+  const int G = kv->Hq / kv->Hkv;
+  const long long units = ((long long)T * G / 256 + kv->B) * kv->Hkv;
+  if (units * (a.kv.t_max / 128 + max_new / 128 + 2) >= (1ll << 31))
+    return abi_fail(PRHS_EUNSUPPORTED, "tree: too many key tiles for one call");
+  const size_t need = tree_ws_bytes(a.kv, max_new, sms);
   if (!ws) return abi_fail(PRHS_EWORKSPACE, "workspace is null");
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return abi_fail(PRHS_EWORKSPACE, "workspace must be 256-byte aligned");
   if (ws_bytes < need) return abi_fail(PRHS_EWORKSPACE, "workspace is smaller than prhs_tree_workspace_size()");
@@ -218,7 +231,10 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   a.mask = tree_mask;
   a.out = out;
   a.lse = lse;
-  return launched(launch_tree(a, stream), "tree attention");
+  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, stream), "tree attention");
+  cudaError_t e;
+  if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
+  return launched(e, "tree attention");
 }
 
 prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,

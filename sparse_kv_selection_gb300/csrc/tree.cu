@@ -218,8 +218,6 @@ static cudaError_t tree_go(const TreeLaunch& a, cudaStream_t st) {
 }
 
 cudaError_t launch_tree(const TreeLaunch& a, cudaStream_t st) {
-  if (a.kv.dtype == PRHS_BF16)
-    return a.kv.d == 128 ? tree_go<__nv_bfloat16, 128>(a, st) : tree_go<__nv_bfloat16, 64>(a, st);
   return a.kv.d == 128 ? tree_go<float, 128>(a, st) : tree_go<float, 64>(a, st);
 }
 

@@ -1,0 +1,887 @@
+// Attention of a batch of new tokens over their sequences' caches and over
+// each other, bf16, on the fifth-generation tensor cores.
+//
+// The G query heads of one KV head see the same keys, so the rows of one
+// (sequence, KV head) are its tokens times G (row = token * G + head of the
+// group), cut into units of UNIT_ROWS = 256 rows. A unit's keys are tiles of 128:
+// the cache's, then the new tokens'. All tiles of all units are one list; every
+// CTA (one per SM) takes an equal run of it, so long caches are split and short
+// ones packed without a plan made on the host. A unit cut by a run's end leaves
+// partial states in the workspace, which a second launch joins row by row.
+//
+// Inside a CTA: one warp loads K and V tiles by TMA into a ring of 128-key
+// slots (128-byte swizzle), another the units' Q tiles into two more (so that
+// neither holds the other back where units change), one thread issues the
+// matrix instructions, and two
+// warpgroups do the softmax, one per stream. A stream is a logit tile S
+// [128 rows][128 keys] and an output tile O [128][D] in tensor memory:
+//   S = Q K^T      (both from shared memory, 8 or 4 instructions of 16 elements)
+//   P = exp2(S - m) in bf16 over S's own columns, one row a thread
+//   O += P V       (P from tensor memory, V read d-major from its slot)
+// With more than 128 rows the streams are the unit's two row tiles and share
+// every K and V tile; with fewer they take the even and the odd key tiles, so
+// that one stream's products run under the other's softmax either way. The two
+// outputs of the second form are joined when the unit ends: both warpgroups
+// read both tiles, half the columns each.
+//
+// The running maximum m of a row follows the true one only when that has grown
+// by more than 8 (a factor 256 in the weights): O is then rescaled in tensor
+// memory, at a few tiles of a row instead of all. The weights stay below 2^8
+// and sums are fp32, so nothing is lost: l and O carry the same factor.
+//
+// P is rounded to bf16 (2^-9 of each weight at most, half a unit of the type
+// the result is rounded to); l is summed before that rounding, m, l and O are fp32.
+//
+// Bound: HBM while a KV head has up to about 256 query rows (K and V are read
+// once: 512 bytes a key at d = 128 against 4 * 128 * rows flops), the tensor
+// cores above.
+#include "tokens.h"
+
+namespace prhs {
+
+constexpr int TT = 128;                  // keys of a tile, rows of a stream
+constexpr int UNIT_ROWS = 2 * TT;
+constexpr int TC_WARPS = 12;             // 8 softmax, K/V producer, matrix issuer, Q producer, idle
+// Registers a thread: the softmax warpgroups hold a row of logits each, so they
+// take over part of the third one's. The three shares add up to what the block
+// is launched with (checked before the launch: a larger sum would wait forever).
+constexpr int TC_REGS_LAUNCH = 168, TC_REGS_SOFTMAX = 224, TC_REGS_REST = 56;
+static_assert(2 * TC_REGS_SOFTMAX + TC_REGS_REST <= 3 * TC_REGS_LAUNCH, "register shares");
+constexpr int TC_THREADS = TC_WARPS * 32;
+constexpr float TC_LOG2E = 1.4426950408889634f;
+constexpr float TC_LN2 = 0.6931471805599453f;
+constexpr float RESCALE_LOG2 = 8.f;
+
+template <int D>
+struct TcShape {
+  static constexpr int SEGS = D / 64;             // 128-byte column segments of a row
+  static constexpr int SEG = TT * 128;            // bytes of one segment of a tile
+  static constexpr int TILE = SEGS * SEG;
+  static constexpr int SLOTS = D == 128 ? 5 : 10; // K and V tiles in flight
+  static constexpr int DATA = (SLOTS + 2) * TILE; // the ring and two Q tiles
+  static constexpr int AUX = 2560;                // barriers, row states, flags
+  static constexpr size_t SMEM = (size_t)DATA + AUX + 512;
+};
+
+struct TcBars {  // one mbarrier each
+  uint64_t full[10], empty[10], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], done;
+};
+struct TcAux {
+  float m[2][TT], l[2][TT];  // row states of the two streams
+  TcBars bar;
+  uint32_t tmem;
+  int bad_page;
+  int start_b, start_off;
+  int wsum[TC_WARPS];
+};
+static_assert(sizeof(TcAux) <= 2560, "aux region");
+
+// A CTA's unit that it starts and does not finish (b < 0: none).
+struct TcSplit {
+  int b, kvh, block, start, tiles, per, pad[2];
+};
+
+struct TcLaunch {
+  TreeLaunch a;
+  int box_rows;      // rows of a cache TMA box
+  int rows_max;      // rows a record may hold
+  TcSplit* split;    // [CTAs]
+  float* rec_ml;     // [2 CTAs][rows_max][2]
+  float* rec_o;      // [2 CTAs][rows_max][D]
+};
+
+// -------------------------------------------------------------------------- //
+// tensor-core primitives (inline PTX)
+// -------------------------------------------------------------------------- //
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte swizzle: start address, the byte
+// distances between 64-element repeats (lead) and between groups of 8 rows (step).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t step) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(step >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128; B is
+// K-major (rows of K) or N-major (V, d contiguous).
+__device__ constexpr uint32_t instr_desc(int n, bool b_nmajor) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_nmajor ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(TT >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void named_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// -------------------------------------------------------------------------- //
+// the list of tiles
+// -------------------------------------------------------------------------- //
+struct TcSeq {  // one sequence's share of the list
+  int c0, n, t;      // first token, tokens, cached keys
+  int blocks;        // units of one KV head
+  int cache_tiles;
+  int tiles;         // tiles of one KV head
+};
+
+// New-token tiles of the units before unit j: a causal unit sees the tokens up
+// to its own last one, a tree unit all of them (one tile).
+__device__ __forceinline__ int new_tiles_before(int j, int blocks, int n, int per_unit, bool causal) {
+  if (!causal) return j;
+  const bool all = j == blocks;
+  const int k = all ? j - 1 : j;  // units that end at their own last token
+  int s;
+  if (per_unit >= TT) {
+    s = (per_unit / TT) * (k * (k + 1) / 2);
+  } else {  // sum over i = 1 .. k of ceil(i / p)
+    const int p = TT / per_unit, q = k / p, r = k - q * p;
+    s = p * (q * (q + 1) / 2) + r * (q + 1);
+  }
+  return all ? s + (n + TT - 1) / TT : s;
+}
+
+__device__ __forceinline__ TcSeq tc_seq(const TreeLaunch& a, int b, int G) {
+  TcSeq s;
+  const int per_unit = UNIT_ROWS / G;
+  s.t = seq_len(a.kv, b);
+  s.n = seq_tokens(a.cu_new, b, a.T, a.max_new, a.kv.err, &s.c0);
+  s.blocks = (s.n + per_unit - 1) / per_unit;
+  s.cache_tiles = (s.t + TT - 1) / TT;
+  s.tiles = s.blocks == 0 ? 0
+                          : s.blocks * s.cache_tiles +
+                                new_tiles_before(s.blocks, s.blocks, s.n, per_unit, a.mask == nullptr);
+  return s;
+}
+
+// The walk over a CTA's run of the list, one unit at a time; every role of the
+// CTA makes the same walk.
+struct TcWalk {
+  TcSeq s;
+  int b, kvh, block;   // the current unit
+  int tile0, tile1;    // its tiles in this run
+  int unit_tiles;
+  int left;            // tiles of the run behind the current unit
+  int loads;           // K and V tiles loaded before the current unit
+  int qtiles;          // Q tiles loaded before the current unit
+  int G, per_unit;
+
+  __device__ __forceinline__ int unit_size(const TreeLaunch& a, int j) const {
+    const bool causal = a.mask == nullptr;
+    return s.cache_tiles + new_tiles_before(j + 1, s.blocks, s.n, per_unit, causal) -
+           new_tiles_before(j, s.blocks, s.n, per_unit, causal);
+  }
+  __device__ __forceinline__ void begin(const TreeLaunch& a, int b0, int off, int count) {
+    G = a.kv.Hq / a.kv.Hkv;
+    per_unit = UNIT_ROWS / G;
+    b = b0;
+    s = tc_seq(a, b, G);
+    kvh = off / s.tiles;
+    off -= kvh * s.tiles;
+    int lo = 0, hi = s.blocks - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      const int before = mid * s.cache_tiles + new_tiles_before(mid, s.blocks, s.n, per_unit, a.mask == nullptr);
+      if (before <= off) lo = mid; else hi = mid - 1;
+    }
+    block = lo;
+    tile0 = off - (lo * s.cache_tiles + new_tiles_before(lo, s.blocks, s.n, per_unit, a.mask == nullptr));
+    unit_tiles = unit_size(a, block);
+    tile1 = min(unit_tiles, tile0 + count);
+    left = count - (tile1 - tile0);
+    loads = qtiles = 0;
+  }
+  __device__ __forceinline__ bool next(const TreeLaunch& a) {
+    if (left == 0) return false;
+    loads += 2 * (tile1 - tile0);
+    qtiles += single() ? 1 : 2;
+    if (++block == s.blocks) {
+      block = 0;
+      if (++kvh == a.kv.Hkv) {
+        kvh = 0;
+        do s = tc_seq(a, ++b, G);
+        while (s.blocks == 0);
+      }
+    }
+    tile0 = 0;
+    unit_tiles = unit_size(a, block);
+    tile1 = min(unit_tiles, left);
+    left -= tile1;
+    return true;
+  }
+  __device__ __forceinline__ int rows() const { return min(UNIT_ROWS, (s.n - block * per_unit) * G); }
+  __device__ __forceinline__ bool single() const { return rows() <= TT; }
+  // steps of the unit: step x is stream x & 1 on tile tile0 + (single ? x : x / 2)
+  __device__ __forceinline__ int steps() const { return single() ? tile1 - tile0 : 2 * (tile1 - tile0); }
+  // Order of the loads: as the issuer first uses them (S of steps 0 and 1, then
+  // O of step x and S of step x + 2).
+  __device__ __forceinline__ int load_k(int i) const { return loads + (single() ? max(0, 2 * i - 1) : 2 * i); }
+  __device__ __forceinline__ int load_v(int i) const {
+    return loads + (single() ? min(2 * i + 2, 2 * (tile1 - tile0) - 1) : 2 * i + 1);
+  }
+};
+
+// -------------------------------------------------------------------------- //
+// the kernel
+// -------------------------------------------------------------------------- //
+template <int D>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap knmap,
+                   const __grid_constant__ CUtensorMap vnmap, const __grid_constant__ TcLaunch p) {
+  using S = TcShape<D>;
+  extern __shared__ __align__(1024) uint8_t tc_smem[];
+  const TreeLaunch& a = p.a;
+  const KVView& kv = a.kv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = kv.Hq / kv.Hkv, B = kv.B;
+  const uint32_t base = (smem_addr(tc_smem) + 1023) & ~1023u;
+  uint8_t* data = tc_smem + (base - smem_addr(tc_smem));
+  TcAux& aux = *reinterpret_cast<TcAux*>(data + S::DATA);
+  TcBars& bar = aux.bar;
+
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's run of the list of all tiles ----
+  const int per_t = (B + TC_THREADS - 1) / TC_THREADS;
+  int mine = 0;
+  for (int k = 0; k < per_t; k++) {
+    const int b = tid * per_t + k;
+    if (b < B) mine += kv.Hkv * tc_seq(a, b, G).tiles;
+  }
+  int run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL_MASK, run, o);
+    if (lane >= o) run += y;
+  }
+  if (lane == 31) aux.wsum[warp] = run;
+  if (tid == 0) {
+    for (int i = 0; i < S::SLOTS; i++) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&bar.qfull[i], 1);
+      mbar_init(&bar.qempty[i], 1);
+      mbar_init(&bar.sfull[i], 1);
+      mbar_init(&bar.pfull[i], TT);
+      mbar_init(&bar.ofull[i], 1);
+    }
+    mbar_init(&bar.done, 1);
+    fence_barrier_init();
+    aux.bad_page = 0;
+    // the alignment of the data region must leave room for the aux region
+    if (base - smem_addr(tc_smem) > 512) raise_error(kv.err, PRHS_DEV_CAPACITY);
+  }
+  __syncthreads();
+  int total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < TC_WARPS; w++) {
+    if (w < warp) before += aux.wsum[w];
+    total += aux.wsum[w];
+  }
+  before += run - mine;
+  const int per = (total + gridDim.x - 1) / (int)gridDim.x;
+  const int g0 = blockIdx.x * per, count = min(total, g0 + per) - g0;
+  if (count <= 0 || base - smem_addr(tc_smem) > 512) {
+    if (tid == 0) p.split[blockIdx.x].b = -1;
+    return;
+  }
+  if (g0 >= before && g0 < before + mine) {
+    int off = g0 - before;
+    for (int k = 0; k < per_t; k++) {
+      const int b = tid * per_t + k, x = kv.Hkv * tc_seq(a, b, G).tiles;
+      if (off < x) {
+        aux.start_b = b;
+        aux.start_off = off;
+        break;
+      }
+      off -= x;
+    }
+  }
+  if (warp == 9) {  // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&aux.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = aux.tmem;
+  TcWalk w;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_REST));
+    w.begin(a, aux.start_b, aux.start_off, count);
+    if (warp == 8) {
+      // ------------------------------ producer ------------------------------ //
+      if (lane == 0) {
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+      }
+      const int box = lane & 7, seg = lane >> 3;  // a lane copies one box of one segment
+      int issued = 0;
+      bool ok = true;
+      do {
+        const bool single = w.single();
+        const int nt = w.tile1 - w.tile0;
+        // row of this lane's box of load l, or -1 where there is none
+        auto lookup = [&](int l, bool& is_v, bool& fresh, int& boxes, int& rows) -> long long {
+          int i;
+          if (single) {
+            is_v = l == 2 * nt - 1 || (l > 0 && (l & 1) == 0);
+            i = l == 2 * nt - 1 ? nt - 1 : is_v ? (l - 2) / 2 : (l + 1) / 2;
+          } else {
+            is_v = l & 1;
+            i = l >> 1;
+          }
+          const int tile = w.tile0 + i;
+          fresh = tile >= w.s.cache_tiles;
+          const int key0 = (fresh ? tile - w.s.cache_tiles : tile) * TT;
+          const int valid = min(TT, (fresh ? w.s.n : w.s.t) - key0);
+          rows = fresh ? 16 : p.box_rows;
+          boxes = (valid + rows - 1) / rows;
+          if (box >= boxes || seg >= S::SEGS) return -1;
+          if (fresh) return w.s.c0 + key0 + box * rows;
+          long long row = kv_row(kv, w.b, w.kvh, key0 + box * rows);
+          if (row < 0) {  // not attended: the softmax masks its keys
+            raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
+            *reinterpret_cast<volatile int*>(&aux.bad_page) = 1;
+            __threadfence_block();
+            row = 0;
+          }
+          return row;
+        };
+        bool is_v, fresh, nv = false, nf = false;
+        int boxes, rows, nb = 0, nr = 0;
+        long long row = lookup(0, is_v, fresh, boxes, rows), nrow = -1;
+        for (int l = 0; ok && l < 2 * nt; l++) {
+          if (l + 1 < 2 * nt) nrow = lookup(l + 1, nv, nf, nb, nr);  // in flight during the wait
+          const int g = w.loads + l, slot = g % S::SLOTS;
+          if (lane == 0) ok = mbar_wait(&bar.empty[slot], ((g / S::SLOTS) & 1) ^ 1, kv.err);
+          ok = __shfl_sync(FULL_MASK, ok, 0);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128 * S::SEGS);
+          __syncwarp();
+          if (row >= 0) {
+            const uint32_t dst = base + slot * S::TILE + seg * S::SEG + box * rows * 128;
+            if (fresh)
+              tma_load_4d(dst, is_v ? &vnmap : &knmap, 0, seg, w.kvh, (int)row, &bar.full[slot]);
+            else
+              tma_load_3d(data + (dst - base), is_v ? &vmap : &kmap, 0, seg, (int)row, &bar.full[slot]);
+          }
+          __syncwarp();
+          issued = g + 1;
+          row = nrow;
+          is_v = nv;
+          fresh = nf;
+          boxes = nb;
+          rows = nr;
+        }
+      } while (ok && w.next(a));
+      // nothing may still be in flight when the CTA ends
+      if (lane == 0)
+        for (int g = max(0, issued - S::SLOTS); g < issued; g++)
+          mbar_wait(&bar.full[g % S::SLOTS], (g / S::SLOTS) & 1, kv.err);
+    } else if (warp == 10) {
+      // ----------------------- Q producer: one tile a unit, or two ----------------------- //
+      int issued = 0;
+      bool ok = true;
+      do {
+        for (int i = 0; ok && i < (w.single() ? 1 : 2); i++) {
+          const int qt = w.qtiles + i, slot = qt & 1;
+          if (lane == 0) ok = mbar_wait(&bar.qempty[slot], ((qt >> 1) & 1) ^ 1, kv.err);
+          ok = __shfl_sync(FULL_MASK, ok, 0);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[slot], S::TILE);
+          __syncwarp();
+          if (lane < S::SEGS)
+            tma_load_4d(base + (S::SLOTS + slot) * S::TILE + lane * S::SEG, &qmap, 0, lane, w.kvh * G,
+                        w.s.c0 + w.block * w.per_unit + i * (TT / G), &bar.qfull[slot]);
+          issued = qt + 1;
+        }
+      } while (ok && w.next(a));
+      if (lane == 0)
+        for (int qt = max(0, issued - 2); qt < issued; qt++)
+          mbar_wait(&bar.qfull[qt & 1], (qt >> 1) & 1, kv.err);
+    } else if (warp == 9) {
+      // ---------------------------- matrix issuer ---------------------------- //
+      if (lane == 0) {
+        constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(D, true);
+        bool ok = true;
+        int np[2] = {0, 0};  // softmax results taken from each stream
+        do {
+          const bool single = w.single();
+          const int steps = w.steps();
+          auto issue_qk = [&](int x) {
+            const int st = x & 1, i = single ? x : x >> 1;
+            const int qt = w.qtiles + (single ? 0 : st), qslot = qt & 1;
+            const int g = w.load_k(i), slot = g % S::SLOTS;
+            ok = ok && mbar_wait(&bar.qfull[qslot], (qt >> 1) & 1, kv.err);
+            ok = ok && mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err);
+            if (!ok) return;
+            const uint32_t q0 = base + (S::SLOTS + qslot) * S::TILE, k0 = base + slot * S::TILE;
+#pragma unroll
+            for (int k = 0; k < D / 16; k++) {
+              const uint32_t off = (k / 4) * S::SEG + (k % 4) * 32;
+              mma_ss(tmem + st * TT, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), QK, k > 0);
+            }
+            if (single || st == 1) tc_commit(&bar.empty[slot]);
+            if (single ? x == steps - 1 : x >= steps - 2) tc_commit(&bar.qempty[qslot]);
+            tc_commit(&bar.sfull[st]);
+          };
+          issue_qk(0);
+          if (steps > 1) issue_qk(1);
+          for (int x = 0; ok && x < steps; x++) {
+            const int st = x & 1, i = single ? x : x >> 1;
+            const int g = w.load_v(i), slot = g % S::SLOTS;
+            ok = ok && mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err);
+            ok = ok && mbar_wait(&bar.pfull[st], np[st] & 1, kv.err);
+            if (!ok) break;
+            np[st]++;
+            tc_fence_after();
+            const uint32_t v0 = base + slot * S::TILE;
+#pragma unroll
+            for (int k = 0; k < TT / 16; k++)
+              mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + k * 8, smem_desc(v0 + k * 2048, S::SEG, 1024), PV,
+                     x > 1 || k > 0);
+            if (single || st == 1) tc_commit(&bar.empty[slot]);
+            if (x + 2 >= steps) tc_commit(&bar.ofull[st]);
+            if (x + 2 < steps) issue_qk(x + 2);
+          }
+        } while (ok && w.next(a));
+        // nothing may still be in flight when tensor memory is freed
+        tc_commit(&bar.done);
+        mbar_wait(&bar.done, 0, kv.err);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_REGS_SOFTMAX));
+    w.begin(a, aux.start_b, aux.start_off, count);
+    // ------------------------------- softmax ------------------------------- //
+    const int st = warp >> 2;                     // stream
+    const int row = (warp & 3) * 32 + lane;       // its row, and the V row it may zero
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + st * TT;
+    const bool flip = a.scale < 0.f;
+    // a zero scale keeps masked logits at -inf (0 * inf is not a number)
+    const float sc = fmaxf(fabsf(a.scale) * TC_LOG2E, 1e-30f);
+    bool dead = false;
+    int ns = 0, no = 0;  // S tiles and O tiles taken
+    do {
+      const bool single = w.single();
+      const int steps = w.steps();
+      const int ur = (single ? 0 : st * TT) + row;         // row of the unit
+      const int tok = w.block * w.per_unit + ur / G;        // token of the sequence
+      const int tok_c = min(tok, w.s.n - 1);
+      const int tok_first = w.block * w.per_unit + (single ? 0 : st * (TT / G));
+      // a warp without rows computes nothing: rows do not mix, so what its part of
+      // S and O holds reaches no result
+      const bool idle = (single ? 0 : st * TT) + (warp & 3) * 32 >= w.rows();
+      float m = -INFINITY, l = 0.f;
+      for (int x = st; x < steps; x += 2) {
+        const int i = single ? x : x >> 1, tile = w.tile0 + i;
+        const bool fresh = tile >= w.s.cache_tiles;
+        const int key0 = (fresh ? tile - w.s.cache_tiles : tile) * TT;
+        const int valid = (fresh ? w.s.n : w.s.t) - key0;   // keys of the tile, at least 1
+        if (!dead) dead = !__all_sync(FULL_MASK, mbar_wait(&bar.sfull[st], ns & 1, kv.err));
+        ns++;
+        if (dead) continue;
+        tc_fence_after();
+        // keys that exist, the same for every row (their V rows are zeroed below)
+        uint32_t have[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool bad = !fresh && kv.block_table != nullptr && *reinterpret_cast<volatile int*>(&aux.bad_page) != 0;
+        const bool cut = valid < TT || bad;
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const int k = valid - c * 32;
+            have[c] = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1;
+            if (bad)
+#pragma unroll
+              for (int h = 0; h < 2; h++)
+                if ((c * 2 + h) * 16 < valid && kv_row(kv, w.b, w.kvh, key0 + (c * 2 + h) * 16) < 0)
+                  have[c] &= h ? 0xffffu : 0xffff0000u;
+          }
+        }
+        if (!idle) {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; c++) tmem_ld32(r[c], s_addr + c * 32);
+          tc_wait_ld();
+          if (flip) {
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+#pragma unroll
+              for (int e = 0; e < 32; e++) r[c][e] ^= 0x80000000u;
+          }
+          const bool by_row = fresh && (a.mask != nullptr || key0 + TT - 1 > tok_first);
+          if (cut || by_row) {
+            uint32_t see[4] = {have[0], have[1], have[2], have[3]};
+            if (by_row) {
+              if (a.mask != nullptr) {
+                const uint4 t4 = reinterpret_cast<const uint4*>(a.mask)[w.s.c0 + tok_c];
+                see[0] &= t4.x;
+                see[1] &= t4.y;
+                see[2] &= t4.z;
+                see[3] &= t4.w;
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                  const int k = tok_c + 1 - key0 - c * 32;
+                  see[c] &= k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1;
+                }
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+#pragma unroll
+              for (int e = 0; e < 32; e++)
+                if (!((see[c] >> e) & 1u)) r[c][e] = 0xff800000u;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; c++)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mx = fmaxf(mx, fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
+          mx *= sc;
+          const bool grow = mx > m + RESCALE_LOG2 || (m == -INFINITY && mx > m);
+          const float corr = grow ? ex2(m - mx) : 1.f;
+          if (grow) m = mx;
+          if (x >= 2 && __any_sync(FULL_MASK, grow)) {
+            // O holds the stream's earlier tiles: S of this step came after them
+            l *= corr;
+#pragma unroll
+            for (int c = 0; c < D / 32; c++) {
+              uint32_t o[32];
+              const uint32_t oa = tmem + lanes + 2 * TT + st * D + c * 32;
+              tmem_ld32(o, oa);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32(oa, o);
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; c++)
+#pragma unroll
+            for (int e = 0; e < 32; e++) {
+              const float v = ex2(fmaf(__uint_as_float(r[c][e]), sc, -mm));
+              sum[e & 3] += v;
+              r[c][e] = __float_as_uint(v);
+            }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            uint32_t q[32];
+#pragma unroll
+            for (int e = 0; e < 32; e++)
+              q[e] = pack2(__uint_as_float(r[2 * c + e / 16][2 * (e % 16)]), __uint_as_float(r[2 * c + e / 16][2 * (e % 16) + 1]));
+            tmem_st32(s_addr + c * 32, q);
+          }
+        }
+        if (cut) {
+          // V rows of keys that do not exist hold whatever was there, possibly not
+          // finite, and 0 * inf would reach every row: they are set to 0
+          const int g = w.load_v(i), slot = g % S::SLOTS;
+          if (!dead) dead = !__all_sync(FULL_MASK, mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
+          const uint32_t hw = row < 32 ? have[0] : row < 64 ? have[1] : row < 96 ? have[2] : have[3];
+          if (!dead && !((hw >> (row & 31)) & 1u)) {
+#pragma unroll
+            for (int sg = 0; sg < S::SEGS; sg++)
+#pragma unroll
+              for (int c = 0; c < 8; c++)
+                *reinterpret_cast<uint4*>(data + slot * S::TILE + sg * S::SEG + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.pfull[st]);
+      }
+
+      // ---- the unit's end in this run: result or partial record ----
+      const bool mine_any = steps > st, both = single;
+      if (mine_any) {
+        if (!dead) dead = !__all_sync(FULL_MASK, mbar_wait(&bar.ofull[st], no & 1, kv.err));
+        no++;
+      }
+      float w0 = 1.f, w1 = 0.f, M = m, L = l;
+      if (both) {
+        aux.m[st][row] = m;
+        aux.l[st][row] = l;
+        tc_fence_before();
+        named_bar(1, 2 * TT);
+        const float m0 = aux.m[0][row], m1 = aux.m[1][row];
+        M = fmaxf(m0, m1);
+        w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
+        w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        L = w0 * aux.l[0][row] + w1 * aux.l[1][row];
+      }
+      tc_fence_after();
+      const bool whole = w.tile0 == 0 && w.tile1 == w.unit_tiles;
+      const int rec = 2 * blockIdx.x + (w.tile0 == 0 ? 1 : 0);
+      const bool live = ur < w.rows() && !dead;
+      const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+      const int h = ur - (ur / G) * G;
+      const long long orow = (long long)(w.s.c0 + tok) * kv.Hq + w.kvh * G + h;
+      // both warpgroups of a shared unit write half the columns each
+      const int c_lo = both ? st * (D / 64) : 0, c_hi = both ? c_lo + D / 64 : D / 32;
+      const bool two = both && steps > 1;
+      for (int c = c_lo; c < c_hi; c++) {
+        uint32_t o[32];
+        tmem_ld32(o, tmem + lanes + 2 * TT + (both ? 0 : st * D) + c * 32);
+        if (two) {
+          uint32_t o1[32];
+          tmem_ld32(o1, tmem + lanes + 2 * TT + D + c * 32);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e++)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * (w0 * inv) + __uint_as_float(o1[e]) * (w1 * inv));
+        } else {
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * (w0 * inv));
+        }
+        if (!live) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            dst[e] = make_uint4(pack2(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                                pack2(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                                pack2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                                pack2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.rec_o + ((long long)rec * p.rows_max + ur) * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (live && (!both || st == 0)) {
+        if (whole) {
+          a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
+        } else {
+          float* ml = p.rec_ml + ((long long)rec * p.rows_max + ur) * 2;
+          ml[0] = M;
+          ml[1] = L;
+        }
+      }
+      tc_fence_before();
+      if (both) named_bar(1, 2 * TT);  // both outputs and the row states are read
+    } while (w.next(a));
+    if (tid == 0) {
+      TcSplit sp;
+      const bool open = w.tile0 == 0 && w.tile1 < w.unit_tiles;
+      sp.b = open ? w.b : -1;
+      sp.kvh = w.kvh;
+      sp.block = w.block;
+      sp.start = g0 + count - w.tile1;
+      sp.tiles = w.unit_tiles;
+      sp.per = per;
+      p.split[blockIdx.x] = sp;
+    }
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// Joins the partial states of the units that a run's end cut: one warp per
+// row, over the records of the CTA that began the unit and of those after it.
+constexpr int JOIN_WARPS = 8;
+template <int D>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TcLaunch p) {
+  pdl_wait();
+  pdl_trigger();
+  const TreeLaunch& a = p.a;
+  const TcSplit sp = p.split[blockIdx.x];
+  if (sp.b < 0) return;
+  const int G = a.kv.Hq / a.kv.Hkv, per_unit = UNIT_ROWS / G;
+  const int c0 = a.cu_new[sp.b], n = a.cu_new[sp.b + 1] - c0;
+  const int rows = min(UNIT_ROWS, (n - sp.block * per_unit) * G);
+  const int lane = threadIdx.x & 31;
+  const int c_first = blockIdx.x, c_last = (sp.start + sp.tiles - 1) / sp.per;
+  constexpr int F = D / 32;  // floats a lane
+  for (int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); row < rows; row += gridDim.y * JOIN_WARPS) {
+    auto rec_of = [&](int c) { return (long long)(2 * c + (c == c_first ? 1 : 0)) * p.rows_max + row; };
+    float M = -INFINITY;
+    for (int c = c_first + lane; c <= c_last; c += 32) M = fmaxf(M, __ldcg(p.rec_ml + rec_of(c) * 2));
+    M = warp_max(M);
+    float L = 0.f, o[F];
+#pragma unroll
+    for (int f = 0; f < F; f++) o[f] = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll 4
+      for (int c = c_first; c <= c_last; c++) {
+        const long long r = rec_of(c);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + r * 2));
+        const float wt = exp2f(ml.x - M);
+        L += wt * ml.y;
+        if (F == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.rec_o + r * D) + lane);
+          o[0] += wt * x.x;
+          o[1] += wt * x.y;
+          o[F - 2] += wt * x.z;
+          o[F - 1] += wt * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(p.rec_o + r * D) + lane);
+          o[0] += wt * x.x;
+          o[1] += wt * x.y;
+        }
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int tok = sp.block * per_unit + row / G;
+    const long long orow = (long long)(c0 + tok) * a.kv.Hq + sp.kvh * G + row % G;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * F;
+    if (F == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[F - 2] * inv, o[F - 1] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack2(o[0] * inv, o[1] * inv);
+    if (lane == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
+  }
+}
+
+// -------------------------------------------------------------------------- //
+// host side
+// -------------------------------------------------------------------------- //
+static int tc_rows_max(const KVView& kv, int max_new) {
+  const long long r = (long long)max_new * (kv.Hq / kv.Hkv);
+  return (int)(r < UNIT_ROWS ? r : UNIT_ROWS);
+}
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t tree_tc_workspace(const KVView& kv, int max_new, int sms) {
+  const size_t rec = (size_t)2 * sms * tc_rows_max(kv, max_new);
+  return up256(sms * sizeof(TcSplit)) + up256(rec * 2 * sizeof(float)) + up256(rec * kv.d * sizeof(float));
+}
+
+// Rows of a TMA box of the cache: the most that a page holds whole boxes of.
+static int tc_box_rows(const KVView& kv) {
+  if (kv.block_table == nullptr) return 32;
+  int r = 16;
+  while (r < TT && kv.block_size % (2 * r) == 0) r *= 2;
+  return r;
+}
+
+template <int D>
+static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cudaStream_t st) {
+  using S = TcShape<D>;
+  auto k = tree_tc_kernel<D>;
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, k);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs < TC_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, dim3(sms), dim3(TC_THREADS), S::SMEM, st, p.a.kv.pdl, maps[0], maps[1], maps[2], maps[3], maps[4], p);
+  if (e != cudaSuccess) return e;
+  abi_count_launch();
+  return launch_pdl(tree_join_kernel<D>, dim3(sms, (p.rows_max + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,
+                    st, true, p);
+}
+
+prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t st, cudaError_t* err) {
+  *err = cudaSuccess;
+  const KVView& kv = a.kv;
+  const int G = kv.Hq / kv.Hkv;
+  TcLaunch p;
+  p.a = a;
+  p.box_rows = tc_box_rows(kv);
+  p.rows_max = tc_rows_max(kv, a.max_new);
+  char* w = static_cast<char*>(ws);
+  p.split = reinterpret_cast<TcSplit*>(w);
+  w += up256(sms * sizeof(TcSplit));
+  p.rec_ml = reinterpret_cast<float*>(w);
+  w += up256((size_t)2 * sms * p.rows_max * 2 * sizeof(float));
+  p.rec_o = reinterpret_cast<float*>(w);
+
+  CUtensorMap maps[5];
+  const uint64_t d = kv.d, row = d * 2, segs = d / 64;
+  const uint64_t cache_rows = kv.block_table != nullptr ? (uint64_t)kv.num_blocks * kv.Hkv * kv.block_size
+                                                        : (uint64_t)kv.B * kv.Hkv * kv.t_max;
+  const uint64_t qd[4] = {64, segs, (uint64_t)kv.Hq, (uint64_t)a.T}, qs[3] = {128, row, row * kv.Hq};
+  const uint32_t qb[4] = {64, 1, (uint32_t)G, (uint32_t)(TT / G)};
+  const uint64_t cd[3] = {64, segs, cache_rows}, cs[2] = {128, row};
+  const uint32_t cb[3] = {64, 1, (uint32_t)p.box_rows};
+  const uint64_t nd[4] = {64, segs, (uint64_t)kv.Hkv, (uint64_t)a.T};
+  const uint64_t ks[3] = {128, row, (uint64_t)a.ks * 2}, vs[3] = {128, row, (uint64_t)a.vs * 2};
+  const uint32_t nb[4] = {64, 1, 1, 16};
+  prhs_status s;
+  if ((s = abi_encode_bf16(&maps[0], a.q, 4, qd, qs, qb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[1], kv.k, 3, cd, cs, cb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[2], kv.v, 3, cd, cs, cb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[3], a.k_new, 4, nd, ks, nb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[4], a.v_new, 4, nd, vs, nb)) != PRHS_OK) return s;
+  *err = kv.d == 128 ? tc_go<128>(p, maps, sms, st) : tc_go<64>(p, maps, sms, st);
+  return PRHS_OK;
+}
+
+}  // namespace prhs
