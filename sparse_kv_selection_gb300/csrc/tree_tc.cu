@@ -41,7 +41,7 @@ namespace prhs {
 
 constexpr int TT = 128;                  // keys of a tile, rows of a stream
 constexpr int UNIT_ROWS = 2 * TT;
-constexpr int TC_WARPS = 12;             // 8 softmax, K/V producer, matrix issuer, Q producer, idle
+constexpr int TC_WARPS = 12;             // 8 softmax, K/V producer, matrix issuer, Q producer, scheduler
 // Registers a thread: the softmax warpgroups hold a row of logits each, so they
 // take over part of the third one's. The three shares add up to what the block
 // is launched with (checked before the launch: a larger sum would wait forever).
@@ -59,22 +59,49 @@ struct TcShape {
   static constexpr int TILE = SEGS * SEG;
   static constexpr int SLOTS = D == 128 ? 5 : 10; // K and V tiles in flight
   static constexpr int DATA = (SLOTS + 2) * TILE; // the ring and two Q tiles
-  static constexpr int AUX = 2560;                // barriers, row states, flags
-  static constexpr size_t SMEM = (size_t)DATA + AUX + 512;
+  static constexpr size_t SMEM = (size_t)DATA + 3072;
+};
+
+// One unit's tiles in a CTA's run, as the scheduler warp hands it to the others.
+constexpr int TC_WORKS = 4;
+struct __align__(16) TcWork {
+  int b, kvh, c0, n;        // sequence, KV head, first token, tokens
+  int t, tok0, rows, tile0; // cached keys, the unit's first token and rows, its first tile here
+  int nt, cache_tiles, loads, qtiles;  // tiles here; K and V / Q tiles loaded before
+  int whole, last, pad[2];  // all of the unit's tiles are here; the run ends with it
+
+  __device__ __forceinline__ bool single() const { return rows <= TT; }
+  // steps of the unit: step x is stream x & 1 on tile tile0 + (single ? x : x / 2)
+  __device__ __forceinline__ int steps() const { return single() ? nt : 2 * nt; }
+  // Order of the loads: as the issuer first uses them (S of steps 0 and 1, then
+  // O of step x and S of step x + 2).
+  __device__ __forceinline__ int load_tile(int l, bool& is_v) const {
+    if (!single()) {
+      is_v = l & 1;
+      return l >> 1;
+    }
+    const bool end = l == 2 * nt - 1;
+    is_v = end || (l > 0 && (l & 1) == 0);
+    return end ? nt - 1 : is_v ? (l - 2) >> 1 : (l + 1) >> 1;
+  }
+  __device__ __forceinline__ int load_k(int i) const { return loads + (single() ? max(0, 2 * i - 1) : 2 * i); }
+  __device__ __forceinline__ int load_v(int i) const { return loads + (single() ? min(2 * i + 2, 2 * nt - 1) : 2 * i + 1); }
 };
 
 struct TcBars {  // one mbarrier each
   uint64_t full[10], empty[10], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], done;
+  uint64_t wfull[TC_WORKS], wempty[TC_WORKS];
 };
 struct TcAux {
   float m[2][TT], l[2][TT];  // row states of the two streams
+  TcWork work[TC_WORKS];
   TcBars bar;
   uint32_t tmem;
   int bad_page;
   int start_b, start_off;
   int wsum[TC_WARPS];
 };
-static_assert(sizeof(TcAux) <= 2560, "aux region");
+static_assert(sizeof(TcAux) <= 3072, "aux region");
 
 // A CTA's unit that it starts and does not finish (b < 0: none).
 struct TcSplit {
@@ -83,7 +110,8 @@ struct TcSplit {
 
 struct TcLaunch {
   TreeLaunch a;
-  int box_rows;      // rows of a cache TMA box
+  int group_log2;    // log2 of the query heads of a KV head
+  int box_log2;      // log2 of the rows of a cache TMA box
   int rows_max;      // rows a record may hold
   TcSplit* split;    // [CTAs]
   float* rec_ml;     // [2 CTAs][rows_max][2]
@@ -127,6 +155,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
+// A whole logit row: 128 columns in four loads.
+__device__ __forceinline__ void tmem_ld_row(uint32_t (&r)[TT], uint32_t addr) {
+#pragma unroll
+  for (int c = 0; c < 4; c++) tmem_ld32(reinterpret_cast<uint32_t(&)[32]>(r[c * 32]), addr + c * 32);
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -158,10 +191,43 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
+// One lane of a converged warp. (A lane chosen by its number compiles to a loop
+// over the lanes around every instruction that takes uniform operands.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 numbers in one 64-bit register pair, and operations on both.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -182,101 +248,31 @@ struct TcSeq {  // one sequence's share of the list
   int tiles;         // tiles of one KV head
 };
 
-// New-token tiles of the units before unit j: a causal unit sees the tokens up
-// to its own last one, a tree unit all of them (one tile).
-__device__ __forceinline__ int new_tiles_before(int j, int blocks, int n, int per_unit, bool causal) {
+// New-token tiles of the units before unit j (1 << ul tokens each): a causal
+// unit sees the tokens up to its own last one, a tree unit all of them (one tile).
+__device__ __forceinline__ int new_tiles_before(int j, int blocks, int n, int ul, bool causal) {
   if (!causal) return j;
   const bool all = j == blocks;
   const int k = all ? j - 1 : j;  // units that end at their own last token
   int s;
-  if (per_unit >= TT) {
-    s = (per_unit / TT) * (k * (k + 1) / 2);
-  } else {  // sum over i = 1 .. k of ceil(i / p)
-    const int p = TT / per_unit, q = k / p, r = k - q * p;
-    s = p * (q * (q + 1) / 2) + r * (q + 1);
+  if (ul >= 7) {
+    s = (k * (k + 1) / 2) << (ul - 7);
+  } else {  // sum over i = 1 .. k of ceil(i / p), p = 2^(7 - ul)
+    const int pl = 7 - ul, q = k >> pl, r = k - (q << pl);
+    s = ((q * (q + 1) / 2) << pl) + r * (q + 1);
   }
-  return all ? s + (n + TT - 1) / TT : s;
+  return all ? s + ((n + TT - 1) >> 7) : s;
 }
 
-__device__ __forceinline__ TcSeq tc_seq(const TreeLaunch& a, int b, int G) {
+__device__ __forceinline__ TcSeq tc_seq(const TreeLaunch& a, int b, int ul) {
   TcSeq s;
-  const int per_unit = UNIT_ROWS / G;
   s.t = seq_len(a.kv, b);
   s.n = seq_tokens(a.cu_new, b, a.T, a.max_new, a.kv.err, &s.c0);
-  s.blocks = (s.n + per_unit - 1) / per_unit;
-  s.cache_tiles = (s.t + TT - 1) / TT;
-  s.tiles = s.blocks == 0 ? 0
-                          : s.blocks * s.cache_tiles +
-                                new_tiles_before(s.blocks, s.blocks, s.n, per_unit, a.mask == nullptr);
+  s.blocks = (s.n + (1 << ul) - 1) >> ul;
+  s.cache_tiles = (s.t + TT - 1) >> 7;
+  s.tiles = s.blocks == 0 ? 0 : s.blocks * s.cache_tiles + new_tiles_before(s.blocks, s.blocks, s.n, ul, a.mask == nullptr);
   return s;
 }
-
-// The walk over a CTA's run of the list, one unit at a time; every role of the
-// CTA makes the same walk.
-struct TcWalk {
-  TcSeq s;
-  int b, kvh, block;   // the current unit
-  int tile0, tile1;    // its tiles in this run
-  int unit_tiles;
-  int left;            // tiles of the run behind the current unit
-  int loads;           // K and V tiles loaded before the current unit
-  int qtiles;          // Q tiles loaded before the current unit
-  int G, per_unit;
-
-  __device__ __forceinline__ int unit_size(const TreeLaunch& a, int j) const {
-    const bool causal = a.mask == nullptr;
-    return s.cache_tiles + new_tiles_before(j + 1, s.blocks, s.n, per_unit, causal) -
-           new_tiles_before(j, s.blocks, s.n, per_unit, causal);
-  }
-  __device__ __forceinline__ void begin(const TreeLaunch& a, int b0, int off, int count) {
-    G = a.kv.Hq / a.kv.Hkv;
-    per_unit = UNIT_ROWS / G;
-    b = b0;
-    s = tc_seq(a, b, G);
-    kvh = off / s.tiles;
-    off -= kvh * s.tiles;
-    int lo = 0, hi = s.blocks - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      const int before = mid * s.cache_tiles + new_tiles_before(mid, s.blocks, s.n, per_unit, a.mask == nullptr);
-      if (before <= off) lo = mid; else hi = mid - 1;
-    }
-    block = lo;
-    tile0 = off - (lo * s.cache_tiles + new_tiles_before(lo, s.blocks, s.n, per_unit, a.mask == nullptr));
-    unit_tiles = unit_size(a, block);
-    tile1 = min(unit_tiles, tile0 + count);
-    left = count - (tile1 - tile0);
-    loads = qtiles = 0;
-  }
-  __device__ __forceinline__ bool next(const TreeLaunch& a) {
-    if (left == 0) return false;
-    loads += 2 * (tile1 - tile0);
-    qtiles += single() ? 1 : 2;
-    if (++block == s.blocks) {
-      block = 0;
-      if (++kvh == a.kv.Hkv) {
-        kvh = 0;
-        do s = tc_seq(a, ++b, G);
-        while (s.blocks == 0);
-      }
-    }
-    tile0 = 0;
-    unit_tiles = unit_size(a, block);
-    tile1 = min(unit_tiles, left);
-    left -= tile1;
-    return true;
-  }
-  __device__ __forceinline__ int rows() const { return min(UNIT_ROWS, (s.n - block * per_unit) * G); }
-  __device__ __forceinline__ bool single() const { return rows() <= TT; }
-  // steps of the unit: step x is stream x & 1 on tile tile0 + (single ? x : x / 2)
-  __device__ __forceinline__ int steps() const { return single() ? tile1 - tile0 : 2 * (tile1 - tile0); }
-  // Order of the loads: as the issuer first uses them (S of steps 0 and 1, then
-  // O of step x and S of step x + 2).
-  __device__ __forceinline__ int load_k(int i) const { return loads + (single() ? max(0, 2 * i - 1) : 2 * i); }
-  __device__ __forceinline__ int load_v(int i) const {
-    return loads + (single() ? min(2 * i + 2, 2 * (tile1 - tile0) - 1) : 2 * i + 1);
-  }
-};
 
 // -------------------------------------------------------------------------- //
 // the kernel
@@ -284,16 +280,17 @@ struct TcWalk {
 template <int D>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap knmap,
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ktail,
+                   const __grid_constant__ CUtensorMap vtail, const __grid_constant__ CUtensorMap knmap,
                    const __grid_constant__ CUtensorMap vnmap, const __grid_constant__ TcLaunch p) {
   using S = TcShape<D>;
   extern __shared__ __align__(1024) uint8_t tc_smem[];
   const TreeLaunch& a = p.a;
   const KVView& kv = a.kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = kv.Hq / kv.Hkv, B = kv.B;
-  const uint32_t base = (smem_addr(tc_smem) + 1023) & ~1023u;
-  uint8_t* data = tc_smem + (base - smem_addr(tc_smem));
+  const int B = kv.B, gl = p.group_log2, ul = 8 - gl;  // log2 of the group and of a unit's tokens
+  const uint32_t base = smem_addr(tc_smem);
+  uint8_t* data = tc_smem;
   TcAux& aux = *reinterpret_cast<TcAux*>(data + S::DATA);
   TcBars& bar = aux.bar;
 
@@ -305,7 +302,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   int mine = 0;
   for (int k = 0; k < per_t; k++) {
     const int b = tid * per_t + k;
-    if (b < B) mine += kv.Hkv * tc_seq(a, b, G).tiles;
+    if (b < B) mine += kv.Hkv * tc_seq(a, b, ul).tiles;
   }
   int run = mine;
 #pragma unroll
@@ -326,15 +323,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(&bar.pfull[i], TT);
       mbar_init(&bar.ofull[i], 1);
     }
+    for (int i = 0; i < TC_WORKS; i++) {
+      mbar_init(&bar.wfull[i], 1);
+      mbar_init(&bar.wempty[i], TC_WARPS - 1);
+    }
     mbar_init(&bar.done, 1);
     fence_barrier_init();
     aux.bad_page = 0;
-    // the alignment of the data region must leave room for the aux region
-    if (base - smem_addr(tc_smem) > 512) raise_error(kv.err, PRHS_DEV_CAPACITY);
+    if ((base & 1023) != 0) raise_error(kv.err, PRHS_DEV_CAPACITY);  // the swizzle needs it
   }
   __syncthreads();
   int total = 0, before = 0;
-#pragma unroll
   for (int w = 0; w < TC_WARPS; w++) {
     if (w < warp) before += aux.wsum[w];
     total += aux.wsum[w];
@@ -342,14 +341,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   before += run - mine;
   const int per = (total + gridDim.x - 1) / (int)gridDim.x;
   const int g0 = blockIdx.x * per, count = min(total, g0 + per) - g0;
-  if (count <= 0 || base - smem_addr(tc_smem) > 512) {
+  if (count <= 0 || (base & 1023) != 0) {
     if (tid == 0) p.split[blockIdx.x].b = -1;
     return;
   }
   if (g0 >= before && g0 < before + mine) {
     int off = g0 - before;
     for (int k = 0; k < per_t; k++) {
-      const int b = tid * per_t + k, x = kv.Hkv * tc_seq(a, b, G).tiles;
+      const int b = tid * per_t + k, x = kv.Hkv * tc_seq(a, b, ul).tiles;
       if (off < x) {
         aux.start_b = b;
         aux.start_off = off;
@@ -367,157 +366,243 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = aux.tmem;
-  TcWalk w;
+
+  // The next unit of the run, false when a wait gave up. Every warp but the
+  // scheduler's takes each one once.
+  int taken = 0;
+  auto take = [&](TcWork& w) -> bool {
+    const int i = taken & (TC_WORKS - 1);
+    const bool ok = __all_sync(FULL_MASK, mbar_wait(&bar.wfull[i], (taken / TC_WORKS) & 1, kv.err));
+    if (ok) w = aux.work[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.wempty[i]);
+    taken++;
+    return ok;
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_REST));
-    w.begin(a, aux.start_b, aux.start_off, count);
-    if (warp == 8) {
-      // ------------------------------ producer ------------------------------ //
-      if (lane == 0) {
-        prefetch_tmap(&kmap);
-        prefetch_tmap(&vmap);
+    if (warp == 11) {
+      // ------------------------------ scheduler ------------------------------ //
+      int b = aux.start_b, off = aux.start_off, left = count, loads = 0, qtiles = 0;
+      const bool causal = a.mask == nullptr;
+      TcSeq s = tc_seq(a, b, ul);
+      int kvh = off / s.tiles;
+      off -= kvh * s.tiles;
+      int block = 0, hi = s.blocks - 1;
+      while (block < hi) {
+        const int mid = (block + hi + 1) >> 1;
+        if (mid * s.cache_tiles + new_tiles_before(mid, s.blocks, s.n, ul, causal) <= off) block = mid; else hi = mid - 1;
       }
-      const int box = lane & 7, seg = lane >> 3;  // a lane copies one box of one segment
-      int issued = 0;
-      bool ok = true;
-      do {
-        const bool single = w.single();
-        const int nt = w.tile1 - w.tile0;
-        // row of this lane's box of load l, or -1 where there is none
-        auto lookup = [&](int l, bool& is_v, bool& fresh, int& boxes, int& rows) -> long long {
-          int i;
-          if (single) {
-            is_v = l == 2 * nt - 1 || (l > 0 && (l & 1) == 0);
-            i = l == 2 * nt - 1 ? nt - 1 : is_v ? (l - 2) / 2 : (l + 1) / 2;
-          } else {
-            is_v = l & 1;
-            i = l >> 1;
+      off -= block * s.cache_tiles + new_tiles_before(block, s.blocks, s.n, ul, causal);
+      for (int k = 0;; k++) {
+        const int tiles = s.cache_tiles + new_tiles_before(block + 1, s.blocks, s.n, ul, causal) -
+                          new_tiles_before(block, s.blocks, s.n, ul, causal);
+        const int nt = min(tiles - off, left);
+        left -= nt;
+        const int i = k & (TC_WORKS - 1);
+        if (!mbar_wait(&bar.wempty[i], ((k / TC_WORKS) & 1) ^ 1, kv.err)) break;
+        const int rows = min(UNIT_ROWS, (s.n - (block << ul)) << gl);
+        if (lane == 0) {
+          TcWork& w = aux.work[i];
+          w.b = b;
+          w.kvh = kvh;
+          w.c0 = s.c0;
+          w.n = s.n;
+          w.t = s.t;
+          w.tok0 = block << ul;
+          w.rows = rows;
+          w.tile0 = off;
+          w.nt = nt;
+          w.cache_tiles = s.cache_tiles;
+          w.loads = loads;
+          w.qtiles = qtiles;
+          w.whole = nt == tiles;
+          w.last = left == 0;
+          mbar_arrive(&bar.wfull[i]);
+          if (left == 0) {
+            TcSplit sp;
+            sp.b = off == 0 && nt < tiles ? b : -1;
+            sp.kvh = kvh;
+            sp.block = block;
+            sp.start = g0 + count - nt;
+            sp.tiles = tiles;
+            sp.per = per;
+            p.split[blockIdx.x] = sp;
           }
-          const int tile = w.tile0 + i;
-          fresh = tile >= w.s.cache_tiles;
-          const int key0 = (fresh ? tile - w.s.cache_tiles : tile) * TT;
-          const int valid = min(TT, (fresh ? w.s.n : w.s.t) - key0);
-          rows = fresh ? 16 : p.box_rows;
-          boxes = (valid + rows - 1) / rows;
-          if (box >= boxes || seg >= S::SEGS) return -1;
-          if (fresh) return w.s.c0 + key0 + box * rows;
-          long long row = kv_row(kv, w.b, w.kvh, key0 + box * rows);
-          if (row < 0) {  // not attended: the softmax masks its keys
+        }
+        if (left == 0) break;
+        loads += 2 * nt;
+        qtiles += rows <= TT ? 1 : 2;
+        off = 0;
+        if (++block == s.blocks) {
+          block = 0;
+          if (++kvh == kv.Hkv) {
+            kvh = 0;
+            do s = tc_seq(a, ++b, ul);
+            while (s.blocks == 0);
+          }
+        }
+      }
+    } else if (warp == 8) {
+      // -------------------------- K and V producer -------------------------- //
+      const bool leader = elect_one();
+      const int br_log2 = p.box_log2, br = 1 << br_log2, per_log2 = 7 - br_log2;
+      int last = -1;
+      TcWork w;
+      bool ok = take(w);
+      while (ok) {
+        // Rows of the cache's boxes, 32 boxes at a time, one a lane; the page of
+        // the next 32 is read while these are used. V is up to two tiles behind K.
+        auto page_of = [&](int box) -> int {
+          const int key = box << br_log2;
+          if (kv.block_table == nullptr || key >= w.t) return 0;
+          return kv.block_table[(long long)w.b * kv.max_blocks + key / kv.block_size];
+        };
+        auto row_of = [&](int page, int box) -> int {
+          const int key = box << br_log2;
+          if (kv.block_table == nullptr) return (w.b * kv.Hkv + w.kvh) * kv.t_max + key;
+          if ((unsigned)page >= (unsigned)kv.num_blocks) {  // the softmax masks its keys
             raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
             *reinterpret_cast<volatile int*>(&aux.bad_page) = 1;
             __threadfence_block();
-            row = 0;
+            page = 0;
           }
-          return row;
+          return (page * kv.Hkv + w.kvh) * kv.block_size + key % kv.block_size;
         };
-        bool is_v, fresh, nv = false, nf = false;
-        int boxes, rows, nb = 0, nr = 0;
-        long long row = lookup(0, is_v, fresh, boxes, rows), nrow = -1;
-        for (int l = 0; ok && l < 2 * nt; l++) {
-          if (l + 1 < 2 * nt) nrow = lookup(l + 1, nv, nf, nb, nr);  // in flight during the wait
+        int win = (w.tile0 << per_log2) - 32, rows = 0, behind = 0, ahead = 0;
+        if (w.tile0 < w.cache_tiles) ahead = page_of(win + 32 + lane);
+        for (int l = 0; ok && l < 2 * w.nt; l++) {
+          bool is_v;
+          const int tile = w.tile0 + w.load_tile(l, is_v);
+          const bool fresh = tile >= w.cache_tiles;
+          const int key0 = (fresh ? tile - w.cache_tiles : tile) * TT;
+          const int valid = min(TT, (fresh ? w.n : w.t) - key0);
+          const int step_log2 = fresh || valid < TT ? 4 : br_log2;  // rows of a box
+          const int boxes = (valid + (1 << step_log2) - 1) >> step_log2;
+          if (!fresh && (tile << per_log2) >= win + 32) {
+            win += 32;
+            behind = rows;
+            rows = row_of(ahead, win + lane);
+            ahead = page_of(win + 32 + lane);
+          }
           const int g = w.loads + l, slot = g % S::SLOTS;
-          if (lane == 0) ok = mbar_wait(&bar.empty[slot], ((g / S::SLOTS) & 1) ^ 1, kv.err);
-          ok = __shfl_sync(FULL_MASK, ok, 0);
+          ok = __all_sync(FULL_MASK, mbar_wait(&bar.empty[slot], ((g / S::SLOTS) & 1) ^ 1, kv.err));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128 * S::SEGS);
-          __syncwarp();
-          if (row >= 0) {
-            const uint32_t dst = base + slot * S::TILE + seg * S::SEG + box * rows * 128;
-            if (fresh)
-              tma_load_4d(dst, is_v ? &vnmap : &knmap, 0, seg, w.kvh, (int)row, &bar.full[slot]);
-            else
-              tma_load_3d(data + (dst - base), is_v ? &vmap : &kmap, 0, seg, (int)row, &bar.full[slot]);
+          if (leader) mbar_arrive_expect_tx(&bar.full[slot], (boxes << step_log2) * 128 * S::SEGS);
+          const CUtensorMap* map = fresh ? (is_v ? &vnmap : &knmap)
+                                         : step_log2 == br_log2 ? (is_v ? &vmap : &kmap) : (is_v ? &vtail : &ktail);
+          const uint32_t dst = base + slot * S::TILE;
+#pragma unroll 2
+          for (int x = 0; x < boxes; x++) {
+            const int key = x << step_log2;  // within the tile
+            const int bx = (tile << per_log2) + (key >> br_log2) - win;
+            const int row = __shfl_sync(FULL_MASK, bx < 0 ? behind : rows, bx & 31) + (key & (br - 1));
+            if (leader) {
+#pragma unroll
+              for (int sg = 0; sg < S::SEGS; sg++)
+                tma_load_4d(dst + sg * S::SEG + key * 128, map, 0, sg, fresh ? w.kvh : row,
+                            fresh ? w.c0 + key0 + key : 0, &bar.full[slot]);
+            }
           }
           __syncwarp();
-          issued = g + 1;
-          row = nrow;
-          is_v = nv;
-          fresh = nf;
-          boxes = nb;
-          rows = nr;
+          last = g;
         }
-      } while (ok && w.next(a));
+        if (!ok || w.last) break;
+        ok = take(w);
+      }
       // nothing may still be in flight when the CTA ends
-      if (lane == 0)
-        for (int g = max(0, issued - S::SLOTS); g < issued; g++)
-          mbar_wait(&bar.full[g % S::SLOTS], (g / S::SLOTS) & 1, kv.err);
+      for (int g = max(0, last - S::SLOTS + 1); g <= last; g++)
+        mbar_wait(&bar.full[g % S::SLOTS], (g / S::SLOTS) & 1, kv.err);
     } else if (warp == 10) {
       // ----------------------- Q producer: one tile a unit, or two ----------------------- //
+      const bool leader = elect_one();
       int issued = 0;
-      bool ok = true;
-      do {
-        for (int i = 0; ok && i < (w.single() ? 1 : 2); i++) {
-          const int qt = w.qtiles + i, slot = qt & 1;
-          if (lane == 0) ok = mbar_wait(&bar.qempty[slot], ((qt >> 1) & 1) ^ 1, kv.err);
-          ok = __shfl_sync(FULL_MASK, ok, 0);
+      TcWork w;
+      bool ok = take(w);
+      while (ok) {
+        const int q_end = w.qtiles + (w.single() ? 1 : 2);
+        for (int qt = w.qtiles; qt < q_end; qt++) {
+          const int slot = qt & 1;
+          ok = __all_sync(FULL_MASK, mbar_wait(&bar.qempty[slot], ((qt >> 1) & 1) ^ 1, kv.err));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[slot], S::TILE);
+          if (leader) {
+            mbar_arrive_expect_tx(&bar.qfull[slot], S::TILE);
+#pragma unroll
+            for (int sg = 0; sg < S::SEGS; sg++)
+              tma_load_4d(base + (S::SLOTS + slot) * S::TILE + sg * S::SEG, &qmap, 0, sg, w.kvh << gl,
+                          w.c0 + w.tok0 + ((qt - w.qtiles) << (7 - gl)), &bar.qfull[slot]);
+          }
           __syncwarp();
-          if (lane < S::SEGS)
-            tma_load_4d(base + (S::SLOTS + slot) * S::TILE + lane * S::SEG, &qmap, 0, lane, w.kvh * G,
-                        w.s.c0 + w.block * w.per_unit + i * (TT / G), &bar.qfull[slot]);
           issued = qt + 1;
         }
-      } while (ok && w.next(a));
-      if (lane == 0)
-        for (int qt = max(0, issued - 2); qt < issued; qt++)
-          mbar_wait(&bar.qfull[qt & 1], (qt >> 1) & 1, kv.err);
-    } else if (warp == 9) {
-      // ---------------------------- matrix issuer ---------------------------- //
-      if (lane == 0) {
-        constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(D, true);
-        bool ok = true;
-        int np[2] = {0, 0};  // softmax results taken from each stream
-        do {
-          const bool single = w.single();
-          const int steps = w.steps();
-          auto issue_qk = [&](int x) {
-            const int st = x & 1, i = single ? x : x >> 1;
-            const int qt = w.qtiles + (single ? 0 : st), qslot = qt & 1;
-            const int g = w.load_k(i), slot = g % S::SLOTS;
-            ok = ok && mbar_wait(&bar.qfull[qslot], (qt >> 1) & 1, kv.err);
-            ok = ok && mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err);
-            if (!ok) return;
-            const uint32_t q0 = base + (S::SLOTS + qslot) * S::TILE, k0 = base + slot * S::TILE;
-#pragma unroll
-            for (int k = 0; k < D / 16; k++) {
-              const uint32_t off = (k / 4) * S::SEG + (k % 4) * 32;
-              mma_ss(tmem + st * TT, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), QK, k > 0);
-            }
-            if (single || st == 1) tc_commit(&bar.empty[slot]);
-            if (single ? x == steps - 1 : x >= steps - 2) tc_commit(&bar.qempty[qslot]);
-            tc_commit(&bar.sfull[st]);
-          };
-          issue_qk(0);
-          if (steps > 1) issue_qk(1);
-          for (int x = 0; ok && x < steps; x++) {
-            const int st = x & 1, i = single ? x : x >> 1;
-            const int g = w.load_v(i), slot = g % S::SLOTS;
-            ok = ok && mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err);
-            ok = ok && mbar_wait(&bar.pfull[st], np[st] & 1, kv.err);
-            if (!ok) break;
-            np[st]++;
-            tc_fence_after();
-            const uint32_t v0 = base + slot * S::TILE;
-#pragma unroll
-            for (int k = 0; k < TT / 16; k++)
-              mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + k * 8, smem_desc(v0 + k * 2048, S::SEG, 1024), PV,
-                     x > 1 || k > 0);
-            if (single || st == 1) tc_commit(&bar.empty[slot]);
-            if (x + 2 >= steps) tc_commit(&bar.ofull[st]);
-            if (x + 2 < steps) issue_qk(x + 2);
-          }
-        } while (ok && w.next(a));
-        // nothing may still be in flight when tensor memory is freed
-        tc_commit(&bar.done);
-        mbar_wait(&bar.done, 0, kv.err);
+        if (!ok || w.last) break;
+        ok = take(w);
       }
+      for (int qt = max(0, issued - 2); qt < issued; qt++)
+        mbar_wait(&bar.qfull[qt & 1], (qt >> 1) & 1, kv.err);
+    } else {
+      // ---------------------------- matrix issuer ---------------------------- //
+      constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(D, true);
+      const bool leader = elect_one();
+      uint32_t np = 0;  // parities of the softmax results taken, a bit a stream
+      TcWork w;
+      bool ok = take(w);
+      while (ok) {
+        const bool single = w.single();
+        const int steps = w.steps();
+        // S of step y, then O of step y - 1: products of one stream run while the
+        // other's softmax does
+        for (int y = 0; ok && y <= steps; y++) {
+          if (y < steps) {
+            const int st = y & 1, qt = w.qtiles + (single ? 0 : st), qslot = qt & 1;
+            const int g = w.load_k(single ? y : y >> 1), slot = g % S::SLOTS;
+            if (y < 2) ok = mbar_wait(&bar.qfull[qslot], (qt >> 1) & 1, kv.err);
+            ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
+            if (!ok) break;
+            if (leader) {
+              const uint64_t qd = smem_desc(base + (S::SLOTS + qslot) * S::TILE, 16, 1024);
+              const uint64_t kd = smem_desc(base + slot * S::TILE, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < D / 16; k++) {
+                const uint32_t off = ((k / 4) * S::SEG + (k % 4) * 32) >> 4;
+                mma_ss(tmem + st * TT, qd + off, kd + off, QK, k > 0);
+              }
+              if (single || st == 1) tc_commit(&bar.empty[slot]);
+              if (single ? y == steps - 1 : y >= steps - 2) tc_commit(&bar.qempty[qslot]);
+              tc_commit(&bar.sfull[st]);
+            }
+            __syncwarp();
+          }
+          if (y > 0) {
+            const int x = y - 1, st = x & 1;
+            const int g = w.load_v(single ? x : x >> 1), slot = g % S::SLOTS;
+            ok = mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err);
+            ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.pfull[st], (np >> st) & 1, kv.err));
+            if (!ok) break;
+            np ^= 1u << st;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t vd = smem_desc(base + slot * S::TILE, S::SEG, 1024);
+#pragma unroll
+              for (int k = 0; k < TT / 16; k++)
+                mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + k * 8, vd + (k * 2048 >> 4), PV, x > 1 || k > 0);
+              if (single || st == 1) tc_commit(&bar.empty[slot]);
+              if (x + 2 >= steps) tc_commit(&bar.ofull[st]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok || w.last) break;
+        ok = take(w);
+      }
+      // nothing may still be in flight when tensor memory is freed
+      if (leader) tc_commit(&bar.done);
       __syncwarp();
+      mbar_wait(&bar.done, 0, kv.err);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_REGS_SOFTMAX));
-    w.begin(a, aux.start_b, aux.start_off, count);
     // ------------------------------- softmax ------------------------------- //
     const int st = warp >> 2;                     // stream
     const int row = (warp & 3) * 32 + lane;       // its row, and the V row it may zero
@@ -528,22 +613,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const float sc = fmaxf(fabsf(a.scale) * TC_LOG2E, 1e-30f);
     bool dead = false;
     int ns = 0, no = 0;  // S tiles and O tiles taken
-    do {
+    TcWork w;
+    for (bool more = take(w); more; more = !w.last && take(w)) {
       const bool single = w.single();
       const int steps = w.steps();
-      const int ur = (single ? 0 : st * TT) + row;         // row of the unit
-      const int tok = w.block * w.per_unit + ur / G;        // token of the sequence
-      const int tok_c = min(tok, w.s.n - 1);
-      const int tok_first = w.block * w.per_unit + (single ? 0 : st * (TT / G));
+      const int ur = (single ? 0 : st * TT) + row;  // row of the unit
+      const int tok = w.tok0 + (ur >> gl);          // token of the sequence
+      const int tok_c = min(tok, w.n - 1);
+      const int tok_first = w.tok0 + (single ? 0 : st << (7 - gl));
       // a warp without rows computes nothing: rows do not mix, so what its part of
       // S and O holds reaches no result
-      const bool idle = (single ? 0 : st * TT) + (warp & 3) * 32 >= w.rows();
+      const bool idle = (single ? 0 : st * TT) + (warp & 3) * 32 >= w.rows;
       float m = -INFINITY, l = 0.f;
       for (int x = st; x < steps; x += 2) {
         const int i = single ? x : x >> 1, tile = w.tile0 + i;
-        const bool fresh = tile >= w.s.cache_tiles;
-        const int key0 = (fresh ? tile - w.s.cache_tiles : tile) * TT;
-        const int valid = (fresh ? w.s.n : w.s.t) - key0;   // keys of the tile, at least 1
+        const bool fresh = tile >= w.cache_tiles;
+        const int key0 = (fresh ? tile - w.cache_tiles : tile) * TT;
+        const int valid = (fresh ? w.n : w.t) - key0;   // keys of the tile, at least 1
         if (!dead) dead = !__all_sync(FULL_MASK, mbar_wait(&bar.sfull[st], ns & 1, kv.err));
         ns++;
         if (dead) continue;
@@ -553,34 +639,32 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const bool bad = !fresh && kv.block_table != nullptr && *reinterpret_cast<volatile int*>(&aux.bad_page) != 0;
         const bool cut = valid < TT || bad;
         if (cut) {
+          uint32_t ok16 = 0xff;  // 16-key groups on pages of the pool
+          if (bad) {
+            const int k = (lane & 7) * 16;
+            ok16 = __ballot_sync(FULL_MASK, k >= valid || kv_row(kv, w.b, w.kvh, key0 + k) >= 0) & 0xff;
+          }
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             const int k = valid - c * 32;
             have[c] = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1;
-            if (bad)
-#pragma unroll
-              for (int h = 0; h < 2; h++)
-                if ((c * 2 + h) * 16 < valid && kv_row(kv, w.b, w.kvh, key0 + (c * 2 + h) * 16) < 0)
-                  have[c] &= h ? 0xffffu : 0xffff0000u;
+            have[c] &= ((ok16 >> (2 * c)) & 1 ? 0xffffu : 0u) | ((ok16 >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
           }
         }
         if (!idle) {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; c++) tmem_ld32(r[c], s_addr + c * 32);
+          uint32_t r[TT];
+          tmem_ld_row(r, s_addr);
           tc_wait_ld();
           if (flip) {
 #pragma unroll
-            for (int c = 0; c < 4; c++)
-#pragma unroll
-              for (int e = 0; e < 32; e++) r[c][e] ^= 0x80000000u;
+            for (int e = 0; e < TT; e++) r[e] ^= 0x80000000u;
           }
           const bool by_row = fresh && (a.mask != nullptr || key0 + TT - 1 > tok_first);
           if (cut || by_row) {
             uint32_t see[4] = {have[0], have[1], have[2], have[3]};
             if (by_row) {
               if (a.mask != nullptr) {
-                const uint4 t4 = reinterpret_cast<const uint4*>(a.mask)[w.s.c0 + tok_c];
+                const uint4 t4 = reinterpret_cast<const uint4*>(a.mask)[w.c0 + tok_c];
                 see[0] &= t4.x;
                 see[1] &= t4.y;
                 see[2] &= t4.z;
@@ -594,67 +678,66 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               }
             }
 #pragma unroll
-            for (int c = 0; c < 4; c++)
-#pragma unroll
-              for (int e = 0; e < 32; e++)
-                if (!((see[c] >> e) & 1u)) r[c][e] = 0xff800000u;
+            for (int e = 0; e < TT; e++)
+              if (!((see[e / 32] >> (e % 32)) & 1u)) r[e] = 0xff800000u;
           }
-          float mx = -INFINITY;
+          float mx4[4];
 #pragma unroll
-          for (int c = 0; c < 4; c++)
+          for (int c = 0; c < 4; c++) mx4[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx = fmaxf(mx, fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
-          mx *= sc;
+          for (int e = 8; e < TT; e += 8)
+#pragma unroll
+            for (int c = 0; c < 4; c++) mx4[c] = max3(mx4[c], __uint_as_float(r[e + c]), __uint_as_float(r[e + c + 4]));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
           const bool grow = mx > m + RESCALE_LOG2 || (m == -INFINITY && mx > m);
-          const float corr = grow ? ex2(m - mx) : 1.f;
-          if (grow) m = mx;
-          if (x >= 2 && __any_sync(FULL_MASK, grow)) {
-            // O holds the stream's earlier tiles: S of this step came after them
+          if (__any_sync(FULL_MASK, grow)) {
+            const float corr = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
             l *= corr;
+            if (x >= 2) {  // O holds the stream's earlier tiles: S of this step came after them
+#pragma unroll 1
+              for (int c = 0; c < D / 32; c++) {
+                uint32_t o[32];
+                const uint32_t oa = tmem + lanes + 2 * TT + st * D + c * 32;
+                tmem_ld32(o, oa);
+                tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < D / 32; c++) {
-              uint32_t o[32];
-              const uint32_t oa = tmem + lanes + 2 * TT + st * D + c * 32;
-              tmem_ld32(o, oa);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              tmem_st32(oa, o);
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st32(oa, o);
+              }
             }
           }
-          const float mm = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float mm = m == -INFINITY ? 0.f : -m;
+          const uint64_t sc2 = f2(sc, sc), mm2 = f2(mm, mm);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < 4; c++)
-#pragma unroll
-            for (int e = 0; e < 32; e++) {
-              const float v = ex2(fmaf(__uint_as_float(r[c][e]), sc, -mm));
-              sum[e & 3] += v;
-              r[c][e] = __float_as_uint(v);
-            }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-          for (int c = 0; c < 2; c++) {
+          for (int h = 0; h < 2; h++) {
             uint32_t q[32];
 #pragma unroll
-            for (int e = 0; e < 32; e++)
-              q[e] = pack2(__uint_as_float(r[2 * c + e / 16][2 * (e % 16)]), __uint_as_float(r[2 * c + e / 16][2 * (e % 16) + 1]));
-            tmem_st32(s_addr + c * 32, q);
+            for (int e = 0; e < 32; e++) {
+              float v0, v1;
+              unf2(fma2(f2(__uint_as_float(r[h * 64 + 2 * e]), __uint_as_float(r[h * 64 + 2 * e + 1])), sc2, mm2), v0, v1);
+              v0 = ex2(v0);
+              v1 = ex2(v1);
+              sum[e & 1] = add2(sum[e & 1], f2(v0, v1));
+              q[e] = pack2(v0, v1);
+            }
+            tmem_st32(s_addr + h * 32, q);
           }
+          float s0, s1;
+          unf2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
         }
         if (cut) {
           // V rows of keys that do not exist hold whatever was there, possibly not
           // finite, and 0 * inf would reach every row: they are set to 0
           const int g = w.load_v(i), slot = g % S::SLOTS;
-          if (!dead) dead = !__all_sync(FULL_MASK, mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
+          dead = !__all_sync(FULL_MASK, mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
           const uint32_t hw = row < 32 ? have[0] : row < 64 ? have[1] : row < 96 ? have[2] : have[3];
           if (!dead && !((hw >> (row & 31)) & 1u)) {
 #pragma unroll
-            for (int sg = 0; sg < S::SEGS; sg++)
-#pragma unroll
-              for (int c = 0; c < 8; c++)
-                *reinterpret_cast<uint4*>(data + slot * S::TILE + sg * S::SEG + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 8 * S::SEGS; c++)
+              *reinterpret_cast<uint4*>(data + slot * S::TILE + (c / 8) * S::SEG + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
@@ -664,8 +747,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
 
       // ---- the unit's end in this run: result or partial record ----
-      const bool mine_any = steps > st, both = single;
-      if (mine_any) {
+      const bool both = single;
+      if (steps > st) {
         if (!dead) dead = !__all_sync(FULL_MASK, mbar_wait(&bar.ofull[st], no & 1, kv.err));
         no++;
       }
@@ -682,32 +765,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         L = w0 * aux.l[0][row] + w1 * aux.l[1][row];
       }
       tc_fence_after();
-      const bool whole = w.tile0 == 0 && w.tile1 == w.unit_tiles;
-      const int rec = 2 * blockIdx.x + (w.tile0 == 0 ? 1 : 0);
-      const bool live = ur < w.rows() && !dead;
-      const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-      const int h = ur - (ur / G) * G;
-      const long long orow = (long long)(w.s.c0 + tok) * kv.Hq + w.kvh * G + h;
+      const bool live = ur < w.rows && !dead;
+      if (w.whole) {
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+      }
+      const long long rec = ((long long)(2 * blockIdx.x + (w.tile0 == 0 ? 1 : 0)) * p.rows_max + ur);
+      const long long orow = (long long)(w.c0 + tok) * kv.Hq + (w.kvh << gl) + (ur & ((1 << gl) - 1));
       // both warpgroups of a shared unit write half the columns each
       const int c_lo = both ? st * (D / 64) : 0, c_hi = both ? c_lo + D / 64 : D / 32;
       const bool two = both && steps > 1;
+#pragma unroll 1
       for (int c = c_lo; c < c_hi; c++) {
-        uint32_t o[32];
+        uint32_t o[32], o1[32];
         tmem_ld32(o, tmem + lanes + 2 * TT + (both ? 0 : st * D) + c * 32);
-        if (two) {
-          uint32_t o1[32];
-          tmem_ld32(o1, tmem + lanes + 2 * TT + D + c * 32);
-          tc_wait_ld();
+        if (two) tmem_ld32(o1, tmem + lanes + 2 * TT + D + c * 32);
+        tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e++)
-            o[e] = __float_as_uint(__uint_as_float(o[e]) * (w0 * inv) + __uint_as_float(o1[e]) * (w1 * inv));
-        } else {
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * (w0 * inv));
+        for (int e = 0; e < 32; e++) {
+          const float v = __uint_as_float(o[e]) * w0;
+          o[e] = __float_as_uint(two ? fmaf(__uint_as_float(o1[e]), w1, v) : v);
         }
         if (!live) continue;
-        if (whole) {
+        if (w.whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
 #pragma unroll
           for (int e = 0; e < 4; e++)
@@ -716,33 +797,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                 pack2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
                                 pack2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.rec_o + ((long long)rec * p.rows_max + ur) * D + c * 32);
+          uint4* dst = reinterpret_cast<uint4*>(p.rec_o + rec * D + c * 32);
 #pragma unroll
           for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (live && (!both || st == 0)) {
-        if (whole) {
-          a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
-        } else {
-          float* ml = p.rec_ml + ((long long)rec * p.rows_max + ur) * 2;
-          ml[0] = M;
-          ml[1] = L;
-        }
+        if (w.whole) a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
+        else *reinterpret_cast<float2*>(p.rec_ml + rec * 2) = make_float2(M, L);
       }
       tc_fence_before();
       if (both) named_bar(1, 2 * TT);  // both outputs and the row states are read
-    } while (w.next(a));
-    if (tid == 0) {
-      TcSplit sp;
-      const bool open = w.tile0 == 0 && w.tile1 < w.unit_tiles;
-      sp.b = open ? w.b : -1;
-      sp.kvh = w.kvh;
-      sp.block = w.block;
-      sp.start = g0 + count - w.tile1;
-      sp.tiles = w.unit_tiles;
-      sp.per = per;
-      p.split[blockIdx.x] = sp;
     }
   }
   __syncthreads();
@@ -823,11 +888,11 @@ size_t tree_tc_workspace(const KVView& kv, int max_new, int sms) {
   return up256(sms * sizeof(TcSplit)) + up256(rec * 2 * sizeof(float)) + up256(rec * kv.d * sizeof(float));
 }
 
-// Rows of a TMA box of the cache: the most that a page holds whole boxes of.
-static int tc_box_rows(const KVView& kv) {
-  if (kv.block_table == nullptr) return 32;
-  int r = 16;
-  while (r < TT && kv.block_size % (2 * r) == 0) r *= 2;
+// Rows of a TMA box of the cache's whole tiles: the most that a page holds whole
+// boxes of. The tile at a cache's end is copied in boxes of 16.
+static int tc_box_log2(const KVView& kv) {
+  int r = 4;
+  while ((1 << r) < TT && (kv.block_table == nullptr || kv.block_size % (2 << r) == 0)) r++;
   return r;
 }
 
@@ -841,7 +906,8 @@ static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cu
   if (at.numRegs < TC_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3(sms), dim3(TC_THREADS), S::SMEM, st, p.a.kv.pdl, maps[0], maps[1], maps[2], maps[3], maps[4], p);
+  e = launch_pdl(k, dim3(sms), dim3(TC_THREADS), S::SMEM, st, p.a.kv.pdl, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
+                 maps[6], p);
   if (e != cudaSuccess) return e;
   abi_count_launch();
   return launch_pdl(tree_join_kernel<D>, dim3(sms, (p.rows_max + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,
@@ -854,7 +920,8 @@ prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t 
   const int G = kv.Hq / kv.Hkv;
   TcLaunch p;
   p.a = a;
-  p.box_rows = tc_box_rows(kv);
+  p.group_log2 = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
+  p.box_log2 = tc_box_log2(kv);
   p.rows_max = tc_rows_max(kv, a.max_new);
   char* w = static_cast<char*>(ws);
   p.split = reinterpret_cast<TcSplit*>(w);
@@ -863,23 +930,26 @@ prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t 
   w += up256((size_t)2 * sms * p.rows_max * 2 * sizeof(float));
   p.rec_o = reinterpret_cast<float*>(w);
 
-  CUtensorMap maps[5];
+  CUtensorMap maps[7];  // q; cache K and V; their partial tiles; new K and V
   const uint64_t d = kv.d, row = d * 2, segs = d / 64;
   const uint64_t cache_rows = kv.block_table != nullptr ? (uint64_t)kv.num_blocks * kv.Hkv * kv.block_size
                                                         : (uint64_t)kv.B * kv.Hkv * kv.t_max;
   const uint64_t qd[4] = {64, segs, (uint64_t)kv.Hq, (uint64_t)a.T}, qs[3] = {128, row, row * kv.Hq};
   const uint32_t qb[4] = {64, 1, (uint32_t)G, (uint32_t)(TT / G)};
-  const uint64_t cd[3] = {64, segs, cache_rows}, cs[2] = {128, row};
-  const uint32_t cb[3] = {64, 1, (uint32_t)p.box_rows};
+  // the cache's rows with a fourth dimension of one, so that one copy serves both
+  const uint64_t cd[4] = {64, segs, cache_rows, 1}, cs[3] = {128, row, row * cache_rows};
+  const uint32_t cb[4] = {64, 1, 1u << p.box_log2, 1}, tb[4] = {64, 1, 16, 1};
   const uint64_t nd[4] = {64, segs, (uint64_t)kv.Hkv, (uint64_t)a.T};
   const uint64_t ks[3] = {128, row, (uint64_t)a.ks * 2}, vs[3] = {128, row, (uint64_t)a.vs * 2};
   const uint32_t nb[4] = {64, 1, 1, 16};
   prhs_status s;
   if ((s = abi_encode_bf16(&maps[0], a.q, 4, qd, qs, qb)) != PRHS_OK) return s;
-  if ((s = abi_encode_bf16(&maps[1], kv.k, 3, cd, cs, cb)) != PRHS_OK) return s;
-  if ((s = abi_encode_bf16(&maps[2], kv.v, 3, cd, cs, cb)) != PRHS_OK) return s;
-  if ((s = abi_encode_bf16(&maps[3], a.k_new, 4, nd, ks, nb)) != PRHS_OK) return s;
-  if ((s = abi_encode_bf16(&maps[4], a.v_new, 4, nd, vs, nb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[1], kv.k, 4, cd, cs, cb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[2], kv.v, 4, cd, cs, cb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[3], kv.k, 4, cd, cs, tb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[4], kv.v, 4, cd, cs, tb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[5], a.k_new, 4, nd, ks, nb)) != PRHS_OK) return s;
+  if ((s = abi_encode_bf16(&maps[6], a.v_new, 4, nd, vs, nb)) != PRHS_OK) return s;
   *err = kv.d == 128 ? tc_go<128>(p, maps, sms, st) : tc_go<64>(p, maps, sms, st);
   return PRHS_OK;
 }
