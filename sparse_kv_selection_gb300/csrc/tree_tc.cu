@@ -88,8 +88,23 @@ struct __align__(16) TcWork {
   __device__ __forceinline__ int load_v(int i) const { return loads + (single() ? min(2 * i + 2, 2 * nt - 1) : 2 * i + 1); }
 };
 
+// A place in the ring of SLOTS slots: the slot and the parity of its use.
+template <int SLOTS>
+struct TcRing {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ explicit TcRing(int g) : slot(g % SLOTS), phase((g / SLOTS) & 1) {}
+  __device__ __forceinline__ void step(int n) {  // n < SLOTS
+    slot += n;
+    if (slot >= SLOTS) {
+      slot -= SLOTS;
+      phase ^= 1;
+    }
+  }
+};
+
 struct TcBars {  // one mbarrier each
-  uint64_t full[10], empty[10], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], done;
+  uint64_t full[10], empty[10], qfull[2], qempty[2], sfull[2], pfull[2][2], ofull[2], done;
   uint64_t wfull[TC_WORKS], wempty[TC_WORKS];
 };
 struct TcAux {
@@ -320,7 +335,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(&bar.qfull[i], 1);
       mbar_init(&bar.qempty[i], 1);
       mbar_init(&bar.sfull[i], 1);
-      mbar_init(&bar.pfull[i], TT);
+      mbar_init(&bar.pfull[i][0], TT);
+      mbar_init(&bar.pfull[i][1], TT);
       mbar_init(&bar.ofull[i], 1);
     }
     for (int i = 0; i < TC_WORKS; i++) {
@@ -470,6 +486,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           return (page * kv.Hkv + w.kvh) * kv.block_size + key % kv.block_size;
         };
+        TcRing<S::SLOTS> at(w.loads);
         int win = (w.tile0 << per_log2) - 32, rows = 0, behind = 0, ahead = 0;
         if (w.tile0 < w.cache_tiles) ahead = page_of(win + 32 + lane);
         for (int l = 0; ok && l < 2 * w.nt; l++) {
@@ -486,27 +503,41 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             rows = row_of(ahead, win + lane);
             ahead = page_of(win + 32 + lane);
           }
-          const int g = w.loads + l, slot = g % S::SLOTS;
-          ok = __all_sync(FULL_MASK, mbar_wait(&bar.empty[slot], ((g / S::SLOTS) & 1) ^ 1, kv.err));
+          const int slot = at.slot;
+          ok = __all_sync(FULL_MASK, mbar_wait(&bar.empty[slot], at.phase ^ 1, kv.err));
           if (!ok) break;
+          at.step(1);
           if (leader) mbar_arrive_expect_tx(&bar.full[slot], (boxes << step_log2) * 128 * S::SEGS);
           const CUtensorMap* map = fresh ? (is_v ? &vnmap : &knmap)
                                          : step_log2 == br_log2 ? (is_v ? &vmap : &kmap) : (is_v ? &vtail : &ktail);
           const uint32_t dst = base + slot * S::TILE;
-#pragma unroll 2
-          for (int x = 0; x < boxes; x++) {
-            const int key = x << step_log2;  // within the tile
-            const int bx = (tile << per_log2) + (key >> br_log2) - win;
-            const int row = __shfl_sync(FULL_MASK, bx < 0 ? behind : rows, bx & 31) + (key & (br - 1));
-            if (leader) {
+          // the boxes' rows first, then all copies from one thread: a copy takes it
+          // about 40 clocks that way, over 100 with a shuffle between two
+          int z[8];
+          const int from = (tile << per_log2) - win;
 #pragma unroll
-              for (int sg = 0; sg < S::SEGS; sg++)
-                tma_load_4d(dst + sg * S::SEG + key * 128, map, 0, sg, fresh ? w.kvh : row,
-                            fresh ? w.c0 + key0 + key : 0, &bar.full[slot]);
+          for (int x = 0; x < 8; x++) {
+            const int key = x << step_log2;  // within the tile
+            const int bx = from + (key >> br_log2);
+            z[x] = __shfl_sync(FULL_MASK, bx < 0 ? behind : rows, bx & 31) + (key & (br - 1));
+            if (fresh) z[x] = w.kvh;
+          }
+          if (leader) {
+            int y = fresh ? w.c0 + key0 : 0;
+            const int y_step = fresh ? 16 : 0;
+            uint32_t to = dst;
+            const uint32_t to_step = 128u << step_log2;
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+              if (x >= boxes) break;
+#pragma unroll
+              for (int sg = 0; sg < S::SEGS; sg++) tma_load_4d(to + sg * S::SEG, map, 0, sg, z[x], y, &bar.full[slot]);
+              to += to_step;
+              y += y_step;
             }
           }
           __syncwarp();
-          last = g;
+          last = w.loads + l;
         }
         if (!ok || w.last) break;
         ok = take(w);
@@ -551,15 +582,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       while (ok) {
         const bool single = w.single();
         const int steps = w.steps();
+        TcRing<S::SLOTS> kr(w.loads), vr(w.load_v(0));
         // S of step y, then O of step y - 1: products of one stream run while the
         // other's softmax does
         for (int y = 0; ok && y <= steps; y++) {
           if (y < steps) {
             const int st = y & 1, qt = w.qtiles + (single ? 0 : st), qslot = qt & 1;
-            const int g = w.load_k(single ? y : y >> 1), slot = g % S::SLOTS;
+            const int slot = kr.slot;
             if (y < 2) ok = mbar_wait(&bar.qfull[qslot], (qt >> 1) & 1, kv.err);
-            ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
+            ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.full[slot], kr.phase, kv.err));
             if (!ok) break;
+            if (single ? true : st == 1) kr.step(single && y == 0 ? 1 : 2);
             if (leader) {
               const uint64_t qd = smem_desc(base + (S::SLOTS + qslot) * S::TILE, 16, 1024);
               const uint64_t kd = smem_desc(base + slot * S::TILE, 16, 1024);
@@ -576,17 +609,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           if (y > 0) {
             const int x = y - 1, st = x & 1;
-            const int g = w.load_v(single ? x : x >> 1), slot = g % S::SLOTS;
-            ok = mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err);
-            ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.pfull[st], (np >> st) & 1, kv.err));
+            const int slot = vr.slot;
+            ok = mbar_wait(&bar.full[slot], vr.phase, kv.err);
+            if (single || st == 1) vr.step(single && x == steps - 2 ? 1 : 2);
+            const uint64_t vd = smem_desc(base + slot * S::TILE, S::SEG, 1024);
+            // the first half of P's keys while the second is computed
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.pfull[st][h], (np >> st) & 1, kv.err));
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int k = h * 4; k < h * 4 + 4; k++)
+                  mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + k * 8, vd + (k * 2048 >> 4), PV, x > 1 || k > 0);
+              }
+              __syncwarp();
+            }
             if (!ok) break;
             np ^= 1u << st;
-            tc_fence_after();
             if (leader) {
-              const uint64_t vd = smem_desc(base + slot * S::TILE, S::SEG, 1024);
-#pragma unroll
-              for (int k = 0; k < TT / 16; k++)
-                mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + k * 8, vd + (k * 2048 >> 4), PV, x > 1 || k > 0);
               if (single || st == 1) tc_commit(&bar.empty[slot]);
               if (x + 2 >= steps) tc_commit(&bar.ofull[st]);
             }
@@ -650,6 +692,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             have[c] = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1;
             have[c] &= ((ok16 >> (2 * c)) & 1 ? 0xffffu : 0u) | ((ok16 >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
           }
+        }
+        if (cut) {
+          // V rows of keys that do not exist hold whatever was there, possibly not
+          // finite, and 0 * inf would reach every row: they are set to 0
+          const int g = w.load_v(i), slot = g % S::SLOTS;
+          dead = !__all_sync(FULL_MASK, mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
+          const uint32_t hw = row < 32 ? have[0] : row < 64 ? have[1] : row < 96 ? have[2] : have[3];
+          if (!dead && !((hw >> (row & 31)) & 1u)) {
+#pragma unroll
+            for (int c = 0; c < 8 * S::SEGS; c++)
+              *reinterpret_cast<uint4*>(data + slot * S::TILE + (c / 8) * S::SEG + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         if (!idle) {
           uint32_t r[TT];
@@ -723,27 +778,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               q[e] = pack2(v0, v1);
             }
             tmem_st32(s_addr + h * 32, q);
+            if (h == 0) {
+              tc_wait_st();
+              tc_fence_before();
+              mbar_arrive(&bar.pfull[st][0]);
+            }
           }
           float s0, s1;
           unf2(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-        }
-        if (cut) {
-          // V rows of keys that do not exist hold whatever was there, possibly not
-          // finite, and 0 * inf would reach every row: they are set to 0
-          const int g = w.load_v(i), slot = g % S::SLOTS;
-          dead = !__all_sync(FULL_MASK, mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
-          const uint32_t hw = row < 32 ? have[0] : row < 64 ? have[1] : row < 96 ? have[2] : have[3];
-          if (!dead && !((hw >> (row & 31)) & 1u)) {
-#pragma unroll
-            for (int c = 0; c < 8 * S::SEGS; c++)
-              *reinterpret_cast<uint4*>(data + slot * S::TILE + (c / 8) * S::SEG + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else {
+          tc_fence_before();
+          mbar_arrive(&bar.pfull[st][0]);
         }
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar.pfull[st]);
+        mbar_arrive(&bar.pfull[st][1]);
       }
 
       // ---- the unit's end in this run: result or partial record ----
