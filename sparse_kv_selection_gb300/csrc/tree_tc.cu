@@ -84,7 +84,6 @@ struct __align__(16) TcWork {
     is_v = end || (l > 0 && (l & 1) == 0);
     return end ? nt - 1 : is_v ? (l - 2) >> 1 : (l + 1) >> 1;
   }
-  __device__ __forceinline__ int load_k(int i) const { return loads + (single() ? max(0, 2 * i - 1) : 2 * i); }
   __device__ __forceinline__ int load_v(int i) const { return loads + (single() ? min(2 * i + 2, 2 * nt - 1) : 2 * i + 1); }
 };
 
@@ -575,73 +574,78 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     } else {
       // ---------------------------- matrix issuer ---------------------------- //
       constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(D, true);
-      const bool leader = elect_one();
-      uint32_t np = 0;  // parities of the softmax results taken, a bit a stream
-      TcWork w;
-      bool ok = take(w);
-      while (ok) {
-        const bool single = w.single();
-        const int steps = w.steps();
-        TcRing<S::SLOTS> kr(w.loads), vr(w.load_v(0));
-        // S of step y, then O of step y - 1: products of one stream run while the
-        // other's softmax does
-        for (int y = 0; ok && y <= steps; y++) {
-          if (y < steps) {
-            const int st = y & 1, qt = w.qtiles + (single ? 0 : st), qslot = qt & 1;
-            const int slot = kr.slot;
-            if (y < 2) ok = mbar_wait(&bar.qfull[qslot], (qt >> 1) & 1, kv.err);
-            ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.full[slot], kr.phase, kv.err));
-            if (!ok) break;
-            if (single ? true : st == 1) kr.step(single && y == 0 ? 1 : 2);
-            if (leader) {
-              const uint64_t qd = smem_desc(base + (S::SLOTS + qslot) * S::TILE, 16, 1024);
-              const uint64_t kd = smem_desc(base + slot * S::TILE, 16, 1024);
+      if (elect_one()) {
+        uint32_t np = 0;  // parities of the softmax results taken, a bit a stream
+        bool ok = true;
+        for (int k = 0; ok; k++) {
+          const int wi = k & (TC_WORKS - 1);
+          if (!mbar_wait(&bar.wfull[wi], (k / TC_WORKS) & 1, kv.err)) break;
+          const int rows = aux.work[wi].rows, nt = aux.work[wi].nt, loads = aux.work[wi].loads;
+          const int qtiles = aux.work[wi].qtiles, last = aux.work[wi].last;
+          mbar_arrive(&bar.wempty[wi]);
+          const bool single = rows <= TT;
+          const int steps = single ? nt : 2 * nt;
+          TcRing<S::SLOTS> kr(loads), vr(loads + (single ? min(2, 2 * nt - 1) : 1));
+          auto issue_qk = [&](int y) {  // S of step y; its K tile is loaded
+            const int st = y & 1, qslot = (qtiles + (single ? 0 : st)) & 1;
+            const uint64_t qd = smem_desc(base + (S::SLOTS + qslot) * S::TILE, 16, 1024);
+            const uint64_t kd = smem_desc(base + kr.slot * S::TILE, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < D / 16; k++) {
-                const uint32_t off = ((k / 4) * S::SEG + (k % 4) * 32) >> 4;
-                mma_ss(tmem + st * TT, qd + off, kd + off, QK, k > 0);
-              }
-              if (single || st == 1) tc_commit(&bar.empty[slot]);
-              if (single ? y == steps - 1 : y >= steps - 2) tc_commit(&bar.qempty[qslot]);
-              tc_commit(&bar.sfull[st]);
+            for (int j = 0; j < D / 16; j++) {
+              const uint32_t off = ((j / 4) * S::SEG + (j % 4) * 32) >> 4;
+              mma_ss(tmem + st * TT, qd + off, kd + off, QK, j > 0);
             }
-            __syncwarp();
-          }
-          if (y > 0) {
-            const int x = y - 1, st = x & 1;
-            const int slot = vr.slot;
-            ok = mbar_wait(&bar.full[slot], vr.phase, kv.err);
-            if (single || st == 1) vr.step(single && x == steps - 2 ? 1 : 2);
-            const uint64_t vd = smem_desc(base + slot * S::TILE, S::SEG, 1024);
-            // the first half of P's keys while the second is computed
+            tc_commit(&bar.sfull[st]);
+            if (single || st == 1) {
+              tc_commit(&bar.empty[kr.slot]);
+              kr.step(single && y == 0 ? 1 : 2);
+            }
+            if (single ? y == steps - 1 : y >= steps - 2) tc_commit(&bar.qempty[qslot]);
+          };
+          ok = mbar_wait(&bar.qfull[qtiles & 1], (qtiles >> 1) & 1, kv.err);
+          // step x of the loop: O of step x, then S of step x + 2 in the same stream; with
+          // two row tiles (bound by the products) every load they need is waited for
+          // before the softmax, so that nothing comes between the two products. Steps
+          // -2 and -1 are S of steps 0 and 1.
+          for (int x = -2; ok && x < steps; x++) {
+            const bool more = x + 2 < steps;
+            if (more && !single && (x & 1) == 0) ok = ok && mbar_wait(&bar.full[kr.slot], kr.phase, kv.err);
+            if (x == -1 && !single) ok = ok && mbar_wait(&bar.qfull[(qtiles + 1) & 1], ((qtiles + 1) >> 1) & 1, kv.err);
+            if (x >= 0) {
+              const int st = x & 1;
+              if (single || st == 0) ok = ok && mbar_wait(&bar.full[vr.slot], vr.phase, kv.err);
+              const uint64_t vd = smem_desc(base + vr.slot * S::TILE, S::SEG, 1024);
+              // the first half of P's keys while the softmax computes the second
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              ok = __all_sync(FULL_MASK, ok && mbar_wait(&bar.pfull[st][h], (np >> st) & 1, kv.err));
+              for (int h = 0; h < 2; h++) {
+                ok = ok && mbar_wait(&bar.pfull[st][h], (np >> st) & 1, kv.err);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int j = h * 4; j < h * 4 + 4; j++)
+                  mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + j * 8, vd + (j * 2048 >> 4), PV, x > 1 || j > 0);
+              }
               if (!ok) break;
-              tc_fence_after();
-              if (leader) {
-#pragma unroll
-                for (int k = h * 4; k < h * 4 + 4; k++)
-                  mma_ts(tmem + 2 * TT + st * D, tmem + st * TT + k * 8, vd + (k * 2048 >> 4), PV, x > 1 || k > 0);
-              }
-              __syncwarp();
+              np ^= 1u << st;
             }
             if (!ok) break;
-            np ^= 1u << st;
-            if (leader) {
-              if (single || st == 1) tc_commit(&bar.empty[slot]);
-              if (x + 2 >= steps) tc_commit(&bar.ofull[st]);
+            if (x >= 0 && (single || (x & 1))) {
+              tc_commit(&bar.empty[vr.slot]);
+              vr.step(single && x == steps - 2 ? 1 : 2);
             }
-            __syncwarp();
+            // (with a tile to itself a step gives back V before it waits for the next K)
+            if (more && single) ok = mbar_wait(&bar.full[kr.slot], kr.phase, kv.err);
+            if (!ok) break;
+            if (more) issue_qk(x + 2);
+            else if (x >= 0) tc_commit(&bar.ofull[x & 1]);
           }
+          if (last) break;
         }
-        if (!ok || w.last) break;
-        ok = take(w);
+        // nothing may still be in flight when tensor memory is freed
+        tc_commit(&bar.done);
+        mbar_wait(&bar.done, 0, kv.err);
       }
-      // nothing may still be in flight when tensor memory is freed
-      if (leader) tc_commit(&bar.done);
       __syncwarp();
-      mbar_wait(&bar.done, 0, kv.err);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_REGS_SOFTMAX));
