@@ -142,6 +142,8 @@ class KVCache:
         self.k, self.v = k.contiguous(), v.contiguous()
         self.seq_lens = seq_lens.to(torch.int32).contiguous()
         self.block_table = None if block_table is None else block_table.to(torch.int32).contiguous()
+        self.device, self.dtype = self.k.device, self.k.dtype
+        self.index = 0 if self.device.index is None else self.device.index
         self.desc = prhs_kv()
         d = self.desc
         d.dtype = PRHS_BF16 if k.dtype == torch.bfloat16 else PRHS_F32
@@ -304,6 +306,8 @@ def _array(t, name, shape, dtype, device, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     if t.dtype != dtype:
@@ -322,17 +326,25 @@ def _rows(t, name, T, heads, d, dtype, device):
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (T, heads, d):
+    if t.shape != (T, heads, d):
         raise ValueError(f"{name} must have shape {(T, heads, d)}, got {tuple(t.shape)}")
-    if t.numel() and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+    s0, s1, s2 = t.stride()
+    if T and ((heads > 1 and s1 != d) or s2 != 1):
         raise ValueError(f"{name}: the rows of one token must be packed")
-    return t.data_ptr(), (t.stride(0) if T > 1 else heads * d)
+    return t.data_ptr(), (s0 if T > 1 else heads * d)
 
 
-def _on(kv, stream):
-    """The cache's device made current, and the stream there to launch on."""
-    with torch.cuda.device(kv.k.device):
-        return torch.cuda.device(kv.k.device), _stream(stream)
+def _call(kv, where, fn, stream, *args) -> None:
+    """fn(*args, stream) with the cache's device current (torch's current
+    stream of that device when none is given); raises on a non-OK status."""
+    if torch.cuda.current_device() != kv.index:
+        with torch.cuda.device(kv.index):
+            return _call(kv, where, fn, stream, *args)
+    # (the device's number spares torch a lookup of the current one)
+    st = torch.cuda.current_stream(kv.index).cuda_stream if stream is None else _stream(stream)
+    status = fn(*args, st)
+    if status != PRHS_OK:
+        _check(status, where)
 
 
 def rope_turns(rot_dim, base=10000.0, kind="plain", factor=1.0, original=0.0, low=0.0, high=0.0):
@@ -376,35 +388,30 @@ def plan_tokens(kv, n_new, cu_new, positions, slots, *, parents=None, tree_mask=
     tokens (prhs_plan_tokens). On a paged cache kv.block_table gets the new
     pages; free_head and n_pages are updated in place unless their _out arrays
     are given."""
-    dev, i32, T, B = kv.k.device, torch.int32, positions.numel(), kv.B
-    paged = kv.block_table is not None
-    if paged:
+    dev, i32, T, B = kv.device, torch.int32, positions.numel(), kv.desc.B
+    if kv.block_table is not None:
         free_head_out = free_head if free_head_out is None else free_head_out
         n_pages_out = n_pages if n_pages_out is None else n_pages_out
         n_free = 0 if free_pages is None else free_pages.numel()
-        pages = [_array(free_pages, "free_pages", (n_free,), i32, dev, optional=True), n_free,
-                 _array(free_head, "free_head", (1,), i32, dev), _array(n_pages, "n_pages", (B,), i32, dev)]
-        pages_out = [_array(free_head_out, "free_head_out", (1,), i32, dev),
-                     _array(n_pages_out, "n_pages_out", (B,), i32, dev)]
+        pages = (_array(free_pages, "free_pages", (n_free,), i32, dev, True), n_free,
+                 _array(free_head, "free_head", (1,), i32, dev), _array(n_pages, "n_pages", (B,), i32, dev))
+        pages_out = (_array(free_head_out, "free_head_out", (1,), i32, dev),
+                     _array(n_pages_out, "n_pages_out", (B,), i32, dev))
     else:
-        pages, pages_out = [None, 0, None, None], [None, None]
-    guard, st = _on(kv, stream)
-    with guard:
-        _check(load().prhs_plan_tokens(
-            kv.ref(), _array(n_new, "n_new", (B,), i32, dev), T,
-            _array(parents, "parents", (T,), i32, dev, optional=True), *pages,
-            _array(cu_new, "cu_new", (B + 1,), i32, dev), _array(positions, "positions", (T,), i32, dev),
-            _array(slots, "slots", (T,), i32, dev),
-            _array(tree_mask, "tree_mask", (T, TREE_WORDS), i32, dev, optional=True), *pages_out, st),
-            "plan_tokens")
+        pages, pages_out = (None, 0, None, None), (None, None)
+    _call(kv, "plan_tokens", load().prhs_plan_tokens, stream, kv.ref(),
+          _array(n_new, "n_new", (B,), i32, dev), T, _array(parents, "parents", (T,), i32, dev, True), *pages,
+          _array(cu_new, "cu_new", (B + 1,), i32, dev), _array(positions, "positions", (T,), i32, dev),
+          _array(slots, "slots", (T,), i32, dev),
+          _array(tree_mask, "tree_mask", (T, TREE_WORDS), i32, dev, True), *pages_out)
 
 
 def rope_append(kv, rope, positions, q, k, v, q_out, *, slots=None, k_out=None, stream=None) -> None:
     """Rotate q [T][Hq][d] and k [T][Hkv][d] at positions [T] into q_out and,
     where given, k_out; with slots, rotated k and v go to those rows of the
     cache (prhs_rope_append). q, k and v may be views with a token stride."""
-    dev, dt, T = kv.k.device, kv.k.dtype, positions.numel()
-    Hq, Hkv, d = kv.Hq, kv.desc.Hkv, kv.desc.d
+    dev, dt, T, desc = kv.device, kv.dtype, positions.numel(), kv.desc
+    Hq, Hkv, d = desc.Hq, desc.Hkv, desc.d
     if rope.turns.device != dev:
         raise ValueError(f"rope is on {rope.turns.device}, the cache on {dev}")
     if v is None and slots is not None:
@@ -412,17 +419,14 @@ def rope_append(kv, rope, positions, q, k, v, q_out, *, slots=None, k_out=None, 
     qp, qs = _rows(q, "q", T, Hq, d, dt, dev)
     kp, ks = _rows(k, "k", T, Hkv, d, dt, dev)
     vp, vs = _rows(v, "v", T, Hkv, d, dt, dev)
-    guard, st = _on(kv, stream)
-    with guard:
-        _check(load().prhs_rope_append(
-            kv.ref(), rope.ref(), T, _array(positions, "positions", (T,), torch.int32, dev),
-            _array(slots, "slots", (T,), torch.int32, dev, optional=True), qp, qs, kp, ks, vp, vs,
-            _array(q_out, "q_out", (T, Hq, d), dt, dev),
-            _array(k_out, "k_out", (T, Hkv, d), dt, dev, optional=True), st), "rope_append")
+    _call(kv, "rope_append", load().prhs_rope_append, stream, kv.ref(), rope.ref(), T,
+          _array(positions, "positions", (T,), torch.int32, dev),
+          _array(slots, "slots", (T,), torch.int32, dev, True), qp, qs, kp, ks, vp, vs,
+          _array(q_out, "q_out", (T, Hq, d), dt, dev), _array(k_out, "k_out", (T, Hkv, d), dt, dev, True))
 
 
 def tree_workspace_size(kv: KVCache, max_new: int) -> int:
-    with torch.cuda.device(kv.k.device):
+    with torch.cuda.device(kv.index):
         n = load().prhs_tree_workspace_size(kv.ref(), int(max_new))
     if n == 0:
         raise PrhsError(PRHS_EINVAL, "tree_workspace_size", load().prhs_last_message().decode())
@@ -432,7 +436,7 @@ def tree_workspace_size(kv: KVCache, max_new: int) -> int:
 def make_tree_workspace(kv: KVCache, max_new: int):
     """Allocate (through torch) the workspace of tree_attn for this cache and
     at most max_new tokens a sequence."""
-    return torch.empty(tree_workspace_size(kv, max_new), dtype=torch.uint8, device=kv.k.device)
+    return torch.empty(tree_workspace_size(kv, max_new), dtype=torch.uint8, device=kv.device)
 
 
 def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree_mask=None,
@@ -440,20 +444,17 @@ def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree
     """Attention of packed new tokens over their caches and each other: by
     tree_mask [T][4] int32, or causal (prhs_tree_attn). out [T][Hq][d] has the
     cache's element type, lse [T][Hq] is float32."""
-    dev, dt, T = kv.k.device, kv.k.dtype, q.shape[0]
-    Hq, Hkv, d = kv.Hq, kv.desc.Hkv, kv.desc.d
+    dev, dt, T, desc = kv.device, kv.dtype, q.shape[0], kv.desc
+    Hq, Hkv, d = desc.Hq, desc.Hkv, desc.d
     kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
     vp, vs = _rows(v_new, "v_new", T, Hkv, d, dt, dev)
     if ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the cache on {dev}")
-    guard, st = _on(kv, stream)
-    with guard:
-        _check(load().prhs_tree_attn(
-            kv.ref(), _array(q, "q", (T, Hq, d), dt, dev), kp, ks, vp, vs, float(scale), T,
-            _array(cu_new, "cu_new", (kv.B + 1,), torch.int32, dev), int(max_new),
-            _array(tree_mask, "tree_mask", (T, TREE_WORDS), torch.int32, dev, optional=True),
-            _array(out, "out", (T, Hq, d), dt, dev), _array(lse, "lse", (T, Hq), torch.float32, dev),
-            _ptr(ws), ws.numel() * ws.element_size(), st), "tree_attn")
+    _call(kv, "tree_attn", load().prhs_tree_attn, stream, kv.ref(), _array(q, "q", (T, Hq, d), dt, dev), kp, ks,
+          vp, vs, float(scale), T, _array(cu_new, "cu_new", (desc.B + 1,), torch.int32, dev), int(max_new),
+          _array(tree_mask, "tree_mask", (T, TREE_WORDS), torch.int32, dev, True),
+          _array(out, "out", (T, Hq, d), dt, dev), _array(lse, "lse", (T, Hq), torch.float32, dev),
+          _ptr(ws), ws.numel() * ws.element_size())
 
 
 def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, accept_idx=None, k_new=None, v_new=None,
@@ -462,8 +463,8 @@ def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, accept_idx=None, k_new
     advance the lengths (prhs_commit_tokens), in place unless new_lens is
     given. Without k_new and v_new only the lengths advance; T then bounds the
     packed tokens (default: B * t_max)."""
-    dev, dt, i32, B = kv.k.device, kv.k.dtype, torch.int32, kv.B
-    Hkv, d = kv.desc.Hkv, kv.desc.d
+    dev, dt, i32, desc = kv.device, kv.dtype, torch.int32, kv.desc
+    B, Hkv, d = desc.B, desc.Hkv, desc.d
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new must be both given or both left out")
     if T is None:
@@ -471,14 +472,11 @@ def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, accept_idx=None, k_new
     kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
     vp, vs = _rows(v_new, "v_new", T, Hkv, d, dt, dev)
     cap = 0 if accept_idx is None else accept_idx.shape[-1]
-    guard, st = _on(kv, stream)
-    with guard:
-        _check(load().prhs_commit_tokens(
-            kv.ref(), int(T), _array(cu_new, "cu_new", (B + 1,), i32, dev),
-            _array(accept_idx, "accept_idx", (B, cap), i32, dev, optional=True), cap,
-            _array(accept_n, "accept_n", (B,), i32, dev), kp, ks, vp, vs,
-            _array(kv.seq_lens if new_lens is None else new_lens, "new_lens", (B,), i32, dev), st),
-            "commit_tokens")
+    _call(kv, "commit_tokens", load().prhs_commit_tokens, stream, kv.ref(), int(T),
+          _array(cu_new, "cu_new", (B + 1,), i32, dev),
+          _array(accept_idx, "accept_idx", (B, cap), i32, dev, True), cap,
+          _array(accept_n, "accept_n", (B,), i32, dev), kp, ks, vp, vs,
+          _array(kv.seq_lens if new_lens is None else new_lens, "new_lens", (B,), i32, dev))
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:

@@ -223,6 +223,29 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Dynamic shared memory above the default 48 KB allowed for `kernel` on the
+// current device; `done` (one per kernel, zero at load) keeps the largest size
+// set on each device, so that a call sets it once and not at every launch.
+constexpr int SMEM_DEVICES = 64;
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t smem, int (&done)[SMEM_DEVICES]) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < SMEM_DEVICES;
+  if (known && __atomic_load_n(&done[dev], __ATOMIC_ACQUIRE) >= (int)smem) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  // a smaller size set by another thread meanwhile would lower the limit: keep the largest
+  if (known) {
+    int old = __atomic_load_n(&done[dev], __ATOMIC_RELAXED);
+    while (old < (int)smem && !__atomic_compare_exchange_n(&done[dev], &old, (int)smem, false, __ATOMIC_RELEASE, __ATOMIC_RELAXED)) {
+    }
+  }
+  return cudaSuccess;
+}
+
 // -------------------------------------------------------------------------- //
 // small reductions
 // -------------------------------------------------------------------------- //

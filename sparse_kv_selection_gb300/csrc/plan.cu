@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) 
 cudaError_t launch_plan(const PlanLaunch& a, cudaStream_t st) {
   const size_t lists = ((size_t)2 * (a.kv.B + 1) * 4 + 15) / 16 * 16;
   const size_t smem = lists + (a.parents != nullptr ? PLAN_WARPS * sizeof(PlanTree) : 0);
-  cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static int smem_set[SMEM_DEVICES];
+  const cudaError_t e = allow_smem(plan_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
   // one CTA for a decode or verification step; a cluster for prompts and for
   // batches with more trees than one CTA's warps

@@ -160,7 +160,8 @@ static cudaError_t rope_go(const RopeLaunch& a, cudaStream_t st) {
   const long long toks = (chunk + rows * tpr - 1) / (rows * tpr) + 1;
   const size_t smem = (size_t)(toks < a.T ? toks : a.T) * (a.rot_dim / 2) * sizeof(float2);
   auto k = rope_kernel<T, PER>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static int smem_set[SMEM_DEVICES];
+  const cudaError_t e = allow_smem(k, smem, smem_set);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3((unsigned)((total + chunk - 1) / chunk)), dim3(ROPE_THREADS), smem, st, a.kv.pdl, a,
                     rows, tpr);

@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_kernel(const TreeLaunch a) 
 template <typename T, int D>
 static cudaError_t tree_go(const TreeLaunch& a, cudaStream_t st) {
   auto k = tree_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TreeShape<D>::SMEM);
+  static int smem_set[SMEM_DEVICES];
+  const cudaError_t e = allow_smem(k, TreeShape<D>::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   const int G = a.kv.Hq / a.kv.Hkv;
   const unsigned blocks = (unsigned)(((long long)a.max_new * G + TR - 1) / TR);

@@ -117,9 +117,10 @@ struct TcAux {
 };
 static_assert(sizeof(TcAux) <= 3072, "aux region");
 
-// A CTA's unit that it starts and does not finish (b < 0: none).
-struct TcSplit {
-  int b, kvh, block, start, tiles, per, pad[2];
+// A CTA's unit that it starts and does not finish.
+struct __align__(16) TcSplit {
+  int rows, kvh, tok, start;  // rows of the unit (0: none), KV head, first token (packed), first tile
+  int tiles, per, pad[2];     // its tiles, the tiles of a run
 };
 
 struct TcLaunch {
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const int per = (total + gridDim.x - 1) / (int)gridDim.x;
   const int g0 = blockIdx.x * per, count = min(total, g0 + per) - g0;
   if (count <= 0 || (base & 1023) != 0) {
-    if (tid == 0) p.split[blockIdx.x].b = -1;
+    if (tid == 0) p.split[blockIdx.x].rows = 0;
     return;
   }
   if (g0 >= before && g0 < before + mine) {
@@ -437,9 +438,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           mbar_arrive(&bar.wfull[i]);
           if (left == 0) {
             TcSplit sp;
-            sp.b = off == 0 && nt < tiles ? b : -1;
+            sp.rows = off == 0 && nt < tiles ? rows : 0;
             sp.kvh = kvh;
-            sp.block = block;
+            sp.tok = s.c0 + (block << ul);
             sp.start = g0 + count - nt;
             sp.tiles = tiles;
             sp.per = per;
@@ -871,59 +872,98 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
 }
 
-// Joins the partial states of the units that a run's end cut: one warp per
-// row, over the records of the CTA that began the unit and of those after it.
-constexpr int JOIN_WARPS = 8;
+// Joins the partial states of the units that a run's end cut, over the records
+// of the CTA that began a unit and of those after it. A lane holds a record's
+// weight and D / 32 columns; eight records' rows are in flight together where a
+// unit has many (a warp takes one row), four rows of two where it has few.
+// Bound: L2 and latency.
+constexpr int JOIN_WARPS = 8, JOIN_FEW = 4;
+
+template <int D, int JOIN_ROWS>
+__device__ __forceinline__ void join_rows(const TcLaunch& p, int row0, int rows, int kvh, int tok0, int n_rec) {
+  const TreeLaunch& a = p.a;
+  const int lane = threadIdx.x & 31, c_first = blockIdx.x;
+  constexpr int F = D / 32;  // floats a lane
+  auto rec_of = [&](int i, int row) {  // record of the unit's i-th CTA
+    return (long long)(i == 0 ? 2 * c_first + 1 : 2 * (c_first + i)) * p.rows_max + row;
+  };
+  float M[JOIN_ROWS], L[JOIN_ROWS], o[JOIN_ROWS][F];
+#pragma unroll
+  for (int j = 0; j < JOIN_ROWS; j++) {
+    M[j] = -INFINITY;
+    L[j] = 0.f;
+#pragma unroll
+    for (int f = 0; f < F; f++) o[j][f] = 0.f;
+  }
+  for (int i0 = 0; i0 < n_rec; i0 += 32) {
+    // this lane's record: its rows' maxima and sums (rows past the unit's repeat the last)
+    float2 ml[JOIN_ROWS];
+#pragma unroll
+    for (int j = 0; j < JOIN_ROWS; j++) {
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < n_rec)
+        ml[j] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml) + rec_of(i0 + lane, min(row0 + j, rows - 1)));
+    }
+    float wt[JOIN_ROWS];
+#pragma unroll
+    for (int j = 0; j < JOIN_ROWS; j++) {
+      const float m = fmaxf(M[j], warp_max(ml[j].x));
+      const float corr = M[j] == -INFINITY ? 0.f : exp2f(M[j] - m);
+      wt[j] = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - m);
+      L[j] = L[j] * corr + warp_sum(wt[j] * ml[j].y);
+      M[j] = m;
+#pragma unroll
+      for (int f = 0; f < F; f++) o[j][f] *= corr;
+    }
+    const int n = min(32, n_rec - i0);
+#pragma unroll(8 / JOIN_ROWS)
+    for (int i = 0; i < n; i++) {
+#pragma unroll
+      for (int j = 0; j < JOIN_ROWS; j++) {
+        const float* src = p.rec_o + rec_of(i0 + i, min(row0 + j, rows - 1)) * D;
+        const float wi = __shfl_sync(FULL_MASK, wt[j], i);
+        if constexpr (F == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+          o[j][0] += wi * x.x;
+          o[j][1] += wi * x.y;
+          o[j][2] += wi * x.z;
+          o[j][3] += wi * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+          o[j][0] += wi * x.x;
+          o[j][1] += wi * x.y;
+        }
+      }
+    }
+  }
+  const int gl = p.group_log2;
+#pragma unroll
+  for (int j = 0; j < JOIN_ROWS; j++) {
+    const int row = row0 + j;
+    if (row >= rows) break;
+    const float inv = L[j] > 0.f ? 1.f / L[j] : 0.f;
+    const long long orow = (long long)(tok0 + (row >> gl)) * a.kv.Hq + (kvh << gl) + (row & ((1 << gl) - 1));
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * F;
+    if constexpr (F == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(o[j][0] * inv, o[j][1] * inv), pack2(o[j][2] * inv, o[j][3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack2(o[j][0] * inv, o[j][1] * inv);
+    if (lane == 0) a.lse[orow] = L[j] > 0.f ? (M[j] + log2f(L[j])) * TC_LN2 : -INFINITY;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TcLaunch p) {
   pdl_wait();
   pdl_trigger();
-  const TreeLaunch& a = p.a;
-  const TcSplit sp = p.split[blockIdx.x];
-  if (sp.b < 0) return;
-  const int G = a.kv.Hq / a.kv.Hkv, per_unit = UNIT_ROWS / G;
-  const int c0 = a.cu_new[sp.b], n = a.cu_new[sp.b + 1] - c0;
-  const int rows = min(UNIT_ROWS, (n - sp.block * per_unit) * G);
-  const int lane = threadIdx.x & 31;
-  const int c_first = blockIdx.x, c_last = (sp.start + sp.tiles - 1) / sp.per;
-  constexpr int F = D / 32;  // floats a lane
-  for (int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); row < rows; row += gridDim.y * JOIN_WARPS) {
-    auto rec_of = [&](int c) { return (long long)(2 * c + (c == c_first ? 1 : 0)) * p.rows_max + row; };
-    float M = -INFINITY;
-    for (int c = c_first + lane; c <= c_last; c += 32) M = fmaxf(M, __ldcg(p.rec_ml + rec_of(c) * 2));
-    M = warp_max(M);
-    float L = 0.f, o[F];
-#pragma unroll
-    for (int f = 0; f < F; f++) o[f] = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-      for (int c = c_first; c <= c_last; c++) {
-        const long long r = rec_of(c);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rec_ml + r * 2));
-        const float wt = exp2f(ml.x - M);
-        L += wt * ml.y;
-        if (F == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.rec_o + r * D) + lane);
-          o[0] += wt * x.x;
-          o[1] += wt * x.y;
-          o[F - 2] += wt * x.z;
-          o[F - 1] += wt * x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(p.rec_o + r * D) + lane);
-          o[0] += wt * x.x;
-          o[1] += wt * x.y;
-        }
-      }
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int tok = sp.block * per_unit + row / G;
-    const long long orow = (long long)(c0 + tok) * a.kv.Hq + sp.kvh * G + row % G;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * F;
-    if (F == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[F - 2] * inv, o[F - 1] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = pack2(o[0] * inv, o[1] * inv);
-    if (lane == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
+  const int4* sw = reinterpret_cast<const int4*>(p.split + blockIdx.x);
+  const int4 s0 = sw[0], s1 = sw[1];  // rows, kvh, tok, start; tiles, per
+  const int n_rec = (s0.w + s1.x - 1) / max(1, s1.y) - (int)blockIdx.x + 1;
+  const int w = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
+  if (n_rec > JOIN_FEW) {
+    if (w < s0.x) join_rows<D, 1>(p, w, s0.x, s0.y, s0.z, n_rec);
+  } else {
+    if (w * 4 < s0.x) join_rows<D, 4>(p, w * 4, s0.x, s0.y, s0.z, n_rec);
   }
 }
 
@@ -954,11 +994,14 @@ template <int D>
 static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cudaStream_t st) {
   using S = TcShape<D>;
   auto k = tree_tc_kernel<D>;
-  cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, k);
-  if (e != cudaSuccess) return e;
-  if (at.numRegs < TC_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+  // the register shares need what the kernel was compiled with, asked once
+  static const int regs = [k] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, k) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs < TC_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+  static int smem_set[SMEM_DEVICES];
+  cudaError_t e = allow_smem(k, S::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(sms), dim3(TC_THREADS), S::SMEM, st, p.a.kv.pdl, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
                  maps[6], p);
