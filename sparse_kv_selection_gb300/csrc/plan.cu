@@ -2,10 +2,12 @@
 //
 // Everything follows from two prefix sums over the sequences (new tokens; new
 // pages), so every CTA of one cluster forms both for itself from the cached
-// lengths (B values, a few loads per thread) and then takes an interleaved
-// share of the tokens, of the new pages and of the trees, finding a token's
-// sequence by a search in the shared prefix. The page counters may be updated
-// in place: they are written after a cluster barrier behind the last read.
+// lengths (B values, a few loads per thread, one scan) and then takes its share
+// of the tokens, of the new pages and of the trees. A chunk's token finds its
+// sequence by a search in the shared prefix, four tokens a thread at once so that
+// their searches and page reads overlap; a tree is one warp's, its slots too. The
+// page counters may be updated in place: they are written after a cluster
+// barrier behind the last read.
 //
 // A tree's masks are its ancestor sets, by pointer doubling: after round r a
 // token knows its ancestors up to 2^r steps up, anc(j) |= anc(up(j)), up(j) =
@@ -20,7 +22,7 @@
 
 namespace prhs {
 
-constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int PLAN_CLUSTER = 8;
 
@@ -29,46 +31,49 @@ struct PlanTree {  // one warp's tree
   int16_t up[PRHS_TREE_MAX];
 };
 
-// Exclusive block scan of one value per thread (64-bit); *total gets the sum.
-__device__ __forceinline__ long long block_scan(long long v, long long* wsum, long long* total) {
+// Exclusive block scan of two values per thread (64-bit); the sums into *tx, *ty.
+__device__ __forceinline__ void block_scan2(long long& x, long long& y, longlong2* wsum, long long* tx, long long* ty) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  const long long x0 = x, y0 = y;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(FULL_MASK, x, o);
-    if (lane >= o) x += y;
+    const long long u = __shfl_up_sync(FULL_MASK, x, o), v = __shfl_up_sync(FULL_MASK, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
   }
-  if (lane == 31) wsum[warp] = x;
+  if (lane == 31) wsum[warp] = make_longlong2(x, y);
   __syncthreads();
-  long long before = 0, all = 0;
+  // every warp scans the warps' sums for itself
+  longlong2 s = lane < PLAN_WARPS ? wsum[lane] : make_longlong2(0, 0);
+  long long bx = 0, by = 0, ax = s.x, ay = s.y;
 #pragma unroll
-  for (int w = 0; w < PLAN_WARPS; w++) {
-    const long long s = wsum[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int o = 16; o > 0; o >>= 1) {
+    ax += __shfl_xor_sync(FULL_MASK, ax, o);
+    ay += __shfl_xor_sync(FULL_MASK, ay, o);
   }
-  __syncthreads();
-  *total = all;
-  return before + x - v;
+  if (lane >= warp) s = make_longlong2(0, 0);
+  bx = s.x;
+  by = s.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    bx += __shfl_xor_sync(FULL_MASK, bx, o);
+    by += __shfl_xor_sync(FULL_MASK, by, o);
+  }
+  x += bx - x0;
+  y += by - y0;
+  *tx = ax;
+  *ty = ay;
 }
 
 __device__ __forceinline__ uint4 or4(uint4 a, uint4 b) {
   return make_uint4(a.x | b.x, a.y | b.y, a.z | b.z, a.w | b.w);
 }
 
-// Index of the last entry of the ascending list v[0..n) that is <= x (v[0] <= x).
-__device__ __forceinline__ int last_le(const int* v, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (v[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) {
   extern __shared__ __align__(16) uint8_t plan_smem[];
-  __shared__ long long wsum[PLAN_WARPS];
+  __shared__ longlong2 wsum[PLAN_WARPS];
   __shared__ int sh_taken;
   const KVView& kv = a.kv;
   const int B = kv.B, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,6 +85,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
 
+  if (tid == 0) sh_taken = 0;
   pdl_wait();
   pdl_trigger();
   const bool paged = a.block_table != nullptr, tree = a.parents != nullptr;
@@ -87,123 +93,88 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) 
   const int per = (B + PLAN_THREADS - 1) / PLAN_THREADS;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
 
-  // ---- prefix of the new tokens ----
-  long long mine = 0, total = 0;
-  for (int b = b0; b < b1; b++) mine += max(0, a.n_new[b]);
-  long long run = block_scan(mine, wsum, &total);
-  for (int b = b0; b < b1; b++) {
-    cu[b] = (int)min(run, (long long)a.T);
-    run += max(0, a.n_new[b]);
-  }
-  if (tid == 0) {
-    cu[B] = (int)min(total, (long long)a.T);
-    sh_taken = 0;
-  }
-  const int T = (int)min(total, (long long)a.T);  // tokens that are not padding
-
-  // ---- prefix of the new pages; a sequence that cannot be placed takes none ----
-  auto pages_of = [&](int b, unsigned& bits) -> int {
-    const int n = a.n_new[b], t = seq_len(kv, b);
+  // New pages of sequence b, 0 (and the reason) when it cannot be placed.
+  auto pages_of = [&](int b, int& n, unsigned& bits) -> int {
+    n = a.n_new[b];
+    const int t = seq_len(kv, b), have = paged ? a.n_pages[b] : 0;
     if (n < 0 || (tree && n > PRHS_TREE_MAX)) bits = PRHS_DEV_BAD_LEN;
-    else if (n > 0 && ((long long)t + n > kv.t_max || (long long)cu[b] + n > a.T)) bits = PRHS_DEV_CAPACITY;
+    else if (n > 0 && ((long long)t + n > kv.t_max || have < 0 || have > kv.max_blocks || head < 0)) bits = PRHS_DEV_CAPACITY;
     if (!paged || n <= 0 || bits != 0) return 0;
-    const int have = a.n_pages[b];
-    if (have < 0 || have > kv.max_blocks || head < 0) {
-      bits = PRHS_DEV_CAPACITY;
-      return 0;
-    }
     return max(0, (t + n + kv.block_size - 1) / kv.block_size - have);
   };
-  mine = 0;
+
+  // ---- prefixes of the new tokens and of the new pages ----
+  // (A sequence cut by T takes no page, but those behind it are cut too, so the
+  // prefix of every sequence that is placed is right without knowing.)
+  long long sum_n = 0, sum_p = 0, total = 0, pages = 0;
   for (int b = b0; b < b1; b++) {
+    int n;
     unsigned bits = 0;
-    mine += pages_of(b, bits);
+    sum_p += pages_of(b, n, bits);
+    sum_n += max(0, n);
   }
-  run = block_scan(mine, wsum, &total);
+  block_scan2(sum_n, sum_p, wsum, &total, &pages);
   for (int b = b0; b < b1; b++) {
+    int n;
     unsigned bits = 0;
-    const int take = pages_of(b, bits);
-    if (take > 0 && head + run + take > a.n_free) bits = PRHS_DEV_CAPACITY;
+    const int take = pages_of(b, n, bits);
+    cu[b] = (int)min(sum_n, (long long)a.T);
+    if (bits == 0 && n > 0 && sum_n + n > a.T) bits = PRHS_DEV_CAPACITY;
+    if (bits == 0 && take > 0 && head + sum_p + take > a.n_free) bits = PRHS_DEV_CAPACITY;
     // the sign bit marks a sequence that cannot be placed
-    pp[b] = (int)min(run, 0x7fffffffll) | (bits == 0 ? 0 : (int)0x80000000);
-    run += take;
-    if (bits == 0 && take > 0) atomicMax(&sh_taken, (int)run);
+    pp[b] = (int)min(sum_p, 0x7fffffffll) | (bits == 0 ? 0 : (int)0x80000000);
+    sum_n += max(0, n);
+    sum_p += take;
+    if (bits == 0 && take > 0) atomicMax(&sh_taken, (int)sum_p);
     if (bits != 0 && rank == 0) raise_error(kv.err, bits);
   }
+  const int T = (int)min(total, (long long)a.T);  // tokens that are not padding
+  if (tid == 0) cu[B] = T;
   __syncthreads();
   const int taken = sh_taken;
   const int step = ranks * PLAN_THREADS, first = rank * PLAN_THREADS + tid;
 
-  for (int b = first; b <= B; b += step) a.cu_new[b] = cu[b];
-
-  // ---- slots and positions ----
-  for (int i = first; i < a.T; i += step) {
-    int slot = -1, position = 0;
-    if (i < T) {
-      const int b = last_le(cu, B, i);
-      const int t = seq_len(kv, b);
-      position = t + (i - cu[b]);
-      const int p = pp[b];
-      if (p >= 0) {
-        if (!paged) {
-          slot = b * kv.t_max + position;
-        } else {
-          const int blk = position / kv.block_size, have = a.n_pages[b];
-          const int page = blk < have ? a.block_table[(long long)b * kv.max_blocks + blk]
-                                      : a.free_pages[head + p + blk - have];
-          if ((unsigned)page < (unsigned)kv.num_blocks)
-            slot = page * kv.block_size + (position - blk * kv.block_size);
-          else
-            raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
-        }
-      }
-    }
-    a.slots[i] = slot;
-    if (!tree || i >= T) a.positions[i] = position;
-    if (tree && i >= T) reinterpret_cast<uint4*>(a.tree_mask)[i] = make_uint4(0, 0, 0, 0);
-  }
-
-  // ---- new entries of the block tables ----
-  if (paged)
-    for (int g = first; g < taken; g += step) {
-      int lo = 0, hi = B - 1;  // the last sequence whose page prefix is <= g
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((pp[mid] & 0x7fffffff) <= g) lo = mid; else hi = mid - 1;
-      }
-      const int p = pp[lo];
-      if (p < 0) continue;
-      const int page = a.free_pages[head + g];
-      if ((unsigned)page >= (unsigned)kv.num_blocks) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
-      a.block_table[(long long)lo * kv.max_blocks + a.n_pages[lo] + (g - p)] = page;
-    }
+  // Slot of position `pos` of sequence b (p: its entry of pp, have: its pages), -1 when there is none.
+  auto slot_of = [&](int b, int pos, int p, int have) -> int {
+    if (p < 0) return -1;
+    if (!paged) return b * kv.t_max + pos;
+    const int blk = pos / kv.block_size;
+    const int page = blk < have ? a.block_table[(long long)b * kv.max_blocks + blk] : a.free_pages[head + p + blk - have];
+    if ((unsigned)page < (unsigned)kv.num_blocks) return page * kv.block_size + (pos - blk * kv.block_size);
+    raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
+    return -1;
+  };
 
   // ---- trees: one warp per sequence ----
   if (tree) {
     PlanTree& tr = trees[warp];
+    constexpr int PL = PRHS_TREE_MAX / 32;
     for (int b = rank * PLAN_WARPS + warp; b < B; b += ranks * PLAN_WARPS) {
-      const int c0 = cu[b], n = cu[b + 1] - c0, t = seq_len(kv, b);
-      if (n > PRHS_TREE_MAX) {  // refused above: no masks
+      const int c0 = cu[b], n = cu[b + 1] - c0, p = pp[b], t = seq_len(kv, b);
+      const int have = paged ? a.n_pages[b] : 0;
+      if (n > PRHS_TREE_MAX) {  // refused above: no masks, no slots
         for (int j = lane; j < n; j += 32) {
           reinterpret_cast<uint4*>(a.tree_mask)[c0 + j] = make_uint4(0, 0, 0, 0);
           a.positions[c0 + j] = t + j;
+          a.slots[c0 + j] = -1;
         }
         continue;
       }
-      constexpr int PL = PRHS_TREE_MAX / 32;
       uint4 anc[PL];
-      int up[PL];
+      int up[PL], slot[PL];
       bool more = false;
 #pragma unroll
       for (int k = 0; k < PL; k++) {
         const int j = k * 32 + lane;
         up[k] = -1;
+        slot[k] = -1;
         anc[k] = make_uint4(k == 0 ? 1u << lane : 0, k == 1 ? 1u << lane : 0, k == 2 ? 1u << lane : 0,
                             k == 3 ? 1u << lane : 0);
         if (j < n) {
-          const int p = a.parents[c0 + j];
-          if (p < -1 || p >= j) raise_error(kv.err, PRHS_DEV_BAD_INDEX);
-          else up[k] = p;
+          const int par = a.parents[c0 + j];
+          slot[k] = slot_of(b, t + j, p, have);
+          if (par < -1 || par >= j) raise_error(kv.err, PRHS_DEV_BAD_INDEX);
+          else up[k] = par;
           tr.anc[j] = anc[k];
           tr.up[j] = (int16_t)up[k];
         }
@@ -240,15 +211,70 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) 
         if (j < n) {
           reinterpret_cast<uint4*>(a.tree_mask)[c0 + j] = anc[k];
           a.positions[c0 + j] = t + __popc(anc[k].x) + __popc(anc[k].y) + __popc(anc[k].z) + __popc(anc[k].w) - 1;
+          a.slots[c0 + j] = slot[k];
         }
       }
       __syncwarp();
     }
+  } else {
+    // ---- chunks: slots and positions, four tokens of a thread at once ----
+    constexpr int TOKS = 4;
+    for (int i0 = first; i0 < T; i0 += step * TOKS) {
+      int b[TOKS], lo[TOKS], hi[TOKS];
+#pragma unroll
+      for (int u = 0; u < TOKS; u++) {
+        lo[u] = 0;
+        hi[u] = B - 1;
+      }
+      for (int w = B - 1; w > 0; w >>= 1)  // the last sequence that starts at or before the token
+#pragma unroll
+        for (int u = 0; u < TOKS; u++) {
+          const int mid = (lo[u] + hi[u] + 1) >> 1;
+          const bool le = cu[mid] <= i0 + u * step;
+          if (lo[u] < hi[u]) {
+            if (le) lo[u] = mid; else hi[u] = mid - 1;
+          }
+        }
+      int pos[TOKS], slot[TOKS];
+#pragma unroll
+      for (int u = 0; u < TOKS; u++) {
+        b[u] = lo[u];
+        pos[u] = seq_len(kv, b[u]) + (i0 + u * step - cu[b[u]]);
+      }
+#pragma unroll
+      for (int u = 0; u < TOKS; u++)
+        slot[u] = i0 + u * step < T ? slot_of(b[u], pos[u], pp[b[u]], paged ? a.n_pages[b[u]] : 0) : -1;
+#pragma unroll
+      for (int u = 0; u < TOKS; u++)
+        if (i0 + u * step < T) {
+          a.slots[i0 + u * step] = slot[u];
+          a.positions[i0 + u * step] = pos[u];
+        }
+    }
   }
 
-  // ---- counters: every CTA has read the old ones ----
+  for (int b = first; b <= B; b += step) a.cu_new[b] = cu[b];
+  for (int i = T + first; i < a.T; i += step) {  // padding
+    a.slots[i] = -1;
+    a.positions[i] = 0;
+    if (tree) reinterpret_cast<uint4*>(a.tree_mask)[i] = make_uint4(0, 0, 0, 0);
+  }
+
+  // ---- new entries of the block tables, then the counters ----
   if (!paged) return;
-  cluster.sync();
+  for (int g = first; g < taken; g += step) {
+    int lo = 0, hi = B - 1;  // the last sequence whose page prefix is <= g
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((pp[mid] & 0x7fffffff) <= g) lo = mid; else hi = mid - 1;
+    }
+    const int p = pp[lo];
+    if (p < 0) continue;
+    const int page = a.free_pages[head + g];
+    if ((unsigned)page >= (unsigned)kv.num_blocks) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
+    a.block_table[(long long)lo * kv.max_blocks + a.n_pages[lo] + (g - p)] = page;
+  }
+  cluster.sync();  // every CTA has read the old counters
   if (rank != 0) return;
   for (int b = tid; b < B; b += PLAN_THREADS) {
     const int have = a.n_pages[b], t = seq_len(kv, b), n = a.n_new[b];
@@ -266,7 +292,7 @@ cudaError_t launch_plan(const PlanLaunch& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // one CTA for a decode or verification step; a cluster for prompts and for
   // batches with more trees than one CTA's warps
-  const long long work = (long long)a.T / (2 * PLAN_THREADS);
+  const long long work = a.parents != nullptr ? 1 : (long long)a.T / (4 * PLAN_THREADS);
   const long long trees = a.parents != nullptr ? (a.kv.B + PLAN_WARPS - 1) / PLAN_WARPS : 1;
   int cl = 1;
   while (cl < PLAN_CLUSTER && (work > cl || trees > cl)) cl *= 2;

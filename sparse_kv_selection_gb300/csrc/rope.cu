@@ -8,10 +8,11 @@
 // bits, read as a signed number, are the angle in [-1/2, 1/2) turns to 2^-33.
 //
 // Every head of a token takes the same rot_dim / 2 angles, so a CTA computes
-// them once into shared memory. The work is cut into tasks of two 16-byte
-// pieces of one head row (the two halves of E pairs, E elements a piece, or
-// two pieces that are only copied), PER tasks a thread: the loads are issued
-// before the angles are computed, which hides one behind the other.
+// them once into shared memory, with the tokens' cache rows. The work is cut
+// into tasks of two 16-byte pieces of one head row (the two halves of E pairs, E
+// elements a piece, or two pieces that are only copied), PER tasks a thread: the
+// loads are issued before the angles are computed, which hides one behind the
+// other.
 //
 // Bound: HBM, each element read once and written once.
 #include "tokens.h"
@@ -37,86 +38,100 @@ __device__ __forceinline__ uint4 pack_piece<__nv_bfloat16>(const float* f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// One token of a CTA: its cache row (KV head 0; -1: nothing of it is written).
+struct RopeToken {
+  long long row;
+};
+
+// `rows` head rows a token (q, k and, with slots, v), 1 << tpr_log2 tasks a row.
 template <typename T, int PER>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeLaunch a, int rows, int tpr) {
+__global__ void __launch_bounds__(ROPE_THREADS, PER == 1 ? 1 : 4)
+    rope_kernel(const RopeLaunch a, int rows, float inv_rows, int tpr_log2, int max_tokens) {
   constexpr int E = Elem<T>::per16;
-  extern __shared__ __align__(16) float2 rope_cs[];  // [tokens of this CTA][rot_dim / 2]
-  pdl_wait();
-  pdl_trigger();
+  extern __shared__ __align__(16) uint8_t rope_smem[];
   const KVView& kv = a.kv;
   const int half = a.rot_dim / 2, rot_tasks = half / E;
-  const long long total = (long long)a.T * rows * tpr;
-  const long long x0 = (long long)blockIdx.x * (ROPE_THREADS * PER);
-  const int tok0 = (int)(x0 / (rows * tpr));
-  const int tok1 = (int)((min(total, x0 + ROPE_THREADS * PER) - 1) / (rows * tpr));
+  float2* cs = reinterpret_cast<float2*>(rope_smem);                    // [max_tokens][half]
+  RopeToken* token = reinterpret_cast<RopeToken*>(cs + max_tokens * half);  // [max_tokens]
+  pdl_wait();
+  pdl_trigger();
+
+  // Thread t takes piece pair x = t mod tasks of the head rows r0, r0 + step, ...
+  const int x = threadIdx.x & ((1 << tpr_log2) - 1), step = ROPE_THREADS >> tpr_log2;
+  const long long first = (long long)blockIdx.x * (step * PER), total = (long long)a.T * rows;
+  const int tok0 = (int)(first / rows);
+  const int base = (int)(first - (long long)tok0 * rows);     // head rows of tok0 before the CTA's
+  const int n_rows = (int)min((long long)step * PER, total - first);
+  const int tokens = (int)((base + n_rows - 1 + 0.5f) * inv_rows) + 1;
+  const bool rotated = x < rot_tasks;
+  const int p0 = rotated && !a.interleaved ? x : 2 * x;       // its two 16-byte pieces
+  const int p1 = rotated && !a.interleaved ? x + rot_tasks : 2 * x + 1;
 
   uint4 lo[PER], hi[PER];
-  int tok[PER], row[PER], x[PER], p0[PER], p1[PER];
 #pragma unroll
   for (int u = 0; u < PER; u++) {
-    const long long g = x0 + u * ROPE_THREADS + threadIdx.x;
-    tok[u] = -1;
-    if (g < total) {
-      const int rem = (int)(g - (long long)tok0 * rows * tpr);  // from the CTA's first token
-      const int r = rem / tpr;
-      x[u] = rem - r * tpr;
-      const int k = r / rows;
-      row[u] = r - k * rows;
-      tok[u] = tok0 + k;
-      const bool rotated = x[u] < rot_tasks;
-      p0[u] = rotated && !a.interleaved ? x[u] : 2 * x[u];
-      p1[u] = rotated && !a.interleaved ? x[u] + rot_tasks : 2 * x[u] + 1;
+    const int r = (threadIdx.x >> tpr_log2) + u * step;
+    if (r < n_rows) {
+      const int k = (int)((base + r + 0.5f) * inv_rows), row = base + r - k * rows;
+      const long long tok = tok0 + k;
       const T* src;
-      if (row[u] < kv.Hq) src = static_cast<const T*>(a.q) + tok[u] * a.qs + (long long)row[u] * kv.d;
-      else if (row[u] < kv.Hq + kv.Hkv) src = static_cast<const T*>(a.k) + tok[u] * a.ks + (long long)(row[u] - kv.Hq) * kv.d;
-      else src = static_cast<const T*>(a.v) + tok[u] * a.vs + (long long)(row[u] - kv.Hq - kv.Hkv) * kv.d;
-      lo[u] = reinterpret_cast<const uint4*>(src)[p0[u]];
-      hi[u] = reinterpret_cast<const uint4*>(src)[p1[u]];
+      if (row < kv.Hq) src = static_cast<const T*>(a.q) + tok * a.qs + (long long)row * kv.d;
+      else if (row < kv.Hq + kv.Hkv) src = static_cast<const T*>(a.k) + tok * a.ks + (long long)(row - kv.Hq) * kv.d;
+      else src = static_cast<const T*>(a.v) + tok * a.vs + (long long)(row - kv.Hq - kv.Hkv) * kv.d;
+      lo[u] = __ldcs(reinterpret_cast<const uint4*>(src) + p0);
+      hi[u] = __ldcs(reinterpret_cast<const uint4*>(src) + p1);
     }
   }
 
-  for (int i = threadIdx.x; i < (tok1 - tok0 + 1) * half; i += ROPE_THREADS) {
+  for (int i = threadIdx.x; i < tokens * half; i += ROPE_THREADS) {
     const int k = i / half, f = i - k * half;
     const uint64_t turn = (uint64_t)(int64_t)a.positions[tok0 + k] * a.turns[f];
     // half turns in [-1, 1)
     const float ht = (float)(int32_t)(turn >> 32) * 0x1p-31f;
     float s, c;
     sincospif(ht, &s, &c);
-    rope_cs[i] = make_float2(c * a.mscale, s * a.mscale);
+    cs[i] = make_float2(c * a.mscale, s * a.mscale);
+  }
+  for (int k = threadIdx.x; k < tokens; k += ROPE_THREADS) {
+    long long row = 0;
+    if (a.slots != nullptr) {
+      const int slot = a.slots[tok0 + k];
+      const int slots = kv.block_table != nullptr ? kv.num_blocks * kv.block_size : kv.B * kv.t_max;
+      int head_rows;
+      row = -1;
+      if (slot >= 0 && slot < slots) row = slot_row(kv, slot, &head_rows);
+      else if (slot != -1) raise_error(kv.err, PRHS_DEV_BAD_INDEX);
+    }
+    token[k].row = row;
   }
   __syncthreads();
+  const int head_rows = kv.block_table != nullptr ? kv.block_size : kv.t_max;
 
 #pragma unroll
   for (int u = 0; u < PER; u++) {
-    if (tok[u] < 0) continue;
-    int slot = 0;
-    if (a.slots != nullptr) {
-      slot = a.slots[tok[u]];
-      const int slots = kv.block_table != nullptr ? kv.num_blocks * kv.block_size : kv.B * kv.t_max;
-      if (slot < 0 || slot >= slots) {
-        if (slot != -1) raise_error(kv.err, PRHS_DEV_BAD_INDEX);
-        continue;
-      }
-    }
-    if (x[u] < rot_tasks && row[u] < kv.Hq + kv.Hkv) {
+    const int r = (threadIdx.x >> tpr_log2) + u * step;
+    if (r >= n_rows) break;
+    const int k = (int)((base + r + 0.5f) * inv_rows), row = base + r - k * rows;
+    const long long tok = tok0 + k, cache_row = token[k].row;
+    if (cache_row < 0) continue;
+    if (rotated && row < kv.Hq + kv.Hkv) {
       float e0[E], e1[E];
       Elem<T>::unpack(lo[u], e0);
       Elem<T>::unpack(hi[u], e1);
-      const float2* cs = rope_cs + (tok[u] - tok0) * half + x[u] * E;
+      const float2* t = cs + k * half + x * E;
       if (!a.interleaved) {
 #pragma unroll
         for (int e = 0; e < E; e++) {
-          const float2 t = cs[e];
-          const float r0 = e0[e] * t.x - e1[e] * t.y;
-          e1[e] = e0[e] * t.y + e1[e] * t.x;
+          const float r0 = e0[e] * t[e].x - e1[e] * t[e].y;
+          e1[e] = e0[e] * t[e].y + e1[e] * t[e].x;
           e0[e] = r0;
         }
       } else {
 #pragma unroll
         for (int e = 0; e < E / 2; e++) {
-          const float2 t = cs[e], w = cs[E / 2 + e];
-          const float r0 = e0[2 * e] * t.x - e0[2 * e + 1] * t.y;
-          e0[2 * e + 1] = e0[2 * e] * t.y + e0[2 * e + 1] * t.x;
+          const float2 v = t[e], w = t[E / 2 + e];
+          const float r0 = e0[2 * e] * v.x - e0[2 * e + 1] * v.y;
+          e0[2 * e + 1] = e0[2 * e] * v.y + e0[2 * e + 1] * v.x;
           e0[2 * e] = r0;
           const float r1 = e1[2 * e] * w.x - e1[2 * e + 1] * w.y;
           e1[2 * e + 1] = e1[2 * e] * w.y + e1[2 * e + 1] * w.x;
@@ -126,25 +141,24 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeLaunch a, 
       lo[u] = pack_piece<T>(e0);
       hi[u] = pack_piece<T>(e1);
     }
-    if (row[u] < kv.Hq) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + ((long long)tok[u] * kv.Hq + row[u]) * kv.d);
-      dst[p0[u]] = lo[u];
-      dst[p1[u]] = hi[u];
+    if (row < kv.Hq) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + (tok * kv.Hq + row) * kv.d);
+      dst[p0] = lo[u];
+      dst[p1] = hi[u];
       continue;
     }
-    const bool is_k = row[u] < kv.Hq + kv.Hkv;
-    const int h = row[u] - kv.Hq - (is_k ? 0 : kv.Hkv);
+    const bool is_k = row < kv.Hq + kv.Hkv;
+    const int h = row - kv.Hq - (is_k ? 0 : kv.Hkv);
     if (is_k && a.k_out != nullptr) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + ((long long)tok[u] * kv.Hkv + h) * kv.d);
-      dst[p0[u]] = lo[u];
-      dst[p1[u]] = hi[u];
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + (tok * kv.Hkv + h) * kv.d);
+      dst[p0] = lo[u];
+      dst[p1] = hi[u];
     }
     if (a.slots != nullptr) {
-      int head_rows;
-      const long long r = slot_row(kv, slot, &head_rows) + (long long)h * head_rows;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(const_cast<void*>(is_k ? kv.k : kv.v)) + r * kv.d);
-      dst[p0[u]] = lo[u];
-      dst[p1[u]] = hi[u];
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(const_cast<void*>(is_k ? kv.k : kv.v)) +
+                                            (cache_row + (long long)h * head_rows) * kv.d);
+      dst[p0] = lo[u];
+      dst[p1] = hi[u];
     }
   }
 }
@@ -153,18 +167,19 @@ template <typename T, int PER>
 static cudaError_t rope_go(const RopeLaunch& a, cudaStream_t st) {
   constexpr int E = Elem<T>::per16;
   const int rows = a.kv.Hq + (a.slots != nullptr ? 2 : 1) * a.kv.Hkv;
-  const int tpr = a.kv.d / (2 * E);
-  const long long total = (long long)a.T * rows * tpr;
-  const int chunk = ROPE_THREADS * PER;
+  int tpr_log2 = 0;
+  while ((2 * E) << tpr_log2 < a.kv.d) tpr_log2++;  // d / (2 E) tasks a row: 4, 8 or 16
+  const int chunk = (ROPE_THREADS >> tpr_log2) * PER;  // head rows of a CTA
   // tokens a CTA may touch: its whole ones and one cut at each end
-  const long long toks = (chunk + rows * tpr - 1) / (rows * tpr) + 1;
-  const size_t smem = (size_t)(toks < a.T ? toks : a.T) * (a.rot_dim / 2) * sizeof(float2);
+  const long long most = (chunk + rows - 1) / rows + 1;
+  const int max_tokens = (int)(most < a.T ? most : a.T);
+  const size_t smem = (size_t)max_tokens * (a.rot_dim / 2 * sizeof(float2) + sizeof(RopeToken));
   auto k = rope_kernel<T, PER>;
   static int smem_set[SMEM_DEVICES];
   const cudaError_t e = allow_smem(k, smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3((unsigned)((total + chunk - 1) / chunk)), dim3(ROPE_THREADS), smem, st, a.kv.pdl, a,
-                    rows, tpr);
+  return launch_pdl(k, dim3((unsigned)(((long long)a.T * rows + chunk - 1) / chunk)), dim3(ROPE_THREADS), smem, st,
+                    a.kv.pdl, a, rows, 1.0f / rows, tpr_log2, max_tokens);
 }
 
 cudaError_t launch_rope(const RopeLaunch& a, int sms, cudaStream_t st) {

@@ -71,7 +71,10 @@ struct TreeLaunch {
   void* out;             // the cache's element type
   float* lse;
 };
-cudaError_t launch_tree(const TreeLaunch& a, cudaStream_t s);  // fp32
+// fp32: one launch, or two where the key tiles are split; ws holds
+// tree_workspace(kv, max_new, sms) bytes.
+cudaError_t launch_tree(const TreeLaunch& a, int max_new, int sms, void* ws, cudaStream_t s);
+size_t tree_workspace(const KVView& kv, int max_new, int sms);
 // bf16: two launches, the first counted by the callee; *err is the launches'
 // result when the descriptors could be made. Workspace bytes of a call.
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);

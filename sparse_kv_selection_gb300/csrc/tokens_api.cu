@@ -27,9 +27,8 @@ prhs_status launched(cudaError_t e, const char* what) {
   return abi_fail(PRHS_ECUDA, cudaGetErrorString(e));
 }
 
-// fp32 caches need none; the size stays positive so that 0 means an error.
 size_t tree_ws_bytes(const KVView& kv, int max_new, int sms) {
-  return kv.dtype == PRHS_BF16 ? tree_tc_workspace(kv, max_new, sms) : 256;
+  return kv.dtype == PRHS_BF16 ? tree_tc_workspace(kv, max_new, sms) : tree_workspace(kv, max_new, sms);
 }
 
 // Checks shared by every entry point: descriptor, device, token count.
@@ -207,12 +206,11 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
     return abi_fail(PRHS_EINVAL, "tree: q, out and tree_mask must be 16-byte aligned");
   if ((s = check_new(*kv, k_new, k_stride, v_new, v_stride, "tree: k_new and v_new must be 16-byte aligned")) != PRHS_OK)
     return s;
-  if (T > 0 && max_new > T) max_new = T;
   if ((s = begin(kv, T, &a.kv, &sms)) != PRHS_OK) return s;
   // 32-bit tile counts: units (256 rows of tokens times group) times their tiles
   const int G = kv->Hq / kv->Hkv;
   const long long units = ((long long)T * G / 256 + kv->B) * kv->Hkv;
-  if (units * (a.kv.t_max / 128 + max_new / 128 + 2) >= (1ll << 31))
+  if (units * (a.kv.t_max / 128 + (max_new < T ? max_new : T) / 128 + 2) >= (1ll << 31))
     return abi_fail(PRHS_EUNSUPPORTED, "tree: too many key tiles for one call");
   const size_t need = tree_ws_bytes(a.kv, max_new, sms);
   if (!ws) return abi_fail(PRHS_EWORKSPACE, "workspace is null");
@@ -227,11 +225,11 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   a.scale = scale;
   a.T = T;
   a.cu_new = cu_new;
-  a.max_new = max_new;
+  a.max_new = max_new < T ? max_new : T;  // (a sequence above T is flagged either way)
   a.mask = tree_mask;
   a.out = out;
   a.lse = lse;
-  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, stream), "tree attention");
+  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, max_new, sms, ws, stream), "tree attention");
   cudaError_t e;
   if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
   return launched(e, "tree attention");

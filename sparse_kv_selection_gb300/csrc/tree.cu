@@ -1,5 +1,6 @@
 // Attention of a batch of new tokens over their sequences' caches and over
-// each other (a tree by its masks, or a causal chunk), on the CUDA cores.
+// each other (a tree by its masks, or a causal chunk), fp32 on the CUDA cores
+// (the tensor cores' fp32 forms drop mantissa bits).
 //
 // The G query heads of one KV head see the same keys, so a CTA takes TR rows of
 // one (sequence, KV head): row r is token r / G, query head r % G of the group.
@@ -7,7 +8,9 @@
 // memory; each thread computes 2 rows by 4 keys of the logits, the 16 threads
 // of a row pair keep its running maximum and sum (base 2) by shuffles, and the
 // weights go through shared memory to the product with V, 2 rows by D / 16
-// columns a thread, in fp32 throughout.
+// columns a thread, in fp32 throughout. Where the row blocks are fewer than the
+// CTAs that fill the SMs, the key tiles of each are split over several CTAs,
+// whose partial states a second launch joins.
 #include "tokens.h"
 
 namespace prhs {
@@ -18,26 +21,37 @@ constexpr int TREE_THREADS = 256;
 constexpr float T_LOG2E = 1.4426950408889634f;
 constexpr float T_LN2 = 0.6931471805599453f;
 
+// Splits of a row block's key tiles: enough CTAs for two waves of two an SM,
+// while each has at least two tiles of the longest cache.
+static int tree_splits(const KVView& kv, long long max_new, int sms) {
+  const long long G = kv.Hq / kv.Hkv;
+  const long long blocks = ((max_new * G + TR - 1) / TR) * kv.Hkv * kv.B;
+  const long long tiles = ((long long)kv.t_max + TK - 1) / TK + 1;
+  long long s = 4ll * sms / blocks;
+  if (s > tiles / 2) s = tiles / 2;
+  return s < 1 ? 1 : (int)s;
+}
+
+// Rows of partial records: (row block, split, row).
+static size_t tree_records(const KVView& kv, long long max_new, int splits) {
+  const long long G = kv.Hq / kv.Hkv;
+  return splits == 1 ? 0 : (size_t)(((max_new * G + TR - 1) / TR) * kv.Hkv * kv.B) * splits * TR;
+}
+
+size_t tree_workspace(const KVView& kv, int max_new, int sms) {
+  const size_t r = tree_records(kv, max_new, tree_splits(kv, max_new, sms));
+  return 256 + r * (kv.d + 2) * sizeof(float);
+}
+
 template <int D>
 struct TreeShape {
   static constexpr int LD = D + 4;  // row stride of Q and K: float4 reads of 8 rows hit distinct banks
   static constexpr size_t SMEM = ((size_t)TR * LD + (size_t)TK * LD + (size_t)TK * D + (size_t)TR * (TK + 1)) * 4;
 };
 
-template <typename T>
-__device__ __forceinline__ void store_out(T* p, const float* f);
-template <>
-__device__ __forceinline__ void store_out<float>(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
-template <>
-__device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* p, const float* f) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(TREE_THREADS) tree_kernel(const TreeLaunch a) {
+template <int D>
+__global__ void __launch_bounds__(TREE_THREADS, 2) tree_kernel(const TreeLaunch a, int splits, float2* rec_ml, float* rec_o) {
+  using T = float;
   using S = TreeShape<D>;
   constexpr int E = Elem<T>::per16, PPR = D / E;
   constexpr int OC = D / 64;  // float4 column groups a thread holds
@@ -52,10 +66,11 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_kernel(const TreeLaunch a) 
   pdl_trigger();
   const KVView& kv = a.kv;
   const int G = kv.Hq / kv.Hkv, kvh = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int block = blockIdx.x / splits, split = blockIdx.x - block * splits;
   const int t = seq_len(kv, b);
   int c0 = 0;
   const int n = seq_tokens(a.cu_new, b, a.T, a.max_new, kv.err, &c0);
-  const int r0 = blockIdx.x * TR;
+  const int r0 = block * TR;
   if (r0 >= n * G) return;
   const int last_tok = min(n, (r0 + TR + G - 1) / G);  // one past the CTA's last token
   const int n_keys = a.mask != nullptr ? n : last_tok;  // new tokens that may be attended
@@ -85,7 +100,9 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_kernel(const TreeLaunch a) 
     for (int c = 0; c < OC * 4; c++) o[i][c] = 0.f;
 
   const int cache_tiles = (t + TK - 1) / TK, new_tiles = (n_keys + TK - 1) / TK;
-  for (int it = 0; it < cache_tiles + new_tiles; it++) {
+  const int per = (cache_tiles + new_tiles + splits - 1) / splits;
+  const int it_end = min(cache_tiles + new_tiles, (split + 1) * per);
+  for (int it = split * per; it < it_end; it++) {
     const bool cached = it < cache_tiles;
     const int key0 = (cached ? it : it - cache_tiles) * TK;
     const int lim = cached ? t : n_keys;
@@ -194,32 +211,87 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_kernel(const TreeLaunch a) 
 #pragma unroll
     for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, s);
     if (j >= n) continue;
+    if (splits > 1) {  // a partial record (m, l and O against m)
+      const long long rec = ((((long long)b * kv.Hkv + kvh) * (gridDim.x / splits) + block) * splits + split) * TR + 2 * ty + i;
+#pragma unroll
+      for (int c = 0; c < OC; c++)
+        *reinterpret_cast<float4*>(rec_o + rec * D + c * 64 + tx * 4) =
+            make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
+      if (tx == 0) rec_ml[rec] = make_float2(m[i], sum);
+      continue;
+    }
     const long long orow = (long long)(c0 + j) * kv.Hq + kvh * G + g;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int c = 0; c < OC; c++) {
-      float f[4];
-#pragma unroll
-      for (int e = 0; e < 4; e++) f[e] = o[i][4 * c + e] * inv;
-      store_out(static_cast<T*>(a.out) + orow * D + c * 64 + tx * 4, f);
+      *reinterpret_cast<float4*>(static_cast<T*>(a.out) + orow * D + c * 64 + tx * 4) =
+          make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
     }
     if (tx == 0) a.lse[orow] = sum > 0.f ? (m[i] + log2f(sum)) * T_LN2 : -INFINITY;
   }
 }
 
-template <typename T, int D>
-static cudaError_t tree_go(const TreeLaunch& a, cudaStream_t st) {
-  auto k = tree_kernel<T, D>;
-  static int smem_set[SMEM_DEVICES];
-  const cudaError_t e = allow_smem(k, TreeShape<D>::SMEM, smem_set);
-  if (e != cudaSuccess) return e;
-  const int G = a.kv.Hq / a.kv.Hkv;
-  const unsigned blocks = (unsigned)(((long long)a.max_new * G + TR - 1) / TR);
-  return launch_pdl(k, dim3(blocks, a.kv.Hkv, a.kv.B), dim3(TREE_THREADS), TreeShape<D>::SMEM, st, a.kv.pdl, a);
+// One warp per row joins its splits' records.
+constexpr int TREE_JOIN_WARPS = 4;
+template <int D>
+__global__ void __launch_bounds__(TREE_JOIN_WARPS * 32) tree_join_f32_kernel(const TreeLaunch a, int splits, int blocks,
+                                                                             const float2* rec_ml, const float* rec_o) {
+  pdl_wait();
+  pdl_trigger();
+  const KVView& kv = a.kv;
+  const int G = kv.Hq / kv.Hkv, kvh = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
+  int c0 = 0;
+  const int n = seq_tokens(a.cu_new, b, a.T, a.max_new, kv.err, &c0);
+  const int row = blockIdx.x * TREE_JOIN_WARPS + (threadIdx.x >> 5);
+  if (row >= n * G) return;
+  const long long rec0 = ((((long long)b * kv.Hkv + kvh) * blocks + row / TR) * splits) * TR + row % TR;
+  float M = -INFINITY;
+  for (int i = lane; i < splits; i += 32) M = fmaxf(M, __ldcg(rec_ml + rec0 + (long long)i * TR).x);
+  M = warp_max(M);
+  constexpr int F = D / 32;
+  float L = 0.f, o[F];
+#pragma unroll
+  for (int f = 0; f < F; f++) o[f] = 0.f;
+  if (M != -INFINITY) {
+#pragma unroll 8
+    for (int i = 0; i < splits; i++) {
+      const long long rec = rec0 + (long long)i * TR;
+      const float2 ml = __ldcg(rec_ml + rec);
+      const float wt = exp2f(ml.x - M);  // 0 where the split had nothing
+      L += wt * ml.y;
+#pragma unroll
+      for (int f = 0; f < F; f++) o[f] += wt * __ldcg(rec_o + rec * D + f * 32 + lane);
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const long long orow = (long long)(c0 + row / G) * kv.Hq + kvh * G + row % G;
+#pragma unroll
+  for (int f = 0; f < F; f++) static_cast<float*>(a.out)[orow * D + f * 32 + lane] = o[f] * inv;
+  if (lane == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * T_LN2 : -INFINITY;
 }
 
-cudaError_t launch_tree(const TreeLaunch& a, cudaStream_t st) {
-  return a.kv.d == 128 ? tree_go<float, 128>(a, st) : tree_go<float, 64>(a, st);
+template <int D>
+static cudaError_t tree_go(const TreeLaunch& a, int splits, float2* rec_ml, float* rec_o, cudaStream_t st) {
+  auto k = tree_kernel<D>;
+  static int smem_set[SMEM_DEVICES];
+  cudaError_t e = allow_smem(k, TreeShape<D>::SMEM, smem_set);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)a.max_new * (a.kv.Hq / a.kv.Hkv);
+  const unsigned blocks = (unsigned)((rows + TR - 1) / TR);
+  e = launch_pdl(k, dim3(blocks * splits, a.kv.Hkv, a.kv.B), dim3(TREE_THREADS), TreeShape<D>::SMEM, st, a.kv.pdl, a, splits,
+                 rec_ml, rec_o);
+  if (e != cudaSuccess || splits == 1) return e;
+  abi_count_launch();
+  return launch_pdl(tree_join_f32_kernel<D>, dim3((unsigned)((rows + TREE_JOIN_WARPS - 1) / TREE_JOIN_WARPS), a.kv.Hkv, a.kv.B),
+                    dim3(TREE_JOIN_WARPS * 32), 0, st, true, a, splits, (int)blocks, (const float2*)rec_ml, (const float*)rec_o);
+}
+
+cudaError_t launch_tree(const TreeLaunch& a, int max_new, int sms, void* ws, cudaStream_t st) {
+  // (the workspace was sized for max_new, of which a.max_new is what T leaves)
+  const int splits = tree_splits(a.kv, max_new, sms);
+  float2* ml = static_cast<float2*>(ws);
+  float* o = reinterpret_cast<float*>(static_cast<char*>(ws) + (tree_records(a.kv, max_new, splits) * 8 + 255) / 256 * 256);
+  return a.kv.d == 128 ? tree_go<128>(a, splits, ml, o, st) : tree_go<64>(a, splits, ml, o, st);
 }
 
 }  // namespace prhs
