@@ -3,9 +3,9 @@
 // Everything follows from two prefix sums over the sequences (new tokens; new
 // pages), so every CTA of one cluster forms both for itself from the cached
 // lengths (B values, a few loads per thread, one scan) and then takes its share
-// of the tokens, of the new pages and of the trees. A chunk's token finds its
-// sequence by a search in the shared prefix, four tokens a thread at once so that
-// their searches and page reads overlap; a tree is one warp's, its slots too. The
+// of the tokens, of the new pages and of the trees. A warp takes 128 tokens of the
+// chunks, whose sequence it finds by a search in the shared prefix (four tokens a
+// thread, so that their page reads overlap); a tree is one warp's, its slots too. The
 // page counters may be updated in place: they are written after a cluster
 // barrier behind the last read.
 //
@@ -24,7 +24,7 @@ namespace prhs {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
-constexpr int PLAN_CLUSTER = 8;
+constexpr int PLAN_CLUSTER = 16;  // above 8 by opt-in
 
 struct PlanTree {  // one warp's tree
   uint4 anc[PRHS_TREE_MAX];
@@ -69,6 +69,15 @@ __device__ __forceinline__ void block_scan2(long long& x, long long& y, longlong
 
 __device__ __forceinline__ uint4 or4(uint4 a, uint4 b) {
   return make_uint4(a.x | b.x, a.y | b.y, a.z | b.z, a.w | b.w);
+}
+
+// Index of the last entry of the ascending list v[lo .. hi] that is <= x (v[lo] <= x).
+__device__ __forceinline__ int last_le(const int* v, int lo, int hi, int x) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) {
@@ -134,11 +143,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) 
   const int taken = sh_taken;
   const int step = ranks * PLAN_THREADS, first = rank * PLAN_THREADS + tid;
 
+  const int shift = __ffs(kv.block_size) - 1;
+  const bool pow2 = kv.block_size == 1 << shift;
   // Slot of position `pos` of sequence b (p: its entry of pp, have: its pages), -1 when there is none.
   auto slot_of = [&](int b, int pos, int p, int have) -> int {
     if (p < 0) return -1;
     if (!paged) return b * kv.t_max + pos;
-    const int blk = pos / kv.block_size;
+    const int blk = pow2 ? pos >> shift : pos / kv.block_size;
     const int page = blk < have ? a.block_table[(long long)b * kv.max_blocks + blk] : a.free_pages[head + p + blk - have];
     if ((unsigned)page < (unsigned)kv.num_blocks) return page * kv.block_size + (pos - blk * kv.block_size);
     raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
@@ -217,39 +228,27 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanLaunch a) 
       __syncwarp();
     }
   } else {
-    // ---- chunks: slots and positions, four tokens of a thread at once ----
+    // ---- chunks: a warp takes 128 consecutive tokens, mostly of one sequence ----
     constexpr int TOKS = 4;
-    for (int i0 = first; i0 < T; i0 += step * TOKS) {
-      int b[TOKS], lo[TOKS], hi[TOKS];
+    for (int w0 = (rank * PLAN_WARPS + warp) * 32 * TOKS; w0 < T; w0 += ranks * PLAN_WARPS * 32 * TOKS) {
+      const int bw = last_le(cu, 0, B - 1, w0);
+      int b[TOKS], pos[TOKS], slot[TOKS];
 #pragma unroll
       for (int u = 0; u < TOKS; u++) {
-        lo[u] = 0;
-        hi[u] = B - 1;
+        const int i = min(w0 + u * 32 + lane, T - 1);
+        b[u] = i < cu[bw + 1] ? bw : last_le(cu, bw + 1, B - 1, i);
+        pos[u] = seq_len(kv, b[u]) + (i - cu[b[u]]);
       }
-      for (int w = B - 1; w > 0; w >>= 1)  // the last sequence that starts at or before the token
 #pragma unroll
-        for (int u = 0; u < TOKS; u++) {
-          const int mid = (lo[u] + hi[u] + 1) >> 1;
-          const bool le = cu[mid] <= i0 + u * step;
-          if (lo[u] < hi[u]) {
-            if (le) lo[u] = mid; else hi[u] = mid - 1;
-          }
-        }
-      int pos[TOKS], slot[TOKS];
+      for (int u = 0; u < TOKS; u++) slot[u] = slot_of(b[u], pos[u], pp[b[u]], paged ? a.n_pages[b[u]] : 0);
 #pragma unroll
       for (int u = 0; u < TOKS; u++) {
-        b[u] = lo[u];
-        pos[u] = seq_len(kv, b[u]) + (i0 + u * step - cu[b[u]]);
-      }
-#pragma unroll
-      for (int u = 0; u < TOKS; u++)
-        slot[u] = i0 + u * step < T ? slot_of(b[u], pos[u], pp[b[u]], paged ? a.n_pages[b[u]] : 0) : -1;
-#pragma unroll
-      for (int u = 0; u < TOKS; u++)
-        if (i0 + u * step < T) {
-          a.slots[i0 + u * step] = slot[u];
-          a.positions[i0 + u * step] = pos[u];
+        const int i = w0 + u * 32 + lane;
+        if (i < T) {
+          a.slots[i] = slot[u];
+          a.positions[i] = pos[u];
         }
+      }
     }
   }
 
@@ -288,7 +287,7 @@ cudaError_t launch_plan(const PlanLaunch& a, cudaStream_t st) {
   const size_t lists = ((size_t)2 * (a.kv.B + 1) * 4 + 15) / 16 * 16;
   const size_t smem = lists + (a.parents != nullptr ? PLAN_WARPS * sizeof(PlanTree) : 0);
   static int smem_set[SMEM_DEVICES];
-  const cudaError_t e = allow_smem(plan_kernel, smem, smem_set);
+  cudaError_t e = allow_smem(plan_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
   // one CTA for a decode or verification step; a cluster for prompts and for
   // batches with more trees than one CTA's warps
@@ -296,6 +295,8 @@ cudaError_t launch_plan(const PlanLaunch& a, cudaStream_t st) {
   const long long trees = a.parents != nullptr ? (a.kv.B + PLAN_WARPS - 1) / PLAN_WARPS : 1;
   int cl = 1;
   while (cl < PLAN_CLUSTER && (work > cl || trees > cl)) cl *= 2;
+  if (cl > 8 && (e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cl);
   cfg.blockDim = dim3(PLAN_THREADS);

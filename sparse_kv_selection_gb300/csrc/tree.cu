@@ -22,13 +22,13 @@ constexpr float T_LOG2E = 1.4426950408889634f;
 constexpr float T_LN2 = 0.6931471805599453f;
 
 // Splits of a row block's key tiles: enough CTAs for two waves of two an SM,
-// while each has at least two tiles of the longest cache.
+// while each has a tile of the longest cache.
 static int tree_splits(const KVView& kv, long long max_new, int sms) {
   const long long G = kv.Hq / kv.Hkv;
   const long long blocks = ((max_new * G + TR - 1) / TR) * kv.Hkv * kv.B;
   const long long tiles = ((long long)kv.t_max + TK - 1) / TK + 1;
   long long s = 4ll * sms / blocks;
-  if (s > tiles / 2) s = tiles / 2;
+  if (s > tiles) s = tiles;
   return s < 1 ? 1 : (int)s;
 }
 

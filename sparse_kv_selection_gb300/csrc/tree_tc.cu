@@ -9,8 +9,10 @@
 // ones packed without a plan made on the host. A unit cut by a run's end leaves
 // partial states in the workspace, which a second launch joins row by row.
 //
-// Inside a CTA: one warp loads K and V tiles by TMA into a ring of 128-key
-// slots (128-byte swizzle), another the units' Q tiles into two more (so that
+// Inside a CTA: two warps load K and V tiles by TMA into a ring of 128-key
+// slots (128-byte swizzle), half the boxes of each tile each (a tile on 16-key
+// pages is 16 copies of 2 KB, more than one thread issues at HBM's rate beside
+// the rest), the scheduler's warp the units' Q tiles into two more (so that
 // neither holds the other back where units change), one thread issues the
 // matrix instructions, and two
 // warpgroups do the softmax, one per stream. A stream is a logit tile S
@@ -41,7 +43,7 @@ namespace prhs {
 
 constexpr int TT = 128;                  // keys of a tile, rows of a stream
 constexpr int UNIT_ROWS = 2 * TT;
-constexpr int TC_WARPS = 12;             // 8 softmax, K/V producer, matrix issuer, Q producer, scheduler
+constexpr int TC_WARPS = 12;             // 8 softmax, two K/V producers, matrix issuer, scheduler
 // Registers a thread: the softmax warpgroups hold a row of logits each, so they
 // take over part of the third one's. The three shares add up to what the block
 // is launched with (checked before the launch: a larger sum would wait forever).
@@ -100,6 +102,13 @@ struct TcRing {
       phase ^= 1;
     }
   }
+};
+
+struct TcSeq {  // one sequence's share of the list
+  int c0, n, t;      // first token, tokens, cached keys
+  int blocks;        // units of one KV head
+  int cache_tiles;
+  int tiles;         // tiles of one KV head
 };
 
 struct TcBars {  // one mbarrier each
@@ -256,13 +265,6 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 // -------------------------------------------------------------------------- //
 // the list of tiles
 // -------------------------------------------------------------------------- //
-struct TcSeq {  // one sequence's share of the list
-  int c0, n, t;      // first token, tokens, cached keys
-  int blocks;        // units of one KV head
-  int cache_tiles;
-  int tiles;         // tiles of one KV head
-};
-
 // New-token tiles of the units before unit j (1 << ul tokens each): a causal
 // unit sees the tokens up to its own last one, a tree unit all of them (one tile).
 __device__ __forceinline__ int new_tiles_before(int j, int blocks, int n, int ul, bool causal) {
@@ -309,26 +311,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   TcAux& aux = *reinterpret_cast<TcAux*>(data + S::DATA);
   TcBars& bar = aux.bar;
 
-  pdl_wait();
-  pdl_trigger();
-
-  // ---- this CTA's run of the list of all tiles ----
-  const int per_t = (B + TC_THREADS - 1) / TC_THREADS;
-  int mine = 0;
-  for (int k = 0; k < per_t; k++) {
-    const int b = tid * per_t + k;
-    if (b < B) mine += kv.Hkv * tc_seq(a, b, ul).tiles;
-  }
-  int run = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(FULL_MASK, run, o);
-    if (lane >= o) run += y;
-  }
-  if (lane == 31) aux.wsum[warp] = run;
-  if (tid == 0) {
+  // ---- what needs nothing of earlier launches: barriers, tensor memory ----
+  if (warp == 10 && lane == 0) {
     for (int i = 0; i < S::SLOTS; i++) {
-      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.full[i], 2);  // one arrival of each producer
       mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < 2; i++) {
@@ -348,20 +334,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     aux.bad_page = 0;
     if ((base & 1023) != 0) raise_error(kv.err, PRHS_DEV_CAPACITY);  // the swizzle needs it
   }
+  if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's run of the list of all tiles ----
+  const int per_t = (B + TC_THREADS - 1) / TC_THREADS, b0 = tid * per_t;
+  int mine = 0;
+  for (int b = b0; b < min(B, b0 + per_t); b++) mine += kv.Hkv * tc_seq(a, b, ul).tiles;
+  int run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL_MASK, run, o);
+    if (lane >= o) run += y;
+  }
+  if (lane == 31) aux.wsum[warp] = run;
   __syncthreads();
   int total = 0, before = 0;
+#pragma unroll
   for (int w = 0; w < TC_WARPS; w++) {
-    if (w < warp) before += aux.wsum[w];
-    total += aux.wsum[w];
+    const int x = aux.wsum[w];
+    if (w < warp) before += x;
+    total += x;
   }
   before += run - mine;
   const int per = (total + gridDim.x - 1) / (int)gridDim.x;
-  const int g0 = blockIdx.x * per, count = min(total, g0 + per) - g0;
-  if (count <= 0 || (base & 1023) != 0) {
-    if (tid == 0) p.split[blockIdx.x].rows = 0;
-    return;
-  }
-  if (g0 >= before && g0 < before + mine) {
+  const int g0 = blockIdx.x * per, count = (base & 1023) != 0 ? 0 : min(total, g0 + per) - g0;
+  if (count > 0 && g0 >= before && g0 < before + mine) {  // the run begins in this thread's sequences
     int off = g0 - before;
     for (int k = 0; k < per_t; k++) {
       const int b = tid * per_t + k, x = kv.Hkv * tc_seq(a, b, ul).tiles;
@@ -372,6 +371,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       off -= x;
     }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (count <= 0) {  // no tiles left for this CTA
+    if (tid == 0) p.split[blockIdx.x].rows = 0;
+    return;
   }
   if (warp == 9) {  // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&aux.tmem))
@@ -399,7 +404,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_REST));
     if (warp == 11) {
-      // ------------------------------ scheduler ------------------------------ //
+      // ---------------------- scheduler, and Q producer ---------------------- //
+      const bool leader = elect_one();
       int b = aux.start_b, off = aux.start_off, left = count, loads = 0, qtiles = 0;
       const bool causal = a.mask == nullptr;
       TcSeq s = tc_seq(a, b, ul);
@@ -447,9 +453,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             p.split[blockIdx.x] = sp;
           }
         }
-        if (left == 0) break;
+        __syncwarp();
+        bool ok = true;
+        const int q_end = qtiles + (rows <= TT ? 1 : 2);
+        for (int j = 0; ok && qtiles < q_end; j++, qtiles++) {
+          const int slot = qtiles & 1;
+          ok = __all_sync(FULL_MASK, mbar_wait(&bar.qempty[slot], ((qtiles >> 1) & 1) ^ 1, kv.err));
+          if (ok && leader) {
+            mbar_arrive_expect_tx(&bar.qfull[slot], S::TILE);
+#pragma unroll
+            for (int sg = 0; sg < S::SEGS; sg++)
+              tma_load_4d(base + (S::SLOTS + slot) * S::TILE + sg * S::SEG, &qmap, 0, sg, kvh << gl,
+                          s.c0 + (block << ul) + (j << (7 - gl)), &bar.qfull[slot]);
+          }
+          __syncwarp();
+        }
+        if (!ok || left == 0) break;
         loads += 2 * nt;
-        qtiles += rows <= TT ? 1 : 2;
         off = 0;
         if (++block == s.blocks) {
           block = 0;
@@ -460,9 +480,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
         }
       }
-    } else if (warp == 8) {
-      // -------------------------- K and V producer -------------------------- //
+      for (int qt = max(0, qtiles - 2); qt < qtiles; qt++)
+        mbar_wait(&bar.qfull[qt & 1], (qt >> 1) & 1, kv.err);
+    } else if (warp != 9) {
+      // -------- K and V producers: a column segment each, or every second box -------- //
       const bool leader = elect_one();
+      const int half = warp == 8 ? 0 : 1;
       const int br_log2 = p.box_log2, br = 1 << br_log2, per_log2 = 7 - br_log2;
       int last = -1;
       TcWork w;
@@ -507,7 +530,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           ok = __all_sync(FULL_MASK, mbar_wait(&bar.empty[slot], at.phase ^ 1, kv.err));
           if (!ok) break;
           at.step(1);
-          if (leader) mbar_arrive_expect_tx(&bar.full[slot], (boxes << step_log2) * 128 * S::SEGS);
+          // this warp's boxes: all of segment `half` (d = 128), or boxes half, half + 2, ...
+          const int mine = S::SEGS == 2 ? boxes : (boxes + 1 - half) >> 1;
+          if (leader) mbar_arrive_expect_tx(&bar.full[slot], (mine << step_log2) * 128);
           const CUtensorMap* map = fresh ? (is_v ? &vnmap : &knmap)
                                          : step_log2 == br_log2 ? (is_v ? &vmap : &kmap) : (is_v ? &vtail : &ktail);
           const uint32_t dst = base + slot * S::TILE;
@@ -525,13 +550,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           if (leader) {
             int y = fresh ? w.c0 + key0 : 0;
             const int y_step = fresh ? 16 : 0;
-            uint32_t to = dst;
+            uint32_t to = dst + (S::SEGS == 2 ? half * S::SEG : 0);
             const uint32_t to_step = 128u << step_log2;
 #pragma unroll
             for (int x = 0; x < 8; x++) {
               if (x >= boxes) break;
-#pragma unroll
-              for (int sg = 0; sg < S::SEGS; sg++) tma_load_4d(to + sg * S::SEG, map, 0, sg, z[x], y, &bar.full[slot]);
+              if (S::SEGS == 2 || (x & 1) == half) tma_load_4d(to, map, 0, S::SEGS == 2 ? half : 0, z[x], y, &bar.full[slot]);
               to += to_step;
               y += y_step;
             }
@@ -545,33 +569,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       // nothing may still be in flight when the CTA ends
       for (int g = max(0, last - S::SLOTS + 1); g <= last; g++)
         mbar_wait(&bar.full[g % S::SLOTS], (g / S::SLOTS) & 1, kv.err);
-    } else if (warp == 10) {
-      // ----------------------- Q producer: one tile a unit, or two ----------------------- //
-      const bool leader = elect_one();
-      int issued = 0;
-      TcWork w;
-      bool ok = take(w);
-      while (ok) {
-        const int q_end = w.qtiles + (w.single() ? 1 : 2);
-        for (int qt = w.qtiles; qt < q_end; qt++) {
-          const int slot = qt & 1;
-          ok = __all_sync(FULL_MASK, mbar_wait(&bar.qempty[slot], ((qt >> 1) & 1) ^ 1, kv.err));
-          if (!ok) break;
-          if (leader) {
-            mbar_arrive_expect_tx(&bar.qfull[slot], S::TILE);
-#pragma unroll
-            for (int sg = 0; sg < S::SEGS; sg++)
-              tma_load_4d(base + (S::SLOTS + slot) * S::TILE + sg * S::SEG, &qmap, 0, sg, w.kvh << gl,
-                          w.c0 + w.tok0 + ((qt - w.qtiles) << (7 - gl)), &bar.qfull[slot]);
-          }
-          __syncwarp();
-          issued = qt + 1;
-        }
-        if (!ok || w.last) break;
-        ok = take(w);
-      }
-      for (int qt = max(0, issued - 2); qt < issued; qt++)
-        mbar_wait(&bar.qfull[qt & 1], (qt >> 1) & 1, kv.err);
     } else {
       // ---------------------------- matrix issuer ---------------------------- //
       constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(D, true);
@@ -873,9 +870,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 }
 
 // Joins the partial states of the units that a run's end cut, over the records
-// of the CTA that began a unit and of those after it. A lane holds a record's
-// weight and D / 32 columns; eight records' rows are in flight together where a
-// unit has many (a warp takes one row), four rows of two where it has few.
+// of the CTA that began a unit and of those after it. A lane holds D / 32
+// columns; eight records' rows are in flight together where a unit has many (a
+// warp takes one row), four rows of two where it has few.
 // Bound: L2 and latency.
 constexpr int JOIN_WARPS = 8, JOIN_FEW = 4;
 
@@ -895,45 +892,47 @@ __device__ __forceinline__ void join_rows(const TcLaunch& p, int row0, int rows,
 #pragma unroll
     for (int f = 0; f < F; f++) o[j][f] = 0.f;
   }
-  for (int i0 = 0; i0 < n_rec; i0 += 32) {
-    // this lane's record: its rows' maxima and sums (rows past the unit's repeat the last)
-    float2 ml[JOIN_ROWS];
+  constexpr int CH = 8 / JOIN_ROWS;  // records in flight
+  for (int i0 = 0; i0 < n_rec; i0 += CH) {
+    // records and their states, all asked for at once (rows past the unit's repeat
+    // the last, records past its last get weight 0)
+    float2 ml[CH][JOIN_ROWS];
+    float x[CH][JOIN_ROWS][F];
 #pragma unroll
-    for (int j = 0; j < JOIN_ROWS; j++) {
-      ml[j] = make_float2(-INFINITY, 0.f);
-      if (i0 + lane < n_rec)
-        ml[j] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml) + rec_of(i0 + lane, min(row0 + j, rows - 1)));
-    }
-    float wt[JOIN_ROWS];
-#pragma unroll
-    for (int j = 0; j < JOIN_ROWS; j++) {
-      const float m = fmaxf(M[j], warp_max(ml[j].x));
-      const float corr = M[j] == -INFINITY ? 0.f : exp2f(M[j] - m);
-      wt[j] = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - m);
-      L[j] = L[j] * corr + warp_sum(wt[j] * ml[j].y);
-      M[j] = m;
-#pragma unroll
-      for (int f = 0; f < F; f++) o[j][f] *= corr;
-    }
-    const int n = min(32, n_rec - i0);
-#pragma unroll(8 / JOIN_ROWS)
-    for (int i = 0; i < n; i++) {
+    for (int i = 0; i < CH; i++)
 #pragma unroll
       for (int j = 0; j < JOIN_ROWS; j++) {
-        const float* src = p.rec_o + rec_of(i0 + i, min(row0 + j, rows - 1)) * D;
-        const float wi = __shfl_sync(FULL_MASK, wt[j], i);
+        const long long r = rec_of(min(i0 + i, n_rec - 1), min(row0 + j, rows - 1));
+        ml[i][j] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml) + r);
         if constexpr (F == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-          o[j][0] += wi * x.x;
-          o[j][1] += wi * x.y;
-          o[j][2] += wi * x.z;
-          o[j][3] += wi * x.w;
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.rec_o + r * D) + lane);
+          x[i][j][0] = v.x;
+          x[i][j][1] = v.y;
+          x[i][j][2] = v.z;
+          x[i][j][3] = v.w;
         } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-          o[j][0] += wi * x.x;
-          o[j][1] += wi * x.y;
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.rec_o + r * D) + lane);
+          x[i][j][0] = v.x;
+          x[i][j][1] = v.y;
         }
       }
+#pragma unroll
+    for (int j = 0; j < JOIN_ROWS; j++) {
+      float m = M[j];
+#pragma unroll
+      for (int i = 0; i < CH; i++) m = fmaxf(m, ml[i][j].x);
+      const float corr = M[j] == -INFINITY ? 0.f : exp2f(M[j] - m);
+      L[j] *= corr;
+#pragma unroll
+      for (int f = 0; f < F; f++) o[j][f] *= corr;
+#pragma unroll
+      for (int i = 0; i < CH; i++) {
+        const float wt = i0 + i < n_rec && ml[i][j].x != -INFINITY ? exp2f(ml[i][j].x - m) : 0.f;
+        L[j] += wt * ml[i][j].y;
+#pragma unroll
+        for (int f = 0; f < F; f++) o[j][f] += wt * x[i][j][f];
+      }
+      M[j] = m;
     }
   }
   const int gl = p.group_log2;
