@@ -583,21 +583,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           mbar_arrive(&bar.wempty[wi]);
           const bool single = rows <= TT;
           const int steps = single ? nt : 2 * nt;
-          TcRing<S::SLOTS> kr(loads), vr(loads + (single ? min(2, 2 * nt - 1) : 1));
+          TcRing<S::SLOTS> kr(loads), kd(loads), vr(loads + (single ? min(2, 2 * nt - 1) : 1));
           auto issue_qk = [&](int y) {  // S of step y; its K tile is loaded
             const int st = y & 1, qslot = (qtiles + (single ? 0 : st)) & 1;
             const uint64_t qd = smem_desc(base + (S::SLOTS + qslot) * S::TILE, 16, 1024);
-            const uint64_t kd = smem_desc(base + kr.slot * S::TILE, 16, 1024);
+            const uint64_t kdesc = smem_desc(base + kr.slot * S::TILE, 16, 1024);
 #pragma unroll
             for (int j = 0; j < D / 16; j++) {
               const uint32_t off = ((j / 4) * S::SEG + (j % 4) * 32) >> 4;
-              mma_ss(tmem + st * TT, qd + off, kd + off, QK, j > 0);
+              mma_ss(tmem + st * TT, qd + off, kdesc + off, QK, j > 0);
             }
             tc_commit(&bar.sfull[st]);
-            if (single || st == 1) {
-              tc_commit(&bar.empty[kr.slot]);
-              kr.step(single && y == 0 ? 1 : 2);
-            }
+            if (single) tc_commit(&bar.empty[kr.slot]);
+            if (single || st == 1) kr.step(single && y == 0 ? 1 : 2);
             if (single ? y == steps - 1 : y >= steps - 2) tc_commit(&bar.qempty[qslot]);
           };
           ok = mbar_wait(&bar.qfull[qtiles & 1], (qtiles >> 1) & 1, kv.err);
@@ -627,6 +625,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               np ^= 1u << st;
             }
             if (!ok) break;
+            if (!single && x >= 0 && (x & 1) == 0) {  // K of the tile whose S were issued before this product
+              tc_commit(&bar.empty[kd.slot]);
+              kd.step(2);
+            }
             if (x >= 0 && (single || (x & 1))) {
               tc_commit(&bar.empty[vr.slot]);
               vr.step(single && x == steps - 2 ? 1 : 2);
