@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/prhs.h"
 
 namespace prhs {
@@ -233,17 +235,14 @@ cudaError_t allow_smem(K kernel, size_t smem, int (&done)[SMEM_DEVICES]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < SMEM_DEVICES;
-  if (known && __atomic_load_n(&done[dev], __ATOMIC_ACQUIRE) >= (int)smem) return cudaSuccess;
+  if (dev < 0 || dev >= SMEM_DEVICES) return cudaErrorInvalidDevice;
+  if (__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE) >= (int)smem) return cudaSuccess;
+  static std::mutex mu;  // a smaller size set by another thread afterwards would lower the limit
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev] >= (int)smem) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  // a smaller size set by another thread meanwhile would lower the limit: keep the largest
-  if (known) {
-    int old = __atomic_load_n(&done[dev], __ATOMIC_RELAXED);
-    while (old < (int)smem && !__atomic_compare_exchange_n(&done[dev], &old, (int)smem, false, __ATOMIC_RELEASE, __ATOMIC_RELAXED)) {
-    }
-  }
-  return cudaSuccess;
+  if (e == cudaSuccess) __atomic_store_n(&done[dev], (int)smem, __ATOMIC_RELEASE);
+  return e;
 }
 
 // -------------------------------------------------------------------------- //

@@ -15,7 +15,7 @@ size_t esize(const prhs_kv& kv) { return kv.dtype == PRHS_BF16 ? 2 : 4; }
 // A token stride in elements: at least the row, whole 16-byte pieces.
 bool stride_ok(const prhs_kv& kv, long long stride, int heads) {
   return stride >= (long long)heads * kv.d && stride % (long long)(16 / esize(kv)) == 0 &&
-         stride < (1ll << 40);
+         stride < (1ll << 38);  // bytes below the 2^40 of a TMA stride
 }
 
 prhs_status launched(cudaError_t e, const char* what) {

@@ -11,12 +11,12 @@
 //
 // Inside a CTA: two warps load K and V tiles by TMA into a ring of 128-key
 // slots (128-byte swizzle), half the boxes of each tile each (a tile on 16-key
-// pages is 16 copies of 2 KB, more than one thread issues at HBM's rate beside
-// the rest), the scheduler's warp the units' Q tiles into two more (so that
-// neither holds the other back where units change), one thread issues the
-// matrix instructions, and two
-// warpgroups do the softmax, one per stream. A stream is a logit tile S
-// [128 rows][128 keys] and an output tile O [128][D] in tensor memory:
+// pages is 16 copies of 2 KB, more than one thread issues at HBM's rate: 658 us
+// with one warp, 640 with two, for the batch below). The scheduler's warp walks
+// the list for the others and loads the units' Q tiles into two more slots.
+// One thread issues the matrix instructions, and two warpgroups do the
+// softmax, one per stream. A stream is a logit tile S [128 rows][128 keys] and an
+// output tile O [128][D] in tensor memory:
 //   S = Q K^T      (both from shared memory, 8 or 4 instructions of 16 elements)
 //   P = exp2(S - m) in bf16 over S's own columns, one row a thread
 //   O += P V       (P from tensor memory, V read d-major from its slot)
@@ -26,17 +26,25 @@
 // outputs of the second form are joined when the unit ends: both warpgroups
 // read both tiles, half the columns each.
 //
-// The running maximum m of a row follows the true one only when that has grown
+// The reference m of a row follows its running maximum only when that has grown
 // by more than 8 (a factor 256 in the weights): O is then rescaled in tensor
 // memory, at a few tiles of a row instead of all. The weights stay below 2^8
 // and sums are fp32, so nothing is lost: l and O carry the same factor.
 //
-// P is rounded to bf16 (2^-9 of each weight at most, half a unit of the type
-// the result is rounded to); l is summed before that rounding, m, l and O are fp32.
+// P is rounded to bf16 (by up to half a unit of the type the result is rounded
+// to, and without bias over the keys); l is summed before that rounding, m, l
+// and O are fp32.
 //
 // Bound: HBM while a KV head has up to about 256 query rows (K and V are read
-// once: 512 bytes a key at d = 128 against 4 * 128 * rows flops), the tensor
-// cores above.
+// once: 512 bytes a key at d = 128 against 4 * 128 * rows flops): 32 sequences of
+// 2K-16K keys on 16-key pages, 32 KV heads, trees of 1-32 tokens, 4.25 GB: 640 us,
+// 0.98 of the measured copy bandwidth. Above that the tensor cores and the
+// softmax between their products: 5250 causal tokens on cached prefixes, 32 / 8
+// heads: 398 us, 1450 TFLOP/s, 0.78 of the measured matrix rate (a step of a
+// stream is 1550 clocks, its two products 1031; the rest is the wait of one
+// product for the softmax, 1250 clocks of 128 exponentials a thread). Few tiles
+// a CTA (4096 keys, 32 heads): latency, 2.3 us to the first copy, 3 us from it to
+// the first weights, 3.5 us of joining.
 #include "tokens.h"
 
 namespace prhs {
@@ -418,8 +426,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       off -= block * s.cache_tiles + new_tiles_before(block, s.blocks, s.n, ul, causal);
       for (int k = 0;; k++) {
-        const int tiles = s.cache_tiles + new_tiles_before(block + 1, s.blocks, s.n, ul, causal) -
-                          new_tiles_before(block, s.blocks, s.n, ul, causal);
+        const int tiles = s.cache_tiles + (causal ? (min(s.n, (block + 1) << ul) + TT - 1) >> 7 : 1);
         const int nt = min(tiles - off, left);
         left -= nt;
         const int i = k & (TC_WORKS - 1);
@@ -583,6 +590,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           mbar_arrive(&bar.wempty[wi]);
           const bool single = rows <= TT;
           const int steps = single ? nt : 2 * nt;
+          // places of the next K to use, the next K to release, the next V
           TcRing<S::SLOTS> kr(loads), kd(loads), vr(loads + (single ? min(2, 2 * nt - 1) : 1));
           auto issue_qk = [&](int y) {  // S of step y; its K tile is loaded
             const int st = y & 1, qslot = (qtiles + (single ? 0 : st)) & 1;
@@ -601,8 +609,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           ok = mbar_wait(&bar.qfull[qtiles & 1], (qtiles >> 1) & 1, kv.err);
           // step x of the loop: O of step x, then S of step x + 2 in the same stream; with
           // two row tiles (bound by the products) every load they need is waited for
-          // before the softmax, so that nothing comes between the two products. Steps
-          // -2 and -1 are S of steps 0 and 1.
+          // before the softmax, so that nothing comes between the two products, and K is
+          // released behind the next product: this thread's polls of a barrier queue
+          // behind what it has issued, releases included (495 -> 404 -> 398 us). Steps -2
+          // and -1 are S of steps 0 and 1.
           for (int x = -2; ok && x < steps; x++) {
             const bool more = x + 2 < steps;
             if (more && !single && (x & 1) == 0) ok = ok && mbar_wait(&bar.full[kr.slot], kr.phase, kv.err);

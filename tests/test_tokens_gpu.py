@@ -688,3 +688,145 @@ def test_two_streams_with_their_own_workspaces():
     assert S.last_error() == 0
     for args, mask, out, lse, ws, o2, l2, st in jobs:
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n,page", [(32, 32, [16], 0), (32, 8, [64, 3], 0), (8, 8, [30, 1, 9, 17], 16),
+                                           (32, 4, [300, 70], 64)])
+def test_results_repeat_from_a_cold_cache(Hq, Hkv, n, page):
+    """Loads that arrive late and out of step change nothing: every call from a
+    flushed L2 gives the same bits."""
+    import sparse_kv_selection_gb300 as S
+    lens = [4096, 2500, 7000, 130][:len(n)]
+    c = Cache(lens, Hq, Hkv, 128, BF16, page=page, room=1, seed=7)
+    q, k, v = tree_inputs(c, n, 0, 3)
+    cu = i32(np.concatenate([[0], np.cumsum(n)]))
+    ws = S.make_tree_workspace(c.kv, max(n))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    first = None
+    for call in range(12):
+        out, lse = torch.empty_like(q), torch.empty(sum(n), Hq, device="cuda")
+        flush.fill_(call)
+        S.tree_attn(c.kv, q, k, v, 128 ** -0.5, cu, max(n), out, lse, ws)
+        if first is None:
+            first = (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), call
+    assert S.last_error() == 0
+
+
+def test_two_graphs_share_a_workspace():
+    import sparse_kv_selection_gb300 as S
+    jobs = []
+    ws = None
+    s = torch.cuda.Stream()
+    for seed, n in ((1, [12, 40]), (2, [3, 5])):
+        c = Cache([2100, 900], 8, 2, 128, BF16, seed=seed)
+        q, k, v = tree_inputs(c, n, 0, seed)
+        args = (c.kv, q, k, v, 128 ** -0.5, i32(np.concatenate([[0], np.cumsum(n)])), 40)
+        ws = S.make_tree_workspace(c.kv, 40) if ws is None else ws
+        out, lse = torch.empty_like(q), torch.empty(sum(n), 8, device="cuda")
+        S.tree_attn(*args, out, lse, ws)
+        torch.cuda.synchronize()
+        want = out.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.tree_attn(*args, out, lse, ws)
+        jobs.append((g, args, out, lse, want))
+    for _ in range(5):
+        for g, args, out, lse, want in jobs:
+            out.zero_()
+            g.replay()
+            assert torch.equal(out, want)
+    assert S.last_error() == 0
+    del s
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (F32, 64), (BF16, 128)])
+def test_many_short_sequences(dtype, d):
+    """More sequences than a CTA has threads, some without tokens or cache."""
+    rng = np.random.default_rng(3)
+    B = 1100
+    lens, n = rng.integers(0, 40, B).tolist(), rng.integers(0, 4, B).tolist()
+    lens[5], n[5], lens[700], n[700] = 900, 120, 300, 0
+    c = Cache(lens, 4, 2, d, dtype, page=16, room=1, seed=1)
+    import sparse_kv_selection_gb300 as S
+    q, k, v = tree_inputs(c, n, 0, 2)
+    cu = np.concatenate([[0], np.cumsum(n)])
+    out, lse = torch.empty_like(q), torch.empty(sum(n), 4, device="cuda")
+    S.tree_attn(c.kv, q, k, v, d ** -0.5, i32(cu), 120, out, lse, S.make_tree_workspace(c.kv, 120))
+    assert S.last_error() == 0
+    for b in [0, 1, 5, 6, 383, 384, 385, 699, 701, 767, 768, B - 1] + rng.integers(0, B, 40).tolist():
+        if n[b] == 0:
+            continue
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        kc, vc = c.rows(b, lens[b])
+        see = torch.ones(n[b], n[b], dtype=torch.bool, device="cuda").tril()
+        wo, wl, eo, el = attn_ref(q[r].double(), kc, vc, k[r].double(), v[r].double(), see, d ** -0.5, d, dtype)
+        assert ((out[r].double() - wo).abs() <= eo).all() and ((lse[r].double() - wl).abs() <= el).all(), b
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 2)])
+def test_one_token_is_dense_attention_after_append(dtype, Hq, Hkv):
+    """The form of plain decode, against the library's own append and dense attention."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([40, 0, 333], Hq, Hkv, 128, dtype, t_max=400, seed=5)
+    q, k, v = tree_inputs(c, [1, 1, 1], 0, 2)
+    out, lse = torch.empty_like(q), torch.empty(3, Hq, device="cuda")
+    S.tree_attn(c.kv, q, k, v, 128 ** -0.5, i32([0, 1, 2, 3]), 1, out, lse, S.make_tree_workspace(c.kv, 1))
+    S.binding.append_kv(c.kv, k.contiguous(), v.contiguous())
+    o2, l2 = torch.empty(3, Hq, 128, device="cuda"), torch.empty(3, Hq, device="cuda")
+    S.dense_attn(c.kv, q, 128 ** -0.5, o2, l2, S.make_workspace(c.kv))
+    assert S.last_error() == 0
+    tol = 2.0 ** -7 if dtype == BF16 else 2.0 ** -16     # weights and result in bf16: 2 * 2^-8 of |v|'s mean
+    assert ((out.float() - o2).abs() <= tol * (1 + o2.abs())).all() and ((lse - l2).abs() <= 2.0 ** -15).all()
+
+
+def test_batches_without_tokens():
+    import sparse_kv_selection_gb300 as S
+    c = Cache([5, 0], 4, 2, 64, BF16, page=16, room=4, seed=1)
+    got, bits = run_plan(c, [0, 0], 0, parents=[])
+    assert bits == 0 and got[0].tolist() == [0, 0, 0]
+    got, bits = run_plan(c, [0, 0], 3)
+    assert bits == 0 and got[2].tolist() == [-1, -1, -1] and got[5] == 0 and got[6] == c.n_pages
+    for T in (0, 3):
+        q, k = torch.full((T, 4, 64), 2.0, device="cuda", dtype=BF16), torch.zeros(T, 2, 64, device="cuda", dtype=BF16)
+        out, lse = torch.full_like(q, 3.0), torch.full((T, 4), 3.0, device="cuda")
+        S.tree_attn(c.kv, q, k, k, 0.125, i32([0, 0, 0]), 7, out, lse, S.make_tree_workspace(c.kv, 7))
+        S.rope_append(c.kv, S.RopeTable(64), i32([0] * T), q, k, k, out, slots=i32([-1] * T))
+        assert (out == 3.0).all() and (lse == 3.0).all()
+    new = i32([9, 9])
+    S.commit_tokens(c.kv, i32([0, 0, 0]), i32([0, 0]), new)
+    assert S.last_error() == 0 and new.tolist() == [5, 0]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page", [0, 128])
+def test_long_cache_of_few_heads(dtype, page):
+    """Many tiles a CTA, whole boxes of 128 rows, windows of 32 boxes crossed."""
+    c = Cache([70000], 2, 1, 128, dtype, page=page, room=1, seed=4)
+    check_tree(c, [5], seed=2)
+    c = Cache([33000, 9000], 8, 1, 128, dtype, page=page, room=1, seed=4)
+    check_tree(c, [40, 2], seed=2)
+
+
+def test_tensors_of_another_kind_are_refused():
+    import sparse_kv_selection_gb300 as S
+    c = Cache([50], 4, 2, 64, BF16, seed=1)
+    q, k, v = tree_inputs(c, [3], 0, 1)
+    out, lse, ws = torch.empty_like(q), torch.empty(3, 4, device="cuda"), S.make_tree_workspace(c.kv, 3)
+    cu = i32([0, 3])
+    bad = [(q.float(), k, v, cu, out, lse, ws), (q, k.cpu(), v, cu, out, lse, ws), (q, k, v[:2], cu, out, lse, ws),
+           (q, k, v, cu.long(), out, lse, ws), (q, k, v, cu[:1], out, lse, ws), (q, k, v, cu, out.float(), lse, ws),
+           (q, k, v, cu, out, lse[:, :2], ws), (q, k, v, cu, out, lse, ws.cpu())]
+    for q_, k_, v_, cu_, out_, lse_, ws_ in bad:
+        with pytest.raises(ValueError):
+            S.tree_attn(c.kv, q_, k_, v_, 0.1, cu_, 3, out_, lse_, ws_)
+    with pytest.raises(S.PrhsError) as e:
+        S.tree_attn(c.kv, q, k, v, 0.1, cu, 3, out, lse, ws[:1024])
+    assert e.value.status == 3
+    with pytest.raises(ValueError):
+        S.tree_attn(c.kv, q, k, v, 0.1, cu, 3, out, lse, ws, tree_mask=torch.zeros(3, 2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        S.rope_append(c.kv, S.RopeTable(64, device="cpu"), i32([0] * 3), q, k, v, out)
+    with pytest.raises(S.PrhsError):
+        S.rope_append(c.kv, S.RopeTable(128), i32([0] * 3), q, k, v, out)     # rot_dim above d
