@@ -208,12 +208,14 @@ def test_rope_scalings_and_far_positions(kind, rot, dtype):
 @pytest.mark.parametrize("big", [False, True])
 def test_rope_append(page, dtype, Hq, Hkv, d, big):
     """k and v land in the rows of their slots, everything else is left alone,
-    padding tokens and bad slots write nothing; one and four tasks a thread."""
+    padding tokens and bad slots write nothing; one and two tasks a thread."""
     import sparse_kv_selection_gb300 as S
     from sparse_kv_selection_gb300.binding import DEV_BAD_INDEX
     n = [700, 3, 0, 2100] if big else [5, 3, 0, 11]
     if big and Hkv == 1:
         n = [n[0], 3, 0, 60000]
+    elif big and dtype == F32:
+        n = [n[0], 3, 0, 4200]
     lens = [20, 0, 9, 33]
     c = Cache(lens, Hq, Hkv, d, dtype, page=page, room=max(n), seed=2)
     T = sum(n) + 4
