@@ -832,3 +832,48 @@ def test_tensors_of_another_kind_are_refused():
         S.rope_append(c.kv, S.RopeTable(64, device="cpu"), i32([0] * 3), q, k, v, out)
     with pytest.raises(S.PrhsError):
         S.rope_append(c.kv, S.RopeTable(128), i32([0] * 3), q, k, v, out)     # rot_dim above d
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(2, 1, 3), (8, 1, 20), (4, 1, 64)])
+def test_growing_maximum_in_every_row_tile(Hq, Hkv, n):
+    """The maximum rises by about 13 (base 2) a tile of keys, above and below the
+    rescaling threshold, with one and with two row tiles, masked new tokens last."""
+    import sparse_kv_selection_gb300 as S
+    t = 2000
+    c = Cache([t], Hq, Hkv, 128, BF16, seed=3)
+    ramp = torch.linspace(0, 140, t, device="cuda")[None, None, :, None]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    noise = torch.randn(1, Hkv, t, 128, generator=g, device="cuda") * 0.1
+    c.k[:, :, :t] = (ramp / 128 ** 0.5 + noise).to(BF16)
+    q = torch.ones(n, Hq, 128, device="cuda", dtype=BF16)
+    k, v = torch.randn(2, n, Hkv, 128, generator=g, device="cuda").to(BF16)
+    out, lse = torch.empty_like(q), torch.empty(n, Hq, device="cuda")
+    S.tree_attn(c.kv, q, k, v, 128 ** -0.5, i32([0, n]), n, out, lse, S.make_tree_workspace(c.kv, n))
+    assert S.last_error() == 0
+    kc, vc = c.rows(0, t)
+    see = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    wo, wl, eo, el = attn_ref(q.double(), kc, vc, k.double(), v.double(), see, 128 ** -0.5, 128, BF16)
+    assert ((out.double() - wo).abs() <= eo).all() and ((lse.double() - wl).abs() <= el).all()
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_tree_random_shapes(seed):
+    rng = np.random.default_rng(1000 + seed)
+    Hq, Hkv = HEADS[rng.integers(len(HEADS))]
+    Hq, Hkv = (Hq * 4, Hkv * 4) if rng.random() < 0.3 else (Hq, Hkv)
+    dtype = BF16 if rng.random() < 0.75 else F32
+    B = int(rng.integers(1, 9))
+    tree = rng.random() < 0.6
+    lens = [int(x) for x in np.exp(rng.uniform(0, np.log(6000), B))]
+    n = [int(x) for x in np.exp(rng.uniform(0, np.log(129 if tree else 700), B))]
+    for b in range(B):
+        if rng.random() < 0.1:
+            lens[b] = 0
+        if rng.random() < 0.1 and B > 1:
+            n[b] = 0
+    n[0] = max(n[0], 1)
+    c = Cache(lens, Hq, Hkv, int(rng.choice([64, 128])), dtype, page=int(rng.choice([0, 16, 32, 48, 64, 128, 256])),
+              room=1, seed=seed)
+    check_tree(c, n, pad=int(rng.integers(0, 20)), seed=seed, sets=random_sets(rng, n) if tree else None,
+               stride_extra=int(rng.choice([0, 64])), scale=float(rng.uniform(0.02, 0.3)))
