@@ -71,9 +71,9 @@ struct TreeLaunch {
   void* out;             // the cache's element type
   float* lse;
 };
-// fp32: one launch, or two where the key tiles are split; ws holds
+// fp32: two launches, the first counted by the callee; ws holds
 // tree_workspace(kv, max_new, sms) bytes.
-cudaError_t launch_tree(const TreeLaunch& a, int max_new, int sms, void* ws, cudaStream_t s);
+cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t s);
 size_t tree_workspace(const KVView& kv, int max_new, int sms);
 // bf16: two launches, the first counted by the callee; *err is the launches'
 // result when the descriptors could be made. Workspace bytes of a call.
@@ -84,6 +84,26 @@ size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
 // innermost first, strides in bytes from dimension 1 on).
 prhs_status abi_encode_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                             const uint64_t* strides, const uint32_t* box);
+
+// Two fp32 numbers in one 64-bit register pair, and operations on both.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Tokens [c0, c0 + n) of sequence b; none (flagged) when cu_new is not
 // ascending within [0, T] or the sequence has more than max_new.

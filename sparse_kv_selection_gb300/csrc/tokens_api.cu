@@ -229,7 +229,7 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   a.mask = tree_mask;
   a.out = out;
   a.lse = lse;
-  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, max_new, sms, ws, stream), "tree attention");
+  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, sms, ws, stream), "tree attention");
   cudaError_t e;
   if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
   return launched(e, "tree attention");

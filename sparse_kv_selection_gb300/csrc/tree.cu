@@ -2,296 +2,642 @@
 // each other (a tree by its masks, or a causal chunk), fp32 on the CUDA cores
 // (the tensor cores' fp32 forms drop mantissa bits).
 //
-// The G query heads of one KV head see the same keys, so a CTA takes TR rows of
-// one (sequence, KV head): row r is token r / G, query head r % G of the group.
-// Key tiles of TK rows (the cache's, then the new tokens') pass through shared
-// memory; each thread computes 2 rows by 4 keys of the logits, the 16 threads
-// of a row pair keep its running maximum and sum (base 2) by shuffles, and the
-// weights go through shared memory to the product with V, 2 rows by D / 16
-// columns a thread, in fp32 throughout. Where the row blocks are fewer than the
-// CTAs that fill the SMs, the key tiles of each are split over several CTAs,
-// whose partial states a second launch joins.
+// The G query heads of one KV head see the same keys, so the rows of one
+// (sequence, KV head) are its tokens times G (row = token * G + head of the
+// group), cut into units of up to 8, 32 or 64 rows. A unit's keys are tiles of 32:
+// the cache's, then the new tokens' (one word of a tree mask each). All tiles of
+// all units are one list; every CTA takes an equal run of it, so long caches are
+// split and short ones packed without a plan made on the host. A unit cut by a
+// run's end leaves partial states in the workspace, which a second launch joins
+// row by row.
+//
+// Inside a CTA the last warp walks the list and looks the pages of a tile up a
+// tile before its copies start; all threads copy the next tiles (16-byte
+// asynchronous copies, eight threads a key) while they work on the current one. A
+// warp holds TY R rows: 32 / TY lanes share a row and take TY keys each for the
+// logits, D TY / 32 columns each for the product with V, so that a row's maximum,
+// sum and weights stay inside the warp. Products are packed pairs of fp32;
+// everything is fp32. A warp without rows in a unit only copies.
+//
+// Bound: shared-memory reads. They move 128 bytes a clock into registers whether
+// lanes share an address or not, and a lane's block of R rows by TY keys costs
+// (R + TY) 16-byte reads for 4 R TY products, 4 (R + TY) / (R TY) times what the
+// products take: 2 at 4 by 4, 3 at 2 by 4, 5 at 1 by 4 (the product with V has more
+// columns a lane: 1.25 at 4 by 4). Hence the forms at the end of this file.
+// Two causal chunks of 1024 tokens on 512 keys, 8 / 2 heads, d = 128: 231 us, 37
+// TFLOP/s; single tokens of 16 heads over 69 206 keys, 4 KV heads, 16-key pages: 64
+// us, 4.4 TB/s; 27 trees of 21 tokens over up to 1899 keys, 8 heads, d = 64: 64 us.
 #include "tokens.h"
 
 namespace prhs {
 
-constexpr int TR = 32;            // query rows of a CTA
-constexpr int TK = 64;            // keys of a tile
-constexpr int TREE_THREADS = 256;
+constexpr int TK = 32;            // keys of a tile: a word of a tree mask
 constexpr float T_LOG2E = 1.4426950408889634f;
 constexpr float T_LN2 = 0.6931471805599453f;
 
-// Splits of a row block's key tiles: enough CTAs for two waves of two an SM,
-// while each has a tile of the longest cache.
-static int tree_splits(const KVView& kv, long long max_new, int sms) {
-  const long long G = kv.Hq / kv.Hkv;
-  const long long blocks = ((max_new * G + TR - 1) / TR) * kv.Hkv * kv.B;
-  const long long tiles = ((long long)kv.t_max + TK - 1) / TK + 1;
-  long long s = 4ll * sms / blocks;
-  if (s > tiles) s = tiles;
-  return s < 1 ? 1 : (int)s;
-}
-
-// Rows of partial records: (row block, split, row).
-static size_t tree_records(const KVView& kv, long long max_new, int splits) {
-  const long long G = kv.Hq / kv.Hkv;
-  return splits == 1 ? 0 : (size_t)(((max_new * G + TR - 1) / TR) * kv.Hkv * kv.B) * splits * TR;
-}
-
-size_t tree_workspace(const KVView& kv, int max_new, int sms) {
-  const size_t r = tree_records(kv, max_new, tree_splits(kv, max_new, sms));
-  return 256 + r * (kv.d + 2) * sizeof(float);
-}
-
-template <int D>
-struct TreeShape {
-  static constexpr int LD = D + 4;  // row stride of Q and K: float4 reads of 8 rows hit distinct banks
-  static constexpr size_t SMEM = ((size_t)TR * LD + (size_t)TK * LD + (size_t)TK * D + (size_t)TR * (TK + 1)) * 4;
+// A tile of a CTA's run.
+struct __align__(16) TreeStep {
+  int b, kvh, block, tile;  // sequence, KV head, unit of theirs, tile of the unit
+  int tiles, c0, n, t;      // the unit's tiles, first token, tokens, cached keys
+  int tile0, left, q, u;    // the unit's first tile in this run, tiles of the run behind this one, Q slot, tokens of a unit
 };
 
-template <int D>
-__global__ void __launch_bounds__(TREE_THREADS, 2) tree_kernel(const TreeLaunch a, int splits, float2* rec_ml, float* rec_o) {
-  using T = float;
-  using S = TreeShape<D>;
-  constexpr int E = Elem<T>::per16, PPR = D / E;
-  constexpr int OC = D / 64;  // float4 column groups a thread holds
+// A unit that does not end in a CTA's run.
+struct __align__(16) TreeSplit {
+  int rows, kvh, tok, n_rec;  // rows of the unit (0: none), KV head, first token (packed), records
+  int first, pad[3];          // the CTA that starts it
+};
+
+struct TreeRun {
+  TreeLaunch a;
+  int group_log2;    // log2 of the query heads of a KV head
+  int rows_max;      // rows a record may hold
+  TreeSplit* split;  // [CTAs]
+  float2* rec_ml;    // [2 CTAs][rows_max]
+  float* rec_o;      // [2 CTAs][rows_max][D]
+};
+
+template <int D, int TY, int R, int W, int CTAS>
+struct TreeShape {
+  static constexpr int TR = TY * R * W;          // rows of a unit
+  static constexpr int TR_LOG2 = TR == 64 ? 6 : TR == 32 ? 5 : 3;
+  static_assert(TR == 1 << TR_LOG2, "rows of a unit");
+  static constexpr int THREADS = 32 * W;
+  static constexpr int LD = D + 4;               // row stride of Q and K: eight rows' 16-byte reads hit distinct banks
+  static constexpr int LP = TK + 4;              // row stride of the weights
+  static constexpr int STAGE = TK * (LD + D);    // floats of a K and a V tile
+  // Q slots: one a stage, so that the next units' Q comes with their first tiles, or one
+  static constexpr int LIMIT = 228 * 1024 / CTAS - 1024 - 2560;  // a CTA's share, less what is reserved and static
+  static constexpr int bytes(int stages, int slots) { return 4 * (stages * STAGE + slots * TR * LD + TR * LP); }
+  static constexpr int STAGES = bytes(3, 3) <= LIMIT ? 3 : 2;
+  static constexpr int STEPS = STAGES == 2 ? 4 : 8;  // tiles known at once: those in flight and two more
+  static constexpr int QS = bytes(STAGES, STAGES) <= LIMIT ? STAGES : 1;
+  static constexpr size_t SMEM = bytes(STAGES, QS);
+  static_assert(bytes(STAGES, QS) <= LIMIT, "shared memory");
+};
+
+struct TreeSeq {  // one sequence's share of the list
+  int c0, n, t, u, blocks, cache_tiles;  // (u: tokens of a unit)
+  long long tiles;  // of one KV head
+};
+
+// Tokens that unit `block` of u tokens may attend, and its tiles: a causal unit
+// sees the tokens up to its own last one, a tree unit all of them.
+__device__ __forceinline__ int tree_keys(int n, int block, int u, bool causal) {
+  const long long end = ((long long)block + 1) * u;
+  return causal && end < n ? (int)end : n;
+}
+__device__ __forceinline__ int tree_tiles(int t, int n, int block, int u, bool causal) {
+  return (int)(((long long)t + TK - 1) / TK) + (int)(((long long)tree_keys(n, block, u, causal) + TK - 1) / TK);
+}
+
+// New-token tiles of the units before unit j.
+constexpr int TREE_EVEN = 4;
+__device__ __forceinline__ long long tree_new_before(const TreeSeq& s, long long j, int ul, bool causal) {
+  const int all_tiles = tree_tiles(0, s.n, 0, s.n, false);
+  if (!causal) return j * all_tiles;
+  long long sum = 0;
+  if (s.blocks <= TREE_EVEN) {
+    for (int i = 0; i < j; i++) sum += tree_tiles(0, s.n, i, s.u, true);
+    return sum;
+  }
+  const bool all = j == s.blocks;
+  const long long k = all ? j - 1 : j;  // units that end at their own last token, of 2^ul tokens
+  if (ul >= 5) {
+    sum = (k * (k + 1) / 2) << (ul - 5);
+  } else {  // sum over i = 1 .. k of ceil(i / p), p = 2^(5 - ul)
+    const int pl = 5 - ul;
+    const long long q = k >> pl, r = k - (q << pl);
+    sum = ((q * (q + 1) / 2) << pl) + r * (q + 1);
+  }
+  return all ? sum + all_tiles : sum;
+}
+
+// A sequence's units hold up to 2^ul tokens: equal shares where they are few or
+// a tree's (9 tokens of 8 query heads in two units of 64 rows: 5 and 4 tokens, not
+// 8 and 1, since the runs count tiles, not rows).
+__device__ __forceinline__ TreeSeq tree_seq(const TreeLaunch& a, int b, int ul) {
+  TreeSeq s;
+  const bool causal = a.mask == nullptr;
+  s.t = seq_len(a.kv, b);
+  s.n = seq_tokens(a.cu_new, b, a.T, a.max_new, a.kv.err, &s.c0);
+  s.u = 1 << ul;
+  s.blocks = (int)(((long long)s.n + s.u - 1) >> ul);
+  s.cache_tiles = (int)(((long long)s.t + TK - 1) / TK);
+  s.tiles = 0;
+  if (s.blocks == 0) return s;
+  if (s.blocks <= TREE_EVEN || !causal) {
+    s.u = (s.n + s.blocks - 1) / s.blocks;
+    s.blocks = (s.n + s.u - 1) / s.u;
+  }
+  s.tiles = (long long)s.blocks * s.cache_tiles + tree_new_before(s, s.blocks, ul, causal);
+  return s;
+}
+
+// 16 bytes of global memory to shared memory, zeros when !have.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(have ? 16 : 0)
+               : "memory");
+}
+
+template <int D, int TY, int R, int W, int CTAS>
+__global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constant__ TreeRun p) {
+  using S = TreeShape<D, TY, R, W, CTAS>;
+  constexpr int TR = S::TR, LD = S::LD, LP = S::LP, THREADS = S::THREADS, STEPS = S::STEPS;
   extern __shared__ __align__(16) float tree_smem[];
-  float* sq = tree_smem;
-  float* sk = sq + TR * S::LD;
-  float* sv = sk + TK * S::LD;
-  float* sp = sv + TK * D;  // [TR][TK + 1]
-  __shared__ int sh_key[TK];  // 1: the tile's key is attended by someone
+  float* sq0 = tree_smem + S::STAGES * S::STAGE;
+  __shared__ TreeStep steps[STEPS];
+  __shared__ long long key_row[STEPS][TK];  // a tile's keys: row of the cache, or the sequence's token; -1: none
+  __shared__ uint32_t have_key[STEPS];      // those that exist
+  __shared__ long long wsum[W];
 
   pdl_wait();
   pdl_trigger();
+  const TreeLaunch& a = p.a;
   const KVView& kv = a.kv;
-  const int G = kv.Hq / kv.Hkv, kvh = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int block = blockIdx.x / splits, split = blockIdx.x - block * splits;
-  const int t = seq_len(kv, b);
-  int c0 = 0;
-  const int n = seq_tokens(a.cu_new, b, a.T, a.max_new, kv.err, &c0);
-  const int r0 = block * TR;
-  if (r0 >= n * G) return;
-  const int last_tok = min(n, (r0 + TR + G - 1) / G);  // one past the CTA's last token
-  const int n_keys = a.mask != nullptr ? n : last_tok;  // new tokens that may be attended
+  const bool causal = a.mask == nullptr;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gl = p.group_log2, ul = S::TR_LOG2 - gl;  // log2 of the group and of a unit's tokens
 
-  // ---- Q rows ----
-  for (int x = tid; x < TR * PPR; x += TREE_THREADS) {
-    const int r = x / PPR, p = x - r * PPR;
-    const int j = (r0 + r) / G, g = (r0 + r) % G;
-    float f[E];
+  // ---- this CTA's run of the list of all tiles ----
+  const int per_t = (kv.B + THREADS - 1) / THREADS, b0 = tid * per_t;
+  long long mine = 0;
+  for (int b = b0; b < min(kv.B, b0 + per_t); b++) mine += kv.Hkv * tree_seq(a, b, ul).tiles;
+  long long run = mine;
 #pragma unroll
-    for (int e = 0; e < E; e++) f[e] = 0.f;
-    if (j < n) {
-      const T* src = static_cast<const T*>(a.q) + ((long long)(c0 + j) * kv.Hq + kvh * G + g) * D;
-      Elem<T>::unpack(reinterpret_cast<const uint4*>(src)[p], f);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(FULL_MASK, run, o);
+    if (lane >= o) run += y;
+  }
+  if (lane == 31) wsum[warp] = run;
+  __syncthreads();
+  long long total = 0, before = run - mine;
+#pragma unroll
+  for (int w = 0; w < W; w++) {
+    if (w < warp) before += wsum[w];
+    total += wsum[w];
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x, g0 = blockIdx.x * per;
+  const int count = (int)(min(total, g0 + per) - g0);  // negative: none are left
+  if (count <= 0) {
+    if (tid == 0) p.split[blockIdx.x] = TreeSplit{};
+    return;
+  }
+  if (g0 >= before && g0 < before + mine) {  // the run begins in this thread's sequences
+    long long off = g0 - before;
+    int b = b0;
+    TreeSeq s = tree_seq(a, b, ul);
+    while (off >= kv.Hkv * s.tiles) {
+      off -= kv.Hkv * s.tiles;
+      s = tree_seq(a, ++b, ul);
     }
+    TreeStep x;
+    x.b = b;
+    x.kvh = (int)(off / s.tiles);
+    off -= x.kvh * s.tiles;
+    int lo = 0, hi = s.blocks - 1;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if ((long long)mid * s.cache_tiles + tree_new_before(s, mid, ul, causal) <= off) lo = mid; else hi = mid - 1;
+    }
+    x.block = lo;
+    x.tile = x.tile0 = (int)(off - (long long)lo * s.cache_tiles - tree_new_before(s, lo, ul, causal));
+    x.tiles = tree_tiles(s.t, s.n, lo, s.u, causal);
+    x.c0 = s.c0;
+    x.n = s.n;
+    x.t = s.t;
+    x.left = count - 1;
+    x.q = 0;
+    x.u = s.u;
+    steps[0] = x;
+  }
+  __syncthreads();
+
+  // One thread: the step behind `x` (x.left > 0).
+  auto advance = [&](TreeStep x) {
+    x.left--;
+    if (++x.tile == x.tiles) {
+      x.tile = x.tile0 = 0;
+      x.q = x.q + 1 == S::QS ? 0 : x.q + 1;
+      if ((long long)++x.block * x.u >= x.n) {
+        x.block = 0;
+        if (++x.kvh == kv.Hkv) {
+          x.kvh = 0;
+          TreeSeq s = {};
+          while (s.n == 0 && ++x.b < kv.B) s = tree_seq(a, x.b, ul);
+          x.c0 = s.c0;
+          x.n = s.n;
+          x.t = s.t;
+          x.u = s.u;
+        }
+      }
+      x.tiles = tree_tiles(x.t, x.n, x.block, x.u, causal);
+    }
+    return x;
+  };
+  // All threads: a unit's Q rows (zeros behind its last), and a tile's K and V.
+  auto copy_q = [&](const TreeStep& x) {
+    float* sq = sq0 + (S::QS > 1 ? x.q : 0) * TR * LD;
 #pragma unroll
-    for (int e = 0; e < E; e++) sq[r * S::LD + p * E + e] = f[e];
+    for (int i = 0; i < TR * D / 4 / THREADS; i++) {
+      const int y = tid + i * THREADS, r = y / (D / 4), c = y % (D / 4) * 4;
+      const int jj = r >> gl;
+      const long long j = (long long)x.block * x.u + jj;
+      const bool have = jj < x.u && j < x.n;
+      copy16(sq + r * LD + c,
+             static_cast<const float*>(a.q) +
+                 (have ? ((x.c0 + j) * kv.Hq + (x.kvh << gl) + (r & ((1 << gl) - 1))) * D + c : 0),
+             have);
+    }
+  };
+  auto copy_tile = [&](const TreeStep& x, int stage, int slot) {
+    float* sk = tree_smem + stage * S::STAGE;
+    float* sv = sk + TK * LD;
+    const int c = (tid & 7) * 4;
+    const bool cached = x.tile < (int)(((long long)x.t + TK - 1) / TK);
+    const float* kb = cached ? static_cast<const float*>(kv.k) : static_cast<const float*>(a.k_new) + x.c0 * a.ks + x.kvh * D;
+    const float* vb = cached ? static_cast<const float*>(kv.v) : static_cast<const float*>(a.v_new) + x.c0 * a.vs + x.kvh * D;
+    const long long ks = cached ? D : a.ks, vs = cached ? D : a.vs;
+#pragma unroll
+    for (int key = tid >> 3; key < TK; key += THREADS / 8) {
+      const long long row = key_row[slot][key];
+      const bool have = row >= 0;
+      const float *kp = kb + (have ? row * ks : 0) + c, *vp = vb + (have ? row * vs : 0) + c;
+#pragma unroll
+      for (int q = 0; q < D / 32; q++) {
+        copy16(sk + key * LD + c + q * 32, kp + q * 32, have);
+        copy16(sv + key * D + c + q * 32, vp + q * 32, have);
+      }
+    }
+  };
+  // One warp: where a tile's keys are, a key a lane.
+  auto find = [&](const TreeStep& x) -> long long {
+    const int ct = (int)(((long long)x.t + TK - 1) / TK);
+    const bool cached = x.tile < ct;
+    const int i = (cached ? x.tile : x.tile - ct) * TK + lane;
+    if (i >= (cached ? x.t : tree_keys(x.n, x.block, x.u, causal))) return -1;
+    return cached ? kv_row(kv, x.b, x.kvh, i) : i;
+  };
+  auto found = [&](const TreeStep& x, int slot, long long row) {
+    key_row[slot][lane] = row;
+    const unsigned have = __ballot_sync(FULL_MASK, row >= 0);
+    if (lane == 0) have_key[slot] = have;
+    if (row < 0 && x.tile * TK + lane < x.t) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
+  };
+
+  constexpr int AHEAD = S::STAGES;  // tiles that have been looked up when the loop begins
+  if (warp == W - 1) {
+    if (lane == 0)
+      for (int i = 1; i < min(AHEAD + 1, count); i++) steps[i] = advance(steps[i - 1]);
+    __syncwarp();
+    long long row[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) row[i] = i < count ? find(steps[i]) : -1;
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++)
+      if (i < count) found(steps[i], i, row[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < S::STAGES - 1; i++) {
+    if (i < count) {
+      if (S::QS > 1 && steps[i].tile == steps[i].tile0) copy_q(steps[i]);
+      copy_tile(steps[i], i, i);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
 
-  const int ty = tid >> 4, tx = tid & 15;  // rows 2 ty, 2 ty + 1; keys tx + 16 i
+  constexpr int TX = 32 / TY, KT = TK / TX, C4 = D / (4 * TX);  // lanes a row, keys and column groups a lane
+  const int ty = lane / TX, tx = lane % TX;  // rows wrow + ty + TY i; keys tx + TX k; columns (tx + TX c) 4
+  const int wrow = warp * TY * R;
   const float qs = a.scale * T_LOG2E;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[2][OC * 4];
-#pragma unroll
-  for (int i = 0; i < 2; i++)
-#pragma unroll
-    for (int c = 0; c < OC * 4; c++) o[i][c] = 0.f;
+  float* sp = sq0 + S::QS * TR * LD + wrow * LP;
+  float m[R], l[R];
+  uint64_t o[R][2 * C4];  // column pairs
+  int stage = 0;
+  for (int it = 0; it < count; it++) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
+    __syncthreads();  // the tile is here, and everyone is done with the one before it
+    const TreeStep x = steps[it & (STEPS - 1)];
+    {
+      const int nx = it + S::STAGES - 1;
+      if (S::QS == 1 && x.tile == x.tile0) {
+        copy_q(x);
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+      }
+      if (nx < count) {
+        const TreeStep& y = steps[nx & (STEPS - 1)];
+        if (S::QS > 1 && y.tile == y.tile0) copy_q(y);
+        copy_tile(y, stage == 0 ? S::STAGES - 1 : stage - 1, nx & (STEPS - 1));
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // the last warp looks the tile after those up (its page numbers come in
+    // while it computes), and one lane walks on
+    const int look = it + AHEAD;
+    long long row = -1;
+    if (warp == W - 1 && look < count) {
+      row = find(steps[look & (STEPS - 1)]);
+      if (lane == 0 && look + 1 < count) steps[(look + 1) & (STEPS - 1)] = advance(steps[look & (STEPS - 1)]);
+    }
+    const float* sk = tree_smem + stage * S::STAGE;
+    const float* sv = sk + TK * LD;
+    const float* sq = sq0 + (S::QS > 1 ? x.q : 0) * TR * LD;
+    if (++stage == S::STAGES) stage = 0;
+    const long long row0 = ((long long)x.block * x.u) << gl;
+    const int rows = (int)min((long long)x.u << gl, ((long long)x.n << gl) - row0);
+    if (wrow >= rows) {
+      if (warp == W - 1 && look < count) found(steps[look & (STEPS - 1)], look & (STEPS - 1), row);
+      continue;
+    }
 
-  const int cache_tiles = (t + TK - 1) / TK, new_tiles = (n_keys + TK - 1) / TK;
-  const int per = (cache_tiles + new_tiles + splits - 1) / splits;
-  const int it_end = min(cache_tiles + new_tiles, (split + 1) * per);
-  for (int it = split * per; it < it_end; it++) {
-    const bool cached = it < cache_tiles;
-    const int key0 = (cached ? it : it - cache_tiles) * TK;
-    const int lim = cached ? t : n_keys;
-    __syncthreads();
-    for (int x = tid; x < TK * PPR; x += TREE_THREADS) {
-      const int key = x / PPR, p = x - key * PPR, i = key0 + key;
-      float kf[E], vf[E];
+    if (x.tile == x.tile0) {
 #pragma unroll
-      for (int e = 0; e < E; e++) kf[e] = vf[e] = 0.f;
-      bool have = i < lim;
-      if (have) {
-        const T *ks, *vs;
-        if (cached) {
-          const long long row = kv_row(kv, b, kvh, i);
-          if (row < 0) {
-            raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
-            have = false;
-          }
-          ks = static_cast<const T*>(kv.k) + row * D;
-          vs = static_cast<const T*>(kv.v) + row * D;
-        } else {
-          ks = static_cast<const T*>(a.k_new) + (c0 + i) * a.ks + kvh * D;
-          vs = static_cast<const T*>(a.v_new) + (c0 + i) * a.vs + kvh * D;
-        }
-        if (have) {
-          Elem<T>::unpack(reinterpret_cast<const uint4*>(ks)[p], kf);
-          Elem<T>::unpack(reinterpret_cast<const uint4*>(vs)[p], vf);
-        }
-      }
-      if (p == 0) sh_key[key] = have;
+      for (int i = 0; i < R; i++) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; e++) {
-        sk[key * S::LD + p * E + e] = kf[e];
-        sv[key * D + p * E + e] = vf[e];
+        for (int c = 0; c < 2 * C4; c++) o[i][c] = 0;
       }
     }
-    __syncthreads();
-    float acc[2][4];
+    // ---- logits ----
+    uint64_t acc[R][KT];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < R; i++)
 #pragma unroll
-      for (int k = 0; k < 4; k++) acc[i][k] = 0.f;
-#pragma unroll 4
+      for (int k = 0; k < KT; k++) acc[i][k] = 0;
+#pragma unroll 8
     for (int e = 0; e < D; e += 4) {
-      const float4 q0 = *reinterpret_cast<const float4*>(sq + (2 * ty) * S::LD + e);
-      const float4 q1 = *reinterpret_cast<const float4*>(sq + (2 * ty + 1) * S::LD + e);
+      ulonglong2 q[R];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const float4 x = *reinterpret_cast<const float4*>(sk + (tx + 16 * k) * S::LD + e);
-        acc[0][k] = fmaf(q0.x, x.x, fmaf(q0.y, x.y, fmaf(q0.z, x.z, fmaf(q0.w, x.w, acc[0][k]))));
-        acc[1][k] = fmaf(q1.x, x.x, fmaf(q1.y, x.y, fmaf(q1.z, x.z, fmaf(q1.w, x.w, acc[1][k]))));
+      for (int i = 0; i < R; i++) q[i] = *reinterpret_cast<const ulonglong2*>(sq + (wrow + ty + TY * i) * LD + e);
+#pragma unroll
+      for (int k = 0; k < KT; k++) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sk + (tx + TX * k) * LD + e);
+#pragma unroll
+        for (int i = 0; i < R; i++) acc[i][k] = fma2(q[i].y, y.y, fma2(q[i].x, y.x, acc[i][k]));
       }
     }
+    // ---- weights ----
+    const int ct = (int)(((long long)x.t + TK - 1) / TK), nt = x.tile - ct;  // nt: tile of the new tokens
+    const uint32_t have = have_key[it & (STEPS - 1)];
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int r = 2 * ty + i, j = (r0 + r) / G;
-      float mx = -INFINITY;
+    for (int i = 0; i < R; i++) {
+      const int r = wrow + ty + TY * i;
+      const long long j = (row0 + r) >> gl;
+      unsigned see = ~0u;
+      if (nt >= 0) {
+        if (!causal) {
+          see = j < x.n ? a.mask[(x.c0 + j) * PRHS_TREE_WORDS + nt] : 0u;
+        } else {
+          const long long past = j - (long long)nt * TK;  // the last key seen
+          see = past >= TK - 1 ? ~0u : past < 0 ? 0u : (2u << past) - 1u;
+        }
+      }
+      float s[KT], mx = m[i];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const int key = tx + 16 * k, p = key0 + key;
-        bool see = sh_key[key] != 0;
-        if (see && !cached)
-          see = a.mask == nullptr ? p <= j
-                                  : j < n && (a.mask[(long long)(c0 + j) * PRHS_TREE_WORDS + (p >> 5)] >> (p & 31)) & 1u;
-        acc[i][k] = see ? acc[i][k] * qs : -INFINITY;
-        mx = fmaxf(mx, acc[i][k]);
+      for (int k = 0; k < KT; k++) {
+        float lo, hi;
+        unf2(acc[i][k], lo, hi);
+        const int key = tx + TX * k;
+        s[k] = ((see & have) >> key) & 1u ? (lo + hi) * qs : -INFINITY;
+        mx = fmaxf(mx, s[k]);
       }
 #pragma unroll
-      for (int s = 8; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, s));
-      mx = fmaxf(m[i], mx);
+      for (int d = TX / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, d));
       const float corr = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mx);
       float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const float w = mx == -INFINITY ? 0.f : exp2f(acc[i][k] - mx);
+      for (int k = 0; k < KT; k++) {
+        const float w = mx == -INFINITY ? 0.f : exp2f(s[k] - mx);
         sum += w;
-        sp[r * (TK + 1) + tx + 16 * k] = w;
+        sp[(ty + TY * i) * LP + tx + TX * k] = w;
       }
       l[i] = l[i] * corr + sum;
       m[i] = mx;
+      const uint64_t c2 = f2(corr, corr);
 #pragma unroll
-      for (int c = 0; c < OC * 4; c++) o[i][c] *= corr;
+      for (int c = 0; c < 2 * C4; c++) o[i][c] = mul2(o[i][c], c2);
     }
-    __syncwarp();  // a row pair's weights are written and read by one half warp
+    __syncwarp();
+    // ---- product with V ----
 #pragma unroll 4
-    for (int key = 0; key < TK; key++) {
-      const float w0 = sp[(2 * ty) * (TK + 1) + key], w1 = sp[(2 * ty + 1) * (TK + 1) + key];
+    for (int key = 0; key < TK; key += 4) {
+      float w[R][4];
 #pragma unroll
-      for (int c = 0; c < OC; c++) {
-        const float4 x = *reinterpret_cast<const float4*>(sv + key * D + c * 64 + tx * 4);
-        o[0][4 * c] = fmaf(w0, x.x, o[0][4 * c]);
-        o[0][4 * c + 1] = fmaf(w0, x.y, o[0][4 * c + 1]);
-        o[0][4 * c + 2] = fmaf(w0, x.z, o[0][4 * c + 2]);
-        o[0][4 * c + 3] = fmaf(w0, x.w, o[0][4 * c + 3]);
-        o[1][4 * c] = fmaf(w1, x.x, o[1][4 * c]);
-        o[1][4 * c + 1] = fmaf(w1, x.y, o[1][4 * c + 1]);
-        o[1][4 * c + 2] = fmaf(w1, x.z, o[1][4 * c + 2]);
-        o[1][4 * c + 3] = fmaf(w1, x.w, o[1][4 * c + 3]);
+      for (int i = 0; i < R; i++) {
+        const float4 y = *reinterpret_cast<const float4*>(sp + (ty + TY * i) * LP + key);
+        w[i][0] = y.x;
+        w[i][1] = y.y;
+        w[i][2] = y.z;
+        w[i][3] = y.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int c = 0; c < C4; c++) {
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sv + (key + k) * D + (c * TX + tx) * 4);
+#pragma unroll
+          for (int i = 0; i < R; i++) {
+            const uint64_t w2 = f2(w[i][k], w[i][k]);
+            o[i][2 * c] = fma2(w2, y.x, o[i][2 * c]);
+            o[i][2 * c + 1] = fma2(w2, y.y, o[i][2 * c + 1]);
+          }
+        }
+    }
+    __syncwarp();  // (the weights are rewritten in the next tile)
+    if (warp == W - 1 && look < count) found(steps[look & (STEPS - 1)], look & (STEPS - 1), row);
+
+    // ---- the unit's last tile here: its result, or a partial record (m, l and O against m) ----
+    if (x.tile + 1 < x.tiles && x.left > 0) continue;
+    const bool whole = x.tile0 == 0 && x.tile + 1 == x.tiles;
+    if (x.left == 0 && tid == 0) {
+      TreeSplit y = {};
+      if (x.tile + 1 < x.tiles) {
+        const long long start = g0 + count - 1 - x.tile;  // the list's number of the unit's first tile
+        y.rows = rows;
+        y.kvh = x.kvh;
+        y.tok = (int)(x.c0 + (long long)x.block * x.u);
+        y.first = (int)(start / per);
+        y.n_rec = (int)((start + x.tiles - 1) / per) - y.first + 1;
+      }
+      p.split[blockIdx.x] = y;
+    }
+    const long long rec = (2ll * blockIdx.x + (x.tile0 == 0 ? 1 : 0)) * p.rows_max;
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      const int r = wrow + ty + TY * i;
+      float sum = l[i];
+#pragma unroll
+      for (int d = TX / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, d);
+      if (r >= rows) continue;
+      const long long orow = (x.c0 + ((row0 + r) >> gl)) * kv.Hq + (x.kvh << gl) + (r & ((1 << gl) - 1));
+      const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+      float* dst = (whole ? static_cast<float*>(a.out) + orow * D : p.rec_o + (rec + r) * D) + tx * 4;
+#pragma unroll
+      for (int c = 0; c < C4; c++) {
+        float4 y;
+        unf2(o[i][2 * c], y.x, y.y);
+        unf2(o[i][2 * c + 1], y.z, y.w);
+        *reinterpret_cast<float4*>(dst + c * TX * 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      }
+      if (tx == 0) {
+        if (whole) a.lse[orow] = sum > 0.f ? (m[i] + log2f(sum)) * T_LN2 : -INFINITY;
+        else p.rec_ml[rec + r] = make_float2(m[i], sum);
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const int r = r0 + 2 * ty + i, j = r / G, g = r % G;
-    float sum = l[i];
-#pragma unroll
-    for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, s);
-    if (j >= n) continue;
-    if (splits > 1) {  // a partial record (m, l and O against m)
-      const long long rec = ((((long long)b * kv.Hkv + kvh) * (gridDim.x / splits) + block) * splits + split) * TR + 2 * ty + i;
-#pragma unroll
-      for (int c = 0; c < OC; c++)
-        *reinterpret_cast<float4*>(rec_o + rec * D + c * 64 + tx * 4) =
-            make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
-      if (tx == 0) rec_ml[rec] = make_float2(m[i], sum);
-      continue;
-    }
-    const long long orow = (long long)(c0 + j) * kv.Hq + kvh * G + g;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int c = 0; c < OC; c++) {
-      *reinterpret_cast<float4*>(static_cast<T*>(a.out) + orow * D + c * 64 + tx * 4) =
-          make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
-    }
-    if (tx == 0) a.lse[orow] = sum > 0.f ? (m[i] + log2f(sum)) * T_LN2 : -INFINITY;
-  }
 }
 
-// One warp per row joins its splits' records.
-constexpr int TREE_JOIN_WARPS = 4;
+// Joins the partial states of the units that a run's end cut. A unit's records
+// are those of its CTAs (which have consecutive numbers); the thread blocks of
+// all of them but the last share its rows: a warp a row where the records are
+// few, a block a row where they are many.
+// Bound: L2 and latency.
+constexpr int TREE_JOIN_WARPS = 8;
+
+// Adds a state (mi, li, x against mi) to (M, L, o).
+template <int F>
+__device__ __forceinline__ void tree_add(float& M, float& L, float (&o)[F], float mi, float li, const float (&x)[F]) {
+  const float m = fmaxf(M, mi);
+  if (m == -INFINITY) return;
+  const float c0 = exp2f(M - m), c1 = exp2f(mi - m);  // (0 for a state with nothing in it)
+  L = L * c0 + li * c1;
+#pragma unroll
+  for (int f = 0; f < F; f++) o[f] = o[f] * c0 + x[f] * c1;
+  M = m;
+}
+
 template <int D>
-__global__ void __launch_bounds__(TREE_JOIN_WARPS * 32) tree_join_f32_kernel(const TreeLaunch a, int splits, int blocks,
-                                                                             const float2* rec_ml, const float* rec_o) {
+__global__ void __launch_bounds__(TREE_JOIN_WARPS * 32) tree_join_f32_kernel(const __grid_constant__ TreeRun p) {
+  constexpr int F = D / 32, CH = 8;  // floats a lane (columns f * 32 + lane), records in flight
+  __shared__ float so[TREE_JOIN_WARPS][D];
+  __shared__ float2 sml[TREE_JOIN_WARPS];
   pdl_wait();
   pdl_trigger();
-  const KVView& kv = a.kv;
-  const int G = kv.Hq / kv.Hkv, kvh = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
-  int c0 = 0;
-  const int n = seq_tokens(a.cu_new, b, a.T, a.max_new, kv.err, &c0);
-  const int row = blockIdx.x * TREE_JOIN_WARPS + (threadIdx.x >> 5);
-  if (row >= n * G) return;
-  const long long rec0 = ((((long long)b * kv.Hkv + kvh) * blocks + row / TR) * splits) * TR + row % TR;
-  float M = -INFINITY;
-  for (int i = lane; i < splits; i += 32) M = fmaxf(M, __ldcg(rec_ml + rec0 + (long long)i * TR).x);
-  M = warp_max(M);
-  constexpr int F = D / 32;
-  float L = 0.f, o[F];
+  const TreeSplit s = p.split[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = p.group_log2;
+  const int at = ((int)blockIdx.x - s.first) * gridDim.y + blockIdx.y, blocks = (s.n_rec - 1) * gridDim.y;
+  const bool few = s.n_rec <= CH;  // a warp a row
+  const int i_first = few ? 0 : warp, i_step = few ? 1 : TREE_JOIN_WARPS;
+  for (int r0 = few ? at * TREE_JOIN_WARPS : at; r0 < s.rows; r0 += few ? blocks * TREE_JOIN_WARPS : blocks) {
+    const int r = few ? r0 + warp : r0;
+    float M = -INFINITY, L = 0.f, o[F];
 #pragma unroll
-  for (int f = 0; f < F; f++) o[f] = 0.f;
-  if (M != -INFINITY) {
-#pragma unroll 8
-    for (int i = 0; i < splits; i++) {
-      const long long rec = rec0 + (long long)i * TR;
-      const float2 ml = __ldcg(rec_ml + rec);
-      const float wt = exp2f(ml.x - M);  // 0 where the split had nothing
-      L += wt * ml.y;
+    for (int f = 0; f < F; f++) o[f] = 0.f;
+    if (r < s.rows) {
+      for (int i0 = i_first; i0 < s.n_rec; i0 += CH * i_step) {
+        float2 ml[CH];
+        float x[CH][F];
 #pragma unroll
-      for (int f = 0; f < F; f++) o[f] += wt * __ldcg(rec_o + rec * D + f * 32 + lane);
+        for (int c = 0; c < CH; c++) {  // (records behind the last repeat it, with nothing in it)
+          const int i = min(i0 + c * i_step, s.n_rec - 1);
+          const long long rec = (i == 0 ? 2ll * s.first + 1 : 2ll * (s.first + i)) * p.rows_max + r;
+          ml[c] = __ldcg(p.rec_ml + rec);
+          if (i0 + c * i_step >= s.n_rec) ml[c] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int f = 0; f < F; f++) x[c][f] = __ldcg(p.rec_o + rec * D + f * 32 + lane);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; c++) tree_add<F>(M, L, o, ml[c].x, ml[c].y, x[c]);
+      }
     }
-  }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const long long orow = (long long)(c0 + row / G) * kv.Hq + kvh * G + row % G;
+    if (!few) {
+      __syncthreads();  // (the row before is done with)
 #pragma unroll
-  for (int f = 0; f < F; f++) static_cast<float*>(a.out)[orow * D + f * 32 + lane] = o[f] * inv;
-  if (lane == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * T_LN2 : -INFINITY;
+      for (int f = 0; f < F; f++) so[warp][f * 32 + lane] = o[f];
+      if (lane == 0) sml[warp] = make_float2(M, L);
+      __syncthreads();
+      if (warp != 0) continue;
+      M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < TREE_JOIN_WARPS; w++) {
+        float x[F];
+#pragma unroll
+        for (int f = 0; f < F; f++) x[f] = so[w][f * 32 + lane];
+        if (w == 0) L = 0.f;
+        tree_add<F>(M, L, o, sml[w].x, sml[w].y, x);
+      }
+    }
+    if (r >= s.rows) continue;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const long long orow = (long long)(s.tok + (r >> gl)) * p.a.kv.Hq + (s.kvh << gl) + (r & ((1 << gl) - 1));
+#pragma unroll
+    for (int f = 0; f < F; f++) static_cast<float*>(p.a.out)[orow * D + f * 32 + lane] = o[f] * inv;
+    if (lane == 0) p.a.lse[orow] = L > 0.f ? (M + log2f(L)) * T_LN2 : -INFINITY;
+  }
 }
 
-template <int D>
-static cudaError_t tree_go(const TreeLaunch& a, int splits, float2* rec_ml, float* rec_o, cudaStream_t st) {
-  auto k = tree_kernel<D>;
+// -------------------------------------------------------------------------- //
+// host side
+// -------------------------------------------------------------------------- //
+// The forms, by the most rows a sequence may have (us of the three workloads named
+// above: of the form, and of others).
+//  8: single tokens and short drafts, bound by the copies: many small CTAs of two
+//     warps; lanes of two rows by two keys 64, of one by four 70, one warp 83.
+// 32: lanes of four rows by two keys in four warps 64; of one by four in eight 104.
+//     At d = 64 four CTAs an SM 64, three 73.
+// 64: lanes of four rows by four keys in four warps 237; of two by four in eight
+//     311; of eight by two 265.
+// CTAs an SM as shared memory and registers allow.
+static int tree_rows(const KVView& kv, int max_new) {
+  const long long r = (long long)max_new * (kv.Hq / kv.Hkv);
+  return r <= 8 ? 8 : r <= 32 ? 32 : 64;
+}
+static constexpr int tree_ctas_sm(int d, int rows) {
+  return d == 128 ? (rows == 8 ? 3 : 2) : (rows == 8 ? 5 : rows == 32 ? 4 : 3);
+}
+static int tree_ctas(const KVView& kv, int rows, int sms) { return tree_ctas_sm(kv.d, rows) * sms; }
+static size_t tree_up(size_t x) { return (x + 255) / 256 * 256; }
+static size_t tree_bytes(const KVView& kv, int rows, int sms) {
+  const size_t ctas = tree_ctas(kv, rows, sms), rec = 2 * ctas * rows;
+  return tree_up(ctas * sizeof(TreeSplit)) + tree_up(rec * sizeof(float2)) + rec * kv.d * sizeof(float);
+}
+
+size_t tree_workspace(const KVView& kv, int max_new, int sms) {
+  // (a call may take fewer rows than max_new names: the form for what its tokens leave)
+  size_t need = 0;
+  for (int rows = tree_rows(kv, max_new); rows >= 8; rows = rows == 64 ? 32 : rows == 32 ? 8 : 0) {
+    const size_t n = tree_bytes(kv, rows, sms);
+    need = n > need ? n : need;
+  }
+  return need;
+}
+
+template <int D, int TY, int R, int W>
+static cudaError_t tree_go(const TreeRun& p, int sms, cudaStream_t st) {
+  constexpr int CTAS = tree_ctas_sm(D, TY * R * W);
+  using S = TreeShape<D, TY, R, W, CTAS>;
+  auto k = tree_kernel<D, TY, R, W, CTAS>;
   static int smem_set[SMEM_DEVICES];
-  cudaError_t e = allow_smem(k, TreeShape<D>::SMEM, smem_set);
+  cudaError_t e = allow_smem(k, S::SMEM, smem_set);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.max_new * (a.kv.Hq / a.kv.Hkv);
-  const unsigned blocks = (unsigned)((rows + TR - 1) / TR);
-  e = launch_pdl(k, dim3(blocks * splits, a.kv.Hkv, a.kv.B), dim3(TREE_THREADS), TreeShape<D>::SMEM, st, a.kv.pdl, a, splits,
-                 rec_ml, rec_o);
-  if (e != cudaSuccess || splits == 1) return e;
+  // no more CTAs than tiles that the longest caches would give
+  const long long units = (((long long)p.a.max_new << p.group_log2) + S::TR - 1) / S::TR * p.a.kv.B * p.a.kv.Hkv;
+  const long long tiles = units * ((p.a.kv.t_max + TK - 1ll) / TK + (p.a.max_new + TK - 1ll) / TK);
+  const unsigned ctas = (unsigned)(tiles < CTAS * sms ? tiles : CTAS * sms);
+  if ((e = launch_pdl(k, dim3(ctas), dim3(S::THREADS), S::SMEM, st, p.a.kv.pdl, p)) != cudaSuccess) return e;
   abi_count_launch();
-  return launch_pdl(tree_join_f32_kernel<D>, dim3((unsigned)((rows + TREE_JOIN_WARPS - 1) / TREE_JOIN_WARPS), a.kv.Hkv, a.kv.B),
-                    dim3(TREE_JOIN_WARPS * 32), 0, st, true, a, splits, (int)blocks, (const float2*)rec_ml, (const float*)rec_o);
+  return launch_pdl(tree_join_f32_kernel<D>, dim3(ctas, S::TR / TREE_JOIN_WARPS), dim3(TREE_JOIN_WARPS * 32), 0, st, true, p);
 }
 
-cudaError_t launch_tree(const TreeLaunch& a, int max_new, int sms, void* ws, cudaStream_t st) {
-  // (the workspace was sized for max_new, of which a.max_new is what T leaves)
-  const int splits = tree_splits(a.kv, max_new, sms);
-  float2* ml = static_cast<float2*>(ws);
-  float* o = reinterpret_cast<float*>(static_cast<char*>(ws) + (tree_records(a.kv, max_new, splits) * 8 + 255) / 256 * 256);
-  return a.kv.d == 128 ? tree_go<128>(a, splits, ml, o, st) : tree_go<64>(a, splits, ml, o, st);
+cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t st) {
+  const KVView& kv = a.kv;
+  const int G = kv.Hq / kv.Hkv, rows = tree_rows(kv, a.max_new), ctas = tree_ctas(kv, rows, sms);
+  TreeRun p;
+  p.a = a;
+  p.group_log2 = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
+  p.rows_max = rows;
+  char* w = static_cast<char*>(ws);
+  p.split = reinterpret_cast<TreeSplit*>(w);
+  w += tree_up(ctas * sizeof(TreeSplit));
+  p.rec_ml = reinterpret_cast<float2*>(w);
+  w += tree_up(2ull * ctas * rows * sizeof(float2));
+  p.rec_o = reinterpret_cast<float*>(w);
+  if (rows == 8) return kv.d == 128 ? tree_go<128, 2, 2, 2>(p, sms, st) : tree_go<64, 2, 2, 2>(p, sms, st);
+  if (rows == 32) return kv.d == 128 ? tree_go<128, 2, 4, 4>(p, sms, st) : tree_go<64, 2, 4, 4>(p, sms, st);
+  return kv.d == 128 ? tree_go<128, 4, 4, 4>(p, sms, st) : tree_go<64, 4, 4, 4>(p, sms, st);
 }
 
 }  // namespace prhs

@@ -877,3 +877,33 @@ def test_tree_random_shapes(seed):
               room=1, seed=seed)
     check_tree(c, n, pad=int(rng.integers(0, 20)), seed=seed, sets=random_sets(rng, n) if tree else None,
                stride_extra=int(rng.choice([0, 64])), scale=float(rng.uniform(0.02, 0.3)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,n,tree", [(1, 1, [1], True), (8, 1, [1], True), (4, 1, [2, 2], True), (8, 1, [4], False),
+                                           (2, 1, [9], True), (8, 1, [5, 9, 13], True), (8, 2, [17, 33], False),
+                                           (8, 1, [128], True), (8, 1, [41, 25], False), (1, 1, [257], False)])
+def test_fp32_forms_and_unit_shares(d, Hq, Hkv, n, tree):
+    """Row counts on both sides of 8, 32 and 64 and of equal shares, over caches
+    whose tiles are cut into more records than a join takes at once, and next to
+    caches that hold less than a tile."""
+    c = Cache([12000] + [40] * (len(n) - 1), Hq, Hkv, d, F32, page=16, room=1, seed=2)
+    check_tree(c, n, seed=3, sets=random_sets(np.random.default_rng(7), n) if tree else None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("max_new", [1, 2, 5, 40, 10 ** 6])
+def test_workspace_of_more_tokens_than_the_batch_has(dtype, max_new):
+    """max_new names the workspace; a batch of one token fits any of them exactly."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([3000], 8, 1, 128, dtype, seed=1)
+    q, k, v = tree_inputs(c, [1], 0, 1)
+    need = S.tree_workspace_size(c.kv, max_new)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = ws[-ws.data_ptr() % 256:]
+    out, lse = torch.empty_like(q), torch.empty(1, 8, device="cuda")
+    S.tree_attn(c.kv, q, k, v, 0.1, i32([0, 1]), max_new, out, lse, ws[:need])
+    assert S.last_error() == 0 and (ws[need:] == 0xA5).all()
+    want, wl = torch.empty_like(q), torch.empty(1, 8, device="cuda")
+    S.tree_attn(c.kv, q, k, v, 0.1, i32([0, 1]), 1, want, wl, S.make_tree_workspace(c.kv, 1))
+    assert torch.equal(out, want) and torch.equal(lse, wl)
