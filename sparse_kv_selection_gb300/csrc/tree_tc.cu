@@ -7,7 +7,8 @@
 // the cache's, then the new tokens'. All tiles of all units are one list; every
 // CTA (one per SM) takes an equal run of it, so long caches are split and short
 // ones packed without a plan made on the host. A unit cut by a run's end leaves
-// partial states in the workspace, which a second launch joins row by row.
+// partial states in the workspace, which a second launch joins row by row (units
+// of a few tiles are not cut).
 //
 // Inside a CTA: two warps load K and V tiles by TMA into a ring of 128-key
 // slots (128-byte swizzle), half the boxes of each tile each (a tile on 16-key
@@ -40,7 +41,7 @@
 // 2K-16K keys on 16-key pages, 32 KV heads, trees of 1-32 tokens, 4.25 GB: 640 us,
 // 0.98 of the measured copy bandwidth. Above that the tensor cores and the
 // softmax between their products: 5250 causal tokens on cached prefixes, 32 / 8
-// heads: 398 us, 1450 TFLOP/s, 0.78 of the measured matrix rate (a step of a
+// heads: 402 us, 1440 TFLOP/s, 0.77 of the measured matrix rate (a step of a
 // stream is 1550 clocks, its two products 1031; the rest is the wait of one
 // product for the softmax, 1250 clocks of 128 exponentials a thread). Few tiles
 // a CTA (4096 keys, 32 heads): latency, 2.3 us to the first copy, 3 us from it to
@@ -61,6 +62,7 @@ constexpr int TC_THREADS = TC_WARPS * 32;
 constexpr float TC_LOG2E = 1.4426950408889634f;
 constexpr float TC_LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr int UNCUT_TILES = 12;  // the most tiles of a unit in a list that is not cut
 
 template <int D>
 struct TcShape {
@@ -129,8 +131,9 @@ struct TcAux {
   TcBars bar;
   uint32_t tmem;
   int bad_page;
-  int start_b, start_off;
-  int wsum[TC_WARPS];
+  int start_b, start_off;  // where the run begins
+  int begin, end;          // the run
+  int wsum[TC_WARPS], wmax[TC_WARPS];
 };
 static_assert(sizeof(TcAux) <= 3072, "aux region");
 
@@ -285,6 +288,26 @@ __device__ __forceinline__ TcSeq tc_seq(const TreeLaunch& a, int b, int ul) {
   s.tiles = s.blocks == 0 ? 0 : s.blocks * s.cache_tiles + new_tiles_before(s.blocks, s.blocks, s.n, ul, a.mask == nullptr);
   return s;
 }
+// Tiles of unit `block`.
+__device__ __forceinline__ int tc_unit_tiles(const TcSeq& s, int block, int ul, bool causal) {
+  return s.cache_tiles + (causal ? (min(s.n, (block + 1) << ul) + TT - 1) >> 7 : 1);
+}
+// The unit that holds tile `off` of a sequence's share: KV head, unit, the tile's
+// number in it and the tiles from there to the next unit's first (0 from a first
+// one).
+__device__ __forceinline__ int4 tc_unit_at(const TreeLaunch& a, int b, int off, int ul) {
+  const bool causal = a.mask == nullptr;
+  const TcSeq s = tc_seq(a, b, ul);
+  const int kvh = off / s.tiles;
+  off -= kvh * s.tiles;
+  int block = 0, hi = s.blocks - 1;
+  while (block < hi) {
+    const int mid = (block + hi + 1) >> 1;
+    if (mid * s.cache_tiles + new_tiles_before(mid, s.blocks, s.n, ul, causal) <= off) block = mid; else hi = mid - 1;
+  }
+  off -= block * s.cache_tiles + new_tiles_before(block, s.blocks, s.n, ul, causal);
+  return make_int4(kvh, block, off, off == 0 ? 0 : tc_unit_tiles(s, block, ul, causal) - off);
+}
 
 // -------------------------------------------------------------------------- //
 // the kernel
@@ -335,15 +358,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (B + TC_THREADS - 1) / TC_THREADS, b0 = tid * per_t;
-  int mine = 0;
-  for (int b = b0; b < min(B, b0 + per_t); b++) mine += kv.Hkv * tc_seq(a, b, ul).tiles;
+  int mine = 0, most = 0;  // tiles of this thread's sequences, of their largest unit
+  for (int b = b0; b < min(B, b0 + per_t); b++) {
+    const TcSeq s = tc_seq(a, b, ul);
+    mine += kv.Hkv * s.tiles;
+    if (s.blocks > 0) most = max(most, tc_unit_tiles(s, s.blocks - 1, ul, a.mask == nullptr));
+  }
+  most = __reduce_max_sync(FULL_MASK, most);
   int run = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(FULL_MASK, run, o);
     if (lane >= o) run += y;
   }
-  if (lane == 31) aux.wsum[warp] = run;
+  if (lane == 31) {
+    aux.wsum[warp] = run;
+    aux.wmax[warp] = most;
+  }
   __syncthreads();
   int total = 0, before = 0;
 #pragma unroll
@@ -351,17 +382,34 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const int x = aux.wsum[w];
     if (w < warp) before += x;
     total += x;
+    most = max(most, aux.wmax[w]);
   }
   before += run - mine;
   const int per = (total + gridDim.x - 1) / (int)gridDim.x;
-  const int g0 = blockIdx.x * per, count = (base & 1023) != 0 ? 0 : min(total, g0 + per) - g0;
-  if (count > 0 && g0 >= before && g0 < before + mine) {  // the run begins in this thread's sequences
-    int off = g0 - before;
+  // Runs are [g0, g1), or, where cutting units costs more than it gives, they begin
+  // at the unit that begins there or next. Joining takes about 4 us, a tile 0.8 or
+  // (two row tiles) 1.6, so runs may be up to five tiles longer instead, on units so
+  // short that they do not differ by more: 512 causal tokens on 512 keys, 32 / 8 heads,
+  // 28.7 us (cut: 33.6); 4 chunks of 184 on 217 keys 25.3 (32.7); 32 drafts of 8 on 500
+  // keys 24.8 (27.3). The search costs long caches 0.3 us.
+  const int g0 = blockIdx.x * per, g1 = min(total, g0 + per);
+  most = max(most, 1);
+  const bool uncut = most <= UNCUT_TILES && (per + most - 1) / most * most - per <= min(2 * per, 5);
+#pragma unroll 1
+  for (int i = 0; i <= (int)uncut; i++) {
+    const int g = i == 0 ? g0 : g1;
+    if (g >= total || g < before || g >= before + mine) continue;  // not in this thread's sequences
+    int off = g - before;
     for (int k = 0; k < per_t; k++) {
       const int b = tid * per_t + k, x = kv.Hkv * tc_seq(a, b, ul).tiles;
       if (off < x) {
-        aux.start_b = b;
-        aux.start_off = off;
+        const int skip = uncut ? tc_unit_at(a, b, off, ul).w : 0;
+        if (i == 0) {
+          aux.start_b = b;
+          aux.start_off = off + skip;  // (may lead to the next sequence)
+          aux.begin = g + skip;
+        }
+        if (i == 1 || !uncut || g1 >= total) aux.end = i == 1 ? g + skip : g1;
         break;
       }
       off -= x;
@@ -369,7 +417,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   __syncthreads();
   tc_fence_after();
-  if (count <= 0) {  // no tiles left for this CTA
+  if (g0 >= g1 || aux.begin >= aux.end || (base & 1023) != 0) {  // no tiles left for this CTA
     if (tid == 0) p.split[blockIdx.x].rows = 0;
     return;
   }
@@ -401,19 +449,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (warp == 11) {
       // ---------------------- scheduler, and Q producer ---------------------- //
       const bool leader = elect_one();
-      int b = aux.start_b, off = aux.start_off, left = count, loads = 0, qtiles = 0;
+      int b = aux.start_b, off = aux.start_off, left = aux.end - aux.begin, loads = 0, qtiles = 0;
       const bool causal = a.mask == nullptr;
       TcSeq s = tc_seq(a, b, ul);
-      int kvh = off / s.tiles;
-      off -= kvh * s.tiles;
-      int block = 0, hi = s.blocks - 1;
-      while (block < hi) {
-        const int mid = (block + hi + 1) >> 1;
-        if (mid * s.cache_tiles + new_tiles_before(mid, s.blocks, s.n, ul, causal) <= off) block = mid; else hi = mid - 1;
+      while (off >= kv.Hkv * s.tiles) {
+        off -= kv.Hkv * s.tiles;
+        s = tc_seq(a, ++b, ul);
       }
-      off -= block * s.cache_tiles + new_tiles_before(block, s.blocks, s.n, ul, causal);
+      const int4 at = tc_unit_at(a, b, off, ul);
+      int kvh = at.x, block = at.y;
+      off = at.z;
       for (int k = 0;; k++) {
-        const int tiles = s.cache_tiles + (causal ? (min(s.n, (block + 1) << ul) + TT - 1) >> 7 : 1);
+        const int tiles = tc_unit_tiles(s, block, ul, causal);
         const int nt = min(tiles - off, left);
         left -= nt;
         const int i = k & (TC_WORKS - 1);
@@ -441,7 +488,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             sp.rows = off == 0 && nt < tiles ? rows : 0;
             sp.kvh = kvh;
             sp.tok = s.c0 + (block << ul);
-            sp.start = g0 + count - nt;
+            sp.start = aux.end - nt;
             sp.tiles = tiles;
             sp.per = per;
             p.split[blockIdx.x] = sp;

@@ -907,3 +907,21 @@ def test_workspace_of_more_tokens_than_the_batch_has(dtype, max_new):
     want, wl = torch.empty_like(q), torch.empty(1, 8, device="cuda")
     S.tree_attn(c.kv, q, k, v, 0.1, i32([0, 1]), 1, want, wl, S.make_tree_workspace(c.kv, 1))
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_tree_random_short_caches(seed):
+    """Units of a few tiles, which are shared out whole, on batches from one unit
+    to many a CTA, with sequences without tokens between them."""
+    rng = np.random.default_rng(2000 + seed)
+    Hq, Hkv = HEADS[rng.integers(len(HEADS))]
+    m = int(rng.choice([1, 2, 4]))
+    B = int(np.exp(rng.uniform(0, np.log(40))))
+    tree = rng.random() < 0.5
+    top = int(rng.choice([1, 100, 400, 1200]))
+    lens = [int(rng.integers(0, top + 1)) for _ in range(B)]
+    n = [0 if rng.random() < 0.2 else int(np.exp(rng.uniform(0, np.log(129 if tree else 260)))) for _ in range(B)]
+    n[int(rng.integers(B))] = 1
+    c = Cache(lens, Hq * m, Hkv * m, int(rng.choice([64, 128])), BF16 if rng.random() < 0.8 else F32,
+              page=int(rng.choice([0, 16, 64])), room=1, seed=seed)
+    check_tree(c, n, pad=int(rng.integers(0, 5)), seed=seed, sets=random_sets(rng, n) if tree else None)
