@@ -27,7 +27,7 @@
 // Two causal chunks of 1024 tokens on 512 keys, 8 / 2 heads, d = 128: 231 us, 37
 // TFLOP/s; single tokens of 16 heads over 69 206 keys, 4 KV heads, 16-key pages: 64
 // us, 4.4 TB/s; 27 trees of 21 tokens over up to 1899 keys, 8 heads, d = 64: 64 us.
-#include "tokens.h"
+#include "tree_join.cuh"
 
 namespace prhs {
 
@@ -40,21 +40,6 @@ struct __align__(16) TreeStep {
   int b, kvh, block, tile;  // sequence, KV head, unit of theirs, tile of the unit
   int tiles, c0, n, t;      // the unit's tiles, first token, tokens, cached keys
   int tile0, left, q, u;    // the unit's first tile in this run, tiles of the run behind this one, Q slot, tokens of a unit
-};
-
-// A unit that does not end in a CTA's run.
-struct __align__(16) TreeSplit {
-  int rows, kvh, tok, n_rec;  // rows of the unit (0: none), KV head, first token (packed), records
-  int first, pad[3];          // the CTA that starts it
-};
-
-struct TreeRun {
-  TreeLaunch a;
-  int group_log2;    // log2 of the query heads of a KV head
-  int rows_max;      // rows a record may hold
-  TreeSplit* split;  // [CTAs]
-  float2* rec_ml;    // [2 CTAs][rows_max]
-  float* rec_o;      // [2 CTAs][rows_max][D]
 };
 
 template <int D, int TY, int R, int W, int CTAS>
@@ -141,7 +126,8 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool have) 
 }
 
 template <int D, int TY, int R, int W, int CTAS>
-__global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constant__ TreeRun p) {
+__global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constant__ TreeLaunch a,
+                                                                 const __grid_constant__ TreeRecords p) {
   using S = TreeShape<D, TY, R, W, CTAS>;
   constexpr int TR = S::TR, LD = S::LD, LP = S::LP, THREADS = S::THREADS, STEPS = S::STEPS;
   extern __shared__ __align__(16) float tree_smem[];
@@ -153,7 +139,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
 
   pdl_wait();
   pdl_trigger();
-  const TreeLaunch& a = p.a;
   const KVView& kv = a.kv;
   const bool causal = a.mask == nullptr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -474,7 +459,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
       if (r >= rows) continue;
       const long long orow = (x.c0 + ((row0 + r) >> gl)) * kv.Hq + (x.kvh << gl) + (r & ((1 << gl) - 1));
       const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
-      float* dst = (whole ? static_cast<float*>(a.out) + orow * D : p.rec_o + (rec + r) * D) + tx * 4;
+      float* dst = (whole ? static_cast<float*>(a.out) + orow * D : reinterpret_cast<float*>(p.o) + (rec + r) * D) + tx * 4;
 #pragma unroll
       for (int c = 0; c < C4; c++) {
         float4 y;
@@ -484,88 +469,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
       }
       if (tx == 0) {
         if (whole) a.lse[orow] = sum > 0.f ? (m[i] + log2f(sum)) * T_LN2 : -INFINITY;
-        else p.rec_ml[rec + r] = make_float2(m[i], sum);
+        else p.ml[rec + r] = make_float2(m[i], sum);
       }
     }
-  }
-}
-
-// Joins the partial states of the units that a run's end cut. A unit's records
-// are those of its CTAs (which have consecutive numbers); the thread blocks of
-// all of them but the last share its rows: a warp a row where the records are
-// few, a block a row where they are many.
-// Bound: L2 and latency.
-constexpr int TREE_JOIN_WARPS = 8;
-
-// Adds a state (mi, li, x against mi) to (M, L, o).
-template <int F>
-__device__ __forceinline__ void tree_add(float& M, float& L, float (&o)[F], float mi, float li, const float (&x)[F]) {
-  const float m = fmaxf(M, mi);
-  if (m == -INFINITY) return;
-  const float c0 = exp2f(M - m), c1 = exp2f(mi - m);  // (0 for a state with nothing in it)
-  L = L * c0 + li * c1;
-#pragma unroll
-  for (int f = 0; f < F; f++) o[f] = o[f] * c0 + x[f] * c1;
-  M = m;
-}
-
-template <int D>
-__global__ void __launch_bounds__(TREE_JOIN_WARPS * 32) tree_join_f32_kernel(const __grid_constant__ TreeRun p) {
-  constexpr int F = D / 32, CH = 8;  // floats a lane (columns f * 32 + lane), records in flight
-  __shared__ float so[TREE_JOIN_WARPS][D];
-  __shared__ float2 sml[TREE_JOIN_WARPS];
-  pdl_wait();
-  pdl_trigger();
-  const TreeSplit s = p.split[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = p.group_log2;
-  const int at = ((int)blockIdx.x - s.first) * gridDim.y + blockIdx.y, blocks = (s.n_rec - 1) * gridDim.y;
-  const bool few = s.n_rec <= CH;  // a warp a row
-  const int i_first = few ? 0 : warp, i_step = few ? 1 : TREE_JOIN_WARPS;
-  for (int r0 = few ? at * TREE_JOIN_WARPS : at; r0 < s.rows; r0 += few ? blocks * TREE_JOIN_WARPS : blocks) {
-    const int r = few ? r0 + warp : r0;
-    float M = -INFINITY, L = 0.f, o[F];
-#pragma unroll
-    for (int f = 0; f < F; f++) o[f] = 0.f;
-    if (r < s.rows) {
-      for (int i0 = i_first; i0 < s.n_rec; i0 += CH * i_step) {
-        float2 ml[CH];
-        float x[CH][F];
-#pragma unroll
-        for (int c = 0; c < CH; c++) {  // (records behind the last repeat it, with nothing in it)
-          const int i = min(i0 + c * i_step, s.n_rec - 1);
-          const long long rec = (i == 0 ? 2ll * s.first + 1 : 2ll * (s.first + i)) * p.rows_max + r;
-          ml[c] = __ldcg(p.rec_ml + rec);
-          if (i0 + c * i_step >= s.n_rec) ml[c] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int f = 0; f < F; f++) x[c][f] = __ldcg(p.rec_o + rec * D + f * 32 + lane);
-        }
-#pragma unroll
-        for (int c = 0; c < CH; c++) tree_add<F>(M, L, o, ml[c].x, ml[c].y, x[c]);
-      }
-    }
-    if (!few) {
-      __syncthreads();  // (the row before is done with)
-#pragma unroll
-      for (int f = 0; f < F; f++) so[warp][f * 32 + lane] = o[f];
-      if (lane == 0) sml[warp] = make_float2(M, L);
-      __syncthreads();
-      if (warp != 0) continue;
-      M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < TREE_JOIN_WARPS; w++) {
-        float x[F];
-#pragma unroll
-        for (int f = 0; f < F; f++) x[f] = so[w][f * 32 + lane];
-        if (w == 0) L = 0.f;
-        tree_add<F>(M, L, o, sml[w].x, sml[w].y, x);
-      }
-    }
-    if (r >= s.rows) continue;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const long long orow = (long long)(s.tok + (r >> gl)) * p.a.kv.Hq + (s.kvh << gl) + (r & ((1 << gl) - 1));
-#pragma unroll
-    for (int f = 0; f < F; f++) static_cast<float*>(p.a.out)[orow * D + f * 32 + lane] = o[f] * inv;
-    if (lane == 0) p.a.lse[orow] = L > 0.f ? (M + log2f(L)) * T_LN2 : -INFINITY;
   }
 }
 
@@ -589,24 +495,18 @@ static constexpr int tree_ctas_sm(int d, int rows) {
   return d == 128 ? (rows == 8 ? 3 : 2) : (rows == 8 ? 5 : rows == 32 ? 4 : 3);
 }
 static int tree_ctas(const KVView& kv, int rows, int sms) { return tree_ctas_sm(kv.d, rows) * sms; }
-static size_t tree_up(size_t x) { return (x + 255) / 256 * 256; }
-static size_t tree_bytes(const KVView& kv, int rows, int sms) {
-  const size_t ctas = tree_ctas(kv, rows, sms), rec = 2 * ctas * rows;
-  return tree_up(ctas * sizeof(TreeSplit)) + tree_up(rec * sizeof(float2)) + rec * kv.d * sizeof(float);
-}
-
 size_t tree_workspace(const KVView& kv, int max_new, int sms) {
   // (a call may take fewer rows than max_new names: the form for what its tokens leave)
   size_t need = 0;
   for (int rows = tree_rows(kv, max_new); rows >= 8; rows = rows == 64 ? 32 : rows == 32 ? 8 : 0) {
-    const size_t n = tree_bytes(kv, rows, sms);
+    const size_t n = tree_record_bytes(kv.d, tree_ctas(kv, rows, sms), rows);
     need = n > need ? n : need;
   }
   return need;
 }
 
 template <int D, int TY, int R, int W>
-static cudaError_t tree_go(const TreeRun& p, int sms, cudaStream_t st) {
+static cudaError_t tree_go(const TreeLaunch& a, const TreeRecords& p, int sms, cudaStream_t st) {
   constexpr int CTAS = tree_ctas_sm(D, TY * R * W);
   using S = TreeShape<D, TY, R, W, CTAS>;
   auto k = tree_kernel<D, TY, R, W, CTAS>;
@@ -614,30 +514,21 @@ static cudaError_t tree_go(const TreeRun& p, int sms, cudaStream_t st) {
   cudaError_t e = allow_smem(k, S::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   // no more CTAs than tiles that the longest caches would give
-  const long long units = (((long long)p.a.max_new << p.group_log2) + S::TR - 1) / S::TR * p.a.kv.B * p.a.kv.Hkv;
-  const long long tiles = units * ((p.a.kv.t_max + TK - 1ll) / TK + (p.a.max_new + TK - 1ll) / TK);
+  const long long units = (((long long)a.max_new << p.group_log2) + S::TR - 1) / S::TR * a.kv.B * a.kv.Hkv;
+  const long long tiles = units * ((a.kv.t_max + TK - 1ll) / TK + (a.max_new + TK - 1ll) / TK);
   const unsigned ctas = (unsigned)(tiles < CTAS * sms ? tiles : CTAS * sms);
-  if ((e = launch_pdl(k, dim3(ctas), dim3(S::THREADS), S::SMEM, st, p.a.kv.pdl, p)) != cudaSuccess) return e;
+  if ((e = launch_pdl(k, dim3(ctas), dim3(S::THREADS), S::SMEM, st, a.kv.pdl, a, p)) != cudaSuccess) return e;
   abi_count_launch();
-  return launch_pdl(tree_join_f32_kernel<D>, dim3(ctas, S::TR / TREE_JOIN_WARPS), dim3(TREE_JOIN_WARPS * 32), 0, st, true, p);
+  return launch_tree_join<float, D, true>(a, p, ctas, st);
 }
 
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t st) {
   const KVView& kv = a.kv;
-  const int G = kv.Hq / kv.Hkv, rows = tree_rows(kv, a.max_new), ctas = tree_ctas(kv, rows, sms);
-  TreeRun p;
-  p.a = a;
-  p.group_log2 = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
-  p.rows_max = rows;
-  char* w = static_cast<char*>(ws);
-  p.split = reinterpret_cast<TreeSplit*>(w);
-  w += tree_up(ctas * sizeof(TreeSplit));
-  p.rec_ml = reinterpret_cast<float2*>(w);
-  w += tree_up(2ull * ctas * rows * sizeof(float2));
-  p.rec_o = reinterpret_cast<float*>(w);
-  if (rows == 8) return kv.d == 128 ? tree_go<128, 2, 2, 2>(p, sms, st) : tree_go<64, 2, 2, 2>(p, sms, st);
-  if (rows == 32) return kv.d == 128 ? tree_go<128, 2, 4, 4>(p, sms, st) : tree_go<64, 2, 4, 4>(p, sms, st);
-  return kv.d == 128 ? tree_go<128, 4, 4, 4>(p, sms, st) : tree_go<64, 4, 4, 4>(p, sms, st);
+  const int G = kv.Hq / kv.Hkv, rows = tree_rows(kv, a.max_new);
+  const TreeRecords p = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, tree_ctas(kv, rows, sms), rows);
+  if (rows == 8) return kv.d == 128 ? tree_go<128, 2, 2, 2>(a, p, sms, st) : tree_go<64, 2, 2, 2>(a, p, sms, st);
+  if (rows == 32) return kv.d == 128 ? tree_go<128, 2, 4, 4>(a, p, sms, st) : tree_go<64, 2, 4, 4>(a, p, sms, st);
+  return kv.d == 128 ? tree_go<128, 4, 4, 4>(a, p, sms, st) : tree_go<64, 4, 4, 4>(a, p, sms, st);
 }
 
 }  // namespace prhs

@@ -46,7 +46,7 @@
 // product for the softmax, 1250 clocks of 128 exponentials a thread). Few tiles
 // a CTA (4096 keys, 32 heads): latency, 2.3 us to the first copy, 3 us from it to
 // the first weights, 3.5 us of joining.
-#include "tokens.h"
+#include "tree_join.cuh"
 
 namespace prhs {
 
@@ -137,20 +137,10 @@ struct TcAux {
 };
 static_assert(sizeof(TcAux) <= 3072, "aux region");
 
-// A CTA's unit that it starts and does not finish.
-struct __align__(16) TcSplit {
-  int rows, kvh, tok, start;  // rows of the unit (0: none), KV head, first token (packed), first tile
-  int tiles, per, pad[2];     // its tiles, the tiles of a run
-};
-
 struct TcLaunch {
   TreeLaunch a;
-  int group_log2;    // log2 of the query heads of a KV head
-  int box_log2;      // log2 of the rows of a cache TMA box
-  int rows_max;      // rows a record may hold
-  TcSplit* split;    // [CTAs]
-  float* rec_ml;     // [2 CTAs][rows_max][2]
-  float* rec_o;      // [2 CTAs][rows_max][D]
+  TreeRecords rec;
+  int box_log2;  // log2 of the rows of a cache TMA box
 };
 
 // -------------------------------------------------------------------------- //
@@ -323,7 +313,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const TreeLaunch& a = p.a;
   const KVView& kv = a.kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = kv.B, gl = p.group_log2, ul = 8 - gl;  // log2 of the group and of a unit's tokens
+  const int B = kv.B, gl = p.rec.group_log2, ul = 8 - gl;  // log2 of the group and of a unit's tokens
   const uint32_t base = smem_addr(tc_smem);
   uint8_t* data = tc_smem;
   TcAux& aux = *reinterpret_cast<TcAux*>(data + S::DATA);
@@ -418,7 +408,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (g0 >= g1 || aux.begin >= aux.end || (base & 1023) != 0) {  // no tiles left for this CTA
-    if (tid == 0) p.split[blockIdx.x].rows = 0;
+    if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
     return;
   }
   if (warp == 9) {  // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
@@ -484,14 +474,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           w.last = left == 0;
           mbar_arrive(&bar.wfull[i]);
           if (left == 0) {
-            TcSplit sp;
-            sp.rows = off == 0 && nt < tiles ? rows : 0;
-            sp.kvh = kvh;
-            sp.tok = s.c0 + (block << ul);
-            sp.start = aux.end - nt;
-            sp.tiles = tiles;
-            sp.per = per;
-            p.split[blockIdx.x] = sp;
+            TreeSplit sp = {};
+            if (off + nt < tiles) {
+              const int start = aux.end - nt - off;  // the list's number of the unit's first tile
+              sp.rows = rows;
+              sp.kvh = kvh;
+              sp.tok = s.c0 + (block << ul);
+              sp.first = start / per;
+              sp.n_rec = (start + tiles - 1) / per - sp.first + 1;
+            }
+            p.rec.split[blockIdx.x] = sp;
           }
         }
         __syncwarp();
@@ -869,7 +861,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         w0 *= inv;
         w1 *= inv;
       }
-      const long long rec = ((long long)(2 * blockIdx.x + (w.tile0 == 0 ? 1 : 0)) * p.rows_max + ur);
+      const int rec = 2 * blockIdx.x + (w.tile0 == 0 ? 1 : 0);
       const long long orow = (long long)(w.c0 + tok) * kv.Hq + (w.kvh << gl) + (ur & ((1 << gl) - 1));
       // both warpgroups of a shared unit write half the columns each
       const int c_lo = both ? st * (D / 64) : 0, c_hi = both ? c_lo + D / 64 : D / 32;
@@ -895,14 +887,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                 pack2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
                                 pack2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.rec_o + rec * D + c * 32);
+          uint4* dst = reinterpret_cast<uint4*>(p.rec.o) + (rec * (D / 4) + c * 8) * p.rec.rows_max + ur;
 #pragma unroll
-          for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 8; e++)
+            dst[e * p.rec.rows_max] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (live && (!both || st == 0)) {
         if (w.whole) a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
-        else *reinterpret_cast<float2*>(p.rec_ml + rec * 2) = make_float2(M, L);
+        else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();
       if (both) named_bar(1, 2 * TT);  // both outputs and the row states are read
@@ -915,103 +908,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
 }
 
-// Joins the partial states of the units that a run's end cut, over the records
-// of the CTA that began a unit and of those after it. A lane holds D / 32
-// columns; eight records' rows are in flight together where a unit has many (a
-// warp takes one row), four rows of two where it has few.
-// Bound: L2 and latency.
-constexpr int JOIN_WARPS = 8, JOIN_FEW = 4;
-
-template <int D, int JOIN_ROWS>
-__device__ __forceinline__ void join_rows(const TcLaunch& p, int row0, int rows, int kvh, int tok0, int n_rec) {
-  const TreeLaunch& a = p.a;
-  const int lane = threadIdx.x & 31, c_first = blockIdx.x;
-  constexpr int F = D / 32;  // floats a lane
-  auto rec_of = [&](int i, int row) {  // record of the unit's i-th CTA
-    return (long long)(i == 0 ? 2 * c_first + 1 : 2 * (c_first + i)) * p.rows_max + row;
-  };
-  float M[JOIN_ROWS], L[JOIN_ROWS], o[JOIN_ROWS][F];
-#pragma unroll
-  for (int j = 0; j < JOIN_ROWS; j++) {
-    M[j] = -INFINITY;
-    L[j] = 0.f;
-#pragma unroll
-    for (int f = 0; f < F; f++) o[j][f] = 0.f;
-  }
-  constexpr int CH = 8 / JOIN_ROWS;  // records in flight
-  for (int i0 = 0; i0 < n_rec; i0 += CH) {
-    // records and their states, all asked for at once (rows past the unit's repeat
-    // the last, records past its last get weight 0)
-    float2 ml[CH][JOIN_ROWS];
-    float x[CH][JOIN_ROWS][F];
-#pragma unroll
-    for (int i = 0; i < CH; i++)
-#pragma unroll
-      for (int j = 0; j < JOIN_ROWS; j++) {
-        const long long r = rec_of(min(i0 + i, n_rec - 1), min(row0 + j, rows - 1));
-        ml[i][j] = __ldcg(reinterpret_cast<const float2*>(p.rec_ml) + r);
-        if constexpr (F == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.rec_o + r * D) + lane);
-          x[i][j][0] = v.x;
-          x[i][j][1] = v.y;
-          x[i][j][2] = v.z;
-          x[i][j][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.rec_o + r * D) + lane);
-          x[i][j][0] = v.x;
-          x[i][j][1] = v.y;
-        }
-      }
-#pragma unroll
-    for (int j = 0; j < JOIN_ROWS; j++) {
-      float m = M[j];
-#pragma unroll
-      for (int i = 0; i < CH; i++) m = fmaxf(m, ml[i][j].x);
-      const float corr = M[j] == -INFINITY ? 0.f : exp2f(M[j] - m);
-      L[j] *= corr;
-#pragma unroll
-      for (int f = 0; f < F; f++) o[j][f] *= corr;
-#pragma unroll
-      for (int i = 0; i < CH; i++) {
-        const float wt = i0 + i < n_rec && ml[i][j].x != -INFINITY ? exp2f(ml[i][j].x - m) : 0.f;
-        L[j] += wt * ml[i][j].y;
-#pragma unroll
-        for (int f = 0; f < F; f++) o[j][f] += wt * x[i][j][f];
-      }
-      M[j] = m;
-    }
-  }
-  const int gl = p.group_log2;
-#pragma unroll
-  for (int j = 0; j < JOIN_ROWS; j++) {
-    const int row = row0 + j;
-    if (row >= rows) break;
-    const float inv = L[j] > 0.f ? 1.f / L[j] : 0.f;
-    const long long orow = (long long)(tok0 + (row >> gl)) * a.kv.Hq + (kvh << gl) + (row & ((1 << gl) - 1));
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * F;
-    if constexpr (F == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(o[j][0] * inv, o[j][1] * inv), pack2(o[j][2] * inv, o[j][3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = pack2(o[j][0] * inv, o[j][1] * inv);
-    if (lane == 0) a.lse[orow] = L[j] > 0.f ? (M[j] + log2f(L[j])) * TC_LN2 : -INFINITY;
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TcLaunch p) {
-  pdl_wait();
-  pdl_trigger();
-  const int4* sw = reinterpret_cast<const int4*>(p.split + blockIdx.x);
-  const int4 s0 = sw[0], s1 = sw[1];  // rows, kvh, tok, start; tiles, per
-  const int n_rec = (s0.w + s1.x - 1) / max(1, s1.y) - (int)blockIdx.x + 1;
-  const int w = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
-  if (n_rec > JOIN_FEW) {
-    if (w < s0.x) join_rows<D, 1>(p, w, s0.x, s0.y, s0.z, n_rec);
-  } else {
-    if (w * 4 < s0.x) join_rows<D, 4>(p, w * 4, s0.x, s0.y, s0.z, n_rec);
-  }
-}
-
 // -------------------------------------------------------------------------- //
 // host side
 // -------------------------------------------------------------------------- //
@@ -1020,11 +916,8 @@ static int tc_rows_max(const KVView& kv, int max_new) {
   return (int)(r < UNIT_ROWS ? r : UNIT_ROWS);
 }
 
-static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms) {
-  const size_t rec = (size_t)2 * sms * tc_rows_max(kv, max_new);
-  return up256(sms * sizeof(TcSplit)) + up256(rec * 2 * sizeof(float)) + up256(rec * kv.d * sizeof(float));
+  return tree_record_bytes(kv.d, sms, tc_rows_max(kv, max_new));
 }
 
 // Rows of a TMA box of the cache's whole tiles: the most that a page holds whole
@@ -1052,8 +945,7 @@ static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cu
                  maps[6], p);
   if (e != cudaSuccess) return e;
   abi_count_launch();
-  return launch_pdl(tree_join_kernel<D>, dim3(sms, (p.rows_max + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,
-                    st, true, p);
+  return launch_tree_join<__nv_bfloat16, D, false>(p.a, p.rec, sms, st);
 }
 
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t st, cudaError_t* err) {
@@ -1062,15 +954,8 @@ prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t 
   const int G = kv.Hq / kv.Hkv;
   TcLaunch p;
   p.a = a;
-  p.group_log2 = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
+  p.rec = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, sms, tc_rows_max(kv, a.max_new));
   p.box_log2 = tc_box_log2(kv);
-  p.rows_max = tc_rows_max(kv, a.max_new);
-  char* w = static_cast<char*>(ws);
-  p.split = reinterpret_cast<TcSplit*>(w);
-  w += up256(sms * sizeof(TcSplit));
-  p.rec_ml = reinterpret_cast<float*>(w);
-  w += up256((size_t)2 * sms * p.rows_max * 2 * sizeof(float));
-  p.rec_o = reinterpret_cast<float*>(w);
 
   CUtensorMap maps[7];  // q; cache K and V; their partial tiles; new K and V
   const uint64_t d = kv.d, row = d * 2, segs = d / 64;
