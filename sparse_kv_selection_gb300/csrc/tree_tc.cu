@@ -62,6 +62,7 @@ constexpr int TC_THREADS = TC_WARPS * 32;
 constexpr float TC_LOG2E = 1.4426950408889634f;
 constexpr float TC_LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr int QUAD_ROWS = 32;
 constexpr int UNCUT_TILES = 12;  // the most tiles of a unit in a list that is not cut
 
 template <int D>
@@ -245,6 +246,18 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// Lanes that differ in bit B trade the second element of the lower for the first
+// of the upper.
+template <int B>
+__device__ __forceinline__ void quad_swap(uint32_t (&x)[4], uint32_t (&y)[4]) {
+  const bool up = threadIdx.x & B;
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const uint32_t z = __shfl_xor_sync(FULL_MASK, up ? x[k] : y[k], B);
+    x[k] = up ? z : x[k];
+    y[k] = up ? y[k] : z;
+  }
 }
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -862,7 +875,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         w1 *= inv;
       }
       const int rec = 2 * blockIdx.x + (w.tile0 == 0 ? 1 : 0);
-      const long long orow = (long long)(w.c0 + tok) * kv.Hq + (w.kvh << gl) + (ur & ((1 << gl) - 1));
+      auto out_row = [&](int r) {
+        return (long long)(w.c0 + w.tok0 + (r >> gl)) * kv.Hq + (w.kvh << gl) + (r & ((1 << gl) - 1));
+      };
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+      // Four lanes exchange their rows' 16-byte pieces, so that a store covers 64 bytes
+      // of eight rows, not 16 of 32: it is issued line by line (causal chunks 398 -> 387
+      // us). With few rows the exchange costs more than it saves.
+      const bool quads = w.rows > QUAD_ROWS;
       // both warpgroups of a shared unit write half the columns each
       const int c_lo = both ? st * (D / 64) : 0, c_hi = both ? c_lo + D / 64 : D / 32;
       const bool two = both && steps > 1;
@@ -877,16 +897,32 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           const float v = __uint_as_float(o[e]) * w0;
           o[e] = __float_as_uint(two ? fmaf(__uint_as_float(o1[e]), w1, v) : v);
         }
-        if (!live) continue;
         if (w.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
+          uint32_t v[4][4];
 #pragma unroll
           for (int e = 0; e < 4; e++)
-            dst[e] = make_uint4(pack2(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                                pack2(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                                pack2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                                pack2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-        } else {
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+              v[e][k] = pack2(__uint_as_float(o[8 * e + 2 * k]), __uint_as_float(o[8 * e + 2 * k + 1]));
+          if (!quads) {
+            uint4* dst = reinterpret_cast<uint4*>(out + out_row(ur) * D + c * 32);
+            if (live)
+#pragma unroll
+              for (int e = 0; e < 4; e++) dst[e] = make_uint4(v[e][0], v[e][1], v[e][2], v[e][3]);
+            continue;
+          }
+          quad_swap<1>(v[0], v[1]);
+          quad_swap<1>(v[2], v[3]);
+          quad_swap<2>(v[0], v[2]);
+          quad_swap<2>(v[1], v[3]);
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const int r = (ur & ~3) + e;
+            if (r < w.rows && !dead)
+              *reinterpret_cast<uint4*>(out + out_row(r) * D + c * 32 + (lane & 3) * 8) =
+                  make_uint4(v[e][0], v[e][1], v[e][2], v[e][3]);
+          }
+        } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(p.rec.o) + (rec * (D / 4) + c * 8) * p.rec.rows_max + ur;
 #pragma unroll
           for (int e = 0; e < 8; e++)
@@ -894,7 +930,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
       }
       if (live && (!both || st == 0)) {
-        if (w.whole) a.lse[orow] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
+        if (w.whole) a.lse[out_row(ur)] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
         else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();
