@@ -41,11 +41,11 @@
 // 2K-16K keys on 16-key pages, 32 KV heads, trees of 1-32 tokens, 4.25 GB: 640 us,
 // 0.98 of the measured copy bandwidth. Above that the tensor cores and the
 // softmax between their products: 5250 causal tokens on cached prefixes, 32 / 8
-// heads: 402 us, 1440 TFLOP/s, 0.77 of the measured matrix rate (a step of a
+// heads: 387 us, 1495 TFLOP/s, 0.80 of the measured matrix rate (a step of a
 // stream is 1550 clocks, its two products 1031; the rest is the wait of one
 // product for the softmax, 1250 clocks of 128 exponentials a thread). Few tiles
 // a CTA (4096 keys, 32 heads): latency, 2.3 us to the first copy, 3 us from it to
-// the first weights, 3.5 us of joining.
+// the first weights, 3 us of joining.
 #include "tree_join.cuh"
 
 namespace prhs {

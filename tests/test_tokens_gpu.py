@@ -925,3 +925,12 @@ def test_tree_random_short_caches(seed):
     c = Cache(lens, Hq * m, Hkv * m, int(rng.choice([64, 128])), BF16 if rng.random() < 0.8 else F32,
               page=int(rng.choice([0, 16, 64])), room=1, seed=seed)
     check_tree(c, n, pad=int(rng.integers(0, 5)), seed=seed, sets=random_sets(rng, n) if tree else None)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,t,n,page", [(40, 32, 32, 64, 1600, 1, 16), (2, 64, 16, 128, 21000, 16, 0),
+                                                 (24, 32, 32, 64, 2100, 6, 64)])
+def test_fp32_sums_in_blocks(B, Hq, Hkv, d, t, n, page):
+    """Runs of many tiles in one CTA, whose sums are folded on the way: in units
+    that end there, begin there and pass through."""
+    c = Cache([t] * B, Hq, Hkv, d, F32, page=page, room=1, seed=6)
+    check_tree(c, [n] * B, seed=5, sets=random_sets(np.random.default_rng(3), [n] * B))
