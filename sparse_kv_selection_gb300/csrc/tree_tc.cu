@@ -748,14 +748,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         if (cut) {
           // V rows of keys that do not exist hold whatever was there, possibly not
-          // finite, and 0 * inf would reach every row: they are set to 0
+          // finite, and 0 * inf would reach every row: they are set to 0 (each row from
+          // another piece on, since the rows' equal pieces share their banks)
           const int g = w.load_v(i), slot = g % S::SLOTS;
           dead = !__all_sync(FULL_MASK, mbar_wait(&bar.full[slot], (g / S::SLOTS) & 1, kv.err));
           const uint32_t hw = row < 32 ? have[0] : row < 64 ? have[1] : row < 96 ? have[2] : have[3];
           if (!dead && !((hw >> (row & 31)) & 1u)) {
 #pragma unroll
             for (int c = 0; c < 8 * S::SEGS; c++)
-              *reinterpret_cast<uint4*>(data + slot * S::TILE + (c / 8) * S::SEG + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(data + slot * S::TILE + (c / 8) * S::SEG + row * 128 + ((c ^ row) % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
