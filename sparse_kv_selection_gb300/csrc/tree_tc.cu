@@ -38,8 +38,8 @@
 //
 // Bound: HBM while a KV head has up to about 256 query rows (K and V are read
 // once: 512 bytes a key at d = 128 against 4 * 128 * rows flops): 32 sequences of
-// 2K-16K keys on 16-key pages, 32 KV heads, trees of 1-32 tokens, 4.25 GB: 640 us,
-// 0.98 of the measured copy bandwidth. Above that the tensor cores and the
+// 2K-16K keys on 16-key pages, 32 KV heads, trees of 1-32 tokens, 4.25 GB: 630 us,
+// the measured copy bandwidth. Above that the tensor cores and the
 // softmax between their products: 5250 causal tokens on cached prefixes, 32 / 8
 // heads: 387 us, 1495 TFLOP/s, 0.80 of the measured matrix rate (a step of a
 // stream is 1550 clocks, its two products 1031; the rest is the wait of one
@@ -358,6 +358,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
   pdl_wait();
   pdl_trigger();
+  // (the join of a CTA that gives up reads this)
+  if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
 
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (B + TC_THREADS - 1) / TC_THREADS, b0 = tid * per_t;
@@ -420,10 +422,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   __syncthreads();
   tc_fence_after();
-  if (g0 >= g1 || aux.begin >= aux.end || (base & 1023) != 0) {  // no tiles left for this CTA
-    if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
-    return;
-  }
+  if (g0 >= g1 || aux.begin >= aux.end || (base & 1023) != 0) return;  // no tiles left for this CTA
   if (warp == 9) {  // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&aux.tmem))
                  : "memory");
