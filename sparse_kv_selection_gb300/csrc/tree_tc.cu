@@ -59,6 +59,7 @@ constexpr int TC_WARPS = 12;             // 8 softmax, two K/V producers, matrix
 constexpr int TC_REGS_LAUNCH = 168, TC_REGS_SOFTMAX = 224, TC_REGS_REST = 56;
 static_assert(2 * TC_REGS_SOFTMAX + TC_REGS_REST <= 3 * TC_REGS_LAUNCH, "register shares");
 constexpr int TC_THREADS = TC_WARPS * 32;
+constexpr int TC_AUX = 3 << 10;          // bytes of shared memory beside the tiles
 constexpr float TC_LOG2E = 1.4426950408889634f;
 constexpr float TC_LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.f;
@@ -72,7 +73,7 @@ struct TcShape {
   static constexpr int TILE = SEGS * SEG;
   static constexpr int SLOTS = D == 128 ? 5 : 10; // K and V tiles in flight
   static constexpr int DATA = (SLOTS + 2) * TILE; // the ring and two Q tiles
-  static constexpr size_t SMEM = (size_t)DATA + 3072;
+  static constexpr size_t SMEM = (size_t)DATA + TC_AUX;
 };
 
 // One unit's tiles in a CTA's run, as the scheduler warp hands it to the others.
@@ -136,7 +137,7 @@ struct TcAux {
   int begin, end;          // the run
   int wsum[TC_WARPS], wmax[TC_WARPS];
 };
-static_assert(sizeof(TcAux) <= 3072, "aux region");
+static_assert(sizeof(TcAux) <= TC_AUX, "aux region");
 
 struct TcLaunch {
   TreeLaunch a;
