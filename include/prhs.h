@@ -382,8 +382,14 @@ size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new);
  * or tokens 0 .. j where tree_mask is null (a causal chunk of any length):
  *   lse = log sum exp(s),  out = sum exp(s - lse) v,  s = scale * <q, k>
  * over the attended keys; out = 0 and lse = -inf where there are none.
- * out [T][Hq][d] has the cache's element type (fp32 accumulation, rounded
- * once), lse [T][Hq] is fp32. Rows of padding tokens are left as they are.
+ * out [T][Hq][d] has the cache's element type, lse [T][Hq] is fp32. Sums are
+ * fp32. On an fp32 cache so are the weights exp(s - m); on a bf16 cache each weight
+ * is rounded to bf16 (by up to 2^-8 of it) before its product with v, beside the
+ * rounding of out: up to 2^-8 of sum exp(s - lse) |v|, together about 1.4 times the
+ * error of out's rounding alone on random values (lse is of the unrounded weights).
+ * prhs_dense_attn keeps fp32 weights and results on either cache. v_new of a
+ * sequence's tokens must be finite: the product takes those that a token does not
+ * attend with weight 0. Rows of padding tokens are left as they are.
  * max_new bounds the tokens of any sequence, at most PRHS_TREE_MAX with
  * tree_mask; a sequence with more, or with cu_new not ascending within [0, T],
  * is flagged (PRHS_DEV_BAD_LEN) and its rows are left as they are. Keys on a

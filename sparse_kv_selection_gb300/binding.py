@@ -452,7 +452,8 @@ def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree
               stream=None) -> None:
     """Attention of packed new tokens over their caches and each other: by
     tree_mask [T][4] int32, or causal (prhs_tree_attn). out [T][Hq][d] has the
-    cache's element type, lse [T][Hq] is float32."""
+    cache's element type, lse [T][Hq] is float32. On a bfloat16 cache the weights
+    are rounded to bfloat16 before they meet v (dense_attn keeps them in float32)."""
     dev, dt, T, desc = kv.device, kv.dtype, q.shape[0], kv.desc
     Hq, Hkv, d = desc.Hq, desc.Hkv, desc.d
     kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
