@@ -2,8 +2,8 @@
 // behind each sequence's cached prefix and its length advances.
 //
 // One cluster of CTAs per sequence. Every CTA checks the sequence's whole
-// request (numbers, room, pages) before anything is written, so a refused
-// sequence keeps its rows and its length; then the cluster copies the rows in
+// request (numbers, room, pages; the pages also where only the length advances)
+// before anything is written, so a refused sequence keeps its rows and its length; then the cluster copies the rows in
 // 16-byte pieces, COMMIT_PER loads of a thread in flight, and the length is
 // written behind a cluster barrier, since it may be the array that every CTA
 // read. Bound: latency (a handful of rows), HBM for long batches.
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_kernel(const CommitLaun
   if (bits != 0) m = 0;
   for (int i = tid; i < m; i += COMMIT_THREADS) {
     if (idx != nullptr && (idx[i] < 0 || idx[i] >= n)) bits |= PRHS_DEV_BAD_INDEX;
-    if (a.k_new != nullptr && kv_row(kv, b, 0, t + i) < 0) bits |= PRHS_DEV_BAD_BLOCK;
+    if (kv_row(kv, b, 0, t + i) < 0) bits |= PRHS_DEV_BAD_BLOCK;
   }
   if (bits != 0 && rank == 0) raise_error(kv.err, bits);
   if (__syncthreads_or((int)bits)) m = 0;
