@@ -282,7 +282,7 @@ prhs_status prhs_append_kv(const prhs_kv* kv, const void* k_new, const void* v_n
  *   prhs_plan_tokens    pages, slots, positions and masks of the new tokens
  *   prhs_rope_append    rotated q; k and v into the cache, or k kept packed
  *   prhs_tree_attn      attention over the cache and the new tokens
- *   prhs_commit_tokens  accepted tokens join the cache, lengths advance
+ *   prhs_commit_planned accepted tokens join the cache, lengths advance
  * and stays on the device: it can be captured into a graph. Token strides are
  * in elements, at least the row's, and multiples of 16 bytes. Arrays of rows
  * are 16-byte aligned.
@@ -404,16 +404,28 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
  * every KV head gets the packed rows of token accept_idx[b][i] (int32
  * [B][accept_cap], numbers within the sequence's new tokens; nullable: token i
  * itself), and new_lens[b] = t_b + m_b (int32 [B]; may be kv->seq_lens itself).
- * The positions must be mapped (prhs_plan_tokens). k_new and v_new nullable
- * together: the rows are in the cache already (prhs_rope_append), only the
- * lengths advance. A sequence with m_b outside [0, n_b] or above accept_cap,
- * a number outside [0, n_b), no room or an unmapped page is flagged
- * (PRHS_DEV_BAD_LEN, _BAD_INDEX, _CAPACITY, _BAD_BLOCK) and keeps its rows and
- * its length. */
+ * k_new and v_new nullable together: the rows are in the cache already
+ * (prhs_rope_append), only the lengths advance. A sequence with m_b outside
+ * [0, n_b] or above accept_cap, a number outside [0, n_b), no room or a position on
+ * no page of the pool is flagged (PRHS_DEV_BAD_LEN, _BAD_INDEX, _CAPACITY,
+ * _BAD_BLOCK) and keeps its rows and its length. The block table is taken at its
+ * word: what a row holds behind the sequence's own pages must not name a page, and
+ * a sequence that planning refused must have m_b = 0. */
 prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,
                                const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
                                const void* k_new, long long k_stride, const void* v_new,
                                long long v_stride, int32_t* new_lens, cudaStream_t stream);
+
+/* The same with the plan's verdict: slots [T] as prhs_plan_tokens gave them for
+ * these tokens. A sequence that planning refused, in whole or in part (an accepted
+ * position whose slot is -1: PRHS_DEV_CAPACITY), and one whose slots are not the
+ * rows of its positions t_b .. t_b + m_b - 1 (a plan made before the length or the
+ * pages changed, or committed already: PRHS_DEV_BAD_INDEX) keep their rows and their
+ * lengths too, whatever else their block table rows hold. */
+prhs_status prhs_commit_planned(const prhs_kv* kv, int T, const int32_t* cu_new, const int32_t* slots,
+                                const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
+                                const void* k_new, long long k_stride, const void* v_new,
+                                long long v_stride, int32_t* new_lens, cudaStream_t stream);
 
 /* Self-test of the kernels' failure path (no counterpart in the paper): one
  * warp waits on a shared-memory mbarrier that nothing arrives on, through the

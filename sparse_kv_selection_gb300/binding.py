@@ -26,7 +26,7 @@ EXPORTS = ["prhs_workspace_size", "prhs_workspace_init", "prhs_score_select", "p
            "prhs_sparse_attn", "prhs_sparse_attn_noalloc", "prhs_set_mass", "prhs_dense_attn",
            "prhs_decode_step", "prhs_append_kv", "prhs_plan_tokens", "prhs_rope_turns",
            "prhs_rope_append", "prhs_tree_workspace_size", "prhs_tree_attn",
-           "prhs_commit_tokens", "prhs_selftest_wait_timeout", "prhs_last_error",
+           "prhs_commit_tokens", "prhs_commit_planned", "prhs_selftest_wait_timeout", "prhs_last_error",
            "prhs_device_error_bits", "prhs_status_str", "prhs_last_message", "prhs_num_sms",
            "prhs_launch_count"]
 
@@ -92,6 +92,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "prhs_tree_workspace_size": (Z, [KV, I]),
         "prhs_tree_attn": (I, [KV, P, P, L, P, L, F, I, P, I, P, P, P, P, Z, P]),
         "prhs_commit_tokens": (I, [KV, I, P, P, I, P, P, L, P, L, P, P]),
+        "prhs_commit_planned": (I, [KV, I, P, P, P, I, P, P, L, P, L, P, P]),
         "prhs_selftest_wait_timeout": (I, [ctypes.c_uint, P]),
         "prhs_last_error": (I, []),
         "prhs_device_error_bits": (ctypes.c_uint, []),
@@ -467,23 +468,29 @@ def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree
           _ptr(ws), ws.numel() * ws.element_size())
 
 
-def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, accept_idx=None, k_new=None, v_new=None,
-                  T=None, stream=None) -> None:
+def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, slots=None, accept_idx=None, k_new=None,
+                  v_new=None, T=None, stream=None) -> None:
     """Write the accepted tokens' packed rows behind each cached prefix and
-    advance the lengths (prhs_commit_tokens), in place unless new_lens is
-    given. Without k_new and v_new only the lengths advance; T then bounds the
-    packed tokens (default: B * t_max)."""
+    advance the lengths, in place unless new_lens is given. With the slots that
+    plan_tokens gave, sequences that it refused are left as they are
+    (prhs_commit_planned); without, the block table alone says where the rows go
+    (prhs_commit_tokens). Without k_new and v_new only the lengths advance; T
+    then bounds the packed tokens (default: those of slots, or B * t_max)."""
     dev, dt, i32, desc = kv.device, kv.dtype, torch.int32, kv.desc
     B, Hkv, d = desc.B, desc.Hkv, desc.d
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new must be both given or both left out")
     if T is None:
-        T = k_new.shape[0] if k_new is not None else min(B * kv.t_max, ((1 << 31) - 1) // (kv.Hq + 2 * Hkv))
+        T = (k_new.shape[0] if k_new is not None else slots.numel() if slots is not None
+             else min(B * kv.t_max, ((1 << 31) - 1) // (kv.Hq + 2 * Hkv)))
     kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
     vp, vs = _rows(v_new, "v_new", T, Hkv, d, dt, dev)
     cap = 0 if accept_idx is None else accept_idx.shape[-1]
-    _call(kv, "commit_tokens", load().prhs_commit_tokens, stream, kv.ref(), int(T),
-          _array(cu_new, "cu_new", (B + 1,), i32, dev),
+    fn, planned = load().prhs_commit_tokens, ()
+    if slots is not None:
+        fn, planned = load().prhs_commit_planned, (_array(slots, "slots", (T,), i32, dev),)
+    _call(kv, "commit_tokens", fn, stream, kv.ref(), int(T),
+          _array(cu_new, "cu_new", (B + 1,), i32, dev), *planned,
           _array(accept_idx, "accept_idx", (B, cap), i32, dev, True), cap,
           _array(accept_n, "accept_n", (B,), i32, dev), kp, ks, vp, vs,
           _array(kv.seq_lens if new_lens is None else new_lens, "new_lens", (B,), i32, dev))

@@ -2,7 +2,7 @@
 // behind each sequence's cached prefix and its length advances.
 //
 // One cluster of CTAs per sequence. Every CTA checks the sequence's whole
-// request (numbers, room, pages; the pages also where only the length advances)
+// request (numbers, room, pages, planned slots; also where only the length advances)
 // before anything is written, so a refused sequence keeps its rows and its length; then the cluster copies the rows in
 // 16-byte pieces, COMMIT_PER loads of a thread in flight, and the length is
 // written behind a cluster barrier, since it may be the array that every CTA
@@ -38,7 +38,12 @@ __global__ void __launch_bounds__(COMMIT_THREADS) commit_kernel(const CommitLaun
   if (bits != 0) m = 0;
   for (int i = tid; i < m; i += COMMIT_THREADS) {
     if (idx != nullptr && (idx[i] < 0 || idx[i] >= n)) bits |= PRHS_DEV_BAD_INDEX;
-    if (kv_row(kv, b, 0, t + i) < 0) bits |= PRHS_DEV_BAD_BLOCK;
+    const long long row = kv_row(kv, b, 0, t + i);
+    const int slot = a.slots != nullptr ? a.slots[c0 + i] : 0;  // what planning gave to position t + i
+    int head_rows;
+    if (slot < 0) bits |= PRHS_DEV_CAPACITY;
+    else if (row < 0) bits |= PRHS_DEV_BAD_BLOCK;
+    else if (a.slots != nullptr && slot_row(kv, slot, &head_rows) != row) bits |= PRHS_DEV_BAD_INDEX;
   }
   if (bits != 0 && rank == 0) raise_error(kv.err, bits);
   if (__syncthreads_or((int)bits)) m = 0;

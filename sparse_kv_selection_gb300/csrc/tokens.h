@@ -47,6 +47,7 @@ struct CommitLaunch {
   KVView kv;
   int T;
   const int32_t* cu_new;
+  const int32_t* slots;  // null: the block table alone says where the rows go
   const int32_t* accept_idx;
   int accept_cap;
   const int32_t* accept_n;

@@ -235,10 +235,10 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   return launched(e, "tree attention");
 }
 
-prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,
-                               const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
-                               const void* k_new, long long k_stride, const void* v_new,
-                               long long v_stride, int32_t* new_lens, cudaStream_t stream) {
+static prhs_status commit(const prhs_kv* kv, int T, const int32_t* cu_new, const int32_t* slots,
+                          const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
+                          const void* k_new, long long k_stride, const void* v_new,
+                          long long v_stride, int32_t* new_lens, cudaStream_t stream) {
   CommitLaunch a = {};
   int sms = 0;
   prhs_status s = abi_check_kv(kv);
@@ -254,6 +254,7 @@ prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,
   if ((s = begin(kv, T, &a.kv, &sms)) != PRHS_OK) return s;
   a.T = T;
   a.cu_new = cu_new;
+  a.slots = slots;
   a.accept_idx = accept_idx;
   a.accept_cap = accept_cap;
   a.accept_n = accept_n;
@@ -263,6 +264,23 @@ prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,
   a.vs = v_stride;
   a.new_lens = new_lens;
   return launched(launch_commit(a, sms, stream), "commit kernel");
+}
+
+prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,
+                               const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
+                               const void* k_new, long long k_stride, const void* v_new,
+                               long long v_stride, int32_t* new_lens, cudaStream_t stream) {
+  return commit(kv, T, cu_new, nullptr, accept_idx, accept_cap, accept_n, k_new, k_stride, v_new, v_stride, new_lens,
+                stream);
+}
+
+prhs_status prhs_commit_planned(const prhs_kv* kv, int T, const int32_t* cu_new, const int32_t* slots,
+                                const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
+                                const void* k_new, long long k_stride, const void* v_new,
+                                long long v_stride, int32_t* new_lens, cudaStream_t stream) {
+  if (!slots) return abi_fail(PRHS_EINVAL, "commit: slots must be non-null");
+  return commit(kv, T, cu_new, slots, accept_idx, accept_cap, accept_n, k_new, k_stride, v_new, v_stride, new_lens,
+                stream);
 }
 
 }  // extern "C"

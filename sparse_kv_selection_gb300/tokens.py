@@ -74,7 +74,8 @@ class TokenBatch:
 
     def commit(self, accept_n: torch.Tensor, accept_idx: torch.Tensor | None = None) -> None:
         """Add accept_n[b] tokens (numbers accept_idx[b], or the first ones) to
-        each sequence's cache and advance its length."""
+        each sequence's cache and advance its length. Sequences that plan refused
+        stay as they are, flagged, whatever accept_n says of them."""
         rows = {} if self._in_cache and accept_idx is None else dict(k_new=self.k, v_new=self.v)
-        _b.commit_tokens(self.kv, self.cu_new, accept_n, accept_idx=accept_idx,
-                         T=self.positions.numel(), stream=self.stream, **rows)
+        _b.commit_tokens(self.kv, self.cu_new, accept_n, slots=self.slots, accept_idx=accept_idx,
+                         stream=self.stream, **rows)

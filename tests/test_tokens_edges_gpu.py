@@ -46,3 +46,105 @@ def test_lengths_only_commit_looks_at_the_pages(entry):
     assert new.tolist() == [16, 764, 16] and c.kv.seq_lens.tolist() == [10, 700, 16]
 
 
+@pytest.mark.parametrize("stale", [False, True])
+def test_a_chunk_that_found_no_pages_is_not_committed(stale):
+    """Pages run out at sequence 1: it keeps its length although its positions were
+    offered, whatever its table row holds beyond its own pages; once there are pages
+    again its chunk goes through."""
+    import sparse_kv_selection_gb300 as S
+    from sparse_kv_selection_gb300.binding import DEV_CAPACITY
+    c = Cache([20, 30, 5], 4, 2, 64, BF16, page=16, room=80, seed=3)
+    if stale:                                      # an earlier occupant's pages, now sequence 0's
+        c.kv.block_table[1, 2:5] = int(c.table[0, 0])
+    free = i32(c.free[:3])
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=120, max_new=60, free_pages=free, n_pages=i32(c.n_pages))
+    n = [40, 40, 8]
+    q, k, v = rows_of(120, c, 1)
+    batch.plan(i32(n))
+    assert S.last_error() == DEV_CAPACITY
+    wk, wv = c.k.clone(), c.v.clone()
+    batch.rotate(q, k, v, append=True)
+    batch.attend()
+    batch.commit(i32(n))
+    assert S.last_error() == DEV_CAPACITY
+    assert c.kv.seq_lens.tolist() == [60, 30, 13]
+    for have, want in ((c.k, wk), (c.v, wv)):      # sequence 1's rows are as they were
+        for p in c.table[1, :2]:
+            assert same(have[int(p)], want[int(p)])
+    # three more pages
+    again = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=120, max_new=60, free_pages=i32(c.free[3:8]),
+                         n_pages=batch.pages["n_pages"])
+    again.plan(i32([0, 40, 0]))
+    again.rotate(q, k, v, append=True)
+    again.commit(i32([0, 40, 0]))
+    assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [60, 70, 13]
+    assert torch.equal(c.rows(1, 70)[1][:, 30:].transpose(0, 1), v[:40].double())
+
+
+def test_accepted_tokens_without_a_slot_stay_out_of_other_pages():
+    """Accepted tokens of a refused tree do not land in the pages that its table row
+    still names."""
+    import sparse_kv_selection_gb300 as S
+    from sparse_kv_selection_gb300.binding import DEV_CAPACITY
+    c = Cache([16, 40], 2, 1, 64, BF16, page=16, room=32, seed=4)
+    c.kv.block_table[0, 1:3] = i32(c.table[1, :2])  # sequence 1's pages
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=12, max_new=8, free_pages=i32([]), n_pages=i32(c.n_pages))
+    batch.plan(i32([6, 5]), i32([-1, 0, 1, 1, 0, 4, -1, 0, 1, 2, 3, -1]))
+    assert S.last_error() == DEV_CAPACITY
+    assert batch.slots[:6].tolist() == [-1] * 6 and (batch.slots[6:11] >= 0).all()
+    q, k, v = rows_of(12, c, 2)
+    batch.rotate(q, k, v)
+    batch.attend()
+    wk, wv = c.k.clone(), c.v.clone()
+    batch.commit(i32([3, 2]), i32([[0, 1, 3], [0, 1, 0]]))
+    assert S.last_error() == DEV_CAPACITY
+    assert c.kv.seq_lens.tolist() == [16, 42]
+    at = int(c.table[1, 2])
+    wk[at, 0, 8:10], wv[at, 0, 8:10] = batch.k[6:8, 0], v[6:8, 0]
+    assert same(c.k, wk) and same(c.v, wv)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("append", [False, True])
+def test_part_of_a_refused_chunk_is_not_committed(page, append):
+    """A chunk beyond t_max, and one cut by the batch's token count, have no slots;
+    accepting only as many tokens as would fit changes nothing."""
+    import sparse_kv_selection_gb300 as S
+    from sparse_kv_selection_gb300.binding import DEV_CAPACITY
+    c = Cache([60, 10, 20], 2, 1, 64, BF16, page=page, room=4, t_max=64, seed=5)
+    kw = {}
+    if page:                                       # every position is mapped, four pages a sequence
+        assert c.t_max == 64
+        c.kv.block_table[1, 1:], c.kv.block_table[2, 2:] = i32([12, 13, 14]), i32([15, 16])
+        c.k, c.v = [torch.randn(17, 1, 16, 64, device="cuda", dtype=BF16) for _ in range(2)]
+        c.kv = S.KVCache(c.k, c.v, c.kv.seq_lens, 2, block_table=c.kv.block_table)
+        kw = dict(free_pages=i32([]), n_pages=i32([4, 4, 4]))
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=14, max_new=8, **kw)
+    q, k, v = rows_of(14, c, 2)
+    batch.plan(i32([6, 5, 7]))                     # 66 positions; placed; cut
+    assert S.last_error() == DEV_CAPACITY
+    batch.rotate(q, k, v, append=append)
+    wk = c.k.clone()
+    batch.commit(i32([2, 5, 3]))
+    assert S.last_error() == DEV_CAPACITY
+    assert c.kv.seq_lens.tolist() == [60, 15, 20]
+    if append:
+        assert same(c.k, wk)
+    else:
+        assert (c.k.nan_to_num(99.0) != wk.nan_to_num(99.0)).any(-1).sum() == 5
+
+
+def test_a_plan_is_committed_once():
+    """The second commit of one plan finds slots that are not the next positions'."""
+    import sparse_kv_selection_gb300 as S
+    from sparse_kv_selection_gb300.binding import DEV_BAD_INDEX
+    c = Cache([20, 7], 2, 1, 64, BF16, page=16, room=40, seed=6)
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=13, max_new=8, free_pages=i32(c.free), n_pages=i32(c.n_pages))
+    batch.plan(i32([8, 4]))
+    batch.rotate(*rows_of(13, c, 2), append=True)
+    batch.commit(i32([4, 0]))
+    assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [24, 7]
+    batch.commit(i32([4, 4]))
+    assert S.last_error() == DEV_BAD_INDEX and c.kv.seq_lens.tolist() == [24, 11]
+
+
