@@ -18,11 +18,16 @@ from . import binding as _b
 
 class TokenBatch:
     def __init__(self, kv: _b.KVCache, rope: _b.RopeTable, *, max_tokens: int, max_new: int,
-                 free_pages=None, n_pages=None, scale: float | None = None, stream=None):
+                 free_pages=None, n_pages=None, free_head=None, scale: float | None = None, stream=None):
         """max_tokens packed tokens at most (padding included), max_new of one
         sequence. A paged cache needs free_pages (int32, the pages that no
-        sequence holds) and n_pages (int32 [B], the pages each row of its block
-        table holds)."""
+        sequence holds), n_pages (int32 [B], the pages each row of its block
+        table holds) and free_head (int32 [1], how many of free_pages have been
+        taken; zero when left out). plan updates free_head and n_pages in place:
+        batches on one cache share all three, TokenBatch(..., **other.pages). A
+        sequence that ends gives its p pages back in front of the free ones
+        (free_head -= p, then free_pages[free_head : free_head + p] = them) and has
+        its n_pages and its length set to 0."""
         dev, B, d = kv.k.device, kv.B, kv.desc.d
         self.kv, self.rope, self.stream = kv, rope, stream
         self.max_new = int(max_new)
@@ -39,7 +44,7 @@ class TokenBatch:
             if free_pages is None or n_pages is None:
                 raise ValueError("a paged cache needs free_pages and n_pages")
             self.pages = dict(free_pages=free_pages, n_pages=n_pages,
-                              free_head=torch.zeros(1, **i32))
+                              free_head=torch.zeros(1, **i32) if free_head is None else free_head)
         self.q = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
         self.k = torch.zeros(T, kv.desc.Hkv, d, device=dev, dtype=kv.k.dtype)
         self.v = None

@@ -148,3 +148,54 @@ def test_a_plan_is_committed_once():
     assert S.last_error() == DEV_BAD_INDEX and c.kv.seq_lens.tolist() == [24, 11]
 
 
+# --------------------------------------------------------------------------- #
+# batches that share a cache
+# --------------------------------------------------------------------------- #
+def test_two_batches_hand_out_different_pages():
+    """A batch for prompts and one for drafts on one cache take pages from one list."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([20, 30], 2, 1, 64, BF16, page=16, room=200, seed=7)
+    state = dict(free_pages=i32(c.free), n_pages=i32(c.n_pages), free_head=i32([0]))
+    prompts = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=100, max_new=90, **state)
+    drafts = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=20, max_new=10, **prompts.pages)
+    for step in range(3):
+        for batch, n in ((prompts, [30, 0]), (drafts, [4, 9]), (prompts, [0, 17])):
+            batch.plan(i32(n))
+            batch.rotate(*rows_of(batch.positions.numel(), c, step), append=True)
+            batch.commit(i32(n))
+    assert S.last_error() == 0
+    assert c.kv.seq_lens.tolist() == [20 + 3 * 34, 30 + 3 * 26]
+    held = c.kv.block_table.cpu().numpy()
+    pages = [int(held[b, i]) for b, t in enumerate(c.kv.seq_lens.tolist()) for i in range(-(-t // 16))]
+    assert len(set(pages)) == len(pages)
+    assert int(state["free_head"][0]) == len(pages) - sum(c.n_pages)
+
+
+def test_pages_of_a_sequence_that_ends_are_handed_out_again():
+    """Given back in front of the free ones, between two steps, without the host
+    reading a counter; what the sequence's table row still names is not used."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([0, 0], 2, 1, 64, BF16, page=16, room=48, seed=7)
+    free = i32(c.free[:5])
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=48, max_new=48, free_pages=free, n_pages=i32(c.n_pages))
+
+    def feed(n):
+        batch.plan(i32(n))
+        batch.rotate(*rows_of(48, c, sum(n)), append=True)
+        batch.commit(i32(n))
+
+    feed([40, 0])
+    feed([0, 20])
+    assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [40, 20]
+    head, n_pages = batch.pages["free_head"], batch.pages["n_pages"]
+    head -= n_pages[0]
+    free[head.long() + torch.arange(3, device="cuda")] = c.kv.block_table[0, :3]
+    n_pages[0] = 0
+    c.kv.seq_lens[0] = 0
+    feed([0, 28])                                  # one page more
+    feed([30, 0])                                  # two
+    assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [30, 48]
+    table = c.kv.block_table.tolist()
+    assert sorted(table[1][:3] + table[0][:2]) == sorted(c.free[:5].tolist())
+
+
