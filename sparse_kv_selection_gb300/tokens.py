@@ -73,7 +73,9 @@ class TokenBatch:
 
     def attend(self, out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> None:
         """Attention of the new tokens into out and lse (the batch's own by default)."""
-        _b.tree_attn(self.kv, self.q, self.k, self.v, self.scale, self.cu_new, self.max_new,
+        tree = self.tree_mask is not None     # (planning refuses trees above TREE_MAX tokens)
+        _b.tree_attn(self.kv, self.q, self.k, self.v, self.scale, self.cu_new,
+                     min(self.max_new, _b.TREE_MAX) if tree else self.max_new,
                      self.out if out is None else out, self.lse if lse is None else lse, self.ws,
                      tree_mask=self.tree_mask, stream=self.stream)
 

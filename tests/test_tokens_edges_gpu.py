@@ -199,3 +199,24 @@ def test_pages_of_a_sequence_that_ends_are_handed_out_again():
     assert sorted(table[1][:3] + table[0][:2]) == sorted(c.free[:5].tolist())
 
 
+def test_a_tree_through_a_batch_for_prompts():
+    """max_new above the largest tree: one batch serves prompts and trees."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([0, 40], 4, 2, 64, BF16, t_max=900, seed=8)
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=710, max_new=700)
+    small = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=710, max_new=128)
+    q, k, v = rows_of(710, c, 1)
+    batch.plan(i32([700, 9]))
+    batch.rotate(q, k, v, append=True)
+    batch.attend()
+    batch.commit(i32([700, 9]))
+    assert S.last_error() == 0
+    parents = i32(list(range(-1, 127)) + [-1, 0, 0, 1] + [-1] * 578)
+    for x in (batch, small):
+        x.plan(i32([128, 4]), parents)
+        x.rotate(q, k, v)
+        x.attend()
+    assert S.last_error() == 0
+    assert torch.equal(batch.out[:132], small.out[:132]) and torch.equal(batch.lse[:132], small.lse[:132])
+
+
