@@ -57,6 +57,7 @@ class TokenBatch:
         """Place n_new[b] tokens behind each sequence's cached prefix. parents
         ([max_tokens] int32, packed) makes them trees; without, they are chunks."""
         self.tree_mask = None if parents is None else self._mask
+        self.v, self._in_cache = None, False     # rows of an earlier plan are not this one's
         _b.plan_tokens(self.kv, n_new, self.cu_new, self.positions, self.slots, parents=parents,
                        tree_mask=self.tree_mask, stream=self.stream, **self.pages)
 

@@ -220,3 +220,17 @@ def test_a_tree_through_a_batch_for_prompts():
     assert torch.equal(batch.out[:132], small.out[:132]) and torch.equal(batch.lse[:132], small.lse[:132])
 
 
+def test_a_new_plan_forgets_the_rotated_rows():
+    """Nothing is committed of a plan whose tokens were not rotated."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([20], 2, 1, 64, BF16, t_max=64, seed=9)
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=8, max_new=8)
+    batch.plan(i32([8]))
+    batch.rotate(*rows_of(8, c, 1), append=True)
+    batch.commit(i32([8]))
+    batch.plan(i32([8]))
+    with pytest.raises(ValueError):
+        batch.commit(i32([8]))
+    assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [28]
+
+
