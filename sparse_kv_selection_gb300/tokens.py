@@ -16,6 +16,14 @@ import torch
 from . import binding as _b
 
 
+def _own_stream(stream, device):
+    """The stream object of a handle (None: the current stream)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 class TokenBatch:
     def __init__(self, kv: _b.KVCache, rope: _b.RopeTable, *, max_tokens: int, max_new: int,
                  free_pages=None, n_pages=None, free_head=None, scale: float | None = None, stream=None):
@@ -32,25 +40,27 @@ class TokenBatch:
         self.kv, self.rope, self.stream = kv, rope, stream
         self.max_new = int(max_new)
         self.scale = scale if scale is not None else d ** -0.5
-        i32 = dict(device=dev, dtype=torch.int32)
-        T = int(max_tokens)
-        self.cu_new = torch.zeros(B + 1, **i32)
-        self.positions = torch.zeros(T, **i32)
-        self.slots = torch.full((T,), -1, **i32)
-        self._mask = torch.zeros(T, _b.TREE_WORDS, **i32)
-        self.tree_mask = None
-        self.pages = {}
-        if kv.block_table is not None:
-            if free_pages is None or n_pages is None:
-                raise ValueError("a paged cache needs free_pages and n_pages")
-            self.pages = dict(free_pages=free_pages, n_pages=n_pages,
-                              free_head=torch.zeros(1, **i32) if free_head is None else free_head)
-        self.q = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
-        self.k = torch.zeros(T, kv.desc.Hkv, d, device=dev, dtype=kv.k.dtype)
-        self.v = None
-        self.out = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
-        self.lse = torch.zeros(T, kv.Hq, device=dev, dtype=torch.float32)
-        self.ws = _b.make_tree_workspace(kv, self.max_new)
+        # on the batch's own stream: it may run a step before this one gets to the fills
+        with torch.cuda.stream(_own_stream(stream, dev)):
+            i32 = dict(device=dev, dtype=torch.int32)
+            T = int(max_tokens)
+            self.cu_new = torch.zeros(B + 1, **i32)
+            self.positions = torch.zeros(T, **i32)
+            self.slots = torch.full((T,), -1, **i32)
+            self._mask = torch.zeros(T, _b.TREE_WORDS, **i32)
+            self.tree_mask = None
+            self.pages = {}
+            if kv.block_table is not None:
+                if free_pages is None or n_pages is None:
+                    raise ValueError("a paged cache needs free_pages and n_pages")
+                self.pages = dict(free_pages=free_pages, n_pages=n_pages,
+                                  free_head=torch.zeros(1, **i32) if free_head is None else free_head)
+            self.q = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
+            self.k = torch.zeros(T, kv.desc.Hkv, d, device=dev, dtype=kv.k.dtype)
+            self.v = None
+            self.out = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
+            self.lse = torch.zeros(T, kv.Hq, device=dev, dtype=torch.float32)
+            self.ws = _b.make_tree_workspace(kv, self.max_new)
         self._in_cache = False
 
     def plan(self, n_new: torch.Tensor, parents: torch.Tensor | None = None) -> None:

@@ -234,3 +234,23 @@ def test_a_new_plan_forgets_the_rotated_rows():
     assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [28]
 
 
+def test_a_batch_made_for_another_stream():
+    """The batch's buffers are set on its own stream: a busy current stream does not
+    set them after they have been used."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([20, 30], 2, 1, 64, BF16, page=16, room=40, seed=7)
+    s = torch.cuda.Stream()
+    rope, n, free, n_pages = S.RopeTable(64), i32([17, 3]), i32(c.free), i32(c.n_pages)
+    for handle in (s, s.cuda_stream):
+        want_lens = c.kv.seq_lens.tolist()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)             # the current stream is busy for about 0.1 s
+        batch = S.TokenBatch(c.kv, rope, max_tokens=20, max_new=17, free_pages=free, n_pages=n_pages, stream=handle)
+        batch.plan(n)
+        torch.cuda.synchronize()
+        assert S.last_error() == 0
+        assert batch.positions.tolist() == list(range(20, 37)) + list(range(30, 33))
+        assert batch.cu_new.tolist() == [0, 17, 20] and (batch.slots >= 0).all()
+        assert c.kv.seq_lens.tolist() == want_lens
+
+
