@@ -381,7 +381,8 @@ size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new);
  * tree_mask row ([T][PRHS_TREE_WORDS] uint32; bits at or above n_b are ignored),
  * or tokens 0 .. j where tree_mask is null (a causal chunk of any length):
  *   lse = log sum exp(s),  out = sum exp(s - lse) v,  s = scale * <q, k>
- * over the attended keys; out = 0 and lse = -inf where there are none.
+ * over the attended keys; out = 0 and lse = -inf where there are none, NaN where q
+ * or an attended key has NaN.
  * out [T][Hq][d] has the cache's element type, lse [T][Hq] is fp32. Sums are
  * fp32. On an fp32 cache so are the weights exp(s - m); on a bf16 cache each weight
  * is rounded to bf16 (by up to 2^-8 of it) before its product with v, beside the

@@ -34,7 +34,6 @@ namespace prhs {
 constexpr int TK = 32;            // keys of a tile: a word of a tree mask
 constexpr int FOLD = 32;          // tiles summed one by one
 constexpr float T_LOG2E = 1.4426950408889634f;
-constexpr float T_LN2 = 0.6931471805599453f;
 
 // A tile of a CTA's run.
 struct __align__(16) TreeStep {
@@ -393,10 +392,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
 #pragma unroll
       for (int d = TX / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, d));
       const float corr = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mx);
+      // (maxima drop NaN: a row of nothing else has -inf, and its weights must be NaN)
+      const float ref = mx == -INFINITY ? 0.f : mx;
       float sum = 0.f;
 #pragma unroll
       for (int k = 0; k < KT; k++) {
-        const float w = mx == -INFINITY ? 0.f : exp2f(s[k] - mx);
+        const float w = exp2f(s[k] - ref);
         sum += w;
         sp[(ty + TY * i) * LP + tx + TX * k] = w;
       }
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
       __syncwarp();  // (read by all lanes of the row before one overwrites it)
       if (r >= rows) continue;
       const long long orow = (x.c0 + ((row0 + r) >> gl)) * kv.Hq + (x.kvh << gl) + (r & ((1 << gl) - 1));
-      const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = whole ? tree_inv(sum) : 1.f;
       float* dst = (whole ? static_cast<float*>(a.out) + orow * D : reinterpret_cast<float*>(p.o) + (rec + r) * D) + tx * 4;
 #pragma unroll
       for (int c = 0; c < C4; c++) {
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
         *reinterpret_cast<float4*>(dst + c * TX * 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       }
       if (tx == 0) {
-        if (whole) a.lse[orow] = sum > 0.f ? (m[i] + log2f(sum)) * T_LN2 : -INFINITY;
+        if (whole) a.lse[orow] = tree_lse(m[i], sum);
         else p.ml[rec + r] = make_float2(m[i], sum);
       }
       if (last) continue;

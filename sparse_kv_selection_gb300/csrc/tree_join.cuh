@@ -31,6 +31,14 @@ struct TreeRecords {
 // Bound: L2 and latency.
 constexpr int JOIN_THREADS = 256, JOIN_CH = 4;  // (records in flight)
 
+// Results of a row from its maximum M (base 2) and sum L: 0 and -inf where it attends
+// nothing (L = 0); NaN in the query or an attended key makes L and O NaN, and M what
+// the other keys leave.
+__device__ __forceinline__ float tree_inv(float L) { return L == 0.f ? 0.f : 1.f / L; }
+__device__ __forceinline__ float tree_lse(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
 // Weight of a state with maximum x against m (0 where it has nothing in it).
 __device__ __forceinline__ float tree_weight(float x, float m) { return x == -INFINITY ? 0.f : exp2f(x - m); }
 __device__ __forceinline__ void tree_fma(float4& o, float w, float4 x) {
@@ -108,10 +116,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const __grid_co
     }
     if (i0 + in >= total) continue;
     const int gl = p.group_log2;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = tree_inv(L);
     const long long orow = (long long)(s.tok + (row >> gl)) * a.kv.Hq + (s.kvh << gl) + (row & ((1 << gl) - 1));
     tree_put(static_cast<T*>(a.out) + orow * D + c * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (c == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (c == 0) a.lse[orow] = tree_lse(M, L);
   }
 }
 

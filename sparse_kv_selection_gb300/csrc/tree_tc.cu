@@ -61,7 +61,6 @@ static_assert(2 * TC_REGS_SOFTMAX + TC_REGS_REST <= 3 * TC_REGS_LAUNCH, "registe
 constexpr int TC_THREADS = TC_WARPS * 32;
 constexpr int TC_AUX = 3 << 10;          // bytes of shared memory beside the tiles
 constexpr float TC_LOG2E = 1.4426950408889634f;
-constexpr float TC_LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr int QUAD_ROWS = 32;
 constexpr int UNCUT_TILES = 12;  // the most tiles of a unit in a list that is not cut
@@ -871,7 +870,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       tc_fence_after();
       const bool live = ur < w.rows && !dead;
       if (w.whole) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = tree_inv(L);
         w0 *= inv;
         w1 *= inv;
       }
@@ -931,7 +930,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
       }
       if (live && (!both || st == 0)) {
-        if (w.whole) a.lse[out_row(ur)] = L > 0.f ? (M + log2f(L)) * TC_LN2 : -INFINITY;
+        if (w.whole) a.lse[out_row(ur)] = tree_lse(M, L);
         else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();

@@ -254,3 +254,46 @@ def test_a_batch_made_for_another_stream():
         assert c.kv.seq_lens.tolist() == want_lens
 
 
+# --------------------------------------------------------------------------- #
+# attention
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 128), (F32, 64)])
+@pytest.mark.parametrize("Hq,Hkv,n,t", [(2, 2, 3, 60), (8, 1, 30, 300), (4, 4, 20, 9000), (2, 1, 1, 20000), (8, 2, 3, 0)])
+def test_nan_reaches_the_rows_that_attend_it(dtype, d, Hq, Hkv, n, t):
+    """A query with NaN in it has NaN for its output and its log-sum-exp, whether its
+    keys are split over CTAs or not, and no other row has; a NaN key of an
+    unattended token changes nothing."""
+    import sparse_kv_selection_gb300 as S
+    c = Cache([t, 40], Hq, Hkv, d, dtype, page=16, room=1, seed=3)
+    T = n + 2
+    q, k, v = rows_of(T, c, 1)
+    mask = torch.zeros(T, 4, dtype=torch.int32, device="cuda")
+    for j in range(n):                             # each sees itself and the first
+        mask[j, 0] = 1 | (1 << j)
+    mask[n, 0] = 1                                 # sequence 1: the second token sees only itself
+    mask[n + 1, 0] = 2
+    cu, ws = i32([0, n, T]), S.make_tree_workspace(c.kv, n + 2)
+
+    def attend(q, k):
+        out, lse = torch.full_like(q, 3.0), torch.full((T, Hq), 3.0, device="cuda")
+        S.tree_attn(c.kv, q, k, v, d ** -0.5, cu, n + 2, out, lse, ws, tree_mask=mask)
+        assert S.last_error() == 0
+        return out, lse
+
+    want, wl = attend(q, k)
+    bad = torch.zeros(T, Hq, dtype=torch.bool, device="cuda")
+    bad[n - 1, Hq - 1] = True
+    q2 = q.clone()
+    q2[n - 1, Hq - 1, d // 2] = float("nan")
+    out, lse = attend(q2, k)
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
+    k2 = k.clone()
+    k2[n + 1, :, 1] = float("nan")                 # only its own rows attend it
+    bad[:] = False
+    bad[n + 1] = True
+    out, lse = attend(q, k2)
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
+
+
