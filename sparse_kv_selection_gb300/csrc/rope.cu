@@ -4,8 +4,10 @@
 // c and s the cosine and sine of position * theta. The angle is taken in turns
 // as a 64-bit binary fraction: position * turns modulo 2^64 wraps exactly where
 // the angle does, so it is as exact at position 2^31 as at 1, without float64
-// (whose rate is low on this part) and without a range reduction. Its top 32
-// bits, read as a signed number, are the angle in [-1/2, 1/2) turns to 2^-33.
+// (whose rate is low on this part). The nearest quarter turn is taken off in
+// integers and the rest, in [-1/8, 1/8) turns to 2^-34, goes to fp32, so that what the
+// conversion rounds is relative to the rest: sine and cosine keep their last bits near
+// their zeros too. (The whole angle in fp32 is 2^-25 of a half turn off.)
 //
 // Every head of a token takes the same rot_dim / 2 angles, so a CTA computes
 // them once into shared memory, with the tokens' cache rows. The work is cut
@@ -91,11 +93,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, PER == 1 ? 1 : 12)
   for (int i = threadIdx.x; i < tokens * half; i += ROPE_THREADS) {
     const int k = i / half, f = i - k * half;
     const uint64_t turn = (uint64_t)(int64_t)a.positions[tok0 + k] * a.turns[f];
-    // half turns in [-1, 1)
-    const float ht = (float)(int32_t)(turn >> 32) * 0x1p-31f;
+    const unsigned quarter = (unsigned)((turn + (1ull << 61)) >> 62);
+    const int32_t rest = (int32_t)((int64_t)(turn - ((uint64_t)quarter << 62)) >> 30);  // 2^-34 turns
     float s, c;
-    sincospif(ht, &s, &c);
-    cs[i] = make_float2(c * a.mscale, s * a.mscale);
+    sincospif((float)rest * 0x1p-33f, &s, &c);
+    float2 r = quarter & 1 ? make_float2(-s, c) : make_float2(c, s);
+    if (quarter & 2) r = make_float2(-r.x, -r.y);
+    cs[i] = make_float2(r.x * a.mscale, r.y * a.mscale);
   }
   for (int k = threadIdx.x; k < tokens; k += ROPE_THREADS) {
     long long row = 0;

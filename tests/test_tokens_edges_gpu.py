@@ -297,3 +297,37 @@ def test_nan_reaches_the_rows_that_attend_it(dtype, d, Hq, Hkv, n, t):
     assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
 
 
+# --------------------------------------------------------------------------- #
+# rotary angles
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_sine_and_cosine_near_their_zeros(interleaved):
+    """Pairs (1, 0) become (cos, sin) exactly, so fp32 results show the angle's own
+    error. The angle is folded to the nearest quarter turn as integers and keeps 34
+    bits behind the point: 2 pi 2^-34; its conversion to fp32 is off by 2^-24 of it
+    and sine or cosine by two units of the last place, 5 * 2^-24 of the value."""
+    import sparse_kv_selection_gb300 as S
+    d, T = 128, 4096
+    c = Cache([3], 1, 1, d, F32, t_max=8, seed=1)
+    rope = S.RopeTable(d, interleaved=interleaved)
+    positions = np.random.default_rng(5).integers(0, 1 << 20, T)
+    q = torch.zeros(T, 1, d, device="cuda")
+    q[..., 0::2] = 1.0 if interleaved else 0.0
+    if not interleaved:
+        q[..., :d // 2] = 1.0
+    got, k = torch.empty_like(q), torch.zeros(T, 1, d, device="cuda")
+    S.rope_append(c.kv, rope, i32(positions), q, k, None, got)
+    assert S.last_error() == 0
+    got = got[:, 0].double().cpu().numpy()
+    cos, sin = (got[:, 0::2], got[:, 1::2]) if interleaved else (got[:, :d // 2], got[:, d // 2:])
+    turn = positions.astype(np.uint64)[:, None] * rope.turns.cpu().numpy().astype(np.uint64)[None]   # modulo 2^64
+    quarter = (turn + np.uint64(1 << 61)) >> np.uint64(62)
+    rest = (turn - (quarter << np.uint64(62))).astype(np.int64).astype(np.float64) * (2 * np.pi * 2.0 ** -64)
+    s, z = np.sin(rest), np.cos(rest)
+    quarter = (quarter & np.uint64(3)).astype(int)
+    want_cos, want_sin = np.choose(quarter, [z, -s, -z, s]), np.choose(quarter, [s, z, -s, -z])
+    assert (np.abs(want_sin) < 2.0 ** -9).sum() > 100 and (np.abs(want_cos) < 2.0 ** -9).sum() > 100
+    for x, w in ((cos, want_cos), (sin, want_sin)):
+        assert (np.abs(x - w) <= 5 * 2.0 ** -24 * np.abs(w) + 2 * np.pi * 2.0 ** -34).all()
+
+
