@@ -392,8 +392,9 @@ size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new);
  * sequence's tokens must be finite: the product takes those that a token does not
  * attend with weight 0. Rows of padding tokens are left as they are.
  * max_new bounds the tokens of any sequence, at most PRHS_TREE_MAX with
- * tree_mask; a sequence with more, or with cu_new not ascending within [0, T],
- * is flagged (PRHS_DEV_BAD_LEN) and its rows are left as they are. Keys on a
+ * tree_mask; a sequence with more, or not within [0, T], is flagged
+ * (PRHS_DEV_BAD_LEN) and its rows are left as they are; where cu_new steps back
+ * anywhere, all rows are. Keys on a
  * page outside the pool are flagged (PRHS_DEV_BAD_BLOCK) and not attended. Rows
  * of the cache at or beyond t_b are not used, whatever they hold. */
 prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,

@@ -147,7 +147,11 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (kv.B + THREADS - 1) / THREADS, b0 = tid * per_t;
   long long mine = 0;
-  for (int b = b0; b < min(kv.B, b0 + per_t); b++) mine += kv.Hkv * tree_seq(a, b, ul).tiles;
+  bool back = false;  // offsets that step back: sequences would overlap, without bound
+  for (int b = b0; b < min(kv.B, b0 + per_t); b++) {
+    mine += kv.Hkv * tree_seq(a, b, ul).tiles;
+    back |= a.cu_new[b + 1] < a.cu_new[b];
+  }
   long long run = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     if (lane >= o) run += y;
   }
   if (lane == 31) wsum[warp] = run;
-  __syncthreads();
+  back = __syncthreads_or(back);  // (flagged by tree_seq)
   long long total = 0, before = run - mine;
 #pragma unroll
   for (int w = 0; w < W; w++) {
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   }
   const long long per = (total + gridDim.x - 1) / gridDim.x, g0 = blockIdx.x * per;
   const int count = (int)(min(total, g0 + per) - g0);  // negative: none are left
-  if (count <= 0) {
+  if (count <= 0 || back) {
     if (tid == 0) p.split[blockIdx.x] = TreeSplit{};
     return;
   }

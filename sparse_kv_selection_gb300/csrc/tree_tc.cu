@@ -364,8 +364,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (B + TC_THREADS - 1) / TC_THREADS, b0 = tid * per_t;
   int mine = 0, most = 0;  // tiles of this thread's sequences, of their largest unit
+  bool back = false;       // offsets that step back: sequences would overlap, and counts pass 32 bits
   for (int b = b0; b < min(B, b0 + per_t); b++) {
     const TcSeq s = tc_seq(a, b, ul);
+    back |= a.cu_new[b + 1] < a.cu_new[b];
     mine += kv.Hkv * s.tiles;
     if (s.blocks > 0) most = max(most, tc_unit_tiles(s, s.blocks - 1, ul, a.mask == nullptr));
   }
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     aux.wsum[warp] = run;
     aux.wmax[warp] = most;
   }
-  __syncthreads();
+  if (__syncthreads_or(back)) return;  // (flagged above)
   int total = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < TC_WARPS; w++) {

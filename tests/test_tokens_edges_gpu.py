@@ -297,6 +297,26 @@ def test_nan_reaches_the_rows_that_attend_it(dtype, d, Hq, Hkv, n, t):
     assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_that_step_back(dtype):
+    """Offsets that go back and forth give every second sequence all tokens, more key
+    tiles than 32 bits count although the call's own sizes are small: the call is
+    flagged and writes nothing."""
+    import sparse_kv_selection_gb300 as S
+    from sparse_kv_selection_gb300.binding import DEV_BAD_LEN
+    B, T, Hq, Hkv, d, page, blocks = 256, 8192, 64, 8, 64, 4096, 256
+    tiles, units = page * blocks // 128, T * (Hq // Hkv) // 256
+    assert (units + B) * Hkv * (tiles + T // 128 + 2) < 1 << 31 <= B // 2 * Hkv * units * tiles
+    pool = torch.zeros(1, Hkv, page, d, device="cuda", dtype=dtype)
+    kv = S.KVCache(pool, pool.clone(), i32([page * blocks] * B), Hq,
+                   block_table=torch.zeros(B, blocks, dtype=torch.int32, device="cuda"))
+    q, k = torch.zeros(T, Hq, d, device="cuda", dtype=dtype), torch.zeros(T, Hkv, d, device="cuda", dtype=dtype)
+    out, lse = torch.full_like(q, 3.0), torch.full((T, Hq), 3.0, device="cuda")
+    S.tree_attn(kv, q, k, k, 0.125, i32([0, T] * (B // 2) + [0]), T, out, lse, S.make_tree_workspace(kv, T))
+    assert S.last_error() == DEV_BAD_LEN
+    assert (out == 3.0).all() and (lse == 3.0).all()
+
+
 # --------------------------------------------------------------------------- #
 # rotary angles
 # --------------------------------------------------------------------------- #
