@@ -259,8 +259,19 @@ __device__ __forceinline__ void quad_swap(uint32_t (&x)[4], uint32_t (&y)[4]) {
     y[k] = up ? y[k] : z;
   }
 }
-__device__ __forceinline__ void named_bar(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+
+// The softmax warps meet: true where all of them are about to leave. A warp that has
+// left its units (at the run's end, or early because a wait gave up) meets the others
+// until that is so, so that none of them waits here for one that is gone.
+__device__ __forceinline__ bool softmax_meet(bool leaving) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)leaving), "n"(2 * TT)
+      : "memory");
+  return r != 0;
 }
 
 // -------------------------------------------------------------------------- //
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const int nt = min(tiles - off, left);
         left -= nt;
         const int i = k & (TC_WORKS - 1);
-        if (!mbar_wait(&bar.wempty[i], ((k / TC_WORKS) & 1) ^ 1, kv.err)) break;
+        if (!__all_sync(FULL_MASK, mbar_wait(&bar.wempty[i], ((k / TC_WORKS) & 1) ^ 1, kv.err))) break;
         const int rows = min(UNIT_ROWS, (s.n - (block << ul)) << gl);
         if (lane == 0) {
           TcWork& w = aux.work[i];
@@ -862,7 +873,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         aux.m[st][row] = m;
         aux.l[st][row] = l;
         tc_fence_before();
-        named_bar(1, 2 * TT);
+        softmax_meet(false);
         const float m0 = aux.m[0][row], m1 = aux.m[1][row];
         M = fmaxf(m0, m1);
         w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
@@ -936,7 +947,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();
-      if (both) named_bar(1, 2 * TT);  // both outputs and the row states are read
+      if (both) softmax_meet(false);  // both outputs and the row states are read
+    }
+    while (!softmax_meet(true)) {
     }
   }
   __syncthreads();
