@@ -317,6 +317,88 @@ def test_offsets_that_step_back(dtype):
     assert (out == 3.0).all() and (lse == 3.0).all()
 
 
+def tiles_a_run(c, n):
+    """Key tiles of 128 that a CTA takes, of how many a unit has (units of 256 rows, one a KV head here)."""
+    import sparse_kv_selection_gb300 as S
+    assert max(n) * (c.Hq // c.Hkv) <= 256
+    unit = [-(-t // 128) + -(-x // 128) for t, x in zip(c.lens, n)]
+    return -(-c.Hkv * sum(unit) // S.num_sms()), max(unit)
+
+
+def check_rows(c, q, k, v, n, out, lse):
+    """Causal results of every sequence against float64."""
+    scale = c.d ** -0.5
+    lo = 0
+    for b, x in enumerate(n):
+        r = slice(lo, lo + x)
+        kc, vc = c.rows(b, c.lens[b])
+        see = torch.ones(x, x, dtype=torch.bool, device="cuda").tril()
+        wo, wl, eo, el = attn_ref(q[r].double(), kc, vc, k[r].double(), v[r].double(), see, scale, c.d, c.dtype)
+        assert ((out[r].double() - wo).abs() <= eo).all(), (b, ((out[r].double() - wo).abs() / eo).max().item())
+        assert ((lse[r].double() - wl).abs() <= el).all(), b
+        lo += x
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("B,Hkv,G,n", [(4, 16, 1, 3), (4, 16, 8, 1), (2, 32, 2, 60), (4, 16, 8, 20), (4, 16, 1, 200)])
+@pytest.mark.parametrize("top", [400, 90, 40, -300])
+def test_maximum_that_grows_along_a_run(d, B, Hkv, G, n, top):
+    """Runs of more than four tiles of one unit, so that a stream's output is
+    rescaled while it is summed: the maximum moves by 37, 8, 4 and -28 (base 2) a
+    tile, with one row tile (streams on every second tile) and with two."""
+    import sparse_kv_selection_gb300 as S
+    t = 2000
+    c = Cache([t] * B, G * Hkv, Hkv, d, BF16, seed=3)
+    run, unit = tiles_a_run(c, [n] * B)
+    assert 4 < run and 12 < unit                   # (units of up to 12 tiles are not cut)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    # queries of ones on key rows of a constant: logits rise by `top` over the cache
+    ramp = torch.linspace(0, top, t, device="cuda")[None, None, :, None] / d ** 0.5
+    c.k[:, :, :t] = (ramp + torch.randn(B, Hkv, t, d, generator=g, device="cuda") * 0.1).to(BF16)
+    q = torch.ones(B * n, G * Hkv, d, device="cuda", dtype=BF16)
+    k, v = torch.randn(2, B * n, Hkv, d, generator=g, device="cuda").to(BF16)
+    out, lse = torch.empty_like(q), torch.empty(B * n, G * Hkv, device="cuda")
+    S.tree_attn(c.kv, q, k, v, d ** -0.5, i32(np.arange(B + 1) * n), n, out, lse, S.make_tree_workspace(c.kv, n))
+    assert S.last_error() == 0
+    check_rows(c, q, k, v, [n] * B, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page", [0, 16, 32, 64, 128, 48])
+@pytest.mark.parametrize("G,n", [(1, 2), (8, 20)])
+def test_every_value_row_counts_on_long_runs(dtype, page, G, n):
+    """Runs of more than 32 tiles of one unit, past every window of page numbers. A
+    value row is one in the column of its 16-key group (modulo 61) and zero
+    elsewhere, so that each column is the weight of few groups, and a group that is
+    lost or taken from another place shows in full."""
+    import sparse_kv_selection_gb300 as S
+    B, Hkv, d, t = 20, 8, 64, 5100
+    c = Cache([t] * B, G * Hkv, Hkv, d, dtype, page=page, room=1, seed=4)
+    run, unit = tiles_a_run(c, [n] * B)
+    assert run > 32 and unit > 32
+    col = (torch.arange(t, device="cuda") // 16) % 61
+    rows = torch.nn.functional.one_hot(col, d).to(dtype)[:, None].expand(t, Hkv, d)
+    for b in range(B):
+        c.set_rows(b, 0, c.rows(b, t)[0].transpose(0, 1).to(dtype), rows)
+    q, k, v = rows_of(B * n, c, 1)
+    q *= 0.5
+    v.zero_()
+    out, lse = torch.empty_like(q), torch.empty(B * n, G * Hkv, device="cuda")
+    S.tree_attn(c.kv, q, k, v, d ** -0.5, i32(np.arange(B + 1) * n), n, out, lse, S.make_tree_workspace(c.kv, n))
+    assert S.last_error() == 0
+    check_rows(c, q, k, v, [n] * B, out, lse)
+    # the bound sees a tile or a 16-key group of V that comes from elsewhere
+    kc, vc = c.rows(0, t)
+    see = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    wo, _, eo, _ = attn_ref(q[:n].double(), kc, vc, k[:n].double(), v[:n].double(), see, d ** -0.5, d, dtype)
+    for to, frm, size in ((4096, 0, 128), (512, 0, 16), (4224, 4096, 128), (4992, 4480, 16)):
+        wrong = vc.clone()
+        wrong[:, to:to + size] = vc[:, frm:frm + size]
+        bad = attn_ref(q[:n].double(), kc, wrong, k[:n].double(), v[:n].double(), see, d ** -0.5, d, dtype)[0]
+        assert ((bad - wo).abs() > 4 * eo).any(-1).all(), (to, frm)
+
+
 # --------------------------------------------------------------------------- #
 # rotary angles
 # --------------------------------------------------------------------------- #
