@@ -1,6 +1,10 @@
 """Token batches at the edges of their contract: sequences that planning refused,
 page state that batches share, NaN, angles near quarter turns, long runs of key
 tiles."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -10,6 +14,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 BF16, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def i32(a):
@@ -433,3 +438,92 @@ def test_sine_and_cosine_near_their_zeros(interleaved):
         assert (np.abs(x - w) <= 5 * 2.0 ** -24 * np.abs(w) + 2 * np.pi * 2.0 ** -34).all()
 
 
+# --------------------------------------------------------------------------- #
+# the ends of the ranges
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tree", [False, True])
+def test_the_most_sequences_a_call_takes(dtype, tree):
+    """16384 sequences, a step from planning to committing: every sequence's pages,
+    rows and length, and the attention of some."""
+    import sparse_kv_selection_gb300 as S
+    rng = np.random.default_rng(5)
+    B, d, page, blocks = 16384, 64, 16, 3
+    lens, n = rng.integers(0, 33, B), rng.integers(0, 3, B)
+    have = -(-lens // page)
+    table = np.full((B, blocks), -1)
+    ids = rng.permutation(B * blocks)
+    for i in range(blocks):
+        table[have > i, i] = ids[i * B:(i + 1) * B][have > i]
+    free = np.setdiff1d(ids, table)
+    pool = torch.randn(B * blocks, 1, page, d, device="cuda", dtype=dtype)
+    kv = S.KVCache(pool, torch.randn_like(pool), i32(lens), 1, block_table=i32(table))
+    T = int(n.sum()) + 3
+    batch = S.TokenBatch(kv, S.RopeTable(d), max_tokens=T, max_new=2, free_pages=i32(free), n_pages=i32(have))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    q, k, v = torch.randn(3, T, 1, d, generator=g, device="cuda").to(dtype)
+    parents = np.full(T, -1)
+    cu = np.concatenate([[0], np.cumsum(n)])
+    parents[cu[:-1][n == 2] + 1] = rng.integers(-1, 1, (n == 2).sum())
+    batch.plan(i32(n), i32(parents) if tree else None)
+    batch.rotate(q, k, v, append=not tree)
+    batch.attend()
+    before = kv.k.clone(), kv.v.clone()
+    batch.commit(i32(n))
+    assert S.last_error() == 0
+    assert kv.seq_lens.cpu().numpy().tolist() == (lens + n).tolist()
+    got = kv.block_table.cpu().numpy()
+    need = -(-(lens + n) // page)
+    held = [got[:, i][need > i] for i in range(blocks)]
+    assert len(np.unique(np.concatenate(held))) == need.sum()
+    b = np.repeat(np.arange(B), n)
+    pos = lens[b] + np.arange(cu[-1]) - cu[b]
+    at, row = torch.tensor(got[b, pos // page], device="cuda"), torch.tensor(pos % page, device="cuda")
+    assert torch.equal(kv.k[at, 0, row], batch.k[:cu[-1], 0]) and torch.equal(kv.v[at, 0, row], v[:cu[-1], 0])
+    for b in rng.integers(0, B, 60).tolist() + [B - 1]:
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        if n[b] == 0:
+            continue
+        p = np.arange(lens[b])
+        kc, vc = [x[torch.tensor(got[b, p // page], device="cuda").long(), :, torch.tensor(p % page, device="cuda")]
+                  .double().transpose(0, 1) for x in before]
+        see = torch.ones(n[b], n[b], dtype=torch.bool, device="cuda").tril()
+        if tree and n[b] == 2:
+            see[1, 0] = bool(parents[cu[b] + 1] == 0)
+        wo, wl, eo, el = attn_ref(batch.q[r].double(), kc, vc, batch.k[r].double(), v[r].double(), see, batch.scale, d, dtype)
+        assert ((batch.out[r].double() - wo).abs() <= eo).all() and ((batch.lse[r].double() - wl).abs() <= el).all()
+
+
+def test_the_first_step_of_a_process_is_captured(tmp_path):
+    """No call has been made before the capture, in a process of its own."""
+    script = tmp_path / "first.py"
+    script.write_text(FIRST)
+    r = subprocess.run([sys.executable, str(script)], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": ROOT})
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+FIRST = """
+import torch
+import sparse_kv_selection_gb300 as S
+for dtype in (torch.bfloat16, torch.float32):
+    k, v = torch.randn(2, 8, 2, 16, 64, device="cuda").to(dtype)
+    z = dict(dtype=torch.int32, device="cuda")
+    kv = S.KVCache(k, v, torch.tensor([20, 0], **z), 4, block_table=torch.tensor([[0, 1, -1], [-1, -1, -1]], **z))
+    batch = S.TokenBatch(kv, S.RopeTable(64), max_tokens=9, max_new=6, free_pages=torch.arange(2, 8, **z),
+                         n_pages=torch.tensor([2, 0], **z))
+    q, kn, vn = torch.randn(9, 4, 64, device="cuda").to(dtype), *torch.randn(2, 9, 2, 64, device="cuda").to(dtype)
+    n, parents = torch.tensor([3, 6], **z), torch.tensor([-1, 0, 0, -1, 0, 1, 2, 3, 4], **z)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        batch.plan(n, parents)
+        batch.rotate(q, kn, vn)
+        batch.attend()
+        batch.commit(n)
+    g.replay()
+    assert S.last_error() == 0
+    assert kv.seq_lens.tolist() == [23, 6], kv.seq_lens
+    assert batch.out.float().isfinite().all() and (batch.lse != 0).all()
+"""
