@@ -45,11 +45,6 @@ __device__ __forceinline__ uint4 pack_piece<__nv_bfloat16>(const float* f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One token of a CTA: its cache row (KV head 0; -1: nothing of it is written).
-struct RopeToken {
-  long long row;
-};
-
 // `rows` head rows a token (q, k and, with slots, v), 1 << tpr_log2 tasks a row.
 template <typename T, int PER>
 __global__ void __launch_bounds__(ROPE_THREADS, PER == 1 ? 1 : 12)
@@ -59,7 +54,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, PER == 1 ? 1 : 12)
   const KVView& kv = a.kv;
   const int half = a.rot_dim / 2, rot_tasks = half / E;
   float2* cs = reinterpret_cast<float2*>(rope_smem);                    // [max_tokens][half]
-  RopeToken* token = reinterpret_cast<RopeToken*>(cs + max_tokens * half);  // [max_tokens]
+  // the tokens' cache rows (KV head 0; -1: nothing of the token is written)
+  long long* token_row = reinterpret_cast<long long*>(cs + max_tokens * half);  // [max_tokens]
   pdl_wait();
   pdl_trigger();
 
@@ -111,7 +107,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, PER == 1 ? 1 : 12)
       if (slot >= 0 && slot < slots) row = slot_row(kv, slot, &head_rows);
       else if (slot != -1) raise_error(kv.err, PRHS_DEV_BAD_INDEX);
     }
-    token[k].row = row;
+    token_row[k] = row;
   }
   __syncthreads();
   const int head_rows = kv.block_table != nullptr ? kv.block_size : kv.t_max;
@@ -121,7 +117,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, PER == 1 ? 1 : 12)
     const int r = (threadIdx.x >> tpr_log2) + u * step;
     if (r >= n_rows) break;
     const int k = (int)((base + r + 0.5f) * inv_rows), row = base + r - k * rows;
-    const long long tok = tok0 + k, cache_row = token[k].row;
+    const long long tok = tok0 + k, cache_row = token_row[k];
     if (cache_row < 0) continue;
     if (rotated && row < kv.Hq + kv.Hkv) {
       float e0[E], e1[E];
@@ -182,7 +178,7 @@ static cudaError_t rope_go(const RopeLaunch& a, cudaStream_t st) {
   // tokens a CTA may touch: its whole ones and one cut at each end
   const long long most = (chunk + rows - 1) / rows + 1;
   const int max_tokens = (int)(most < a.T ? most : a.T);
-  const size_t smem = (size_t)max_tokens * (a.rot_dim / 2 * sizeof(float2) + sizeof(RopeToken));
+  const size_t smem = (size_t)max_tokens * (a.rot_dim / 2 * sizeof(float2) + sizeof(long long));
   auto k = rope_kernel<T, PER>;
   static int smem_set[SMEM_DEVICES];
   const cudaError_t e = allow_smem(k, smem, smem_set);

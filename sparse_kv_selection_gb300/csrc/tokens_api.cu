@@ -18,12 +18,11 @@ bool stride_ok(const prhs_kv& kv, long long stride, int heads) {
          stride < (1ll << 38);  // bytes below the 2^40 of a TMA stride
 }
 
-prhs_status launched(cudaError_t e, const char* what) {
+prhs_status launched(cudaError_t e) {
   if (e == cudaSuccess) {
     abi_count_launch();
     return PRHS_OK;
   }
-  (void)what;
   return abi_fail(PRHS_ECUDA, cudaGetErrorString(e));
 }
 
@@ -91,7 +90,7 @@ prhs_status prhs_plan_tokens(const prhs_kv* kv, const int32_t* n_new, int T,
   a.tree_mask = tree_mask;
   a.free_head_out = free_head_out;
   a.n_pages_out = n_pages_out;
-  return launched(launch_plan(a, stream), "plan kernel");
+  return launched(launch_plan(a, stream));
 }
 
 prhs_status prhs_rope_turns(prhs_rope_kind kind, int rot_dim, double base, double factor,
@@ -174,7 +173,7 @@ prhs_status prhs_rope_append(const prhs_kv* kv, const prhs_rope* rope, int T,
   a.vs = v_stride;
   a.q_out = q_out;
   a.k_out = k_out;
-  return launched(launch_rope(a, sms, stream), "rope kernel");
+  return launched(launch_rope(a, sms, stream));
 }
 
 size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new) {
@@ -229,10 +228,10 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   a.mask = tree_mask;
   a.out = out;
   a.lse = lse;
-  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, sms, ws, stream), "tree attention");
+  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, sms, ws, stream));
   cudaError_t e;
   if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
-  return launched(e, "tree attention");
+  return launched(e);
 }
 
 static prhs_status commit(const prhs_kv* kv, int T, const int32_t* cu_new, const int32_t* slots,
@@ -263,7 +262,7 @@ static prhs_status commit(const prhs_kv* kv, int T, const int32_t* cu_new, const
   a.ks = k_stride;
   a.vs = v_stride;
   a.new_lens = new_lens;
-  return launched(launch_commit(a, sms, stream), "commit kernel");
+  return launched(launch_commit(a, sms, stream));
 }
 
 prhs_status prhs_commit_tokens(const prhs_kv* kv, int T, const int32_t* cu_new,

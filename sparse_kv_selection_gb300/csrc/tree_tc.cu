@@ -757,8 +757,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             have[c] = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1;
             have[c] &= ((ok16 >> (2 * c)) & 1 ? 0xffffu : 0u) | ((ok16 >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
           }
-        }
-        if (cut) {
           // V rows of keys that do not exist hold whatever was there, possibly not
           // finite, and 0 * inf would reach every row: they are set to 0 (each row from
           // another piece on, since the rows' equal pieces share their banks)
