@@ -945,7 +945,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();
-      if (both) softmax_meet(false);  // both outputs and the row states are read
+      if (both && !w.last) softmax_meet(false);  // both outputs and the row states are read (the last: below)
     }
     while (!softmax_meet(true)) {
     }
