@@ -24,9 +24,9 @@
 // (R + TY) 16-byte reads for 4 R TY products, 4 (R + TY) / (R TY) times what the
 // products take: 2 at 4 by 4, 3 at 2 by 4, 5 at 1 by 4 (the product with V has more
 // columns a lane: 1.25 at 4 by 4). Hence the forms at the end of this file.
-// Two causal chunks of 1024 tokens on 512 keys, 8 / 2 heads, d = 128: 231 us, 37
-// TFLOP/s; single tokens of 16 heads over 69 206 keys, 4 KV heads, 16-key pages: 64
-// us, 4.4 TB/s; 27 trees of 21 tokens over up to 1899 keys, 8 heads, d = 64: 64 us.
+// Two causal chunks of 1024 tokens on 512 keys, 8 / 2 heads, d = 128: 227 us, 38
+// TFLOP/s; single tokens of 16 heads over 69 206 keys, 4 KV heads, 16-key pages: 63
+// us, 4.5 TB/s; 27 trees of 21 tokens over up to 1899 keys, 8 heads, d = 64: 63 us.
 #include "tree_join.cuh"
 
 namespace prhs {
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     // ---- the unit's last tile here: its result, or a partial record (m, l and O
     // against m), which also takes the sums of every FOLD tiles on the way: thousands of
     // terms added one by one lose more than blocks of them do (10 tokens over 20K keys,
-    // 64 heads: 1.15e-6 of the result against 6.1e-7; runs of hundreds of tiles take 2 to
-    // 4% longer for it) ----
+    // 64 heads: 1.15e-6 of the result against 6.1e-7; runs of hundreds of tiles take 1%
+    // longer for it) ----
     const int done = x.tile - x.tile0 + 1;
     const bool last = x.tile + 1 == x.tiles || x.left == 0;
     if (!last && done % FOLD != 0) continue;

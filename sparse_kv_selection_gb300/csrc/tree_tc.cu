@@ -41,7 +41,8 @@
 // 2K-16K keys on 16-key pages, 32 KV heads, trees of 1-32 tokens, 4.25 GB: 630 us,
 // the measured copy bandwidth. Above that the tensor cores and the
 // softmax between their products: 5250 causal tokens on cached prefixes, 32 / 8
-// heads: 387 us, 1495 TFLOP/s, 0.80 of the measured matrix rate (a step of a
+// heads: 388-391 us from a graph, 1480-1490 TFLOP/s, 0.80 of the measured matrix rate;
+// single calls back to back 414-420 us, 0.74, at the power cap's clocks (a step of a
 // stream is 1550 clocks, its two products 1031; the rest is the wait of one
 // product for the softmax, 1250 clocks of 128 exponentials a thread). Few tiles
 // a CTA (4096 keys, 32 heads): latency, 2.3 us to the first copy, 3 us from it to
@@ -262,7 +263,8 @@ __device__ __forceinline__ void quad_swap(uint32_t (&x)[4], uint32_t (&y)[4]) {
 
 // The softmax warps meet: true where all of them are about to leave. A warp that has
 // left its units (at the run's end, or early because a wait gave up) meets the others
-// until that is so, so that none of them waits here for one that is gone.
+// until that is so, so that none of them waits here for one that is gone. (An
+// mbarrier and a bounded wait instead: 4096 keys 19.5 -> 20.0 us, causal chunks 387 -> 394.)
 __device__ __forceinline__ bool softmax_meet(bool leaving) {
   uint32_t r;
   asm volatile(
@@ -408,8 +410,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   // at the unit that begins there or next. Joining takes about 4 us, a tile 0.8 or
   // (two row tiles) 1.6, so runs may be up to five tiles longer instead, on units so
   // short that they do not differ by more: 512 causal tokens on 512 keys, 32 / 8 heads,
-  // 28.7 us (cut: 33.6); 4 chunks of 184 on 217 keys 25.3 (32.7); 32 drafts of 8 on 500
-  // keys 24.8 (27.3). The search costs long caches 0.3 us.
+  // 24.2 us (cut: 26.8); 4 chunks of 184 on 217 keys 19.6 (26.1); 32 drafts of 8 on 500
+  // keys 23.3 (24.5). The search costs long caches 0.6 us at most.
   const int g0 = blockIdx.x * per, g1 = min(total, g0 + per);
   most = max(most, 1);
   const bool uncut = most <= UNCUT_TILES && (per + most - 1) / most * most - per <= min(2 * per, 5);

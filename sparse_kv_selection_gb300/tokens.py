@@ -74,8 +74,9 @@ class TokenBatch:
     def rotate(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, append: bool = False) -> None:
         """Rotate q [max_tokens][Hq][d] and k [max_tokens][Hkv][d] at the planned
         positions; append writes k and v into the cache at the planned slots
-        (chunks whose tokens will all be committed). v is kept for attend and
-        commit: it must not change before them."""
+        (chunks whose tokens will all be committed), and leaves out those that
+        plan refused, whose attention then has no meaning. v is kept for attend
+        and commit: it must not change before them."""
         if append and self.tree_mask is not None:
             raise ValueError("a tree's tokens join the cache when they are committed")
         _b.rope_append(self.kv, self.rope, self.positions, q, k, v, self.q,
