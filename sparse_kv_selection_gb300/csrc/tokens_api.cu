@@ -277,7 +277,7 @@ prhs_status prhs_commit_planned(const prhs_kv* kv, int T, const int32_t* cu_new,
                                 const int32_t* accept_idx, int accept_cap, const int32_t* accept_n,
                                 const void* k_new, long long k_stride, const void* v_new,
                                 long long v_stride, int32_t* new_lens, cudaStream_t stream) {
-  if (!slots) return abi_fail(PRHS_EINVAL, "commit: slots must be non-null");
+  if (T > 0 && !slots) return abi_fail(PRHS_EINVAL, "commit: slots must be non-null");
   return commit(kv, T, cu_new, slots, accept_idx, accept_cap, accept_n, k_new, k_stride, v_new, v_stride, new_lens,
                 stream);
 }

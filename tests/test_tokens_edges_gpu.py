@@ -153,6 +153,16 @@ def test_a_plan_is_committed_once():
     assert S.last_error() == DEV_BAD_INDEX and c.kv.seq_lens.tolist() == [24, 11]
 
 
+def test_a_batch_of_no_tokens_is_committed():
+    import sparse_kv_selection_gb300 as S
+    c = Cache([20, 7], 2, 1, 64, BF16, page=16, room=40, seed=6)
+    batch = S.TokenBatch(c.kv, S.RopeTable(64), max_tokens=0, max_new=1, free_pages=i32(c.free), n_pages=i32(c.n_pages))
+    batch.plan(i32([0, 0]))
+    batch.rotate(*rows_of(0, c, 2), append=True)
+    batch.commit(i32([0, 0]))
+    assert S.last_error() == 0 and c.kv.seq_lens.tolist() == [20, 7]
+
+
 # --------------------------------------------------------------------------- #
 # batches that share a cache
 # --------------------------------------------------------------------------- #
