@@ -429,6 +429,84 @@ prhs_status prhs_commit_planned(const prhs_kv* kv, int T, const int32_t* cu_new,
                                 const void* k_new, long long k_stride, const void* v_new,
                                 long long v_stride, int32_t* new_lens, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------- *
+ * Sequences that share pages: samples or beams of one prompt, requests behind one
+ * system prompt. Several rows of a paged cache's block table may name one page;
+ * page_shares[p] is the number of rows that do, less one (0: one row, or free).
+ * New tokens are written behind a row's length only, so nothing writes to a shared
+ * page as long as a row holds its last, partly filled page alone: fork and compact
+ * keep it so, and prhs_plan_tokens takes pages that nobody holds.
+ *
+ * Fork and compact turn the state `now` into `next` (equal arrays: in place) and
+ * list the cache rows to copy, slot by slot, which prhs_copy_rows then does in the
+ * cache of every layer that the block table serves. A call is carried out whole or
+ * not at all: refused, it is flagged in the device error word, `next` is `now`,
+ * and there is nothing to copy. Paged caches only. ws: prhs_pages_workspace_size()
+ * bytes, 256-byte aligned, no initialisation.
+ * ------------------------------------------------------------------------- */
+typedef struct prhs_pages {
+  int32_t* block_table;  /* [B][max_blocks]; now: null or the descriptor's, next: null for in place */
+  int32_t* seq_lens;     /* [B]; the same */
+  int32_t* n_pages;      /* [B] pages that each row holds, those behind its length too */
+  int32_t* page_shares;  /* [num_blocks] */
+  int32_t* free_pages;   /* [n_free]; [free_head[0], n_free) are held by no row */
+  int n_free;            /* the same in now and next */
+  int32_t* free_head;    /* [1] */
+} prhs_pages;
+
+size_t prhs_pages_workspace_size(const prhs_kv* kv);
+
+/* Row b becomes what row parent[b] (int32 [B]) was before the call: parent[b] = b
+ * stays as it is, -1 ends the sequence (length and pages 0). A new row names its
+ * parent's whole pages; of a last page that is partly filled it gets a copy on a
+ * free page, taken in the order of the rows: src and dst (int32 [B][block_size])
+ * are then the slots of its rows, elsewhere -1. The first of the rows that fork from
+ * a row which is itself replaced or ended takes that page over instead, if no other
+ * row holds it. Pages that rows give up and nobody holds go back in front of the
+ * free ones, in the order of the first (row, column) that gave them up; columns that
+ * a row no longer uses are set to -1.
+ * Refused: a parent outside [-1, B) (PRHS_DEV_BAD_INDEX); a length or page count
+ * out of range, or fewer pages than a parent's length needs (PRHS_DEV_BAD_LEN); a
+ * page outside the pool in what is named or given up (PRHS_DEV_BAD_BLOCK); too few
+ * free pages, or more pages given back than have been taken (PRHS_DEV_CAPACITY). */
+prhs_status prhs_fork_seqs(const prhs_kv* kv, const prhs_pages* now, const int32_t* parent,
+                           const prhs_pages* next, int32_t* src, int32_t* dst, void* ws,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/* Row b keeps the positions keep[b][0 .. m) (int32 [B][cap], strictly ascending),
+ * m = keep_n[b], which become its positions 0 .. m - 1; m < 0 leaves the row as it is.
+ * The whole pages of the leading positions that keep their places stay, as does the
+ * last page of a row that is only cut short and holds it alone. The others go to free
+ * pages, taken in the order of the rows (src and dst int32 [B][cap]: the slots of
+ * each moved position, elsewhere -1), and the old pages are given back as in fork.
+ * Keys keep the rotation they were cached with: positions of later tokens count the
+ * kept ones, so add what was dropped to them where that matters.
+ * Refused: as fork, and positions that do not ascend within [0, t_b)
+ * (PRHS_DEV_BAD_INDEX), m above cap or t_b (PRHS_DEV_BAD_LEN). */
+prhs_status prhs_compact_seqs(const prhs_kv* kv, const prhs_pages* now, const int32_t* keep, int cap,
+                              const int32_t* keep_n, const prhs_pages* next, int32_t* src,
+                              int32_t* dst, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Copies n cache rows, K and V of every KV head: slot src[i] of `source` (null: of
+ * the same cache; else one of the same element type, KV heads and d, paged or not) to
+ * slot dst[i] of the cache (slots as prhs_plan_tokens counts them). An entry with -1
+ * in either is no copy, a slot outside its cache is flagged (PRHS_DEV_BAD_INDEX) and
+ * none either. Targets must differ from each other and from every source. */
+prhs_status prhs_copy_rows(const prhs_kv* kv, const prhs_kv* source, int n, const int32_t* src,
+                           const int32_t* dst, cudaStream_t stream);
+
+/* Groups of consecutive rows that share leading pages, for prhs_shared_attn:
+ * shared[b] (int32 [B][4], 16-byte aligned) = (first row of b's group, rows of the
+ * group, keys that all its rows share, 0), or (b, 1, 0, 0) for a row that is alone.
+ * Two rows share the leading pages that both name, whole ones within both lengths.
+ * Rows without new tokens (cu_new) are passed over. A row joins the group above it
+ * if the shared keys stay at least min_keys (and 1) and the group then saves no
+ * less, counted as (rows - 1) * shared keys. A row with 256 query rows a KV head or
+ * more (new tokens times Hq / Hkv) stays alone: its queries use each key often
+ * enough. On a contiguous cache every row is alone. */
+prhs_status prhs_find_shared(const prhs_kv* kv, const int32_t* cu_new, int min_keys, int32_t* shared,
+                             cudaStream_t stream);
+
 /* Self-test of the kernels' failure path (no counterpart in the paper): one
  * warp waits on a shared-memory mbarrier that nothing arrives on, through the
  * same bounded wait every TMA pipeline of the library uses, but giving up

@@ -26,7 +26,8 @@ EXPORTS = ["prhs_workspace_size", "prhs_workspace_init", "prhs_score_select", "p
            "prhs_sparse_attn", "prhs_sparse_attn_noalloc", "prhs_set_mass", "prhs_dense_attn",
            "prhs_decode_step", "prhs_append_kv", "prhs_plan_tokens", "prhs_rope_turns",
            "prhs_rope_append", "prhs_tree_workspace_size", "prhs_tree_attn",
-           "prhs_commit_tokens", "prhs_commit_planned", "prhs_selftest_wait_timeout", "prhs_last_error",
+           "prhs_commit_tokens", "prhs_commit_planned", "prhs_pages_workspace_size", "prhs_fork_seqs",
+           "prhs_compact_seqs", "prhs_copy_rows", "prhs_find_shared", "prhs_selftest_wait_timeout", "prhs_last_error",
            "prhs_device_error_bits", "prhs_status_str", "prhs_last_message", "prhs_num_sms",
            "prhs_launch_count"]
 
@@ -56,6 +57,12 @@ class prhs_rope(ctypes.Structure):
                 ("turns", ctypes.c_void_p), ("mscale", ctypes.c_float)]
 
 
+class prhs_pages(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("n_pages", ctypes.c_void_p),
+                ("page_shares", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_int),
+                ("free_head", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -71,6 +78,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     P, I, F, D, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
     KV = ctypes.POINTER(prhs_kv)
     ROPE, L = ctypes.POINTER(prhs_rope), ctypes.c_longlong
+    PAGES = ctypes.POINTER(prhs_pages)
     sig = {
         "prhs_workspace_size": (Z, [KV, I]),
         "prhs_workspace_init": (I, [P, Z, P]),
@@ -93,6 +101,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "prhs_tree_attn": (I, [KV, P, P, L, P, L, F, I, P, I, P, P, P, P, Z, P]),
         "prhs_commit_tokens": (I, [KV, I, P, P, I, P, P, L, P, L, P, P]),
         "prhs_commit_planned": (I, [KV, I, P, P, P, I, P, P, L, P, L, P, P]),
+        "prhs_pages_workspace_size": (Z, [KV]),
+        "prhs_fork_seqs": (I, [KV, PAGES, P, PAGES, P, P, P, Z, P]),
+        "prhs_compact_seqs": (I, [KV, PAGES, P, I, P, PAGES, P, P, P, Z, P]),
+        "prhs_copy_rows": (I, [KV, KV, I, P, P, P]),
+        "prhs_find_shared": (I, [KV, P, I, P, P]),
         "prhs_selftest_wait_timeout": (I, [ctypes.c_uint, P]),
         "prhs_last_error": (I, []),
         "prhs_device_error_bits": (ctypes.c_uint, []),
@@ -494,6 +507,95 @@ def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, slots=None, accept_idx
           _array(accept_idx, "accept_idx", (B, cap), i32, dev, True), cap,
           _array(accept_n, "accept_n", (B,), i32, dev), kp, ks, vp, vs,
           _array(kv.seq_lens if new_lens is None else new_lens, "new_lens", (B,), i32, dev))
+
+
+# --------------------------------------------------------------------------- #
+# sequences that share pages
+# --------------------------------------------------------------------------- #
+def pages_workspace_size(kv: KVCache) -> int:
+    n = load().prhs_pages_workspace_size(kv.ref())
+    if n == 0:
+        raise PrhsError(PRHS_EINVAL, "pages_workspace_size", load().prhs_last_message().decode())
+    return n
+
+
+def make_pages_workspace(kv: KVCache):
+    """Allocate (through torch) the workspace of fork_seqs and compact_seqs."""
+    return torch.empty(pages_workspace_size(kv), dtype=torch.uint8, device=kv.device)
+
+
+def _pages(kv, names, table, lens, n_pages, shares, free, head):
+    """The prhs_pages of one state, its arrays checked."""
+    dev, i32, d = kv.device, torch.int32, kv.desc
+    n_free = 0 if free is None else free.numel()
+    return prhs_pages(_array(table, names[0], (d.B, d.max_blocks), i32, dev, True),
+                      _array(lens, names[1], (d.B,), i32, dev, True), _array(n_pages, names[2], (d.B,), i32, dev),
+                      _array(shares, names[3], (d.num_blocks,), i32, dev),
+                      _array(free, names[4], (n_free,), i32, dev, True), n_free, _array(head, names[5], (1,), i32, dev))
+
+
+_PAGES = ("table", "lens", "n_pages", "page_shares", "free_pages", "free_head")
+_PAGES_OUT = tuple(n + "_out" for n in _PAGES)
+
+
+def _pages_call(kv, where, fn, stream, args, src, dst, cap, ws, n_pages, page_shares, free_pages, free_head, out):
+    dev, i32, B = kv.device, torch.int32, kv.desc.B
+    if kv.block_table is None:
+        raise ValueError(f"{where} needs a paged cache")
+    if ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, the cache on {dev}")
+    now = _pages(kv, _PAGES, None, None, n_pages, page_shares, free_pages, free_head)
+    table_out, lens_out, *rest = out
+    rest = [a if b is None else b for a, b in zip((n_pages, page_shares, free_pages, free_head), rest)]
+    nxt = _pages(kv, _PAGES_OUT, table_out, lens_out, *rest)
+    _call(kv, where, fn, stream, kv.ref(), ctypes.byref(now), *args, ctypes.byref(nxt),
+          _array(src, "src", (B, cap), i32, dev), _array(dst, "dst", (B, cap), i32, dev), _ptr(ws),
+          ws.numel() * ws.element_size())
+
+
+def fork_seqs(kv, parent, src, dst, ws, *, n_pages, page_shares, free_pages, free_head, table_out=None, lens_out=None,
+              n_pages_out=None, page_shares_out=None, free_pages_out=None, free_head_out=None, stream=None) -> None:
+    """Row b of the paged cache becomes a copy of row parent[b] as it was, or ends
+    (-1); shared pages are counted in page_shares (prhs_fork_seqs). src and dst
+    [B][block_size] int32 get the slots that copy_rows has to copy. Everything is
+    updated in place, kv.block_table and kv.seq_lens too, unless its _out array is given."""
+    _pages_call(kv, "fork_seqs", load().prhs_fork_seqs, stream,
+                (_array(parent, "parent", (kv.desc.B,), torch.int32, kv.device),), src, dst, kv.desc.block_size, ws,
+                n_pages, page_shares, free_pages, free_head,
+                (table_out, lens_out, n_pages_out, page_shares_out, free_pages_out, free_head_out))
+
+
+def compact_seqs(kv, keep, keep_n, src, dst, ws, *, n_pages, page_shares, free_pages, free_head, table_out=None,
+                 lens_out=None, n_pages_out=None, page_shares_out=None, free_pages_out=None, free_head_out=None,
+                 stream=None) -> None:
+    """Row b keeps the positions keep[b][:keep_n[b]] (ascending; keep_n[b] < 0: all)
+    and gives back the pages it no longer needs (prhs_compact_seqs). src and dst (the
+    shape of keep) get the slots that copy_rows has to copy; outputs as fork_seqs."""
+    dev, i32, cap = kv.device, torch.int32, keep.shape[-1]
+    _pages_call(kv, "compact_seqs", load().prhs_compact_seqs, stream,
+                (_array(keep, "keep", (kv.desc.B, cap), i32, dev), cap, _array(keep_n, "keep_n", (kv.desc.B,), i32, dev)),
+                src, dst, cap, ws, n_pages, page_shares, free_pages, free_head,
+                (table_out, lens_out, n_pages_out, page_shares_out, free_pages_out, free_head_out))
+
+
+def copy_rows(kv, src, dst, *, source=None, stream=None) -> None:
+    """Copy cache rows (K and V of every head) from slots src of `source` (another
+    KVCache, or the same one) to slots dst of the cache; -1: none (prhs_copy_rows)."""
+    n = src.numel()
+    if source is not None and source.device != kv.device:
+        raise ValueError(f"source is on {source.device}, the cache on {kv.device}")
+    if dst.shape != src.shape:
+        raise ValueError(f"dst must have the shape of src, {tuple(src.shape)}, got {tuple(dst.shape)}")
+    _call(kv, "copy_rows", load().prhs_copy_rows, stream, kv.ref(), None if source is None else source.ref(), n,
+          _array(src, "src", src.shape, torch.int32, kv.device), _array(dst, "dst", src.shape, torch.int32, kv.device))
+
+
+def find_shared(kv, cu_new, shared, *, min_keys=256, stream=None) -> None:
+    """Groups of consecutive rows that share leading pages, into shared [B][4] int32
+    for shared_attn: (first row, rows, shared keys, 0) (prhs_find_shared)."""
+    dev, i32, B = kv.device, torch.int32, kv.desc.B
+    _call(kv, "find_shared", load().prhs_find_shared, stream, kv.ref(), _array(cu_new, "cu_new", (B + 1,), i32, dev),
+          int(min_keys), _array(shared, "shared", (B, 4), i32, dev))
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:
