@@ -507,6 +507,28 @@ prhs_status prhs_copy_rows(const prhs_kv* kv, const prhs_kv* source, int n, cons
 prhs_status prhs_find_shared(const prhs_kv* kv, const int32_t* cu_new, int min_keys, int32_t* shared,
                              cudaStream_t stream);
 
+/* Bytes of workspace prhs_shared_attn needs for T packed tokens, at most max_new of
+ * a sequence (0 for an invalid argument). It needs no initialisation. */
+size_t prhs_shared_workspace_size(const prhs_kv* kv, int T, int max_new);
+
+/* prhs_tree_attn for a batch in which groups of consecutive rows share leading keys:
+ * the new tokens of a group attend keys [0, P) of its first row in one pass, read
+ * once for the whole group, and each sequence its own keys [P, t_b) and new tokens as
+ * in prhs_tree_attn; the two states of a token are joined in fp32. Where the keys
+ * [0, P) of a group's rows are the same, so is the result, but for the order of sums.
+ * shared[b] (int32 [B][4], 16-byte aligned) as prhs_find_shared fills it, or a caller
+ * that knows its batch: every row of a group has the same (first row, rows, P, 0); a
+ * row that is alone has (b, 1, 0, 0). Groups must not overlap. P counts whole pages (it
+ * is rounded down to them; on a contiguous cache it is any number). A row whose entry
+ * does not fit its group's first row, or with P above either row's length, is flagged
+ * (PRHS_DEV_BAD_INDEX) and attends all its own keys. Everything else, errors too, as
+ * prhs_tree_attn. */
+prhs_status prhs_shared_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,
+                             const void* v_new, long long v_stride, float scale, int T,
+                             const int32_t* cu_new, int max_new, const uint32_t* tree_mask,
+                             const int32_t* shared, void* out, float* lse, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
 /* Self-test of the kernels' failure path (no counterpart in the paper): one
  * warp waits on a shared-memory mbarrier that nothing arrives on, through the
  * same bounded wait every TMA pipeline of the library uses, but giving up

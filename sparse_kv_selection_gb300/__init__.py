@@ -8,16 +8,16 @@ every call raises.
 """
 from .binding import (KVCache, PrhsError, RopeTable, cis_dilate, commit_tokens, compact_seqs, copy_rows,
                       decode_step, dense_attn, find_shared, fork_seqs, last_error, load,
-                      make_pages_workspace, make_tree_workspace, make_workspace, num_sms,
-                      pages_workspace_size, plan_tokens, retrieve, rope_append, rope_turns,
-                      score_select, set_mass, sparse_attn, tree_attn, tree_workspace_size,
-                      workspace_init, workspace_size)
+                      make_pages_workspace, make_shared_workspace, make_tree_workspace, make_workspace,
+                      num_sms, pages_workspace_size, plan_tokens, retrieve, rope_append, rope_turns,
+                      score_select, set_mass, shared_attn, shared_workspace_size, sparse_attn,
+                      tree_attn, tree_workspace_size, workspace_init, workspace_size)
 from .decoder import SparseDecoder
 from .tokens import TokenBatch
 
 __all__ = ["KVCache", "PrhsError", "RopeTable", "SparseDecoder", "TokenBatch", "cis_dilate",
            "commit_tokens", "compact_seqs", "copy_rows", "decode_step", "dense_attn", "find_shared",
-           "fork_seqs", "last_error", "load", "make_pages_workspace", "make_tree_workspace",
-           "make_workspace", "num_sms", "pages_workspace_size", "plan_tokens", "retrieve",
-           "rope_append", "rope_turns", "score_select", "set_mass", "sparse_attn", "tree_attn",
+           "fork_seqs", "last_error", "load", "make_pages_workspace", "make_shared_workspace",
+           "make_tree_workspace", "make_workspace", "num_sms", "pages_workspace_size", "plan_tokens", "retrieve",
+           "rope_append", "rope_turns", "score_select", "set_mass", "shared_attn", "shared_workspace_size", "sparse_attn", "tree_attn",
            "tree_workspace_size", "workspace_init", "workspace_size"]

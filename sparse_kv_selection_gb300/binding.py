@@ -27,7 +27,8 @@ EXPORTS = ["prhs_workspace_size", "prhs_workspace_init", "prhs_score_select", "p
            "prhs_decode_step", "prhs_append_kv", "prhs_plan_tokens", "prhs_rope_turns",
            "prhs_rope_append", "prhs_tree_workspace_size", "prhs_tree_attn",
            "prhs_commit_tokens", "prhs_commit_planned", "prhs_pages_workspace_size", "prhs_fork_seqs",
-           "prhs_compact_seqs", "prhs_copy_rows", "prhs_find_shared", "prhs_selftest_wait_timeout", "prhs_last_error",
+           "prhs_compact_seqs", "prhs_copy_rows", "prhs_find_shared",
+           "prhs_shared_workspace_size", "prhs_shared_attn", "prhs_selftest_wait_timeout", "prhs_last_error",
            "prhs_device_error_bits", "prhs_status_str", "prhs_last_message", "prhs_num_sms",
            "prhs_launch_count"]
 
@@ -106,6 +107,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "prhs_compact_seqs": (I, [KV, PAGES, P, I, P, PAGES, P, P, P, Z, P]),
         "prhs_copy_rows": (I, [KV, KV, I, P, P, P]),
         "prhs_find_shared": (I, [KV, P, I, P, P]),
+        "prhs_shared_workspace_size": (Z, [KV, I, I]),
+        "prhs_shared_attn": (I, [KV, P, P, L, P, L, F, I, P, I, P, P, P, P, P, Z, P]),
         "prhs_selftest_wait_timeout": (I, [ctypes.c_uint, P]),
         "prhs_last_error": (I, []),
         "prhs_device_error_bits": (ctypes.c_uint, []),
@@ -462,23 +465,28 @@ def make_tree_workspace(kv: KVCache, max_new: int):
     return torch.empty(tree_workspace_size(kv, max_new), dtype=torch.uint8, device=kv.device)
 
 
-def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree_mask=None,
-              stream=None) -> None:
-    """Attention of packed new tokens over their caches and each other: by
-    tree_mask [T][4] int32, or causal (prhs_tree_attn). out [T][Hq][d] has the
-    cache's element type, lse [T][Hq] is float32. On a bfloat16 cache the weights
-    are rounded to bfloat16 before they meet v (dense_attn keeps them in float32)."""
+def _attend(kv, where, fn, q, k_new, v_new, scale, cu_new, max_new, tree_mask, shared, out, lse, ws, stream):
     dev, dt, T, desc = kv.device, kv.dtype, q.shape[0], kv.desc
     Hq, Hkv, d = desc.Hq, desc.Hkv, desc.d
     kp, ks = _rows(k_new, "k_new", T, Hkv, d, dt, dev)
     vp, vs = _rows(v_new, "v_new", T, Hkv, d, dt, dev)
     if ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the cache on {dev}")
-    _call(kv, "tree_attn", load().prhs_tree_attn, stream, kv.ref(), _array(q, "q", (T, Hq, d), dt, dev), kp, ks,
+    _call(kv, where, fn, stream, kv.ref(), _array(q, "q", (T, Hq, d), dt, dev), kp, ks,
           vp, vs, float(scale), T, _array(cu_new, "cu_new", (desc.B + 1,), torch.int32, dev), int(max_new),
-          _array(tree_mask, "tree_mask", (T, TREE_WORDS), torch.int32, dev, True),
+          _array(tree_mask, "tree_mask", (T, TREE_WORDS), torch.int32, dev, True), *shared,
           _array(out, "out", (T, Hq, d), dt, dev), _array(lse, "lse", (T, Hq), torch.float32, dev),
           _ptr(ws), ws.numel() * ws.element_size())
+
+
+def tree_attn(kv, q, k_new, v_new, scale, cu_new, max_new, out, lse, ws, *, tree_mask=None,
+              stream=None) -> None:
+    """Attention of packed new tokens over their caches and each other: by
+    tree_mask [T][4] int32, or causal (prhs_tree_attn). out [T][Hq][d] has the
+    cache's element type, lse [T][Hq] is float32. On a bfloat16 cache the weights
+    are rounded to bfloat16 before they meet v (dense_attn keeps them in float32)."""
+    _attend(kv, "tree_attn", load().prhs_tree_attn, q, k_new, v_new, scale, cu_new, max_new, tree_mask, (), out, lse, ws,
+            stream)
 
 
 def commit_tokens(kv, cu_new, accept_n, new_lens=None, *, slots=None, accept_idx=None, k_new=None,
@@ -596,6 +604,29 @@ def find_shared(kv, cu_new, shared, *, min_keys=256, stream=None) -> None:
     dev, i32, B = kv.device, torch.int32, kv.desc.B
     _call(kv, "find_shared", load().prhs_find_shared, stream, kv.ref(), _array(cu_new, "cu_new", (B + 1,), i32, dev),
           int(min_keys), _array(shared, "shared", (B, 4), i32, dev))
+
+
+def shared_workspace_size(kv: KVCache, T: int, max_new: int) -> int:
+    with torch.cuda.device(kv.index):
+        n = load().prhs_shared_workspace_size(kv.ref(), int(T), int(max_new))
+    if n == 0:
+        raise PrhsError(PRHS_EINVAL, "shared_workspace_size", load().prhs_last_message().decode())
+    return n
+
+
+def make_shared_workspace(kv: KVCache, T: int, max_new: int):
+    """Allocate (through torch) the workspace of shared_attn for T packed tokens, at
+    most max_new of a sequence."""
+    return torch.empty(shared_workspace_size(kv, T, max_new), dtype=torch.uint8, device=kv.device)
+
+
+def shared_attn(kv, q, k_new, v_new, scale, cu_new, max_new, shared, out, lse, ws, *, tree_mask=None,
+                stream=None) -> None:
+    """tree_attn for a batch whose groups of consecutive rows share leading keys, which
+    are read once for the group: shared [B][4] int32 as find_shared fills it
+    (prhs_shared_attn)."""
+    _attend(kv, "shared_attn", load().prhs_shared_attn, q, k_new, v_new, scale, cu_new, max_new, tree_mask,
+            (_array(shared, "shared", (kv.desc.B, 4), torch.int32, kv.device),), out, lse, ws, stream)
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:

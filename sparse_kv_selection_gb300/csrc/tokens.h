@@ -71,15 +71,26 @@ struct TreeLaunch {
   const uint32_t* mask;  // null: causal
   void* out;             // the cache's element type
   float* lse;
+  // rows that share leading keys (shared_attn; null: none do), and the partial
+  // states of tokens that have two: against the shared keys, against the others
+  const int4* shared;
+  float* part_o;    // [2][T * Hq][d], against the state's maximum
+  float2* part_ml;  // [2][T * Hq]: maximum (base 2) and sum
+  int* part_ok;     // 0: the offsets step back, there are no states
 };
 // fp32: two launches, the first counted by the callee; ws holds
 // tree_workspace(kv, max_new, sms) bytes.
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t s);
-size_t tree_workspace(const KVView& kv, int max_new, int sms);
+size_t tree_workspace(const KVView& kv, int max_new, int sms);  // (max_new: tree_most_new)
 // bf16: two launches, the first counted by the callee; *err is the launches'
 // result when the descriptors could be made. Workspace bytes of a call.
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
+
+// One launch: the result of the tokens with two partial states.
+cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t s);
+// The most tokens that a unit's rows may come from.
+inline int tree_most_new(const TreeLaunch& a) { return a.shared != nullptr ? a.T : a.max_new; }
 
 // TMA descriptor of a bf16 tensor with the 128-byte swizzle (dims and box
 // innermost first, strides in bytes from dimension 1 on).
@@ -117,6 +128,59 @@ __device__ __forceinline__ int seq_tokens(const int32_t* cu_new, int b, int T, i
     return 0;
   }
   return hi - lo;
+}
+
+// Leading keys that sequence b, of t cached keys, shares with its group, 0 if it is
+// alone. An entry that does not fit (its group, a length below the shared keys) is
+// flagged and read as alone. Whole pages only.
+__device__ __forceinline__ int shared_keys(const KVView& kv, const int4* shared, int b, int t) {
+  const int4 s = shared[b];
+  if (s.x == b && (s.y <= 1 || s.z == 0)) return 0;
+  bool ok = s.x >= 0 && s.x <= b;
+  const int4 g = ok ? shared[s.x] : s;
+  const int keys = kv.block_table != nullptr ? g.z / kv.block_size * kv.block_size : g.z;
+  ok = ok && g.x == s.x && b - s.x < g.y && keys >= 0 && keys <= t && keys <= kv.seq_lens[s.x];
+  if (ok) return keys;
+  raise_error(kv.err, PRHS_DEV_BAD_INDEX);
+  return 0;
+}
+
+// What the rows of a launch attend, item by item: sequence b's tokens over its own
+// cached keys from `base` on and over each other; or, for rows that share leading
+// keys, an item in front of that of a group's first row: all its rows' tokens over
+// the shared keys of that row. (Items 2 b and 2 b + 1; without sharing, item b.)
+struct TreeItem {
+  int b, base, t;  // row of the cache; its first key here, keys
+  int c0, n;       // tokens
+  int part;        // the state is the result (0), the one against the shared keys (1) or the others (2)
+};
+template <bool SHARED>
+__device__ __forceinline__ TreeItem tree_item(const TreeLaunch& a, int e) {
+  TreeItem x;
+  x.b = SHARED ? e >> 1 : e;
+  x.base = x.part = 0;
+  x.t = seq_len(a.kv, x.b);
+  if constexpr (SHARED) {
+    const int keys = shared_keys(a.kv, a.shared, x.b, x.t);
+    if (!(e & 1)) {
+      const int4 s = a.shared[x.b];
+      x.c0 = x.n = 0;
+      x.part = 1;
+      x.t = keys;
+      if (s.x != x.b || keys == 0) return x;
+      // (rows that are not within [0, T] are flagged by their own items)
+      x.c0 = max(0, a.cu_new[x.b]);
+      x.n = max(0, min(a.T, a.cu_new[min((long long)a.kv.B, (long long)x.b + s.y)]) - x.c0);
+      return x;
+    }
+    if (keys > 0) {
+      x.base = keys;
+      x.t -= keys;
+      x.part = 2;
+    }
+  }
+  x.n = seq_tokens(a.cu_new, x.b, a.T, a.max_new, a.kv.err, &x.c0);
+  return x;
 }
 
 // Row of KV head 0 of cache slot `slot`, and the rows from one head to the

@@ -188,10 +188,28 @@ size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new) {
   return tree_ws_bytes(abi_view(*kv, err), max_new, sms);
 }
 
-prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,
-                           const void* v_new, long long v_stride, float scale, int T,
-                           const int32_t* cu_new, int max_new, const uint32_t* tree_mask, void* out,
-                           float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// Workspace of shared attention: that of tree attention over units of up to T
+// tokens, and two partial states of every token.
+struct SharedWs {
+  size_t part_o, part_ml, part_ok, total;
+};
+SharedWs shared_ws(const KVView& kv, int T, int sms) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  SharedWs w;
+  w.part_o = up(tree_ws_bytes(kv, T, sms));
+  w.part_ml = w.part_o + up((size_t)2 * T * kv.Hq * kv.d * sizeof(float));
+  w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
+  w.total = w.part_ok + 256;
+  return w;
+}
+
+prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride, const void* v_new,
+                   long long v_stride, float scale, int T, const int32_t* cu_new, int max_new, const uint32_t* tree_mask,
+                   const int32_t* shared, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
   TreeLaunch a = {};
   int sms = 0;
   prhs_status s = abi_check_kv(kv);
@@ -201,20 +219,20 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   if (max_new <= 0) return abi_fail(PRHS_EINVAL, "tree: max_new must be positive");
   if (tree_mask && max_new > PRHS_TREE_MAX)
     return abi_fail(PRHS_EINVAL, "tree: max_new above PRHS_TREE_MAX with tree_mask");
-  if (!al16(q) || !al16(out) || !al16(tree_mask))
-    return abi_fail(PRHS_EINVAL, "tree: q, out and tree_mask must be 16-byte aligned");
+  if (!al16(q) || !al16(out) || !al16(tree_mask) || !al16(shared))
+    return abi_fail(PRHS_EINVAL, "tree: q, out, tree_mask and shared must be 16-byte aligned");
   if ((s = check_new(*kv, k_new, k_stride, v_new, v_stride, "tree: k_new and v_new must be 16-byte aligned")) != PRHS_OK)
     return s;
   if ((s = begin(kv, T, &a.kv, &sms)) != PRHS_OK) return s;
   // 32-bit tile counts: units (256 rows of tokens times group) times their tiles
   const int G = kv->Hq / kv->Hkv;
-  const long long units = ((long long)T * G / 256 + kv->B) * kv->Hkv;
+  const long long units = ((long long)T * G / 256 + kv->B) * kv->Hkv * (shared ? 2 : 1);
   if (units * (a.kv.t_max / 128 + (max_new < T ? max_new : T) / 128 + 2) >= (1ll << 31))
     return abi_fail(PRHS_EUNSUPPORTED, "tree: too many key tiles for one call");
-  const size_t need = tree_ws_bytes(a.kv, max_new, sms);
   if (!ws) return abi_fail(PRHS_EWORKSPACE, "workspace is null");
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return abi_fail(PRHS_EWORKSPACE, "workspace must be 256-byte aligned");
-  if (ws_bytes < need) return abi_fail(PRHS_EWORKSPACE, "workspace is smaller than prhs_tree_workspace_size()");
+  if (!shared && ws_bytes < tree_ws_bytes(a.kv, max_new, sms))
+    return abi_fail(PRHS_EWORKSPACE, "workspace is smaller than prhs_tree_workspace_size()");
   if (T == 0) return PRHS_OK;
   a.q = q;
   a.k_new = k_new;
@@ -228,10 +246,53 @@ prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, 
   a.mask = tree_mask;
   a.out = out;
   a.lse = lse;
-  if (kv->dtype != PRHS_BF16) return launched(launch_tree(a, sms, ws, stream));
-  cudaError_t e;
-  if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
-  return launched(e);
+  if (shared) {
+    const SharedWs w = shared_ws(a.kv, T, sms);
+    if (ws_bytes < w.total) return abi_fail(PRHS_EWORKSPACE, "workspace is smaller than prhs_shared_workspace_size()");
+    a.shared = reinterpret_cast<const int4*>(shared);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part_o);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part_ml);
+    a.part_ok = reinterpret_cast<int*>(static_cast<char*>(ws) + w.part_ok);
+  }
+  cudaError_t e = cudaSuccess;
+  if (kv->dtype != PRHS_BF16) e = launch_tree(a, sms, ws, stream);
+  else if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
+  if (e != cudaSuccess || !shared) return launched(e);
+  abi_count_launch();
+  return launched(launch_shared_join(a, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+prhs_status prhs_tree_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,
+                           const void* v_new, long long v_stride, float scale, int T,
+                           const int32_t* cu_new, int max_new, const uint32_t* tree_mask, void* out,
+                           float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return attend(kv, q, k_new, k_stride, v_new, v_stride, scale, T, cu_new, max_new, tree_mask, nullptr, out, lse, ws,
+                ws_bytes, stream);
+}
+
+size_t prhs_shared_workspace_size(const prhs_kv* kv, int T, int max_new) {
+  KVView view;
+  int sms = 0;
+  if (T <= 0 || max_new <= 0) {
+    abi_fail(PRHS_EINVAL, "shared: T and max_new must be positive");
+    return 0;
+  }
+  if (begin(kv, T, &view, &sms) != PRHS_OK) return 0;
+  return shared_ws(view, T, sms).total;
+}
+
+prhs_status prhs_shared_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,
+                             const void* v_new, long long v_stride, float scale, int T,
+                             const int32_t* cu_new, int max_new, const uint32_t* tree_mask,
+                             const int32_t* shared, void* out, float* lse, void* ws, size_t ws_bytes,
+                             cudaStream_t stream) {
+  if (!shared) return abi_fail(PRHS_EINVAL, "shared: shared must be non-null");
+  return attend(kv, q, k_new, k_stride, v_new, v_stride, scale, T, cu_new, max_new, tree_mask, shared, out, lse, ws,
+                ws_bytes, stream);
 }
 
 static prhs_status commit(const prhs_kv* kv, int T, const int32_t* cu_new, const int32_t* slots,

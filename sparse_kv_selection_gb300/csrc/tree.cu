@@ -37,8 +37,9 @@ constexpr float T_LOG2E = 1.4426950408889634f;
 
 // A tile of a CTA's run.
 struct __align__(16) TreeStep {
-  int b, kvh, block, tile;  // sequence, KV head, unit of theirs, tile of the unit
+  int e, kvh, block, tile;  // item, KV head, unit of theirs, tile of the unit
   int tiles, c0, n, t;      // the unit's tiles, first token, tokens, cached keys
+  int b, base, part, pad;   // row of the cache, its first key here, where the state goes (TreeItem)
   int tile0, left, q, u;    // the unit's first tile in this run, tiles of the run behind this one, Q slot, tokens of a unit
 };
 
@@ -61,29 +62,31 @@ struct TreeShape {
   static_assert(bytes(STAGES, QS) <= LIMIT, "shared memory");
 };
 
-struct TreeSeq {  // one sequence's share of the list
-  int c0, n, t, u, blocks, cache_tiles;  // (u: tokens of a unit)
+struct TreeSeq : TreeItem {  // one item's share of the list
+  int u, blocks, cache_tiles;  // (u: tokens of a unit)
   long long tiles;  // of one KV head
 };
 
 // Tokens that unit `block` of u tokens may attend, and its tiles: a causal unit
-// sees the tokens up to its own last one, a tree unit all of them.
+// sees the tokens up to its own last one, a tree unit all of them, a unit over
+// shared keys (part 1) none.
 __device__ __forceinline__ int tree_keys(int n, int block, int u, bool causal) {
   const long long end = ((long long)block + 1) * u;
   return causal && end < n ? (int)end : n;
 }
-__device__ __forceinline__ int tree_tiles(int t, int n, int block, int u, bool causal) {
-  return (int)(((long long)t + TK - 1) / TK) + (int)(((long long)tree_keys(n, block, u, causal) + TK - 1) / TK);
+__device__ __forceinline__ int tree_tiles(int t, int n, int block, int u, bool causal, int part) {
+  return (int)(((long long)t + TK - 1) / TK) +
+         (part == 1 ? 0 : (int)(((long long)tree_keys(n, block, u, causal) + TK - 1) / TK));
 }
 
 // New-token tiles of the units before unit j.
 constexpr int TREE_EVEN = 4;
 __device__ __forceinline__ long long tree_new_before(const TreeSeq& s, long long j, int ul, bool causal) {
-  const int all_tiles = tree_tiles(0, s.n, 0, s.n, false);
-  if (!causal) return j * all_tiles;
+  const int all_tiles = tree_tiles(0, s.n, 0, s.n, false, s.part);
+  if (!causal || s.part == 1) return j * all_tiles;
   long long sum = 0;
   if (s.blocks <= TREE_EVEN) {
-    for (int i = 0; i < j; i++) sum += tree_tiles(0, s.n, i, s.u, true);
+    for (int i = 0; i < j; i++) sum += tree_tiles(0, s.n, i, s.u, true, s.part);
     return sum;
   }
   const bool all = j == s.blocks;
@@ -101,11 +104,11 @@ __device__ __forceinline__ long long tree_new_before(const TreeSeq& s, long long
 // A sequence's units hold up to 2^ul tokens: equal shares where they are few or
 // a tree's (9 tokens of 8 query heads in two units of 64 rows: 5 and 4 tokens, not
 // 8 and 1, since the runs count tiles, not rows).
-__device__ __forceinline__ TreeSeq tree_seq(const TreeLaunch& a, int b, int ul) {
+template <bool SHARED>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeLaunch& a, int e, int ul) {
   TreeSeq s;
   const bool causal = a.mask == nullptr;
-  s.t = seq_len(a.kv, b);
-  s.n = seq_tokens(a.cu_new, b, a.T, a.max_new, a.kv.err, &s.c0);
+  static_cast<TreeItem&>(s) = tree_item<SHARED>(a, e);
   s.u = 1 << ul;
   s.blocks = (int)(((long long)s.n + s.u - 1) >> ul);
   s.cache_tiles = (int)(((long long)s.t + TK - 1) / TK);
@@ -125,7 +128,7 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool have) 
                : "memory");
 }
 
-template <int D, int TY, int R, int W, int CTAS>
+template <int D, int TY, int R, int W, int CTAS, bool SHARED>
 __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constant__ TreeLaunch a,
                                                                  const __grid_constant__ TreeRecords p) {
   using S = TreeShape<D, TY, R, W, CTAS>;
@@ -145,12 +148,14 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   const int gl = p.group_log2, ul = S::TR_LOG2 - gl;  // log2 of the group and of a unit's tokens
 
   // ---- this CTA's run of the list of all tiles ----
-  const int per_t = (kv.B + THREADS - 1) / THREADS, b0 = tid * per_t;
+  const int items = SHARED ? 2 * kv.B : kv.B;
+  const int per_t = (items + THREADS - 1) / THREADS, e0 = tid * per_t;
   long long mine = 0;
   bool back = false;  // offsets that step back: sequences would overlap, without bound
-  for (int b = b0; b < min(kv.B, b0 + per_t); b++) {
-    mine += kv.Hkv * tree_seq(a, b, ul).tiles;
-    back |= a.cu_new[b + 1] < a.cu_new[b];
+  for (int e = e0; e < min(items, e0 + per_t); e++) {
+    const TreeSeq s = tree_seq<SHARED>(a, e, ul);
+    mine += kv.Hkv * s.tiles;
+    back |= a.cu_new[s.b + 1] < a.cu_new[s.b];
   }
   long long run = mine;
 #pragma unroll
@@ -160,6 +165,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   }
   if (lane == 31) wsum[warp] = run;
   back = __syncthreads_or(back);  // (flagged by tree_seq)
+  if (SHARED && blockIdx.x == 0 && tid == 0) *a.part_ok = !back;
   long long total = 0, before = run - mine;
 #pragma unroll
   for (int w = 0; w < W; w++) {
@@ -172,16 +178,19 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     if (tid == 0) p.split[blockIdx.x] = TreeSplit{};
     return;
   }
-  if (g0 >= before && g0 < before + mine) {  // the run begins in this thread's sequences
+  if (g0 >= before && g0 < before + mine) {  // the run begins in this thread's items
     long long off = g0 - before;
-    int b = b0;
-    TreeSeq s = tree_seq(a, b, ul);
+    int e = e0;
+    TreeSeq s = tree_seq<SHARED>(a, e, ul);
     while (off >= kv.Hkv * s.tiles) {
       off -= kv.Hkv * s.tiles;
-      s = tree_seq(a, ++b, ul);
+      s = tree_seq<SHARED>(a, ++e, ul);
     }
     TreeStep x;
-    x.b = b;
+    x.e = e;
+    x.b = s.b;
+    x.base = s.base;
+    x.part = s.part;
     x.kvh = (int)(off / s.tiles);
     off -= x.kvh * s.tiles;
     int lo = 0, hi = s.blocks - 1;
@@ -191,7 +200,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     }
     x.block = lo;
     x.tile = x.tile0 = (int)(off - (long long)lo * s.cache_tiles - tree_new_before(s, lo, ul, causal));
-    x.tiles = tree_tiles(s.t, s.n, lo, s.u, causal);
+    x.tiles = tree_tiles(s.t, s.n, lo, s.u, causal, s.part);
     x.c0 = s.c0;
     x.n = s.n;
     x.t = s.t;
@@ -213,14 +222,17 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
         if (++x.kvh == kv.Hkv) {
           x.kvh = 0;
           TreeSeq s = {};
-          while (s.n == 0 && ++x.b < kv.B) s = tree_seq(a, x.b, ul);
+          while (s.n == 0 && ++x.e < items) s = tree_seq<SHARED>(a, x.e, ul);
+          x.b = s.b;
+          x.base = s.base;
+          x.part = s.part;
           x.c0 = s.c0;
           x.n = s.n;
           x.t = s.t;
           x.u = s.u;
         }
       }
-      x.tiles = tree_tiles(x.t, x.n, x.block, x.u, causal);
+      x.tiles = tree_tiles(x.t, x.n, x.block, x.u, causal, x.part);
     }
     return x;
   };
@@ -265,7 +277,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     const bool cached = x.tile < ct;
     const int i = (cached ? x.tile : x.tile - ct) * TK + lane;
     if (i >= (cached ? x.t : tree_keys(x.n, x.block, x.u, causal))) return -1;
-    return cached ? kv_row(kv, x.b, x.kvh, i) : i;
+    return cached ? kv_row(kv, x.b, x.kvh, (SHARED ? x.base : 0) + i) : i;
   };
   auto found = [&](const TreeStep& x, int slot, long long row) {
     key_row[slot][lane] = row;
@@ -457,6 +469,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
         y.kvh = x.kvh;
         y.tok = (int)(x.c0 + (long long)x.block * x.u);
         y.first = (int)(start / per);
+        y.part = x.part;
         y.n_rec = (int)((start + x.tiles - 1) / per) - y.first + 1;
       }
       p.split[blockIdx.x] = y;
@@ -484,8 +497,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
       __syncwarp();  // (read by all lanes of the row before one overwrites it)
       if (r >= rows) continue;
       const long long orow = (x.c0 + ((row0 + r) >> gl)) * kv.Hq + (x.kvh << gl) + (r & ((1 << gl) - 1));
-      const float inv = whole ? tree_inv(sum) : 1.f;
-      float* dst = (whole ? static_cast<float*>(a.out) + orow * D : reinterpret_cast<float*>(p.o) + (rec + r) * D) + tx * 4;
+      const bool result = whole && (!SHARED || x.part == 0);
+      const long long prow = SHARED ? tree_part_row(a, x.part, orow) : 0;
+      const float inv = result ? tree_inv(sum) : 1.f;
+      float* dst = (result            ? static_cast<float*>(a.out) + orow * D
+                    : SHARED && whole ? a.part_o + prow * D
+                                      : reinterpret_cast<float*>(p.o) + (rec + r) * D) + tx * 4;
 #pragma unroll
       for (int c = 0; c < C4; c++) {
         float4 y;
@@ -494,7 +511,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
         *reinterpret_cast<float4*>(dst + c * TX * 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       }
       if (tx == 0) {
-        if (whole) a.lse[orow] = tree_lse(m[i], sum);
+        if (result) a.lse[orow] = tree_lse(m[i], sum);
+        else if (SHARED && whole) a.part_ml[prow] = make_float2(m[i], sum);
         else p.ml[rec + r] = make_float2(m[i], sum);
       }
       if (last) continue;
@@ -535,30 +553,37 @@ size_t tree_workspace(const KVView& kv, int max_new, int sms) {
   return need;
 }
 
-template <int D, int TY, int R, int W>
+template <int D, int TY, int R, int W, bool SHARED>
 static cudaError_t tree_go(const TreeLaunch& a, const TreeRecords& p, int sms, cudaStream_t st) {
   constexpr int CTAS = tree_ctas_sm(D, TY * R * W);
   using S = TreeShape<D, TY, R, W, CTAS>;
-  auto k = tree_kernel<D, TY, R, W, CTAS>;
+  auto k = tree_kernel<D, TY, R, W, CTAS, SHARED>;
   static int smem_set[SMEM_DEVICES];
   cudaError_t e = allow_smem(k, S::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   // no more CTAs than tiles that the longest caches would give
-  const long long units = (((long long)a.max_new << p.group_log2) + S::TR - 1) / S::TR * a.kv.B * a.kv.Hkv;
-  const long long tiles = units * ((a.kv.t_max + TK - 1ll) / TK + (a.max_new + TK - 1ll) / TK);
+  const long long units = (((long long)tree_most_new(a) << p.group_log2) + S::TR - 1) / S::TR * a.kv.B * a.kv.Hkv;
+  const long long tiles = (SHARED ? 2 : 1) * units * ((a.kv.t_max + TK - 1ll) / TK + (a.max_new + TK - 1ll) / TK);
   const unsigned ctas = (unsigned)(tiles < CTAS * sms ? tiles : CTAS * sms);
   if ((e = launch_pdl(k, dim3(ctas), dim3(S::THREADS), S::SMEM, st, a.kv.pdl, a, p)) != cudaSuccess) return e;
   abi_count_launch();
   return launch_tree_join<float, D, true>(a, p, ctas, st);
 }
 
+template <bool SHARED>
+static cudaError_t tree_form(const TreeLaunch& a, const TreeRecords& p, int rows, int sms, cudaStream_t st) {
+  const bool wide = a.kv.d == 128;
+  if (rows == 8) return wide ? tree_go<128, 2, 2, 2, SHARED>(a, p, sms, st) : tree_go<64, 2, 2, 2, SHARED>(a, p, sms, st);
+  if (rows == 32) return wide ? tree_go<128, 2, 4, 4, SHARED>(a, p, sms, st) : tree_go<64, 2, 4, 4, SHARED>(a, p, sms, st);
+  return wide ? tree_go<128, 4, 4, 4, SHARED>(a, p, sms, st) : tree_go<64, 4, 4, 4, SHARED>(a, p, sms, st);
+}
+
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t st) {
   const KVView& kv = a.kv;
-  const int G = kv.Hq / kv.Hkv, rows = tree_rows(kv, a.max_new);
+  const int G = kv.Hq / kv.Hkv, rows = tree_rows(kv, tree_most_new(a));
   const TreeRecords p = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, tree_ctas(kv, rows, sms), rows);
-  if (rows == 8) return kv.d == 128 ? tree_go<128, 2, 2, 2>(a, p, sms, st) : tree_go<64, 2, 2, 2>(a, p, sms, st);
-  if (rows == 32) return kv.d == 128 ? tree_go<128, 2, 4, 4>(a, p, sms, st) : tree_go<64, 2, 4, 4>(a, p, sms, st);
-  return kv.d == 128 ? tree_go<128, 4, 4, 4>(a, p, sms, st) : tree_go<64, 4, 4, 4>(a, p, sms, st);
+  if (a.shared != nullptr) return tree_form<true>(a, p, rows, sms, st);
+  return tree_form<false>(a, p, rows, sms, st);
 }
 
 }  // namespace prhs

@@ -10,7 +10,7 @@ namespace prhs {
 // What a CTA's run leaves behind: the unit that does not end in it.
 struct __align__(16) TreeSplit {
   int rows, kvh, tok, n_rec;  // rows of the unit (0: none), KV head, first token (packed), records
-  int first, pad[3];          // the CTA that begins it
+  int first, part, pad[2];    // the CTA that begins it; where its state goes (TreeItem)
 };
 
 // Partial states: the running maximum (base 2), the sum and O against that
@@ -48,6 +48,11 @@ __device__ __forceinline__ void tree_put(float* dst, float4 x) { *reinterpret_ca
 __device__ __forceinline__ void tree_put(__nv_bfloat16* dst, float4 x) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
   *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Row of the partial states of a result's row.
+__device__ __forceinline__ long long tree_part_row(const TreeLaunch& a, int part, long long orow) {
+  return (part == 2 ? (long long)a.T * a.kv.Hq : 0ll) + orow;
 }
 
 template <typename T, int D, bool ROW_MAJOR>
@@ -118,6 +123,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const __grid_co
     const int gl = p.group_log2;
     const float inv = tree_inv(L);
     const long long orow = (long long)(s.tok + (row >> gl)) * a.kv.Hq + (s.kvh << gl) + (row & ((1 << gl) - 1));
+    if (s.part != 0) {
+      const long long prow = tree_part_row(a, s.part, orow);
+      tree_put(a.part_o + prow * D + c * 4, o);
+      if (c == 0) a.part_ml[prow] = make_float2(M, L);
+      continue;
+    }
     tree_put(static_cast<T*>(a.out) + orow * D + c * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     if (c == 0) a.lse[orow] = tree_lse(M, L);
   }

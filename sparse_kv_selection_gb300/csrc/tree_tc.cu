@@ -82,7 +82,8 @@ struct __align__(16) TcWork {
   int b, kvh, c0, n;        // sequence, KV head, first token, tokens
   int t, tok0, rows, tile0; // cached keys, the unit's first token and rows, its first tile here
   int nt, cache_tiles, loads, qtiles;  // tiles here; K and V / Q tiles loaded before
-  int whole, last, pad[2];  // all of the unit's tiles are here; the run ends with it
+  int whole, last;          // all of the unit's tiles are here; the run ends with it
+  int base, part;           // the first cached key; where its state goes (TreeItem)
 
   __device__ __forceinline__ bool single() const { return rows <= TT; }
   // steps of the unit: step x is stream x & 1 on tile tile0 + (single ? x : x / 2)
@@ -116,8 +117,7 @@ struct TcRing {
   }
 };
 
-struct TcSeq {  // one sequence's share of the list
-  int c0, n, t;      // first token, tokens, cached keys
+struct TcSeq : TreeItem {  // one item's share of the list
   int blocks;        // units of one KV head
   int cache_tiles;
   int tiles;         // tiles of one KV head
@@ -133,7 +133,7 @@ struct TcAux {
   TcBars bar;
   uint32_t tmem;
   int bad_page;
-  int start_b, start_off;  // where the run begins
+  int start_item, start_off;  // where the run begins
   int begin, end;          // the run
   int wsum[TC_WARPS], wmax[TC_WARPS];
 };
@@ -295,40 +295,46 @@ __device__ __forceinline__ int new_tiles_before(int j, int blocks, int n, int ul
   return all ? s + ((n + TT - 1) >> 7) : s;
 }
 
-__device__ __forceinline__ TcSeq tc_seq(const TreeLaunch& a, int b, int ul) {
+// Tiles of the units of item s before unit j.
+__device__ __forceinline__ int tiles_before(const TcSeq& s, int j, int ul, bool causal) {
+  return j * s.cache_tiles + (s.part == 1 ? 0 : new_tiles_before(j, s.blocks, s.n, ul, causal));
+}
+template <bool SHARED>
+__device__ __forceinline__ TcSeq tc_seq(const TreeLaunch& a, int e, int ul) {
   TcSeq s;
-  s.t = seq_len(a.kv, b);
-  s.n = seq_tokens(a.cu_new, b, a.T, a.max_new, a.kv.err, &s.c0);
+  static_cast<TreeItem&>(s) = tree_item<SHARED>(a, e);
   s.blocks = (s.n + (1 << ul) - 1) >> ul;
   s.cache_tiles = (s.t + TT - 1) >> 7;
-  s.tiles = s.blocks == 0 ? 0 : s.blocks * s.cache_tiles + new_tiles_before(s.blocks, s.blocks, s.n, ul, a.mask == nullptr);
+  s.tiles = s.blocks == 0 ? 0 : tiles_before(s, s.blocks, ul, a.mask == nullptr);
   return s;
 }
 // Tiles of unit `block`.
 __device__ __forceinline__ int tc_unit_tiles(const TcSeq& s, int block, int ul, bool causal) {
+  if (s.part == 1) return s.cache_tiles;
   return s.cache_tiles + (causal ? (min(s.n, (block + 1) << ul) + TT - 1) >> 7 : 1);
 }
-// The unit that holds tile `off` of a sequence's share: KV head, unit, the tile's
+// The unit that holds tile `off` of an item's share: KV head, unit, the tile's
 // number in it and the tiles from there to the next unit's first (0 from a first
 // one).
-__device__ __forceinline__ int4 tc_unit_at(const TreeLaunch& a, int b, int off, int ul) {
+template <bool SHARED>
+__device__ __forceinline__ int4 tc_unit_at(const TreeLaunch& a, int e, int off, int ul) {
   const bool causal = a.mask == nullptr;
-  const TcSeq s = tc_seq(a, b, ul);
+  const TcSeq s = tc_seq<SHARED>(a, e, ul);
   const int kvh = off / s.tiles;
   off -= kvh * s.tiles;
   int block = 0, hi = s.blocks - 1;
   while (block < hi) {
     const int mid = (block + hi + 1) >> 1;
-    if (mid * s.cache_tiles + new_tiles_before(mid, s.blocks, s.n, ul, causal) <= off) block = mid; else hi = mid - 1;
+    if (tiles_before(s, mid, ul, causal) <= off) block = mid; else hi = mid - 1;
   }
-  off -= block * s.cache_tiles + new_tiles_before(block, s.blocks, s.n, ul, causal);
+  off -= tiles_before(s, block, ul, causal);
   return make_int4(kvh, block, off, off == 0 ? 0 : tc_unit_tiles(s, block, ul, causal) - off);
 }
 
 // -------------------------------------------------------------------------- //
 // the kernel
 // -------------------------------------------------------------------------- //
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ktail,
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const TreeLaunch& a = p.a;
   const KVView& kv = a.kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = kv.B, gl = p.rec.group_log2, ul = 8 - gl;  // log2 of the group and of a unit's tokens
+  const int items = SHARED ? 2 * kv.B : kv.B, gl = p.rec.group_log2, ul = 8 - gl;  // log2 of the group and of a unit's tokens
   const uint32_t base = smem_addr(tc_smem);
   uint8_t* data = tc_smem;
   TcAux& aux = *reinterpret_cast<TcAux*>(data + S::DATA);
@@ -375,12 +381,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
 
   // ---- this CTA's run of the list of all tiles ----
-  const int per_t = (B + TC_THREADS - 1) / TC_THREADS, b0 = tid * per_t;
-  int mine = 0, most = 0;  // tiles of this thread's sequences, of their largest unit
+  const int per_t = (items + TC_THREADS - 1) / TC_THREADS, e0 = tid * per_t;
+  int mine = 0, most = 0;  // tiles of this thread's items, of their largest unit
   bool back = false;       // offsets that step back: sequences would overlap, and counts pass 32 bits
-  for (int b = b0; b < min(B, b0 + per_t); b++) {
-    const TcSeq s = tc_seq(a, b, ul);
-    back |= a.cu_new[b + 1] < a.cu_new[b];
+  for (int e = e0; e < min(items, e0 + per_t); e++) {
+    const TcSeq s = tc_seq<SHARED>(a, e, ul);
+    back |= a.cu_new[s.b + 1] < a.cu_new[s.b];
     mine += kv.Hkv * s.tiles;
     if (s.blocks > 0) most = max(most, tc_unit_tiles(s, s.blocks - 1, ul, a.mask == nullptr));
   }
@@ -395,7 +401,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     aux.wsum[warp] = run;
     aux.wmax[warp] = most;
   }
-  if (__syncthreads_or(back)) return;  // (flagged above)
+  back = __syncthreads_or(back);
+  if (SHARED && blockIdx.x == 0 && tid == 0) *a.part_ok = !back;
+  if (back) return;  // (flagged above)
   int total = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < TC_WARPS; w++) {
@@ -418,15 +426,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll 1
   for (int i = 0; i <= (int)uncut; i++) {
     const int g = i == 0 ? g0 : g1;
-    if (g >= total || g < before || g >= before + mine) continue;  // not in this thread's sequences
+    if (g >= total || g < before || g >= before + mine) continue;  // not in this thread's items
     int off = g - before;
     for (int k = 0; k < per_t; k++) {
-      const int b = tid * per_t + k, x = kv.Hkv * tc_seq(a, b, ul).tiles;
+      const int e = tid * per_t + k, x = kv.Hkv * tc_seq<SHARED>(a, e, ul).tiles;
       if (off < x) {
-        const int skip = uncut ? tc_unit_at(a, b, off, ul).w : 0;
+        const int skip = uncut ? tc_unit_at<SHARED>(a, e, off, ul).w : 0;
         if (i == 0) {
-          aux.start_b = b;
-          aux.start_off = off + skip;  // (may lead to the next sequence)
+          aux.start_item = e;
+          aux.start_off = off + skip;  // (may lead to the next item)
           aux.begin = g + skip;
         }
         if (i == 1 || !uncut || g1 >= total) aux.end = i == 1 ? g + skip : g1;
@@ -466,14 +474,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (warp == 11) {
       // ---------------------- scheduler, and Q producer ---------------------- //
       const bool leader = elect_one();
-      int b = aux.start_b, off = aux.start_off, left = aux.end - aux.begin, loads = 0, qtiles = 0;
+      int item = aux.start_item, off = aux.start_off, left = aux.end - aux.begin, loads = 0, qtiles = 0;
       const bool causal = a.mask == nullptr;
-      TcSeq s = tc_seq(a, b, ul);
+      TcSeq s = tc_seq<SHARED>(a, item, ul);
       while (off >= kv.Hkv * s.tiles) {
         off -= kv.Hkv * s.tiles;
-        s = tc_seq(a, ++b, ul);
+        s = tc_seq<SHARED>(a, ++item, ul);
       }
-      const int4 at = tc_unit_at(a, b, off, ul);
+      const int4 at = tc_unit_at<SHARED>(a, item, off, ul);
       int kvh = at.x, block = at.y;
       off = at.z;
       for (int k = 0;; k++) {
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const int rows = min(UNIT_ROWS, (s.n - (block << ul)) << gl);
         if (lane == 0) {
           TcWork& w = aux.work[i];
-          w.b = b;
+          w.b = s.b;
           w.kvh = kvh;
           w.c0 = s.c0;
           w.n = s.n;
@@ -499,6 +507,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           w.qtiles = qtiles;
           w.whole = nt == tiles;
           w.last = left == 0;
+          w.base = s.base;
+          w.part = s.part;
           mbar_arrive(&bar.wfull[i]);
           if (left == 0) {
             TreeSplit sp = {};
@@ -508,6 +518,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               sp.kvh = kvh;
               sp.tok = s.c0 + (block << ul);
               sp.first = start / per;
+              sp.part = s.part;
               sp.n_rec = (start + tiles - 1) / per - sp.first + 1;
             }
             p.rec.split[blockIdx.x] = sp;
@@ -535,7 +546,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           block = 0;
           if (++kvh == kv.Hkv) {
             kvh = 0;
-            do s = tc_seq(a, ++b, ul);
+            do s = tc_seq<SHARED>(a, ++item, ul);
             while (s.blocks == 0);
           }
         }
@@ -545,6 +556,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     } else if (warp != 9) {
       // -------- K and V producers: a column segment each, or every second box -------- //
       const bool leader = elect_one();
+      auto base_key = [](const TcWork& w) { return SHARED ? w.base : 0; };
       const int half = warp == 8 ? 0 : 1;
       const int br_log2 = p.box_log2, br = 1 << br_log2, per_log2 = 7 - br_log2;
       int last = -1;
@@ -556,10 +568,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         auto page_of = [&](int box) -> int {
           const int key = box << br_log2;
           if (kv.block_table == nullptr || key >= w.t) return 0;
-          return kv.block_table[(long long)w.b * kv.max_blocks + key / kv.block_size];
+          return kv.block_table[(long long)w.b * kv.max_blocks + (base_key(w) + key) / kv.block_size];
         };
         auto row_of = [&](int page, int box) -> int {
-          const int key = box << br_log2;
+          const int key = base_key(w) + (box << br_log2);
           if (kv.block_table == nullptr) return (w.b * kv.Hkv + w.kvh) * kv.t_max + key;
           if ((unsigned)page >= (unsigned)kv.num_blocks) {  // the softmax masks its keys
             raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           uint32_t ok16 = 0xff;  // 16-key groups on pages of the pool
           if (bad) {
             const int k = (lane & 7) * 16;
-            ok16 = __ballot_sync(FULL_MASK, k >= valid || kv_row(kv, w.b, w.kvh, key0 + k) >= 0) & 0xff;
+            ok16 = __ballot_sync(FULL_MASK, k >= valid || kv_row(kv, w.b, w.kvh, (SHARED ? w.base : 0) + key0 + k) >= 0) & 0xff;
           }
 #pragma unroll
           for (int c = 0; c < 4; c++) {
@@ -882,7 +894,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       tc_fence_after();
       const bool live = ur < w.rows && !dead;
-      if (w.whole) {
+      const bool result = w.whole && (!SHARED || w.part == 0);
+      if (result) {
         const float inv = tree_inv(L);
         w0 *= inv;
         w1 *= inv;
@@ -910,7 +923,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           const float v = __uint_as_float(o[e]) * w0;
           o[e] = __float_as_uint(two ? fmaf(__uint_as_float(o1[e]), w1, v) : v);
         }
-        if (w.whole) {
+        if (result) {
           uint32_t v[4][4];
 #pragma unroll
           for (int e = 0; e < 4; e++)
@@ -935,6 +948,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               *reinterpret_cast<uint4*>(out + out_row(r) * D + c * 32 + (lane & 3) * 8) =
                   make_uint4(v[e][0], v[e][1], v[e][2], v[e][3]);
           }
+        } else if (SHARED && w.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + tree_part_row(a, w.part, out_row(ur)) * D + c * 32);
+          if (live)
+#pragma unroll
+            for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(p.rec.o) + (rec * (D / 4) + c * 8) * p.rec.rows_max + ur;
 #pragma unroll
@@ -943,7 +961,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
       }
       if (live && (!both || st == 0)) {
-        if (w.whole) a.lse[out_row(ur)] = tree_lse(M, L);
+        if (result) a.lse[out_row(ur)] = tree_lse(M, L);
+        else if (SHARED && w.whole) a.part_ml[tree_part_row(a, w.part, out_row(ur))] = make_float2(M, L);
         else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();
@@ -979,10 +998,10 @@ static int tc_box_log2(const KVView& kv) {
   return r;
 }
 
-template <int D>
+template <int D, bool SHARED>
 static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cudaStream_t st) {
   using S = TcShape<D>;
-  auto k = tree_tc_kernel<D>;
+  auto k = tree_tc_kernel<D, SHARED>;
   // the register shares need what the kernel was compiled with, asked once
   static const int regs = [k] {
     cudaFuncAttributes at;
@@ -1005,7 +1024,7 @@ prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t 
   const int G = kv.Hq / kv.Hkv;
   TcLaunch p;
   p.a = a;
-  p.rec = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, sms, tc_rows_max(kv, a.max_new));
+  p.rec = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, sms, tc_rows_max(kv, tree_most_new(a)));
   p.box_log2 = tc_box_log2(kv);
 
   CUtensorMap maps[7];  // q; cache K and V; their partial tiles; new K and V
@@ -1028,7 +1047,8 @@ prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t 
   if ((s = abi_encode_bf16(&maps[4], kv.v, 4, cd, cs, tb)) != PRHS_OK) return s;
   if ((s = abi_encode_bf16(&maps[5], a.k_new, 4, nd, ks, nb)) != PRHS_OK) return s;
   if ((s = abi_encode_bf16(&maps[6], a.v_new, 4, nd, vs, nb)) != PRHS_OK) return s;
-  *err = kv.d == 128 ? tc_go<128>(p, maps, sms, st) : tc_go<64>(p, maps, sms, st);
+  if (a.shared != nullptr) *err = kv.d == 128 ? tc_go<128, true>(p, maps, sms, st) : tc_go<64, true>(p, maps, sms, st);
+  else *err = kv.d == 128 ? tc_go<128, false>(p, maps, sms, st) : tc_go<64, false>(p, maps, sms, st);
   return PRHS_OK;
 }
 

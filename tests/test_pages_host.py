@@ -76,3 +76,21 @@ def test_find_shared_refusals(lib, over):  # noqa: F811
     a = {**dict(cu=64, min_keys=16, shared=64), **over}
     assert lib.prhs_find_shared(ctypes.byref(paged(b)), *a.values(), None) == b.PRHS_EINVAL
     assert lib.prhs_last_message().decode() != ""
+
+
+SHARED = dict(q=64, k=64, ks=512, v=64, vs=512, scale=0.1, T=4, cu=64, max_new=4, mask=None, shared=64, out=64, lse=64,
+              ws=256, bytes=1 << 40)
+
+
+@pytest.mark.parametrize("over", [dict(q=None), dict(k=None), dict(v=None), dict(cu=None), dict(shared=None), dict(out=None),
+                                  dict(lse=None), dict(q=72), dict(k=72), dict(v=72), dict(out=72), dict(mask=72),
+                                  dict(shared=72), dict(ks=510), dict(vs=100), dict(T=-1), dict(max_new=0),
+                                  dict(max_new=129, mask=64)])
+def test_shared_attn_refusals(lib, over):  # noqa: F811
+    from sparse_kv_selection_gb300 import binding as b
+    a = {**SHARED, **over}
+    assert lib.prhs_shared_attn(ctypes.byref(_kv(b)), *a.values(), None) == b.PRHS_EINVAL
+    assert lib.prhs_last_message().decode() != ""
+    assert lib.prhs_shared_workspace_size(ctypes.byref(_kv(b)), 0, 4) == 0
+    assert lib.prhs_shared_workspace_size(ctypes.byref(_kv(b)), 4, 0) == 0
+    assert lib.prhs_shared_workspace_size(ctypes.byref(_kv(b, d=96)), 4, 4) == 0
