@@ -73,11 +73,28 @@ struct TreeLaunch {
   float* lse;
   // rows that share leading keys (shared_attn; null: none do), and the partial
   // states of tokens that have two: against the shared keys, against the others
+  // (fp32: [2][T * Hq][d] and [2][T * Hq]; bf16: [2][Hkv][d / 4][T * G] of four columns
+  // and [2][Hkv][T * G])
   const int4* shared;
-  float* part_o;    // [2][T * Hq][d], against the state's maximum
-  float2* part_ml;  // [2][T * Hq]: maximum (base 2) and sum
+  float* part_o;    // against the state's maximum
+  float2* part_ml;  // maximum (base 2) and sum
   int* part_ok;     // 0: the offsets step back, there are no states
+  // bf16: sequences whose own keys the joining launch attends (few_item): query rows
+  // of a CTA, CTAs of rows a KV head
+  int few_rows, few_blocks;
+  int few_units, few_split;  // units, CTAs of a unit at most
+  void* few_states;          // [units][few_split] states of units that several CTAs share
+  int* few_ticket;           // [units] of those CTAs, how many have written theirs
 };
+// Whether the joining launch attends a sequence's own t keys with its n tokens of G
+// query heads a KV head: a tile of the matrix units costs a few microseconds to begin
+// and to end, more than a short run of keys takes to read. Every CTA of rows reads
+// the keys again, from L2.
+constexpr int FEW_KEYS = 4096;
+__device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
+  const long long blocks = ((long long)n * (a.kv.Hq / a.kv.Hkv) + a.few_rows - 1) / max(a.few_rows, 1);
+  return a.few_rows > 0 && blocks <= a.few_blocks && blocks * ((long long)t + n) <= FEW_KEYS;
+}
 // fp32: two launches, the first counted by the callee; ws holds
 // tree_workspace(kv, max_new, sms) bytes.
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t s);
@@ -87,7 +104,11 @@ size_t tree_workspace(const KVView& kv, int max_new, int sms);  // (max_new: tre
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
 
-// One launch: the result of the tokens with two partial states.
+// One launch: the result of the tokens with two partial states; bf16: also the
+// attention of few_item's sequences.
+void few_shape(TreeLaunch* a);
+size_t few_state_bytes(const KVView& kv, int max_new);
+size_t few_ticket_bytes(const KVView& kv, int max_new);
 cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t s);
 // The most tokens that a unit's rows may come from.
 inline int tree_most_new(const TreeLaunch& a) { return a.shared != nullptr ? a.T : a.max_new; }
@@ -148,14 +169,15 @@ __device__ __forceinline__ int shared_keys(const KVView& kv, const int4* shared,
 // What the rows of a launch attend, item by item: sequence b's tokens over its own
 // cached keys from `base` on and over each other; or, for rows that share leading
 // keys, an item in front of that of a group's first row: all its rows' tokens over
-// the shared keys of that row. (Items 2 b and 2 b + 1; without sharing, item b.)
+// the shared keys of that row. (Items 2 b and 2 b + 1; without sharing, item b.) Not
+// those that the joining launch attends, unless `all`.
 struct TreeItem {
   int b, base, t;  // row of the cache; its first key here, keys
   int c0, n;       // tokens
   int part;        // the state is the result (0), the one against the shared keys (1) or the others (2)
 };
 template <bool SHARED>
-__device__ __forceinline__ TreeItem tree_item(const TreeLaunch& a, int e) {
+__device__ __forceinline__ TreeItem tree_item(const TreeLaunch& a, int e, bool all = false) {
   TreeItem x;
   x.b = SHARED ? e >> 1 : e;
   x.base = x.part = 0;
@@ -180,6 +202,7 @@ __device__ __forceinline__ TreeItem tree_item(const TreeLaunch& a, int e) {
     }
   }
   x.n = seq_tokens(a.cu_new, x.b, a.T, a.max_new, a.kv.err, &x.c0);
+  if (SHARED && !all && few_item(a, x.n, x.t)) x.n = 0;
   return x;
 }
 

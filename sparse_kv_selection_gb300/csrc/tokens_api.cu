@@ -195,15 +195,17 @@ namespace {
 // Workspace of shared attention: that of tree attention over units of up to T
 // tokens, and two partial states of every token.
 struct SharedWs {
-  size_t part_o, part_ml, part_ok, total;
+  size_t part_o, part_ml, part_ok, states, ticket, total;
 };
-SharedWs shared_ws(const KVView& kv, int T, int sms) {
+SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   SharedWs w;
   w.part_o = up(tree_ws_bytes(kv, T, sms));
   w.part_ml = w.part_o + up((size_t)2 * T * kv.Hq * kv.d * sizeof(float));
   w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
-  w.total = w.part_ok + 256;
+  w.states = w.part_ok + 256;
+  w.ticket = w.states + up(few_state_bytes(kv, max_new));
+  w.total = w.ticket + up(few_ticket_bytes(kv, max_new));
   return w;
 }
 
@@ -247,12 +249,15 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
   a.out = out;
   a.lse = lse;
   if (shared) {
-    const SharedWs w = shared_ws(a.kv, T, sms);
+    const SharedWs w = shared_ws(a.kv, T, a.max_new, sms);
     if (ws_bytes < w.total) return abi_fail(PRHS_EWORKSPACE, "workspace is smaller than prhs_shared_workspace_size()");
     a.shared = reinterpret_cast<const int4*>(shared);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part_o);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part_ml);
     a.part_ok = reinterpret_cast<int*>(static_cast<char*>(ws) + w.part_ok);
+    a.few_states = static_cast<char*>(ws) + w.states;
+    a.few_ticket = reinterpret_cast<int*>(static_cast<char*>(ws) + w.ticket);
+    few_shape(&a);
   }
   cudaError_t e = cudaSuccess;
   if (kv->dtype != PRHS_BF16) e = launch_tree(a, sms, ws, stream);
@@ -282,7 +287,7 @@ size_t prhs_shared_workspace_size(const prhs_kv* kv, int T, int max_new) {
     return 0;
   }
   if (begin(kv, T, &view, &sms) != PRHS_OK) return 0;
-  return shared_ws(view, T, sms).total;
+  return shared_ws(view, T, max_new < T ? max_new : T, sms).total;
 }
 
 prhs_status prhs_shared_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,

@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
       if (r >= rows) continue;
       const long long orow = (x.c0 + ((row0 + r) >> gl)) * kv.Hq + (x.kvh << gl) + (r & ((1 << gl) - 1));
       const bool result = whole && (!SHARED || x.part == 0);
-      const long long prow = SHARED ? tree_part_row(a, x.part, orow) : 0;
+      const long long prow = SHARED ? (long long)(x.part - 1) * a.T * kv.Hq + orow : 0;
       const float inv = result ? tree_inv(sum) : 1.f;
       float* dst = (result            ? static_cast<float*>(a.out) + orow * D
                     : SHARED && whole ? a.part_o + prow * D

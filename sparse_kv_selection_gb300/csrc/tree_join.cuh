@@ -50,9 +50,18 @@ __device__ __forceinline__ void tree_put(__nv_bfloat16* dst, float4 x) {
   *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// Row of the partial states of a result's row.
-__device__ __forceinline__ long long tree_part_row(const TreeLaunch& a, int part, long long orow) {
-  return (part == 2 ? (long long)a.T * a.kv.Hq : 0ll) + orow;
+// Where a row's partial state is kept: its maximum and sum, and its columns 4 c .. 4 c + 3.
+template <typename T>
+__device__ __forceinline__ long long part_row(const TreeLaunch& a, int part, long long tok, int kvh, int g, int gl) {
+  const TreeLaunch& x = a;
+  if (sizeof(T) == 4) return ((long long)(part - 1) * x.T + tok) * x.kv.Hq + (kvh << gl) + g;
+  return ((long long)(part - 1) * x.kv.Hkv + kvh) * ((long long)x.T << gl) + (tok << gl) + g;
+}
+template <typename T, int D>
+__device__ __forceinline__ float4* part_at(const TreeLaunch& a, int part, long long tok, int kvh, int g, int c, int gl) {
+  float4* o = reinterpret_cast<float4*>(a.part_o);
+  if (sizeof(T) == 4) return o + part_row<T>(a, part, tok, kvh, g, gl) * (D / 4) + c;
+  return o + (((long long)(part - 1) * a.kv.Hkv + kvh) * (D / 4) + c) * ((long long)a.T << gl) + (tok << gl) + g;
 }
 
 template <typename T, int D, bool ROW_MAJOR>
@@ -61,6 +70,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const __grid_co
   constexpr int C4 = D / 4, CH = JOIN_CH;
   __shared__ float4 so[JOIN_THREADS];
   __shared__ float2 sml[JOIN_THREADS];
+  if (a.shared != nullptr) pdl_trigger();  // (the launch behind it has its own work first)
   pdl_wait();
   pdl_trigger();
   const TreeSplit s = p.split[blockIdx.x];
@@ -124,9 +134,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const __grid_co
     const float inv = tree_inv(L);
     const long long orow = (long long)(s.tok + (row >> gl)) * a.kv.Hq + (s.kvh << gl) + (row & ((1 << gl) - 1));
     if (s.part != 0) {
-      const long long prow = tree_part_row(a, s.part, orow);
-      tree_put(a.part_o + prow * D + c * 4, o);
-      if (c == 0) a.part_ml[prow] = make_float2(M, L);
+      const int tok = s.tok + (row >> gl), g = row & ((1 << gl) - 1);
+      *part_at<T, D>(a, s.part, tok, s.kvh, g, c, gl) = o;
+      if (c == 0) a.part_ml[part_row<T>(a, s.part, tok, s.kvh, g, gl)] = make_float2(M, L);
       continue;
     }
     tree_put(static_cast<T*>(a.out) + orow * D + c * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));

@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   pdl_trigger();
   // (the join of a CTA that gives up reads this)
   if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
+  if (SHARED && a.few_split > 1)
+    for (int i = blockIdx.x * TC_THREADS + tid; i < a.few_units; i += gridDim.x * TC_THREADS) a.few_ticket[i] = 0;
 
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (items + TC_THREADS - 1) / TC_THREADS, e0 = tid * per_t;
@@ -949,10 +951,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                   make_uint4(v[e][0], v[e][1], v[e][2], v[e][3]);
           }
         } else if (SHARED && w.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + tree_part_row(a, w.part, out_row(ur)) * D + c * 32);
+          float4* dst = part_at<__nv_bfloat16, D>(a, w.part, w.c0 + tok, w.kvh, ur & ((1 << gl) - 1), c * 8, gl);
           if (live)
 #pragma unroll
-            for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; e++)
+              *reinterpret_cast<uint4*>(dst + e * ((long long)a.T << gl)) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(p.rec.o) + (rec * (D / 4) + c * 8) * p.rec.rows_max + ur;
 #pragma unroll
@@ -962,7 +966,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       if (live && (!both || st == 0)) {
         if (result) a.lse[out_row(ur)] = tree_lse(M, L);
-        else if (SHARED && w.whole) a.part_ml[tree_part_row(a, w.part, out_row(ur))] = make_float2(M, L);
+        else if (SHARED && w.whole) a.part_ml[part_row<__nv_bfloat16>(a, w.part, w.c0 + tok, w.kvh, ur & ((1 << gl) - 1), gl)] = make_float2(M, L);
         else p.rec.ml[rec * p.rec.rows_max + ur] = make_float2(M, L);
       }
       tc_fence_before();

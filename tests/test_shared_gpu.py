@@ -160,18 +160,25 @@ def test_long_causal_chunks_share(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_same_as_tree_attention(dtype):
-    """Alone, rows are computed as tree_attn computes them, bit for bit."""
+@pytest.mark.parametrize("rest", [(0, 90), (5000, 6000)])
+def test_alone_as_tree_attention(dtype, rest):
+    """Without groups it is tree_attn."""
     import sparse_kv_selection_gb300 as S
-    b = Batch([(5, 300), (2, 64)], (0, 90), (0, 5), 4, 2, 64, dtype, 16, seed=7)
-    alone = [[i, 1, 0, 0] for i in range(7)]
-    out = b.run(share=alone)
-    o, l = torch.full_like(out[0], 7.0), torch.full_like(out[1], 7.0)
+    b = Batch([(5, 300), (2, 64)], rest, (0, 5), 4, 2, 64, dtype, 16, seed=7)
+    b.check(b.run(share=[[i, 1, 0, 0] for i in range(7)]))
+    o, l = torch.full((b.T, 4, 64), 7.0, dtype=dtype, device="cuda"), torch.full((b.T, 4), 7.0, device="cuda")
     S.tree_attn(b.c.kv, b.q, b.kn, b.vn, b.scale, i32(b.cu), max(b.n), o, l, S.make_tree_workspace(b.c.kv, max(b.n)))
     assert S.last_error() == 0
-    if dtype == BF16:
-        assert torch.equal(o, out[0]) and torch.equal(l, out[1])
-    b.check(out)
+    b.check((o, l))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 4, 64), (8, 2, 128), (8, 1, 64)])
+@pytest.mark.parametrize("n,rest", [((1, 1), (400, 4200)), ((1, 9), (500, 2100)), ((1, 64), (0, 700)), ((1, 1), (4000, 9000)),
+                                    ((30, 128), (900, 1100))])
+def test_own_keys_of_every_length(Hq, Hkv, d, n, rest):
+    """Own keys that several CTAs share, and those left to the tcgen05 kernel."""
+    full([(3, 130), (2, 64), (1, 0)], rest, n, Hq, Hkv, d, BF16, 16, seed=rest[1])
+    full([(3, 130), (1, 0)], rest, n, Hq, Hkv, d, BF16, 0, tree=n[1] > 1, seed=n[1])
 
 
 def test_shared_keys_are_whole_pages():
