@@ -79,36 +79,38 @@ struct TreeLaunch {
   float* part_o;    // against the state's maximum
   float2* part_ml;  // maximum (base 2) and sum
   int* part_ok;     // 0: the offsets step back, there are no states
-  // bf16: sequences whose own keys the joining launch attends (few_item): query rows
-  // of a CTA, CTAs of rows a KV head
-  int few_rows, few_blocks;
-  int few_units, few_split;  // units, CTAs of a unit at most
-  void* few_states;          // [units][few_split] states of units that several CTAs share
-  int* few_ticket;           // [units] of those CTAs, how many have written theirs
+  // bf16: sequences whose own keys the joining launch attends (few_item)
+  int few_rows;      // query rows of a unit
+  int few_most;      // tasks of cut units at most
+  void* few_states;  // their states
+  int* few_ticket;   // [few_most] at a unit's first task: how many have written theirs
 };
 // Whether the joining launch attends a sequence's own t keys with its n tokens of G
-// query heads a KV head: a tile of the matrix units costs a few microseconds to begin
-// and to end, more than a short run of keys takes to read. Every CTA of rows reads
-// the keys again, from L2.
+// query heads a KV head: a unit of the matrix units' kernel takes a few microseconds
+// to begin and to end, more than a short run of keys takes to read. Every unit of
+// rows reads the keys again, from L2.
 constexpr int FEW_KEYS = 4096;
+constexpr int FEW_BLOCKS = 64;  // units of a KV head at most
 __device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
   const long long blocks = ((long long)n * (a.kv.Hq / a.kv.Hkv) + a.few_rows - 1) / max(a.few_rows, 1);
-  return a.few_rows > 0 && blocks <= a.few_blocks && blocks * ((long long)t + n) <= FEW_KEYS;
+  return a.few_rows > 0 && blocks <= FEW_BLOCKS && blocks * ((long long)t + n) <= FEW_KEYS;
 }
 // fp32: two launches, the first counted by the callee; ws holds
 // tree_workspace(kv, max_new, sms) bytes.
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t s);
 size_t tree_workspace(const KVView& kv, int max_new, int sms);  // (max_new: tree_most_new)
-// bf16: two launches, the first counted by the callee; *err is the launches'
+// bf16: two launches, with shared keys three, all but the last counted by the callee; *err is the launches'
 // result when the descriptors could be made. Workspace bytes of a call.
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
 
-// One launch: the result of the tokens with two partial states; bf16: also the
-// attention of few_item's sequences.
-void few_shape(TreeLaunch* a);
-size_t few_state_bytes(const KVView& kv, int max_new);
-size_t few_ticket_bytes(const KVView& kv, int max_new);
+// One launch: the result of the tokens with two partial states; bf16 (issued by
+// launch_tree_tc, with the descriptors of the cache's K and V in boxes of 16 rows and
+// of the new tokens'): also the attention of few_item's sequences.
+void few_shape(TreeLaunch* a, int sms);
+size_t few_state_bytes(const KVView& kv, int max_new, int sms);
+size_t few_ticket_bytes(const KVView& kv, int max_new, int sms);
+cudaError_t launch_few(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t s);
 cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t s);
 // The most tokens that a unit's rows may come from.
 inline int tree_most_new(const TreeLaunch& a) { return a.shared != nullptr ? a.T : a.max_new; }
@@ -117,6 +119,24 @@ inline int tree_most_new(const TreeLaunch& a) { return a.shared != nullptr ? a.T
 // innermost first, strides in bytes from dimension 1 on).
 prhs_status abi_encode_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                             const uint64_t* strides, const uint32_t* box);
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+// One lane of a converged warp. (A lane chosen by its number compiles to a loop
+// over the lanes around every instruction that takes uniform operands.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 
 // Two fp32 numbers in one 64-bit register pair, and operations on both.
 __device__ __forceinline__ uint64_t f2(float x, float y) {

@@ -204,8 +204,8 @@ SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   w.part_ml = w.part_o + up((size_t)2 * T * kv.Hq * kv.d * sizeof(float));
   w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
   w.states = w.part_ok + 256;
-  w.ticket = w.states + up(few_state_bytes(kv, max_new));
-  w.total = w.ticket + up(few_ticket_bytes(kv, max_new));
+  w.ticket = w.states + up(few_state_bytes(kv, max_new, sms));
+  w.total = w.ticket + up(few_ticket_bytes(kv, max_new, sms));
   return w;
 }
 
@@ -257,11 +257,14 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
     a.part_ok = reinterpret_cast<int*>(static_cast<char*>(ws) + w.part_ok);
     a.few_states = static_cast<char*>(ws) + w.states;
     a.few_ticket = reinterpret_cast<int*>(static_cast<char*>(ws) + w.ticket);
-    few_shape(&a);
+    few_shape(&a, sms);
   }
   cudaError_t e = cudaSuccess;
-  if (kv->dtype != PRHS_BF16) e = launch_tree(a, sms, ws, stream);
-  else if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
+  if (kv->dtype == PRHS_BF16) {
+    if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
+    return launched(e);
+  }
+  e = launch_tree(a, sms, ws, stream);
   if (e != cudaSuccess || !shared) return launched(e);
   abi_count_launch();
   return launched(launch_shared_join(a, stream));

@@ -210,23 +210,6 @@ __device__ constexpr uint32_t instr_desc(int n, bool b_nmajor) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_nmajor ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(TT >> 4) << 24);
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-      : "memory");
-}
-// One lane of a converged warp. (A lane chosen by its number compiles to a loop
-// over the lanes around every instruction that takes uniform operands.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -379,8 +362,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   pdl_trigger();
   // (the join of a CTA that gives up reads this)
   if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
-  if (SHARED && a.few_split > 1)
-    for (int i = blockIdx.x * TC_THREADS + tid; i < a.few_units; i += gridDim.x * TC_THREADS) a.few_ticket[i] = 0;
+  if (SHARED)
+    for (int i = blockIdx.x * TC_THREADS + tid; i < a.few_most; i += gridDim.x * TC_THREADS) a.few_ticket[i] = 0;
 
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (items + TC_THREADS - 1) / TC_THREADS, e0 = tid * per_t;
@@ -1019,7 +1002,10 @@ static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cu
                  maps[6], p);
   if (e != cudaSuccess) return e;
   abi_count_launch();
-  return launch_tree_join<__nv_bfloat16, D, false>(p.a, p.rec, sms, st);
+  e = launch_tree_join<__nv_bfloat16, D, false>(p.a, p.rec, sms, st);
+  if (!SHARED || e != cudaSuccess) return e;
+  abi_count_launch();
+  return launch_few(p.a, maps + 3, sms, st);
 }
 
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t st, cudaError_t* err) {
