@@ -25,55 +25,75 @@
 namespace prhs {
 
 // -------------------------------------------------------------------------- //
-// fp32: two states of every token
+// the join
 // -------------------------------------------------------------------------- //
-constexpr int SJ_THREADS = 256, SJ_PER = 4;
+constexpr int SJ_THREADS = 256;
 
-template <int D>
+// A thread takes four columns of a row. On bf16 the state against the other keys may
+// lie in pieces, one for each warp of few_kernel that had steps of its unit (a warp's
+// state 2 w + 1 is of the unit that it begins, 2 w of one begun before).
+template <typename T, int D>
 __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ TreeLaunch a) {
   constexpr int C4 = D / 4;
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x;
-  const TreeItem x = tree_item<true>(a, 2 * b + 1);
-  if (x.part != 2 || *a.part_ok == 0) return;
-  const long long total = (long long)x.n * a.kv.Hq * C4, row0 = (long long)x.c0 * a.kv.Hq, other = (long long)a.T * a.kv.Hq;
-  for (long long i0 = (long long)blockIdx.y * SJ_THREADS * SJ_PER + threadIdx.x; i0 < total;
-       i0 += (long long)gridDim.y * SJ_THREADS * SJ_PER) {
-    float2 ml[SJ_PER][2];
-    float4 o[SJ_PER][2];
+  const KVView& kv = a.kv;
+  const int G = kv.Hq / kv.Hkv, gl = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, b = blockIdx.x;
+  const TreeItem x = tree_item<true>(a, 2 * b + 1, true);
+  const bool few = few_item(a, x.n, x.t);
+  if (x.n == 0 || (x.part != 2 && !few) || *a.part_ok == 0) return;
+  const int rows = x.n << gl;
+  const long long total = (long long)rows * kv.Hkv * C4;
+  for (long long i = (long long)blockIdx.y * SJ_THREADS + threadIdx.x; i < total; i += (long long)gridDim.y * SJ_THREADS) {
+    const int c4 = (int)(i % C4), hr = (int)(i / C4), kvh = hr / rows, r = hr - kvh * rows;
+    const int tok = x.c0 + (r >> gl), h = r & (G - 1);
+    int2 where = make_int2(0, 1);
+    if (few) where = __ldcg(a.few_where + (long long)kvh * ((long long)a.T << gl) + (tok << gl) + h);
+    if (where.y == 1 && x.part != 2) continue;  // its result stands
+    float M = -INFINITY, L = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, float4 o) {  // (a state that holds NaN has it in its sum, whatever its maximum)
+      const float m = fmaxf(M, ml.x), w0 = tree_weight(M, m), w1 = tree_weight(ml.x, m);
+      L = fmaf(w1, ml.y, w0 * L);
+      y = make_float4(y.x * w0, y.y * w0, y.z * w0, y.w * w0);
+      tree_fma(y, w1, o);
+      M = m;
+    };
+    float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
+    float4 o[2] = {y, y};
 #pragma unroll
-    for (int k = 0; k < SJ_PER; k++) {
-      const long long i = min(i0 + k * SJ_THREADS, total - 1), row = row0 + i / C4;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        ml[k][h] = __ldcg(a.part_ml + row + h * other);
-        o[k][h] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (row + h * other) * C4 + i % C4);
+    for (int k = 0; k < 2; k++) {
+      if (k == 0 ? x.part != 2 : where.y > 1) continue;
+      ml[k] = __ldcg(a.part_ml + part_row<T>(a, k + 1, tok, kvh, h, gl));
+      o[k] = __ldcg(part_at<T, D>(a, k + 1, tok, kvh, h, c4, gl));
+    }
+    if (where.y > 1) {
+      const int RB = a.few_rows, in = r % RB;
+      const float4* states = static_cast<const float4*>(a.few_states);
+      const float2* sums = reinterpret_cast<const float2*>(states + (long long)2 * a.few_warps * C4 * RB);
+#pragma unroll 4
+      for (int w = 0; w < where.y; w++) {
+        const long long slot = 2ll * (where.x + w) + (w == 0);
+        add(__ldcg(sums + slot * RB + in), __ldcg(states + (slot * C4 + c4) * RB + in));
       }
     }
 #pragma unroll
-    for (int k = 0; k < SJ_PER; k++) {
-      const long long i = i0 + k * SJ_THREADS, row = row0 + i / C4;
-      if (i >= total) break;
-      const float M = fmaxf(ml[k][0].x, ml[k][1].x);
-      const float w0 = tree_weight(ml[k][0].x, M), w1 = tree_weight(ml[k][1].x, M);
-      // (a state that holds NaN has it in its sum, whatever its maximum)
-      const float L = fmaf(w1, ml[k][1].y, w0 * ml[k][0].y), inv = tree_inv(L);
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      tree_fma(y, w0, o[k][0]);
-      tree_fma(y, w1, o[k][1]);
-      tree_put(static_cast<float*>(a.out) + row * D + i % C4 * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-      if (i % C4 == 0) a.lse[row] = tree_lse(M, L);
-    }
+    for (int k = 0; k < 2; k++) add(ml[k], o[k]);
+    const float inv = tree_inv(L);
+    const long long orow = (long long)tok * kv.Hq + (kvh << gl) + h;
+    tree_put(static_cast<T*>(a.out) + orow * D + c4 * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    if (c4 == 0) a.lse[orow] = tree_lse(M, L);
   }
 }
 
 // -------------------------------------------------------------------------- //
-// bf16: few rows on few keys, and the join
+// bf16: few rows on few keys
 // -------------------------------------------------------------------------- //
 constexpr int FEW_WARPS = 8, FEW_THREADS = FEW_WARPS * 32;
 constexpr int FEW_STEP = 16;        // keys of a warp's step: a box, never over a page's end
 constexpr int FEW_RING = 24 << 10;  // bytes of a warp's ring: 3 steps at d = 128, 6 at 64
+constexpr int FEW_RUN = 8;          // steps of a warp at least
+constexpr int few_smem_bytes(int d) { return FEW_WARPS * (FEW_RING + 8 * d * 4); }
 constexpr float FEW_LOG2E = 1.4426950408889634f;
 constexpr float FEW_RESCALE = 8.f;  // growth of a maximum (base 2) that rescales, as in the tcgen05 kernel
 
@@ -114,13 +134,12 @@ __device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// The warp tasks of one sequence, KV head by KV head: units of RB query rows, each
-// cut into `cuts` equal runs of its steps; or, where the other launch attended its
-// keys, joins of 32 rows.
+// One sequence's share of the list of steps, KV head by KV head: units of RB query
+// rows, each of as many steps as the longest (causal ones that see fewer new tokens
+// leave the last empty).
 struct FewSeq {
   TreeItem x;
-  int blocks, steps, tasks, cuts;  // units of a KV head, steps of the longest, tasks
-  bool few;
+  int blocks, steps;  // units of a KV head, steps of a unit
 };
 template <int RB>
 __device__ __forceinline__ int few_steps(const TreeLaunch& a, const TreeItem& x, int gl, int blk, int* fresh) {
@@ -132,23 +151,24 @@ template <int RB>
 __device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, int b, int gl) {
   FewSeq s;
   s.x = tree_item<true>(a, 2 * b + 1, true);
-  s.few = few_item(a, s.x.n, s.x.t);
-  s.blocks = s.steps = s.tasks = 0;
-  s.cuts = 1;
-  if (s.few) {
-    s.blocks = ((s.x.n << gl) + RB - 1) / RB;
-    int fresh;
-    if (s.blocks > 0) s.steps = few_steps<RB>(a, s.x, gl, s.blocks - 1, &fresh);
-  } else if (s.x.part == 2) {
-    s.blocks = ((s.x.n << gl) + 31) / 32;
-  }
+  s.blocks = s.steps = 0;
+  if (!few_item(a, s.x.n, s.x.t)) return s;
+  s.blocks = ((s.x.n << gl) + RB - 1) / RB;
+  int fresh;
+  if (s.blocks > 0) s.steps = few_steps<RB>(a, s.x, gl, s.blocks - 1, &fresh);
   return s;
 }
-// With runs of about `run` steps.
-__device__ __forceinline__ void few_cut(FewSeq& s, int Hkv, int run) {
-  if (s.few) s.cuts = max(1, (2 * s.steps + run) / (2 * run));
-  s.tasks = Hkv * s.blocks * s.cuts;
-}
+
+// A unit's steps in a warp's run of the list.
+struct FewTask {
+  TreeItem x;
+  int kvh, blk, s0, s1;    // KV head, unit, steps here
+  int taken;               // of the list
+  int cached, fresh;       // steps over the cache, new tokens that the unit sees
+  int first, cuts;         // the warp that begins the unit, the warps that have steps of it
+  int window, at;          // rows of steps window .. window + 31, one a lane
+  bool some;               // (none: the run is done)
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
@@ -157,11 +177,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                const __grid_constant__ TreeLaunch a) {
   // a step's K, then its V: SEGS column segments of 16 rows of 128 bytes
   constexpr int RB = 8 * NT, C4 = D / 4, SEGS = D / 64, SEG = FEW_STEP * 128, STAGE = 2 * SEGS * SEG, STAGES = FEW_RING / STAGE;
-  static_assert(RB * D * 4 <= FEW_RING, "a warp's state takes its ring's place");
+  constexpr int WARP_SMEM = few_smem_bytes(D) / FEW_WARPS;  // the ring, and eight rows of a state
   extern __shared__ __align__(1024) uint8_t few_smem[];
   __shared__ uint64_t full[FEW_WARPS][STAGES];
-  __shared__ int wsum[3][FEW_WARPS];
-  __shared__ int tasks_to[FEW_THREADS], cut_to[FEW_THREADS];  // up to a thread's sequences: tasks, and those of cut units
+  __shared__ int wsum[FEW_WARPS];
+  __shared__ int steps_to[FEW_THREADS];  // of the list, up to a thread's sequences
   const KVView& kv = a.kv;
   const int G = kv.Hq / kv.Hkv, gl = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -172,144 +192,102 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     fence_barrier_init();
   }
 
-  // ---- the list of tasks: prefixes over the sequences, a run of them a thread ----
+  // ---- the list of all steps, a prefix over the sequences (a run of them a thread) ----
   const int per = (kv.B + FEW_THREADS - 1) / FEW_THREADS, b0 = min(kv.B, tid * per), b1 = min(kv.B, b0 + per);
-  auto block_sum = [&](int v, int slot) {  // (inclusive prefix and sum over the block)
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(FULL_MASK, v, o);
-      if (lane >= o) v += y;
-    }
-    if (lane == 31) wsum[slot][warp] = v;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < FEW_WARPS; w++) {
-      const int y = wsum[slot][w];
-      if (w < warp) before += y;
-      all += y;
-    }
-    return make_int2(before + v, all);
-  };
-  FewSeq mine = {};
-  int steps = 0;
+  int steps = 0, total = 0;
+  bool back = false;  // (flagged by the launch in front: no row is written)
   for (int b = b0; b < b1; b++) {
-    mine = few_seq<RB>(a, b, gl);
-    steps += kv.Hkv * mine.blocks * mine.steps;
+    const FewSeq s = few_seq<RB>(a, b, gl);
+    back |= a.cu_new[b + 1] < a.cu_new[b];
+    steps += kv.Hkv * s.blocks * s.steps;
   }
-  steps = block_sum(steps, 0).y;
-  // Runs of a third of a warp's share (so that warps end together), of 8 to 16 steps
-  // where there are few. The cut units' tasks then number four a warp at most.
-  const int run = max((steps + 3 * gws - 1) / (3 * gws), min(16, max(8, steps / gws)));
-  int tasks = 0, cut = 0;
-  for (int b = b0; b < b1; b++) {
-    if (per > 1) mine = few_seq<RB>(a, b, gl);
-    few_cut(mine, kv.Hkv, run);
-    tasks += mine.tasks;
-    cut += mine.cuts > 1 ? mine.tasks : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL_MASK, steps, o);
+    if (lane >= o) steps += y;
   }
-  const int2 t2 = block_sum(tasks, 1), c2 = block_sum(cut, 2);
-  tasks_to[tid] = t2.x;
-  cut_to[tid] = c2.x;
+  if (lane == 31) wsum[warp] = steps;
+  back = __syncthreads_or(back);
+#pragma unroll
+  for (int w = 0; w < FEW_WARPS; w++) {
+    const int y = wsum[w];
+    if (w < warp) steps += y;
+    total += y;
+  }
+  steps_to[tid] = steps;
   __syncthreads();
+  // Every warp takes an equal run. A unit cut by the end of one leaves states, joined by the
+  // last warp to come to its end in it; runs of fewer than eight steps would cost more than they give.
+  const int run = max((total + gws - 1) / gws, FEW_RUN);
+  if (back) total = 0;
+  int pos = min(total, gw * run);
+  const int end = min(total, pos + run);
   if ((smem_addr(few_smem) & 1023) != 0) {  // the swizzle needs it
     raise_error(kv.err, PRHS_DEV_CAPACITY);
     return;
   }
 
   const bool causal = a.mask == nullptr;
-  const uint32_t ring = smem_addr(few_smem) + warp * FEW_RING;
-  float4* staged = reinterpret_cast<float4*>(few_smem + warp * FEW_RING);  // [C4][RB]
+  const uint32_t ring = smem_addr(few_smem) + warp * WARP_SMEM;
+  float4* staged = reinterpret_cast<float4*>(few_smem + warp * WARP_SMEM + FEW_RING);  // [C4][8]
   const float sc = a.scale * FEW_LOG2E;
-  int stage = 0;
-  uint32_t phase = 0;
-  bool dead = false;
-  for (int task = gw; task < t2.y && !dead; task += gws) {
-    // ---- what it is ----
+
+  // Rows of the task's next steps' first keys (-1: on no page).
+  auto look_up = [&](FewTask& t, int window) {
+    t.window = window;
+    t.at = 0;
+    const int s = window + lane, key = t.x.base + s * FEW_STEP;
+    if (s >= min(t.s1, t.cached)) return;
+    if (kv.block_table == nullptr) {
+      t.at = (t.x.b * kv.Hkv + t.kvh) * kv.t_max + key;
+      return;
+    }
+    const int page = kv.block_table[(long long)t.x.b * kv.max_blocks + key / kv.block_size];
+    const bool ok = (unsigned)page < (unsigned)kv.num_blocks;
+    if (!ok) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
+    t.at = ok ? (page * kv.Hkv + t.kvh) * kv.block_size + key % kv.block_size : -1;
+  };
+  auto fetch = [&]() {  // at pos, which moves on
+    FewTask t = {};
+    if (pos >= end) return t;
     int lo = 0, hi = FEW_THREADS - 1;  // the first thread whose sequences end behind it
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (tasks_to[mid] > task) hi = mid; else lo = mid + 1;
+      if (steps_to[mid] > pos) hi = mid; else lo = mid + 1;
     }
-    int off = task - (lo > 0 ? tasks_to[lo - 1] : 0), slot = lo > 0 ? cut_to[lo - 1] : 0, b = lo * per;
+    int off = pos - (lo > 0 ? steps_to[lo - 1] : 0), b = lo * per;
     FewSeq s = few_seq<RB>(a, b, gl);
-    few_cut(s, kv.Hkv, run);
-    while (off >= s.tasks) {
-      off -= s.tasks;
-      slot += s.cuts > 1 ? s.tasks : 0;
+    for (int x; off >= (x = kv.Hkv * s.blocks * s.steps);) {
+      off -= x;
       s = few_seq<RB>(a, ++b, gl);
-      few_cut(s, kv.Hkv, run);
     }
-    const TreeItem x = s.x;
-    slot += off;
-    const int part_of = off % s.cuts, blk = off / s.cuts % s.blocks, kvh = off / s.cuts / s.blocks;
-    if (!s.few) {  // only a join
-      pdl_wait();
-      if (*a.part_ok == 0) continue;
-      const int r = blk * 32 + lane, tok = x.c0 + (r >> gl), h = r & (G - 1);
-      if (r >= x.n << gl) continue;
-      float2 ml[2];
-#pragma unroll
-      for (int k = 0; k < 2; k++) ml[k] = __ldcg(a.part_ml + part_row<__nv_bfloat16>(a, k + 1, tok, kvh, h, gl));
-      const float M = fmaxf(ml[0].x, ml[1].x), w0 = tree_weight(ml[0].x, M), w1 = tree_weight(ml[1].x, M);
-      const float L = fmaf(w1, ml[1].y, w0 * ml[0].y), inv = tree_inv(L);
-      const long long orow = (long long)tok * kv.Hq + (kvh << gl) + h;
-#pragma unroll 4
-      for (int c4 = 0; c4 < C4; c4++) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        tree_fma(y, w0, __ldcg(part_at<__nv_bfloat16, D>(a, 1, tok, kvh, h, c4, gl)));
-        tree_fma(y, w1, __ldcg(part_at<__nv_bfloat16, D>(a, 2, tok, kvh, h, c4, gl)));
-        tree_put(static_cast<__nv_bfloat16*>(a.out) + orow * D + c4 * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-      }
-      a.lse[orow] = tree_lse(M, L);
-      continue;
-    }
-    int fresh;
-    const int all_steps = few_steps<RB>(a, x, gl, blk, &fresh), cached = (x.t + FEW_STEP - 1) / FEW_STEP;
-    const int s0 = all_steps * part_of / s.cuts, s1 = all_steps * (part_of + 1) / s.cuts;
-    const int rows = min(RB, (x.n << gl) - blk * RB), tok0 = (blk * RB) >> gl;
-  // Q as the products take it: rows g of each eight, columns 16 j + 2 c and 16 j + 8 + 2 c
-  uint32_t q[NT][D / 16][2];
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-    const int r = blk * RB + 8 * t + g;
-    const bool have = 8 * t + g < rows;
-    const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
-                               ((long long)(x.c0 + (have ? r >> gl : tok0)) * kv.Hq + (kvh << gl) + (have ? r & (G - 1) : 0)) * D;
-#pragma unroll
-    for (int j = 0; j < D / 16; j++)
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        q[t][j][h] = have ? *reinterpret_cast<const uint32_t*>(row + 16 * j + 8 * h + 2 * c) : 0u;
-  }
-
-  // Rows of the steps' first keys, 32 steps at a time, one a lane (-1: on no page).
-  auto row_at = [&](int s) -> int {
-    if (s >= min(s1, cached)) return 0;
-    const int key = x.base + s * FEW_STEP;
-    if (kv.block_table == nullptr) return (b * kv.Hkv + kvh) * kv.t_max + key;
-    const int page = kv.block_table[(long long)b * kv.max_blocks + key / kv.block_size];
-    if ((unsigned)page >= (unsigned)kv.num_blocks) {
-      raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
-      return -1;
-    }
-    return (page * kv.Hkv + kvh) * kv.block_size + key % kv.block_size;
+    const int unit = off / s.steps, in = off - unit * s.steps, start = pos - in;
+    t.x = s.x;
+    t.kvh = unit / s.blocks;
+    t.blk = unit - t.kvh * s.blocks;
+    t.taken = min(s.steps - in, end - pos);
+    pos += t.taken;
+    t.some = true;
+    t.first = start / run;
+    t.cuts = (start + s.steps - 1) / run - t.first + 1;
+    const int all = few_steps<RB>(a, t.x, gl, t.blk, &t.fresh);
+    t.cached = (t.x.t + FEW_STEP - 1) / FEW_STEP;
+    t.s0 = min(in, all);
+    t.s1 = min(in + t.taken, all);
+    look_up(t, t.s0);
+    return t;
   };
-  int window = s0, at = row_at(window + lane);
   int counts = 0;  // keys of the ring's steps, five bits each
-  auto load = [&](int s, int stage) {
-    if (s >= window + 32) {
-      window += 32;
-      at = row_at(window + lane);
-    }
-    const int row = __shfl_sync(FULL_MASK, at, s - window), j = (s - cached) * FEW_STEP;
-    const bool is_new = s >= cached;
-    const int n = is_new ? min(FEW_STEP, fresh - j) : row < 0 ? 0 : min(FEW_STEP, x.t - s * FEW_STEP);
+  auto load = [&](FewTask& t, int s, int stage) {
+    if (s >= t.window + 32) look_up(t, t.window + 32);
+    const int row = __shfl_sync(FULL_MASK, t.at, s - t.window), j = (s - t.cached) * FEW_STEP;
+    const bool is_new = s >= t.cached;
+    const int n = is_new ? min(FEW_STEP, t.fresh - j) : row < 0 ? 0 : min(FEW_STEP, t.x.t - s * FEW_STEP);
     counts = (counts & ~(31 << 5 * stage)) | n << 5 * stage;
     if (lane == 0) {
       mbar_arrive_expect_tx(&full[warp][stage], STAGE);
       const CUtensorMap *km = is_new ? &knmap : &kmap, *vm = is_new ? &vnmap : &vmap;
-      const int z = is_new ? kvh : max(row, 0), w = is_new ? x.c0 + j : 0;
+      const int z = is_new ? t.kvh : max(row, 0), w = is_new ? t.x.c0 + j : 0;
 #pragma unroll
       for (int i = 0; i < SEGS; i++) tma_load_4d(ring + stage * STAGE + i * SEG, km, 0, i, z, w, &full[warp][stage]);
 #pragma unroll
@@ -317,6 +295,33 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     }
     __syncwarp();
   };
+  // The copies run ahead of the products into the next task, which is known while this one is worked on.
+  int fill = 0, held = 0, stage = 0;  // the stage to fill next, stages filled, the stage to use next
+  uint32_t phase = 0;
+  bool dead = false, in_next = false;
+  FewTask cur = fetch(), nxt;
+  int cursor = cur.s0;
+  for (; cur.some; cur = nxt) {
+    if (!in_next) cursor = cur.s0;
+    in_next = false;
+    bool known = false;
+    const TreeItem x = cur.x;
+    const int blk = cur.blk, kvh = cur.kvh;
+    const int rows = min(RB, (x.n << gl) - blk * RB), tok0 = (blk * RB) >> gl, cached = cur.cached;
+    // Q as the products take it: rows g of each eight, columns 16 j + 2 c and 16 j + 8 + 2 c
+    uint32_t q[NT][D / 16][2];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      const int r = blk * RB + 8 * t + g;
+      const bool have = 8 * t + g < rows;
+      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
+                                 ((long long)(x.c0 + (have ? r >> gl : tok0)) * kv.Hq + (kvh << gl) + (have ? r & (G - 1) : 0)) * D;
+#pragma unroll
+      for (int j = 0; j < D / 16; j++)
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          q[t][j][h] = have ? *reinterpret_cast<const uint32_t*>(row + 16 * j + 8 * h + 2 * c) : 0u;
+    }
 
   float m[NT][2], l[NT][2], o[NT][D / 16][4];  // rows 8 t + 2 c, + 1; O's columns 16 e + g, + 8
 #pragma unroll
@@ -326,15 +331,27 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 #pragma unroll
     for (int e = 0; e < D / 16; e++) o[t][e][0] = o[t][e][1] = o[t][e][2] = o[t][e][3] = 0.f;
   }
-  for (int i = 0, to = stage; i < min(STAGES, s1 - s0); i++) {
-    load(s0 + i, to);
-    if (++to == STAGES) to = 0;
-  }
   // a lane's row of the four matrices of a product's operand: K's rows lane % 16, columns 8 (lane / 16) ..;
   // V's the other way about (its matrices come in the order of d, then keys)
   const int krow = lane & 15, kcol = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vcol = lane >> 3 & 1;
   const uint32_t k_at = ring + krow * 128, v_at = ring + SEGS * SEG + vrow * 128;
-  for (int s = s0; s < s1; s++) {
+  for (int s = cur.s0;; s++) {
+    while (held < STAGES) {
+      if (!in_next && cursor >= cur.s1) {
+        if (!known || !nxt.some) break;
+        in_next = true;
+        cursor = nxt.s0;
+      }
+      if (in_next && cursor >= nxt.s1) break;
+      load(in_next ? nxt : cur, cursor++, fill);
+      fill = fill + 1 == STAGES ? 0 : fill + 1;
+      held++;
+    }
+    if (!known) {
+      nxt = fetch();
+      known = true;
+    }
+    if (s >= cur.s1) break;
     dead = !__all_sync(FULL_MASK, mbar_wait(&full[warp][stage], phase, kv.err));
     if (dead) break;
     const int n = counts >> 5 * stage & 31;
@@ -411,7 +428,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       for (int t = 0; t < NT; t++) mma16(o[t][e], v[0], v[1], v[2], v[3], pb[t][0], pb[t][1]);
     }
     __syncwarp();  // (the stage has been read)
-    if (s + STAGES < s1) load(s + STAGES, stage);
+    held--;
     if (++stage == STAGES) {
       stage = 0;
       phase ^= 1;
@@ -419,138 +436,99 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   }
   if (dead) break;
 
-  // ---- its state: columns by rows in the ring's place, then four columns a lane ----
-  __syncwarp();
+  // ---- its state, four columns a lane: row lane % 8 of each eight, columns 4 (lane / 8 + 4 k) .. ----
+  const int sr = lane & 7, sq = lane >> 3;
+  float2 ml[NT];
+  float4 y[NT][C4 / 4];
 #pragma unroll
-  for (int t = 0; t < NT; t++)
+  for (int t = 0; t < NT; t++) {
+    __syncwarp();
 #pragma unroll
     for (int r = 0; r < 2; r++) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[t][r] += __shfl_xor_sync(FULL_MASK, l[t][r], d);
-      const int row = 8 * t + 2 * c + r;
 #pragma unroll
       for (int e = 0; e < D / 16; e++)
 #pragma unroll
         for (int h = 0; h < 2; h++)
-          reinterpret_cast<float*>(staged + (4 * e + 2 * h + g / 4) * RB + row)[g % 4] = o[t][e][2 * h + r];
+          reinterpret_cast<float*>(staged + (4 * e + 2 * h + g / 4) * 8 + 2 * c + r)[g % 4] = o[t][e][2 * h + r];
     }
-  __syncwarp();
-  // lane: row lane % 8 of each eight, columns 4 (lane / 8 + 4 k) ..
-  const int sr = lane & 7, sq = lane >> 3;
-  float2 ml[NT];
-#pragma unroll
-  for (int t = 0; t < NT; t++) {  // (row 8 t + 2 c + r is in lanes c of any g)
+    __syncwarp();
+    // (row 8 t + 2 c + r is in lanes c of any g)
     const float m0 = __shfl_sync(FULL_MASK, m[t][0], sr >> 1), m1 = __shfl_sync(FULL_MASK, m[t][1], sr >> 1);
     const float l0 = __shfl_sync(FULL_MASK, l[t][0], sr >> 1), l1 = __shfl_sync(FULL_MASK, l[t][1], sr >> 1);
     ml[t] = sr & 1 ? make_float2(m1, l1) : make_float2(m0, l0);
-  }
-  float4 y[NT][C4 / 4];
 #pragma unroll
-  for (int t = 0; t < NT; t++)
-#pragma unroll
-    for (int k = 0; k < C4 / 4; k++) y[t][k] = staged[(sq + 4 * k) * RB + 8 * t + sr];
-  __syncwarp();
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the ring's next copies come behind these reads)
-
-  pdl_wait();  // (the tickets are set, the states against the shared keys written by the launches in front)
-  if (*a.part_ok == 0) continue;
-  if (s.cuts > 1) {  // the last of a unit's tasks to arrive joins their states, in their order
-    float4* states = static_cast<float4*>(a.few_states);  // [tasks][C4][RB], then (maximum, sum) [tasks][RB]
-    float2* sums = reinterpret_cast<float2*>(states + (long long)a.few_most * C4 * RB);
-    const int slot0 = slot - part_of;
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-#pragma unroll
-      for (int k = 0; k < C4 / 4; k++) __stcg(states + ((long long)slot * C4 + sq + 4 * k) * RB + 8 * t + sr, y[t][k]);
-      if (sq == 0) __stcg(sums + (long long)slot * RB + 8 * t + sr, ml[t]);
-    }
-    __threadfence();
-    __syncwarp();
-    int arrived = 0;
-    if (lane == 0) arrived = atomicAdd(a.few_ticket + slot0, 1);
-    if (__shfl_sync(FULL_MASK, arrived, 0) != s.cuts - 1) continue;
-    __threadfence();
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      float M = -INFINITY, L = 0.f;
-      for (int w = 0; w < s.cuts; w++) M = fmaxf(M, __ldcg(sums + (long long)(slot0 + w) * RB + 8 * t + sr).x);
-#pragma unroll
-      for (int k = 0; k < C4 / 4; k++) y[t][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-      for (int w = 0; w < s.cuts; w++) {
-        const float2 z = __ldcg(sums + (long long)(slot0 + w) * RB + 8 * t + sr);
-        const float wt = tree_weight(z.x, M);
-        L = fmaf(wt, z.y, L);
-#pragma unroll
-        for (int k = 0; k < C4 / 4; k++)
-          tree_fma(y[t][k], wt, __ldcg(states + ((long long)(slot0 + w) * C4 + sq + 4 * k) * RB + 8 * t + sr));
-      }
-      ml[t] = make_float2(M, L);
-    }
+    for (int k = 0; k < C4 / 4; k++) y[t][k] = staged[(sq + 4 * k) * 8 + sr];
   }
 
-  // ---- the result, with the state against the shared keys ----
+  // a unit cut by the run's end, or with a state against shared keys, is for the join; nothing
+  // here waits for what it writes (or for the launch in front)
+  const bool cut = cur.cuts > 1, result = !cut && x.part == 0;
+  float4* states = static_cast<float4*>(a.few_states);  // [2 warps][C4][RB], then (maximum, sum) [2 warps][RB]
+  float2* sums = reinterpret_cast<float2*>(states + (long long)2 * gws * C4 * RB);
+  const long long slot = 2ll * gw + (cur.first == gw);
 #pragma unroll
   for (int t = 0; t < NT; t++) {
     const int r = blk * RB + 8 * t + sr, tok = x.c0 + (r >> gl), h = r & (G - 1);
     if (8 * t + sr >= rows) continue;
-    float M = ml[t].x, L = ml[t].y, w1 = 1.f, w0 = 0.f;
-    if (x.part == 2) {
-      const float2 z = __ldcg(a.part_ml + part_row<__nv_bfloat16>(a, 1, tok, kvh, h, gl));
-      M = fmaxf(M, z.x);
-      w1 = tree_weight(ml[t].x, M);
-      w0 = tree_weight(z.x, M);
-      L = fmaf(w0, z.y, w1 * L);
-    }
-    const float inv = tree_inv(L);
-    const long long orow = (long long)tok * kv.Hq + (kvh << gl) + h;
+    const long long prow = part_row<__nv_bfloat16>(a, 2, tok, kvh, h, gl), orow = (long long)tok * kv.Hq + (kvh << gl) + h;
+    const float inv = tree_inv(ml[t].y);
 #pragma unroll
     for (int k = 0; k < C4 / 4; k++) {
-      float4 v = make_float4(y[t][k].x * w1, y[t][k].y * w1, y[t][k].z * w1, y[t][k].w * w1);
-      if (x.part == 2) tree_fma(v, w0, __ldcg(part_at<__nv_bfloat16, D>(a, 1, tok, kvh, h, sq + 4 * k, gl)));
-      tree_put(static_cast<__nv_bfloat16*>(a.out) + orow * D + (sq + 4 * k) * 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      const int c4 = sq + 4 * k;
+      if (result)
+        tree_put(static_cast<__nv_bfloat16*>(a.out) + orow * D + c4 * 4,
+                 make_float4(y[t][k].x * inv, y[t][k].y * inv, y[t][k].z * inv, y[t][k].w * inv));
+      else if (cut)
+        __stcg(states + (slot * C4 + c4) * RB + 8 * t + sr, y[t][k]);
+      else
+        __stcg(part_at<__nv_bfloat16, D>(a, 2, tok, kvh, h, c4, gl), y[t][k]);
     }
-    if (sq == 0) a.lse[orow] = tree_lse(M, L);
+    if (sq != 0) continue;
+    if (result) a.lse[orow] = tree_lse(ml[t].x, ml[t].y);
+    else if (cut) __stcg(sums + slot * RB + 8 * t + sr, ml[t]);
+    else __stcg(a.part_ml + prow, ml[t]);
+    // (warps that begin no step of a unit do not know its first)
+    if (cur.first == gw) a.few_where[(long long)kvh * ((long long)a.T << gl) + (tok << gl) + h] = make_int2(cur.first, cur.cuts);
   }
   }
   if (dead)  // nothing may still be in flight when the CTA ends
-    for (int i = 0; i < STAGES; i++) mbar_wait(&full[warp][i], phase ^ (i < stage), kv.err);
-  pdl_wait();  // (whatever it had to do: this launch does not end before those in front of it)
+    for (int i = 0; i < held; i++) {
+      mbar_wait(&full[warp][stage], phase, kv.err);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
   pdl_trigger();
+  pdl_wait();  // (this launch does not end before those in front of it)
 }
 
 // -------------------------------------------------------------------------- //
 // host side
 // -------------------------------------------------------------------------- //
-// Cut units have at most 4/3 as many tasks as runs of the steps' share, three a warp.
-static long long few_most(const KVView& kv, int max_new, int sms) {
-  const long long G = kv.Hq / kv.Hkv, rows = max_new * G, blocks = (rows + 15) / 16;
-  const long long cuts = (FEW_KEYS / FEW_STEP + 3) / 8 + 1;  // (of runs of 8 steps)
-  const long long unit_tasks = (long long)kv.B * kv.Hkv * (blocks < FEW_BLOCKS ? blocks : FEW_BLOCKS) * cuts;
-  const long long most = 4ll * FEW_WARPS * sms;
-  return unit_tasks < most ? unit_tasks : most;
-}
 void few_shape(TreeLaunch* a, int sms) {
   if (a->kv.dtype != PRHS_BF16) return;
   a->few_rows = (long long)a->max_new * (a->kv.Hq / a->kv.Hkv) <= 8 ? 8 : 16;
-  a->few_most = (int)few_most(a->kv, a->max_new, sms);
+  a->few_warps = FEW_WARPS * sms;
 }
 size_t few_state_bytes(const KVView& kv, int max_new, int sms) {
   if (kv.dtype != PRHS_BF16) return 0;
   const size_t rows = (long long)max_new * (kv.Hq / kv.Hkv) <= 8 ? 8 : 16;
-  return few_most(kv, max_new, sms) * rows * (kv.d * sizeof(float) + sizeof(float2));
+  return (size_t)2 * FEW_WARPS * sms * rows * (kv.d * sizeof(float) + sizeof(float2));
 }
-size_t few_ticket_bytes(const KVView& kv, int max_new, int sms) {
-  return kv.dtype != PRHS_BF16 ? 0 : few_most(kv, max_new, sms) * sizeof(int);
+size_t few_where_bytes(const KVView& kv, int T) {
+  return kv.dtype != PRHS_BF16 ? 0 : (size_t)T * kv.Hq * sizeof(int2);
 }
 
 template <int D, int NT>
 static cudaError_t few_go(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t st) {
   auto k = few_kernel<D, NT>;
   static int smem_set[SMEM_DEVICES];
-  const cudaError_t e = allow_smem(k, FEW_WARPS * FEW_RING, smem_set);
+  const cudaError_t e = allow_smem(k, few_smem_bytes(D), smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(sms), dim3(FEW_THREADS), FEW_WARPS * FEW_RING, st, true, maps[0],
+  return launch_pdl(k, dim3(sms), dim3(FEW_THREADS), few_smem_bytes(D), st, true, maps[0],
                     maps[1], maps[2], maps[3], a);
 }
 cudaError_t launch_few(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t st) {
@@ -558,11 +536,14 @@ cudaError_t launch_few(const TreeLaunch& a, const CUtensorMap* maps, int sms, cu
   return a.kv.d == 128 ? few_go<128, 2>(a, maps, sms, st) : few_go<64, 2>(a, maps, sms, st);
 }
 
+template <typename T, int D>
+static cudaError_t join_go(const TreeLaunch& a, cudaStream_t st) {
+  const long long y = ((long long)a.max_new * a.kv.Hq * D / 4 + SJ_THREADS - 1) / SJ_THREADS;
+  return launch_pdl(shared_join_kernel<T, D>, dim3(a.kv.B, (unsigned)(y < 64 ? y : 64)), dim3(SJ_THREADS), 0, st, true, a);
+}
 cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t st) {
-  const long long pass = (long long)SJ_THREADS * SJ_PER, y = ((long long)a.max_new * a.kv.Hq * a.kv.d / 4 + pass - 1) / pass;
-  const dim3 grid(a.kv.B, (unsigned)(y < 64 ? y : 64));
-  if (a.kv.d == 128) return launch_pdl(shared_join_kernel<128>, grid, dim3(SJ_THREADS), 0, st, true, a);
-  return launch_pdl(shared_join_kernel<64>, grid, dim3(SJ_THREADS), 0, st, true, a);
+  if (a.kv.dtype == PRHS_BF16) return a.kv.d == 128 ? join_go<__nv_bfloat16, 128>(a, st) : join_go<__nv_bfloat16, 64>(a, st);
+  return a.kv.d == 128 ? join_go<float, 128>(a, st) : join_go<float, 64>(a, st);
 }
 
 }  // namespace prhs

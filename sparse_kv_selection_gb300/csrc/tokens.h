@@ -79,13 +79,13 @@ struct TreeLaunch {
   float* part_o;    // against the state's maximum
   float2* part_ml;  // maximum (base 2) and sum
   int* part_ok;     // 0: the offsets step back, there are no states
-  // bf16: sequences whose own keys the joining launch attends (few_item)
+  // bf16: sequences whose own keys few_kernel attends (few_item)
   int few_rows;      // query rows of a unit
-  int few_most;      // tasks of cut units at most
-  void* few_states;  // their states
-  int* few_ticket;   // [few_most] at a unit's first task: how many have written theirs
+  int few_warps;     // warps of that launch
+  void* few_states;  // states of units that several warps share, two a warp
+  int2* few_where;   // [Hkv][T * G] the warps that have a row's unit: the first, how many
 };
-// Whether the joining launch attends a sequence's own t keys with its n tokens of G
+// Whether few_kernel attends a sequence's own t keys with its n tokens of G
 // query heads a KV head: a unit of the matrix units' kernel takes a few microseconds
 // to begin and to end, more than a short run of keys takes to read. Every unit of
 // rows reads the keys again, from L2.
@@ -104,12 +104,12 @@ size_t tree_workspace(const KVView& kv, int max_new, int sms);  // (max_new: tre
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
 
-// One launch: the result of the tokens with two partial states; bf16 (issued by
-// launch_tree_tc, with the descriptors of the cache's K and V in boxes of 16 rows and
-// of the new tokens'): also the attention of few_item's sequences.
+// bf16, issued by launch_tree_tc with the descriptors of the cache's K and V in boxes of
+// 16 rows and of the new tokens': the attention of few_item's sequences. Then, on both
+// types, one launch more joins the states of tokens with several.
 void few_shape(TreeLaunch* a, int sms);
 size_t few_state_bytes(const KVView& kv, int max_new, int sms);
-size_t few_ticket_bytes(const KVView& kv, int max_new, int sms);
+size_t few_where_bytes(const KVView& kv, int T);
 cudaError_t launch_few(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t s);
 cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t s);
 // The most tokens that a unit's rows may come from.
@@ -190,7 +190,7 @@ __device__ __forceinline__ int shared_keys(const KVView& kv, const int4* shared,
 // cached keys from `base` on and over each other; or, for rows that share leading
 // keys, an item in front of that of a group's first row: all its rows' tokens over
 // the shared keys of that row. (Items 2 b and 2 b + 1; without sharing, item b.) Not
-// those that the joining launch attends, unless `all`.
+// those that few_kernel attends, unless `all`.
 struct TreeItem {
   int b, base, t;  // row of the cache; its first key here, keys
   int c0, n;       // tokens

@@ -195,7 +195,7 @@ namespace {
 // Workspace of shared attention: that of tree attention over units of up to T
 // tokens, and two partial states of every token.
 struct SharedWs {
-  size_t part_o, part_ml, part_ok, states, ticket, total;
+  size_t part_o, part_ml, part_ok, states, where, total;
 };
 SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -204,8 +204,8 @@ SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   w.part_ml = w.part_o + up((size_t)2 * T * kv.Hq * kv.d * sizeof(float));
   w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
   w.states = w.part_ok + 256;
-  w.ticket = w.states + up(few_state_bytes(kv, max_new, sms));
-  w.total = w.ticket + up(few_ticket_bytes(kv, max_new, sms));
+  w.where = w.states + up(few_state_bytes(kv, max_new, sms));
+  w.total = w.where + up(few_where_bytes(kv, T));
   return w;
 }
 
@@ -256,15 +256,15 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part_ml);
     a.part_ok = reinterpret_cast<int*>(static_cast<char*>(ws) + w.part_ok);
     a.few_states = static_cast<char*>(ws) + w.states;
-    a.few_ticket = reinterpret_cast<int*>(static_cast<char*>(ws) + w.ticket);
+    a.few_where = reinterpret_cast<int2*>(static_cast<char*>(ws) + w.where);
     few_shape(&a, sms);
   }
   cudaError_t e = cudaSuccess;
   if (kv->dtype == PRHS_BF16) {
     if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
-    return launched(e);
+  } else {
+    e = launch_tree(a, sms, ws, stream);
   }
-  e = launch_tree(a, sms, ws, stream);
   if (e != cudaSuccess || !shared) return launched(e);
   abi_count_launch();
   return launched(launch_shared_join(a, stream));

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const __grid_co
   constexpr int C4 = D / 4, CH = JOIN_CH;
   __shared__ float4 so[JOIN_THREADS];
   __shared__ float2 sml[JOIN_THREADS];
-  if (a.shared != nullptr) pdl_trigger();  // (the launch behind it has its own work first)
   pdl_wait();
   pdl_trigger();
   const TreeSplit s = p.split[blockIdx.x];

@@ -362,8 +362,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   pdl_trigger();
   // (the join of a CTA that gives up reads this)
   if (tid == 0) p.rec.split[blockIdx.x] = TreeSplit{};
-  if (SHARED)
-    for (int i = blockIdx.x * TC_THREADS + tid; i < a.few_most; i += gridDim.x * TC_THREADS) a.few_ticket[i] = 0;
 
   // ---- this CTA's run of the list of all tiles ----
   const int per_t = (items + TC_THREADS - 1) / TC_THREADS, e0 = tid * per_t;
@@ -1002,10 +1000,11 @@ static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cu
                  maps[6], p);
   if (e != cudaSuccess) return e;
   abi_count_launch();
-  e = launch_tree_join<__nv_bfloat16, D, false>(p.a, p.rec, sms, st);
-  if (!SHARED || e != cudaSuccess) return e;
-  abi_count_launch();
-  return launch_few(p.a, maps + 3, sms, st);
+  if (SHARED) {  // (it begins while this launch ends; the joins come behind both)
+    if ((e = launch_few(p.a, maps + 3, sms, st)) != cudaSuccess) return e;
+    abi_count_launch();
+  }
+  return launch_tree_join<__nv_bfloat16, D, false>(p.a, p.rec, sms, st);
 }
 
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t st, cudaError_t* err) {
