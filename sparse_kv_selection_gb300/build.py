@@ -18,7 +18,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libprhs.so")
 SOURCES = ["api.cu", "score.cu", "cis.cu", "attn.cu", "attn_cluster.cu", "select.cu", "retrieve.cu", "dense.cu",
            "noalloc.cu", "mass.cu", "grow.cu", "plan.cu", "rope.cu", "tree.cu", "tree_tc.cu", "commit.cu", "tokens_api.cu",
-           "pages.cu", "copy.cu", "share.cu", "shared.cu", "pages_api.cu"]
+           "pages.cu", "copy.cu", "share.cu", "shared.cu", "shared_tc.cu", "pages_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -4,36 +4,19 @@
 //
 //   m = max(m1, m2),  o = (2^(m1 - m) o1 + 2^(m2 - m) o2) / (2^(m1 - m) l1 + 2^(m2 - m) l2)
 //
-// On bf16 caches this launch also computes the second state of sequences with few
-// query rows on few keys (few_item): single tokens, drafts, short prompts. A unit of
-// the tcgen05 kernel begins and ends in 3 to 4 us, whatever it holds, and a CTA has
-// one at a time; here units of 8 or 16 rows are CTAs of four warps, several an SM.
-//
-// Inside: a warp takes 16 keys at a time. They are the 16 rows of mma.sync, query rows
-// its 8 columns, so that a warp reads every key once and 8 rows cost 8 columns:
-//   S^T = K Q^T,  P^T = exp2(S^T - m) in bf16 (transposed by movmatrix),  O^T += V^T P^T
-// Every warp has its own ring in shared memory, which its first lane fills by TMA
-// (128-byte swizzle), so that warps wait for nobody but their copies. (Loads by all
-// lanes straight into the registers of the products: 540 MB of own keys 120 us, four
-// times the instructions; with asynchronous 16-byte copies 173.) The warps' states meet in shared memory; a unit of many keys is shared by up
-// to FEW_SPLIT CTAs, the last of which to arrive (a ticket) joins their states.
-//
-// Bound: HBM (the keys, once), and latency: lengths, page numbers, keys, states are
-// four dependent reads. All but the last run before the launches it waits for end.
+// On bf16 each may lie in pieces, one for each CTA or warp of the launch before that had
+// a run of its unit's keys (`where`: the first, how many). A thread takes four columns of
+// a row; eight consecutive rows are neighbours, as the pieces keep them. Bound: L2
+// and latency (where, then the states).
 #include "tree_join.cuh"
 
 namespace prhs {
 
-// -------------------------------------------------------------------------- //
-// the join
-// -------------------------------------------------------------------------- //
 constexpr int SJ_THREADS = 256;
 
-// A thread takes four columns of a row. On bf16 the state against the other keys may
-// lie in pieces, one for each warp of few_kernel that had steps of its unit (a warp's
-// state 2 w + 1 is of the unit that it begins, 2 w of one begun before).
 template <typename T, int D>
-__global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ TreeLaunch a) {
+__global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ TreeLaunch a,
+                                                                 const __grid_constant__ TreeRecords rec, int ctas) {
   constexpr int C4 = D / 4;
   pdl_wait();
   pdl_trigger();
@@ -41,15 +24,22 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
   const int G = kv.Hq / kv.Hkv, gl = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, b = blockIdx.x;
   const TreeItem x = tree_item<true>(a, 2 * b + 1, true);
   const bool few = few_item(a, x.n, x.t);
-  if (x.n == 0 || (x.part != 2 && !few) || *a.part_ok == 0) return;
-  const int rows = x.n << gl;
-  const long long total = (long long)rows * kv.Hkv * C4;
+  if (x.n == 0 || (sizeof(T) == 4 && x.part != 2) || *a.part_ok == 0) return;
+  // the group's first token (its units of the shared keys count rows from there)
+  const int group0 = x.part == 2 ? max(0, a.cu_new[a.shared[b].x]) : 0;
+  const int rows = x.n << gl, blocks = (rows + 7) / 8;
+  const long long total = (long long)kv.Hkv * blocks * 8 * C4;
   for (long long i = (long long)blockIdx.y * SJ_THREADS + threadIdx.x; i < total; i += (long long)gridDim.y * SJ_THREADS) {
-    const int c4 = (int)(i % C4), hr = (int)(i / C4), kvh = hr / rows, r = hr - kvh * rows;
+    const int in = (int)i & 7, c4 = (int)(i / 8 % C4), hr = (int)(i / (8 * C4)), kvh = hr / blocks, r = (hr - kvh * blocks) * 8 + in;
+    if (r >= rows) continue;
     const int tok = x.c0 + (r >> gl), h = r & (G - 1);
-    int2 where = make_int2(0, 1);
-    if (few) where = __ldcg(a.few_where + (long long)kvh * ((long long)a.T << gl) + (tok << gl) + h);
-    if (where.y == 1 && x.part != 2) continue;  // its result stands
+    int2 at[2] = {make_int2(0, 1), make_int2(0, 1)};  // of the states against the shared and the other keys
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < 2; k++)
+        if (k == 1 || x.part == 2) at[k] = __ldcg(a.where + part_row<T>(a, k + 1, tok, kvh, h, gl));
+    }
+    if (x.part != 2 && at[1].y == 1) continue;  // its result stands
     float M = -INFINITY, L = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, float4 o) {  // (a state that holds NaN has it in its sum, whatever its maximum)
@@ -59,26 +49,31 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
       tree_fma(y, w1, o);
       M = m;
     };
-    float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
-    float4 o[2] = {y, y};
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      if (k == 0 ? x.part != 2 : where.y > 1) continue;
-      ml[k] = __ldcg(a.part_ml + part_row<T>(a, k + 1, tok, kvh, h, gl));
-      o[k] = __ldcg(part_at<T, D>(a, k + 1, tok, kvh, h, c4, gl));
-    }
-    if (where.y > 1) {
-      const int RB = a.few_rows, in = r % RB;
-      const float4* states = static_cast<const float4*>(a.few_states);
-      const float2* sums = reinterpret_cast<const float2*>(states + (long long)2 * a.few_warps * C4 * RB);
+      if (k == 0 && x.part != 2) continue;
+      if (at[k].y == 1) {
+        add(__ldcg(a.part_ml + part_row<T>(a, k + 1, tok, kvh, h, gl)), __ldcg(part_at<T, D>(a, k + 1, tok, kvh, h, c4, gl)));
+        continue;
+      }
+      if constexpr (sizeof(T) == 2) {
+        // piece w: the first writer's second slot, the others' first ones; rows as their unit counts them
+        const bool warps = k == 1 && few;
+        const int writers = warps ? a.few_warps : ctas, unit = warps ? a.few_rows : 256;
+        const int first = max(0, min(at[k].x, writers - 1)), n = max(1, min(at[k].y, writers - first));
+        const int row = (k == 0 ? ((tok - group0) << gl) + h : r) & (unit - 1);
+        const float2* ml = warps ? reinterpret_cast<const float2*>(static_cast<const float4*>(a.few_states) +
+                                                                   (long long)2 * writers * C4 * unit)
+                                 : rec.ml;
+        const float4* o = warps ? static_cast<const float4*>(a.few_states) : rec.o;
+        const int stride = warps ? unit : rec.rows_max;
 #pragma unroll 4
-      for (int w = 0; w < where.y; w++) {
-        const long long slot = 2ll * (where.x + w) + (w == 0);
-        add(__ldcg(sums + slot * RB + in), __ldcg(states + (slot * C4 + c4) * RB + in));
+        for (int w = 0; w < n; w++) {
+          const long long slot = 2ll * (first + w) + (w == 0);
+          add(__ldcg(ml + slot * stride + row), __ldcg(o + (slot * C4 + c4) * stride + row));
+        }
       }
     }
-#pragma unroll
-    for (int k = 0; k < 2; k++) add(ml[k], o[k]);
     const float inv = tree_inv(L);
     const long long orow = (long long)tok * kv.Hq + (kvh << gl) + h;
     tree_put(static_cast<T*>(a.out) + orow * D + c4 * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -86,464 +81,16 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
   }
 }
 
-// -------------------------------------------------------------------------- //
-// bf16: few rows on few keys
-// -------------------------------------------------------------------------- //
-constexpr int FEW_WARPS = 8, FEW_THREADS = FEW_WARPS * 32;
-constexpr int FEW_STEP = 16;        // keys of a warp's step: a box, never over a page's end
-constexpr int FEW_RING = 24 << 10;  // bytes of a warp's ring: 3 steps at d = 128, 6 at 64
-constexpr int FEW_RUN = 8;          // steps of a warp at least
-constexpr int few_smem_bytes(int d) { return FEW_WARPS * (FEW_RING + 8 * d * 4); }
-constexpr float FEW_LOG2E = 1.4426950408889634f;
-constexpr float FEW_RESCALE = 8.f;  // growth of a maximum (base 2) that rescales, as in the tcgen05 kernel
-
-// D += A B, 16 x 8 x 16, bf16.
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t few_pack(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float few_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Four 8 x 8 matrices of 16-bit elements, a row's address a lane; as they are or transposed.
-__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-// One sequence's share of the list of steps, KV head by KV head: units of RB query
-// rows, each of as many steps as the longest (causal ones that see fewer new tokens
-// leave the last empty).
-struct FewSeq {
-  TreeItem x;
-  int blocks, steps;  // units of a KV head, steps of a unit
-};
-template <int RB>
-__device__ __forceinline__ int few_steps(const TreeLaunch& a, const TreeItem& x, int gl, int blk, int* fresh) {
-  const int end = min(x.n << gl, (blk + 1) * RB);  // (causal: new tokens up to the unit's last one)
-  *fresh = a.mask == nullptr ? ((end - 1) >> gl) + 1 : x.n;
-  return (x.t + FEW_STEP - 1) / FEW_STEP + (*fresh + FEW_STEP - 1) / FEW_STEP;
-}
-template <int RB>
-__device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, int b, int gl) {
-  FewSeq s;
-  s.x = tree_item<true>(a, 2 * b + 1, true);
-  s.blocks = s.steps = 0;
-  if (!few_item(a, s.x.n, s.x.t)) return s;
-  s.blocks = ((s.x.n << gl) + RB - 1) / RB;
-  int fresh;
-  if (s.blocks > 0) s.steps = few_steps<RB>(a, s.x, gl, s.blocks - 1, &fresh);
-  return s;
-}
-
-// A unit's steps in a warp's run of the list.
-struct FewTask {
-  TreeItem x;
-  int kvh, blk, s0, s1;    // KV head, unit, steps here
-  int taken;               // of the list
-  int cached, fresh;       // steps over the cache, new tokens that the unit sees
-  int first, cuts;         // the warp that begins the unit, the warps that have steps of it
-  int window, at;          // rows of steps window .. window + 31, one a lane
-  bool some;               // (none: the run is done)
-};
-
-template <int D, int NT>
-__global__ void __launch_bounds__(FEW_THREADS, 1)
-    few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-               const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
-               const __grid_constant__ TreeLaunch a) {
-  // a step's K, then its V: SEGS column segments of 16 rows of 128 bytes
-  constexpr int RB = 8 * NT, C4 = D / 4, SEGS = D / 64, SEG = FEW_STEP * 128, STAGE = 2 * SEGS * SEG, STAGES = FEW_RING / STAGE;
-  constexpr int WARP_SMEM = few_smem_bytes(D) / FEW_WARPS;  // the ring, and eight rows of a state
-  extern __shared__ __align__(1024) uint8_t few_smem[];
-  __shared__ uint64_t full[FEW_WARPS][STAGES];
-  __shared__ int wsum[FEW_WARPS];
-  __shared__ int steps_to[FEW_THREADS];  // of the list, up to a thread's sequences
-  const KVView& kv = a.kv;
-  const int G = kv.Hq / kv.Hkv, gl = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int gw = blockIdx.x * FEW_WARPS + warp, gws = gridDim.x * FEW_WARPS;
-  if (warp == 0 && lane < 4) prefetch_tmap(lane == 0 ? &kmap : lane == 1 ? &vmap : lane == 2 ? &knmap : &vnmap);
-  if (lane == 0) {
-    for (int i = 0; i < STAGES; i++) mbar_init(&full[warp][i], 1);
-    fence_barrier_init();
-  }
-
-  // ---- the list of all steps, a prefix over the sequences (a run of them a thread) ----
-  const int per = (kv.B + FEW_THREADS - 1) / FEW_THREADS, b0 = min(kv.B, tid * per), b1 = min(kv.B, b0 + per);
-  int steps = 0, total = 0;
-  bool back = false;  // (flagged by the launch in front: no row is written)
-  for (int b = b0; b < b1; b++) {
-    const FewSeq s = few_seq<RB>(a, b, gl);
-    back |= a.cu_new[b + 1] < a.cu_new[b];
-    steps += kv.Hkv * s.blocks * s.steps;
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(FULL_MASK, steps, o);
-    if (lane >= o) steps += y;
-  }
-  if (lane == 31) wsum[warp] = steps;
-  back = __syncthreads_or(back);
-#pragma unroll
-  for (int w = 0; w < FEW_WARPS; w++) {
-    const int y = wsum[w];
-    if (w < warp) steps += y;
-    total += y;
-  }
-  steps_to[tid] = steps;
-  __syncthreads();
-  // Every warp takes an equal run. A unit cut by the end of one leaves states, joined by the
-  // last warp to come to its end in it; runs of fewer than eight steps would cost more than they give.
-  const int run = max((total + gws - 1) / gws, FEW_RUN);
-  if (back) total = 0;
-  int pos = min(total, gw * run);
-  const int end = min(total, pos + run);
-  if ((smem_addr(few_smem) & 1023) != 0) {  // the swizzle needs it
-    raise_error(kv.err, PRHS_DEV_CAPACITY);
-    return;
-  }
-
-  const bool causal = a.mask == nullptr;
-  const uint32_t ring = smem_addr(few_smem) + warp * WARP_SMEM;
-  float4* staged = reinterpret_cast<float4*>(few_smem + warp * WARP_SMEM + FEW_RING);  // [C4][8]
-  const float sc = a.scale * FEW_LOG2E;
-
-  // Rows of the task's next steps' first keys (-1: on no page).
-  auto look_up = [&](FewTask& t, int window) {
-    t.window = window;
-    t.at = 0;
-    const int s = window + lane, key = t.x.base + s * FEW_STEP;
-    if (s >= min(t.s1, t.cached)) return;
-    if (kv.block_table == nullptr) {
-      t.at = (t.x.b * kv.Hkv + t.kvh) * kv.t_max + key;
-      return;
-    }
-    const int page = kv.block_table[(long long)t.x.b * kv.max_blocks + key / kv.block_size];
-    const bool ok = (unsigned)page < (unsigned)kv.num_blocks;
-    if (!ok) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
-    t.at = ok ? (page * kv.Hkv + t.kvh) * kv.block_size + key % kv.block_size : -1;
-  };
-  auto fetch = [&]() {  // at pos, which moves on
-    FewTask t = {};
-    if (pos >= end) return t;
-    int lo = 0, hi = FEW_THREADS - 1;  // the first thread whose sequences end behind it
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (steps_to[mid] > pos) hi = mid; else lo = mid + 1;
-    }
-    int off = pos - (lo > 0 ? steps_to[lo - 1] : 0), b = lo * per;
-    FewSeq s = few_seq<RB>(a, b, gl);
-    for (int x; off >= (x = kv.Hkv * s.blocks * s.steps);) {
-      off -= x;
-      s = few_seq<RB>(a, ++b, gl);
-    }
-    const int unit = off / s.steps, in = off - unit * s.steps, start = pos - in;
-    t.x = s.x;
-    t.kvh = unit / s.blocks;
-    t.blk = unit - t.kvh * s.blocks;
-    t.taken = min(s.steps - in, end - pos);
-    pos += t.taken;
-    t.some = true;
-    t.first = start / run;
-    t.cuts = (start + s.steps - 1) / run - t.first + 1;
-    const int all = few_steps<RB>(a, t.x, gl, t.blk, &t.fresh);
-    t.cached = (t.x.t + FEW_STEP - 1) / FEW_STEP;
-    t.s0 = min(in, all);
-    t.s1 = min(in + t.taken, all);
-    look_up(t, t.s0);
-    return t;
-  };
-  int counts = 0;  // keys of the ring's steps, five bits each
-  auto load = [&](FewTask& t, int s, int stage) {
-    if (s >= t.window + 32) look_up(t, t.window + 32);
-    const int row = __shfl_sync(FULL_MASK, t.at, s - t.window), j = (s - t.cached) * FEW_STEP;
-    const bool is_new = s >= t.cached;
-    const int n = is_new ? min(FEW_STEP, t.fresh - j) : row < 0 ? 0 : min(FEW_STEP, t.x.t - s * FEW_STEP);
-    counts = (counts & ~(31 << 5 * stage)) | n << 5 * stage;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&full[warp][stage], STAGE);
-      const CUtensorMap *km = is_new ? &knmap : &kmap, *vm = is_new ? &vnmap : &vmap;
-      const int z = is_new ? t.kvh : max(row, 0), w = is_new ? t.x.c0 + j : 0;
-#pragma unroll
-      for (int i = 0; i < SEGS; i++) tma_load_4d(ring + stage * STAGE + i * SEG, km, 0, i, z, w, &full[warp][stage]);
-#pragma unroll
-      for (int i = 0; i < SEGS; i++) tma_load_4d(ring + stage * STAGE + (SEGS + i) * SEG, vm, 0, i, z, w, &full[warp][stage]);
-    }
-    __syncwarp();
-  };
-  // The copies run ahead of the products into the next task, which is known while this one is worked on.
-  int fill = 0, held = 0, stage = 0;  // the stage to fill next, stages filled, the stage to use next
-  uint32_t phase = 0;
-  bool dead = false, in_next = false;
-  FewTask cur = fetch(), nxt;
-  int cursor = cur.s0;
-  for (; cur.some; cur = nxt) {
-    if (!in_next) cursor = cur.s0;
-    in_next = false;
-    bool known = false;
-    const TreeItem x = cur.x;
-    const int blk = cur.blk, kvh = cur.kvh;
-    const int rows = min(RB, (x.n << gl) - blk * RB), tok0 = (blk * RB) >> gl, cached = cur.cached;
-    // Q as the products take it: rows g of each eight, columns 16 j + 2 c and 16 j + 8 + 2 c
-    uint32_t q[NT][D / 16][2];
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      const int r = blk * RB + 8 * t + g;
-      const bool have = 8 * t + g < rows;
-      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
-                                 ((long long)(x.c0 + (have ? r >> gl : tok0)) * kv.Hq + (kvh << gl) + (have ? r & (G - 1) : 0)) * D;
-#pragma unroll
-      for (int j = 0; j < D / 16; j++)
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-          q[t][j][h] = have ? *reinterpret_cast<const uint32_t*>(row + 16 * j + 8 * h + 2 * c) : 0u;
-    }
-
-  float m[NT][2], l[NT][2], o[NT][D / 16][4];  // rows 8 t + 2 c, + 1; O's columns 16 e + g, + 8
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-    m[t][0] = m[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 16; e++) o[t][e][0] = o[t][e][1] = o[t][e][2] = o[t][e][3] = 0.f;
-  }
-  // a lane's row of the four matrices of a product's operand: K's rows lane % 16, columns 8 (lane / 16) ..;
-  // V's the other way about (its matrices come in the order of d, then keys)
-  const int krow = lane & 15, kcol = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vcol = lane >> 3 & 1;
-  const uint32_t k_at = ring + krow * 128, v_at = ring + SEGS * SEG + vrow * 128;
-  for (int s = cur.s0;; s++) {
-    while (held < STAGES) {
-      if (!in_next && cursor >= cur.s1) {
-        if (!known || !nxt.some) break;
-        in_next = true;
-        cursor = nxt.s0;
-      }
-      if (in_next && cursor >= nxt.s1) break;
-      load(in_next ? nxt : cur, cursor++, fill);
-      fill = fill + 1 == STAGES ? 0 : fill + 1;
-      held++;
-    }
-    if (!known) {
-      nxt = fetch();
-      known = true;
-    }
-    if (s >= cur.s1) break;
-    dead = !__all_sync(FULL_MASK, mbar_wait(&full[warp][stage], phase, kv.err));
-    if (dead) break;
-    const int n = counts >> 5 * stage & 31;
-    float p[NT][4];  // keys g: rows 2 c, 2 c + 1; keys g + 8
-#pragma unroll
-    for (int t = 0; t < NT; t++) p[t][0] = p[t][1] = p[t][2] = p[t][3] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; j++) {
-      uint32_t k[4];
-      ldm4(k, k_at + stage * STAGE + j / 4 * SEG + (((j % 4 * 2 + kcol) ^ (krow & 7)) << 4));
-#pragma unroll
-      for (int t = 0; t < NT; t++) mma16(p[t], k[0], k[1], k[2], k[3], q[t][j][0], q[t][j][1]);
-    }
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      const int key0 = (s - cached) * FEW_STEP;  // (new tokens)
-#pragma unroll
-      for (int i = 0; i < 4; i++) p[t][i] *= sc;
-      if (s >= cached || n < FEW_STEP) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int key = g + 8 * (i >> 1);
-          bool see = key < n;
-          if (s >= cached && see) {
-            const int tok = min((blk * RB + 8 * t + 2 * c + (i & 1)) >> gl, x.n - 1);
-            see = causal ? key0 + key <= tok
-                         : (a.mask[(long long)(x.c0 + tok) * PRHS_TREE_WORDS + ((key0 + key) >> 5)] >> ((key0 + key) & 31)) & 1u;
-          }
-          if (!see) p[t][i] = -INFINITY;
-        }
-      }
-      float mx[2] = {fmaxf(p[t][0], p[t][2]), fmaxf(p[t][1], p[t][3])};
-      auto grows = [&](int r) { return mx[r] > m[t][r] + FEW_RESCALE || (m[t][r] == -INFINITY && mx[r] > -INFINITY); };
-      if (__any_sync(FULL_MASK, grows(0) || grows(1))) {
-#pragma unroll
-        for (int r = 0; r < 2; r++) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(FULL_MASK, mx[r], d));
-          const bool grow = grows(r);
-          const float corr = grow ? few_ex2(m[t][r] - mx[r]) : 1.f;
-          if (grow) m[t][r] = mx[r];
-          l[t][r] *= corr;
-#pragma unroll
-          for (int e = 0; e < D / 16; e++) {
-            o[t][e][r] *= corr;
-            o[t][e][2 + r] *= corr;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float ref = m[t][i & 1] == -INFINITY ? 0.f : m[t][i & 1];
-        p[t][i] = few_ex2(p[t][i] - ref);
-        l[t][i & 1] += p[t][i];
-      }
-      pb[t][0] = transpose8(few_pack(p[t][0], p[t][1]));
-      pb[t][1] = transpose8(few_pack(p[t][2], p[t][3]));
-    }
-    // rows of V that do not exist hold whatever was there, and 0 * inf is not 0
-    const uint32_t keep0 = (2 * c < n ? 0xffffu : 0u) | (2 * c + 1 < n ? 0xffff0000u : 0u);
-    const uint32_t keep1 = (2 * c + 8 < n ? 0xffffu : 0u) | (2 * c + 9 < n ? 0xffff0000u : 0u);
-#pragma unroll
-    for (int e = 0; e < D / 16; e++) {
-      uint32_t v[4];  // columns 16 e + g, + 8: keys 2 c, + 1; then keys + 8
-      ldm4_trans(v, v_at + stage * STAGE + e / 4 * SEG + (((e % 4 * 2 + vcol) ^ (vrow & 7)) << 4));
-      if (n < FEW_STEP) {
-        v[0] &= keep0;
-        v[1] &= keep0;
-        v[2] &= keep1;
-        v[3] &= keep1;
-      }
-#pragma unroll
-      for (int t = 0; t < NT; t++) mma16(o[t][e], v[0], v[1], v[2], v[3], pb[t][0], pb[t][1]);
-    }
-    __syncwarp();  // (the stage has been read)
-    held--;
-    if (++stage == STAGES) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-  if (dead) break;
-
-  // ---- its state, four columns a lane: row lane % 8 of each eight, columns 4 (lane / 8 + 4 k) .. ----
-  const int sr = lane & 7, sq = lane >> 3;
-  float2 ml[NT];
-  float4 y[NT][C4 / 4];
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[t][r] += __shfl_xor_sync(FULL_MASK, l[t][r], d);
-#pragma unroll
-      for (int e = 0; e < D / 16; e++)
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-          reinterpret_cast<float*>(staged + (4 * e + 2 * h + g / 4) * 8 + 2 * c + r)[g % 4] = o[t][e][2 * h + r];
-    }
-    __syncwarp();
-    // (row 8 t + 2 c + r is in lanes c of any g)
-    const float m0 = __shfl_sync(FULL_MASK, m[t][0], sr >> 1), m1 = __shfl_sync(FULL_MASK, m[t][1], sr >> 1);
-    const float l0 = __shfl_sync(FULL_MASK, l[t][0], sr >> 1), l1 = __shfl_sync(FULL_MASK, l[t][1], sr >> 1);
-    ml[t] = sr & 1 ? make_float2(m1, l1) : make_float2(m0, l0);
-#pragma unroll
-    for (int k = 0; k < C4 / 4; k++) y[t][k] = staged[(sq + 4 * k) * 8 + sr];
-  }
-
-  // a unit cut by the run's end, or with a state against shared keys, is for the join; nothing
-  // here waits for what it writes (or for the launch in front)
-  const bool cut = cur.cuts > 1, result = !cut && x.part == 0;
-  float4* states = static_cast<float4*>(a.few_states);  // [2 warps][C4][RB], then (maximum, sum) [2 warps][RB]
-  float2* sums = reinterpret_cast<float2*>(states + (long long)2 * gws * C4 * RB);
-  const long long slot = 2ll * gw + (cur.first == gw);
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-    const int r = blk * RB + 8 * t + sr, tok = x.c0 + (r >> gl), h = r & (G - 1);
-    if (8 * t + sr >= rows) continue;
-    const long long prow = part_row<__nv_bfloat16>(a, 2, tok, kvh, h, gl), orow = (long long)tok * kv.Hq + (kvh << gl) + h;
-    const float inv = tree_inv(ml[t].y);
-#pragma unroll
-    for (int k = 0; k < C4 / 4; k++) {
-      const int c4 = sq + 4 * k;
-      if (result)
-        tree_put(static_cast<__nv_bfloat16*>(a.out) + orow * D + c4 * 4,
-                 make_float4(y[t][k].x * inv, y[t][k].y * inv, y[t][k].z * inv, y[t][k].w * inv));
-      else if (cut)
-        __stcg(states + (slot * C4 + c4) * RB + 8 * t + sr, y[t][k]);
-      else
-        __stcg(part_at<__nv_bfloat16, D>(a, 2, tok, kvh, h, c4, gl), y[t][k]);
-    }
-    if (sq != 0) continue;
-    if (result) a.lse[orow] = tree_lse(ml[t].x, ml[t].y);
-    else if (cut) __stcg(sums + slot * RB + 8 * t + sr, ml[t]);
-    else __stcg(a.part_ml + prow, ml[t]);
-    // (warps that begin no step of a unit do not know its first)
-    if (cur.first == gw) a.few_where[(long long)kvh * ((long long)a.T << gl) + (tok << gl) + h] = make_int2(cur.first, cur.cuts);
-  }
-  }
-  if (dead)  // nothing may still be in flight when the CTA ends
-    for (int i = 0; i < held; i++) {
-      mbar_wait(&full[warp][stage], phase, kv.err);
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
-  pdl_trigger();
-  pdl_wait();  // (this launch does not end before those in front of it)
-}
-
-// -------------------------------------------------------------------------- //
-// host side
-// -------------------------------------------------------------------------- //
-void few_shape(TreeLaunch* a, int sms) {
-  if (a->kv.dtype != PRHS_BF16) return;
-  a->few_rows = (long long)a->max_new * (a->kv.Hq / a->kv.Hkv) <= 8 ? 8 : 16;
-  a->few_warps = FEW_WARPS * sms;
-}
-size_t few_state_bytes(const KVView& kv, int max_new, int sms) {
-  if (kv.dtype != PRHS_BF16) return 0;
-  const size_t rows = (long long)max_new * (kv.Hq / kv.Hkv) <= 8 ? 8 : 16;
-  return (size_t)2 * FEW_WARPS * sms * rows * (kv.d * sizeof(float) + sizeof(float2));
-}
-size_t few_where_bytes(const KVView& kv, int T) {
-  return kv.dtype != PRHS_BF16 ? 0 : (size_t)T * kv.Hq * sizeof(int2);
-}
-
-template <int D, int NT>
-static cudaError_t few_go(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t st) {
-  auto k = few_kernel<D, NT>;
-  static int smem_set[SMEM_DEVICES];
-  const cudaError_t e = allow_smem(k, few_smem_bytes(D), smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(sms), dim3(FEW_THREADS), few_smem_bytes(D), st, true, maps[0],
-                    maps[1], maps[2], maps[3], a);
-}
-cudaError_t launch_few(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t st) {
-  if (a.few_rows == 8) return a.kv.d == 128 ? few_go<128, 1>(a, maps, sms, st) : few_go<64, 1>(a, maps, sms, st);
-  return a.kv.d == 128 ? few_go<128, 2>(a, maps, sms, st) : few_go<64, 2>(a, maps, sms, st);
-}
-
 template <typename T, int D>
-static cudaError_t join_go(const TreeLaunch& a, cudaStream_t st) {
-  const long long y = ((long long)a.max_new * a.kv.Hq * D / 4 + SJ_THREADS - 1) / SJ_THREADS;
-  return launch_pdl(shared_join_kernel<T, D>, dim3(a.kv.B, (unsigned)(y < 64 ? y : 64)), dim3(SJ_THREADS), 0, st, true, a);
+static cudaError_t join_go(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
+  const long long rows = ((long long)a.max_new * (a.kv.Hq / a.kv.Hkv) + 7) / 8 * 8;
+  const long long y = (rows * a.kv.Hkv * D / 4 + SJ_THREADS - 1) / SJ_THREADS;
+  return launch_pdl(shared_join_kernel<T, D>, dim3(a.kv.B, (unsigned)(y < 256 ? y : 256)), dim3(SJ_THREADS), 0, st, true, a, rec, sms);
 }
-cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t st) {
-  if (a.kv.dtype == PRHS_BF16) return a.kv.d == 128 ? join_go<__nv_bfloat16, 128>(a, st) : join_go<__nv_bfloat16, 64>(a, st);
-  return a.kv.d == 128 ? join_go<float, 128>(a, st) : join_go<float, 64>(a, st);
+cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
+  if (a.kv.dtype == PRHS_BF16)
+    return a.kv.d == 128 ? join_go<__nv_bfloat16, 128>(a, rec, sms, st) : join_go<__nv_bfloat16, 64>(a, rec, sms, st);
+  return a.kv.d == 128 ? join_go<float, 128>(a, rec, sms, st) : join_go<float, 64>(a, rec, sms, st);
 }
 
 }  // namespace prhs

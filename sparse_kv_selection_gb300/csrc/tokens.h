@@ -79,39 +79,40 @@ struct TreeLaunch {
   float* part_o;    // against the state's maximum
   float2* part_ml;  // maximum (base 2) and sum
   int* part_ok;     // 0: the offsets step back, there are no states
-  // bf16: sequences whose own keys few_kernel attends (few_item)
+  // bf16: which CTAs or warps have pieces of a row's states, [2][Hkv][T * G]: the first, how many
+  int2* where;
+  // and the few rows' part of the launch (few_item)
   int few_rows;      // query rows of a unit
-  int few_warps;     // warps of that launch
-  void* few_states;  // states of units that several warps share, two a warp
-  int2* few_where;   // [Hkv][T * G] the warps that have a row's unit: the first, how many
+  int few_warps;     // warps that it may have
+  void* few_states;  // [2 few_warps] states of units that several warps share, two a warp
 };
-// Whether few_kernel attends a sequence's own t keys with its n tokens of G
-// query heads a KV head: a unit of the matrix units' kernel takes a few microseconds
-// to begin and to end, more than a short run of keys takes to read. Every unit of
-// rows reads the keys again, from L2.
+// Whether a sequence's own t keys with its n tokens of G query heads a KV head go to
+// that part. Its units of few_rows rows read the keys each, at the cost of a step of 16
+// and five more to begin and end; a tile of 128 of the other part costs it about twice
+// as much as they take to read, and a unit as much as 45.
 constexpr int FEW_KEYS = 4096;
-constexpr int FEW_BLOCKS = 64;  // units of a KV head at most
 __device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
-  const long long blocks = ((long long)n * (a.kv.Hq / a.kv.Hkv) + a.few_rows - 1) / max(a.few_rows, 1);
-  return a.few_rows > 0 && blocks <= FEW_BLOCKS && blocks * ((long long)t + n) <= FEW_KEYS;
+  if (a.few_rows == 0 || t + n > FEW_KEYS) return false;
+  const int blocks = (int)(((long long)n * (a.kv.Hq / a.kv.Hkv) + a.few_rows - 1) / a.few_rows), steps = (t + n + 15) / 16;
+  return (long long)blocks * (steps + 5) <= 2 * steps + 45;
 }
 // fp32: two launches, the first counted by the callee; ws holds
 // tree_workspace(kv, max_new, sms) bytes.
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t s);
 size_t tree_workspace(const KVView& kv, int max_new, int sms);  // (max_new: tree_most_new)
-// bf16: two launches, with shared keys three, all but the last counted by the callee; *err is the launches'
+// bf16: two launches, the first counted by the callee; *err is the launches'
 // result when the descriptors could be made. Workspace bytes of a call.
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
 
-// bf16, issued by launch_tree_tc with the descriptors of the cache's K and V in boxes of
-// 16 rows and of the new tokens': the attention of few_item's sequences. Then, on both
-// types, one launch more joins the states of tokens with several.
+// With shared keys: fp32 launch_tree, then the join; bf16 one launch (counted) and the
+// join. rec: the partial states of the launch's `ctas` CTAs.
+struct TreeRecords;
+prhs_status launch_shared_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
+cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int ctas, cudaStream_t s);
 void few_shape(TreeLaunch* a, int sms);
 size_t few_state_bytes(const KVView& kv, int max_new, int sms);
-size_t few_where_bytes(const KVView& kv, int T);
-cudaError_t launch_few(const TreeLaunch& a, const CUtensorMap* maps, int sms, cudaStream_t s);
-cudaError_t launch_shared_join(const TreeLaunch& a, cudaStream_t s);
+size_t shared_where_bytes(const KVView& kv, int T);
 // The most tokens that a unit's rows may come from.
 inline int tree_most_new(const TreeLaunch& a) { return a.shared != nullptr ? a.T : a.max_new; }
 
@@ -190,7 +191,7 @@ __device__ __forceinline__ int shared_keys(const KVView& kv, const int4* shared,
 // cached keys from `base` on and over each other; or, for rows that share leading
 // keys, an item in front of that of a group's first row: all its rows' tokens over
 // the shared keys of that row. (Items 2 b and 2 b + 1; without sharing, item b.) Not
-// those that few_kernel attends, unless `all`.
+// those of the few rows' part, unless `all`.
 struct TreeItem {
   int b, base, t;  // row of the cache; its first key here, keys
   int c0, n;       // tokens

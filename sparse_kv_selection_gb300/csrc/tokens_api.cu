@@ -2,7 +2,7 @@
 // contract of every entry point is in include/prhs.h.
 #include <cmath>
 
-#include "tokens.h"
+#include "tree_join.cuh"
 
 using namespace prhs;
 
@@ -205,7 +205,7 @@ SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
   w.states = w.part_ok + 256;
   w.where = w.states + up(few_state_bytes(kv, max_new, sms));
-  w.total = w.where + up(few_where_bytes(kv, T));
+  w.total = w.where + up(shared_where_bytes(kv, T));
   return w;
 }
 
@@ -256,18 +256,18 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part_ml);
     a.part_ok = reinterpret_cast<int*>(static_cast<char*>(ws) + w.part_ok);
     a.few_states = static_cast<char*>(ws) + w.states;
-    a.few_where = reinterpret_cast<int2*>(static_cast<char*>(ws) + w.where);
+    a.where = reinterpret_cast<int2*>(static_cast<char*>(ws) + w.where);
     few_shape(&a, sms);
   }
   cudaError_t e = cudaSuccess;
   if (kv->dtype == PRHS_BF16) {
-    if ((s = launch_tree_tc(a, sms, ws, stream, &e)) != PRHS_OK) return s;
-  } else {
-    e = launch_tree(a, sms, ws, stream);
+    s = shared ? launch_shared_tc(a, sms, ws, stream, &e) : launch_tree_tc(a, sms, ws, stream, &e);
+    return s != PRHS_OK ? s : launched(e);
   }
+  e = launch_tree(a, sms, ws, stream);
   if (e != cudaSuccess || !shared) return launched(e);
   abi_count_launch();
-  return launched(launch_shared_join(a, stream));
+  return launched(launch_shared_join(a, TreeRecords{}, 0, stream));
 }
 
 }  // namespace
