@@ -1,6 +1,6 @@
-// Attention of few query rows over few keys, on bf16 caches whose rows share leading
-// keys: the part of the tcgen05 kernel's launch (tree_tc.cuh) that computes the state of
-// single tokens, drafts and short prompts against their sequences' own keys (few_item).
+// Attention of few query rows, on bf16 caches whose rows share leading
+// keys: the part of the tcgen05 kernel's launch (tree_tc.cuh) that computes the states of
+// single tokens and drafts against their sequences' own keys (few_item).
 // A unit of the tcgen05 part begins and ends in 3 to 4 us, whatever it holds; here
 // units are 8 or 16 rows of one KV head, and a warp takes a run of their steps of 16
 // keys.
@@ -24,9 +24,15 @@ namespace prhs {
 
 constexpr int FEW_WARPS = 8;
 constexpr int FEW_STEP = 16;        // keys of a warp's step: a box, never over a page's end
-constexpr int few_ring(int d) { return d == 128 ? 24 << 10 : 20 << 10; }  // bytes of a warp's ring: 3 steps, 5 at d = 64
-constexpr int FEW_RUN = 8;          // steps of a warp at least
-constexpr int few_smem_bytes(int d) { return FEW_WARPS * (few_ring(d) + 8 * d * 4); }
+constexpr int few_ring(int d) { return d == 128 ? 16 << 10 : 12 << 10; }  // bytes of a warp's ring: 2 steps, 3 at d = 64
+constexpr int FEW_TABLE = 384;      // sequences whose lengths are kept at hand
+constexpr int FEW_REST = 4;         // steps that the list counts more behind each unit, which are nothing: what a unit takes beside its own
+constexpr int FEW_RUN = 4;          // steps of a warp at least
+// A warp's share: its ring, eight rows of a state, the next unit's Q (rows 16 bytes apart, so
+// that eight rows' reads hit distinct banks). Behind the shares: the table.
+constexpr int few_q(int d) { return few_ring(d) + 8 * d * 4; }
+constexpr int few_warp_bytes(int d) { return (few_q(d) + 16 * (d * 2 + 16) + 1023) / 1024 * 1024; }
+constexpr int few_smem_bytes(int d) { return FEW_WARPS * few_warp_bytes(d) + FEW_TABLE * 5 * (int)sizeof(int); }
 constexpr float FEW_LOG2E = 1.4426950408889634f;
 constexpr float FEW_RESCALE = 8.f;  // growth of a maximum (base 2) that rescales, as in the tcgen05 kernel
 
@@ -72,7 +78,7 @@ __device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t addr) {
 // leave the last empty).
 struct FewSeq {
   TreeItem x;
-  int blocks, steps;  // units of a KV head, steps of a unit
+  int blocks, steps;  // units of a KV head, steps of a unit (FEW_REST with them)
 };
 template <int RB>
 __device__ __forceinline__ int few_steps(const TreeLaunch& a, const TreeItem& x, int gl, int blk, int* fresh) {
@@ -81,14 +87,14 @@ __device__ __forceinline__ int few_steps(const TreeLaunch& a, const TreeItem& x,
   return (x.t + FEW_STEP - 1) / FEW_STEP + (*fresh + FEW_STEP - 1) / FEW_STEP;
 }
 template <int RB>
-__device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, int b, int gl) {
+__device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, const TreeItem& x, int gl) {
   FewSeq s;
-  s.x = tree_item<true>(a, 2 * b + 1, true);
+  s.x = x;
   s.blocks = s.steps = 0;
-  if (!few_item(a, s.x.n, s.x.t)) return s;
+  if (s.x.part == 1 || !few_item(a, s.x.n, s.x.t)) return s;
   s.blocks = ((s.x.n << gl) + RB - 1) / RB;
   int fresh;
-  if (s.blocks > 0) s.steps = few_steps<RB>(a, s.x, gl, s.blocks - 1, &fresh);
+  if (s.blocks > 0) s.steps = few_steps<RB>(a, s.x, gl, s.blocks - 1, &fresh) + FEW_REST;
   return s;
 }
 
@@ -99,7 +105,7 @@ struct FewTask {
   int taken;               // of the list
   int cached, fresh;       // steps over the cache, new tokens that the unit sees
   int first, cuts;         // the warp that begins the unit, the warps that have steps of it
-  int window, at;          // rows of steps window .. window + 31, one a lane
+  int window, page;        // pages of steps window .. window + 31, one a lane (not looked at before they are used)
   bool some;               // (none: the run is done)
 };
 
@@ -108,6 +114,14 @@ struct FewAux {
   uint64_t full[FEW_WARPS][6];
   int steps_to[384];  // of the list, up to a thread's items
 };
+// The table: five arrays of FEW_TABLE numbers.
+__device__ __forceinline__ void few_note(int* table, int b, const TreeItem& x) {
+  table[b] = x.base;
+  table[FEW_TABLE + b] = x.t;
+  table[2 * FEW_TABLE + b] = x.c0;
+  table[3 * FEW_TABLE + b] = x.n;
+  table[4 * FEW_TABLE + b] = x.part;
+}
 
 // A CTA's part: warps 0 .. 7 of CTA `cta` of `ctas` take runs of the list of all_steps
 // steps; a thread of the launch has per_t items (steps_to).
@@ -117,7 +131,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
                                          int per_t, int all_steps, int cta, int ctas, int gl) {
   // a step's K, then its V: SEGS column segments of 16 rows of 128 bytes
   constexpr int RB = 8 * NT, C4 = D / 4, SEGS = D / 64, SEG = FEW_STEP * 128, STAGE = 2 * SEGS * SEG, STAGES = few_ring(D) / STAGE;
-  constexpr int WARP_SMEM = few_smem_bytes(D) / FEW_WARPS;  // the ring, and eight rows of a state
+  constexpr int WARP_SMEM = few_warp_bytes(D), QS = D * 2 + 16;  // (bytes from one row of Q to the next)
   static_assert(STAGES <= 6 && few_ring(D) % STAGE == 0 && WARP_SMEM % 1024 == 0, "ring");
   const KVView& kv = a.kv;
   const int G = 1 << gl;
@@ -141,36 +155,47 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
   float4* staged = reinterpret_cast<float4*>(few_smem + warp * WARP_SMEM + few_ring(D));  // [C4][8]
   const float sc = a.scale * FEW_LOG2E;
 
-  // Rows of the task's next steps' first keys (-1: on no page).
+  uint8_t* next_q = few_smem + warp * WARP_SMEM + few_q(D);
+  const int* table = reinterpret_cast<const int*>(few_smem + FEW_WARPS * WARP_SMEM);
+  auto seq_at = [&](int b) {
+    if (kv.B > FEW_TABLE) return few_seq<RB>(a, tree_item<true>(a, 2 * b + 1, true), gl);
+    TreeItem x;
+    x.b = b;
+    x.base = table[b];
+    x.t = table[FEW_TABLE + b];
+    x.c0 = table[2 * FEW_TABLE + b];
+    x.n = table[3 * FEW_TABLE + b];
+    x.part = table[4 * FEW_TABLE + b];
+    return few_seq<RB>(a, x, gl);
+  };
   auto look_up = [&](FewTask& t, int window) {
     t.window = window;
-    t.at = 0;
-    const int s = window + lane, key = t.x.base + s * FEW_STEP;
-    if (s >= min(t.s1, t.cached)) return;
-    if (kv.block_table == nullptr) {
-      t.at = (t.x.b * kv.Hkv + t.kvh) * kv.t_max + key;
-      return;
-    }
-    const int page = kv.block_table[(long long)t.x.b * kv.max_blocks + key / kv.block_size];
-    const bool ok = (unsigned)page < (unsigned)kv.num_blocks;
-    if (!ok) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
-    t.at = ok ? (page * kv.Hkv + t.kvh) * kv.block_size + key % kv.block_size : -1;
+    const int s = window + lane;
+    if (kv.block_table != nullptr && s < min(t.s1, t.cached))
+      t.page = kv.block_table[(long long)t.x.b * kv.max_blocks + (t.x.base + s * FEW_STEP) / kv.block_size];
   };
   auto fetch = [&]() {  // at pos, which moves on
     FewTask t = {};
-    if (pos >= end) return t;
-    int lo = 0, hi = 383;  // the first thread whose items end behind it
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (aux.steps_to[mid] > pos) hi = mid; else lo = mid + 1;
+    FewSeq s = {};
+    int unit = 0, in = 0;
+    for (;; pos += s.steps - in) {
+      if (pos >= end) return t;
+      int lo = 0, hi = 383;  // the first thread whose items end behind it
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (aux.steps_to[mid] > pos) hi = mid; else lo = mid + 1;
+      }
+      int off = pos - (lo > 0 ? aux.steps_to[lo - 1] : 0), b = (lo * per_t) >> 1;  // (items 2 b + 1 have steps)
+      s = seq_at(b);
+      for (int x; off >= (x = kv.Hkv * s.blocks * s.steps);) {
+        off -= x;
+        s = seq_at(++b);
+      }
+      unit = off / s.steps;
+      in = off - unit * s.steps;
+      if (in < s.steps - FEW_REST) break;
     }
-    int off = pos - (lo > 0 ? aux.steps_to[lo - 1] : 0), b = (lo * per_t) >> 1;  // (items 2 b + 1 have steps)
-    FewSeq s = few_seq<RB>(a, b, gl);
-    for (int x; off >= (x = kv.Hkv * s.blocks * s.steps);) {
-      off -= x;
-      s = few_seq<RB>(a, ++b, gl);
-    }
-    const int unit = off / s.steps, in = off - unit * s.steps, start = pos - in;
+    const int start = pos - in;
     t.x = s.x;
     t.kvh = unit / s.blocks;
     t.blk = unit - t.kvh * s.blocks;
@@ -178,19 +203,39 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     pos += t.taken;
     t.some = true;
     t.first = start / run;
-    t.cuts = (start + s.steps - 1) / run - t.first + 1;
+    t.cuts = (start + s.steps - FEW_REST - 1) / run - t.first + 1;
     const int all = few_steps<RB>(a, t.x, gl, t.blk, &t.fresh);
     t.cached = (t.x.t + FEW_STEP - 1) / FEW_STEP;
     t.s0 = min(in, all);
     t.s1 = min(in + t.taken, all);
     look_up(t, t.s0);
+    // its Q rows, zeros behind its last
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < RB * D / 8 / 32; i++) {
+      const int y = lane + 32 * i, r = t.blk * RB + y / (D / 8), piece = y % (D / 8);
+      const bool have = r < t.x.n << gl;
+      const __nv_bfloat16* from =
+          static_cast<const __nv_bfloat16*>(a.q) +
+          (have ? ((long long)(t.x.c0 + (r >> gl)) * kv.Hq + (t.kvh << gl) + (r & (G - 1))) * D + piece * 8 : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(next_q + y / (D / 8) * QS + piece * 16)),
+                   "l"(from), "r"(have ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     return t;
   };
   int counts = 0;  // keys of the ring's steps, five bits each
   auto load = [&](FewTask& t, int s, int stage) {
     if (s >= t.window + 32) look_up(t, t.window + 32);
-    const int row = __shfl_sync(FULL_MASK, t.at, s - t.window), j = (s - t.cached) * FEW_STEP;
+    const int page = __shfl_sync(FULL_MASK, t.page, s - t.window), j = (s - t.cached) * FEW_STEP, key = t.x.base + s * FEW_STEP;
     const bool is_new = s >= t.cached;
+    int row = (t.x.b * kv.Hkv + t.kvh) * kv.t_max + key;  // of the cache
+    if (kv.block_table != nullptr) row = (page * kv.Hkv + t.kvh) * kv.block_size + key % kv.block_size;
+    if (!is_new && kv.block_table != nullptr && (unsigned)page >= (unsigned)kv.num_blocks) {
+      if (lane == 0) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
+      row = -1;
+    }
     const int n = is_new ? min(FEW_STEP, t.fresh - j) : row < 0 ? 0 : min(FEW_STEP, t.x.t - s * FEW_STEP);
     counts = (counts & ~(31 << 5 * stage)) | n << 5 * stage;
     if (lane == 0) {
@@ -216,21 +261,18 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     bool known = false;
     const TreeItem x = cur.x;
     const int blk = cur.blk, kvh = cur.kvh;
-    const int rows = min(RB, (x.n << gl) - blk * RB), tok0 = (blk * RB) >> gl, cached = cur.cached;
+    const int rows = min(RB, (x.n << gl) - blk * RB), cached = cur.cached;
     // Q as the products take it: rows g of each eight, columns 16 j + 2 c and 16 j + 8 + 2 c
     uint32_t q[NT][D / 16][2];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-      const int r = blk * RB + 8 * t + g;
-      const bool have = 8 * t + g < rows;
-      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
-                                 ((long long)(x.c0 + (have ? r >> gl : tok0)) * kv.Hq + (kvh << gl) + (have ? r & (G - 1) : 0)) * D;
+    for (int t = 0; t < NT; t++)
 #pragma unroll
       for (int j = 0; j < D / 16; j++)
 #pragma unroll
         for (int h = 0; h < 2; h++)
-          q[t][j][h] = have ? *reinterpret_cast<const uint32_t*>(row + 16 * j + 8 * h + 2 * c) : 0u;
-    }
+          q[t][j][h] = *reinterpret_cast<const uint32_t*>(next_q + (8 * t + g) * QS + (16 * j + 8 * h + 2 * c) * 2);
 
   float m[NT][2], l[NT][2], o[NT][D / 16][4];  // rows 8 t + 2 c, + 1; O's columns 16 e + g, + 8
 #pragma unroll

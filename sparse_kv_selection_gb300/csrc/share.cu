@@ -7,7 +7,7 @@
 // own query rows fill a tile of the attention (GROUP_FULL a KV head) have nothing to
 // gain and stay alone.
 //
-// One cluster of CTAs: a warp compares two rows, 256 entries at a time; then one
+// One cluster of CTAs: a warp compares two rows, 512 entries at a time; then one
 // CTA forms the groups, a thread for each run of rows between two that share
 // nothing, and writes them. Bound: latency (the tables are read twice, from L2).
 #include <cooperative_groups.h>
@@ -21,7 +21,7 @@ namespace cg = cooperative_groups;
 constexpr int FIND_THREADS = 1024;
 constexpr int FIND_WARPS = FIND_THREADS / 32;
 constexpr int FIND_CLUSTER = 8;
-constexpr int FIND_COLS = 8;
+constexpr int FIND_COLS = 16;
 constexpr int GROUP_FULL = 256;
 
 __global__ void __launch_bounds__(FIND_THREADS) find_kernel(const __grid_constant__ FindLaunch a) {

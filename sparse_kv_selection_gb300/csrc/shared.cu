@@ -5,87 +5,122 @@
 //   m = max(m1, m2),  o = (2^(m1 - m) o1 + 2^(m2 - m) o2) / (2^(m1 - m) l1 + 2^(m2 - m) l2)
 //
 // On bf16 each may lie in pieces, one for each CTA or warp of the launch before that had
-// a run of its unit's keys (`where`: the first, how many). A thread takes four columns of
-// a row; eight consecutive rows are neighbours, as the pieces keep them. Bound: L2
-// and latency (where, then the states).
+// a run of its unit's keys (`where`: the first, how many). A warp takes eight rows and 32
+// columns, a lane eight columns of a row. Bound: latency, four dependent reads through L2
+// (the sequence, its group; the pieces' places, the pieces), the first two of which do not wait
+// for the launch in front.
 #include "tree_join.cuh"
 
 namespace prhs {
 
-constexpr int SJ_THREADS = 256;
+constexpr int SJ_THREADS = 128, SJ_PIECES = 4;  // (pieces in flight)
 
 template <typename T, int D>
 __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ TreeLaunch a,
                                                                  const __grid_constant__ TreeRecords rec, int ctas) {
-  constexpr int C4 = D / 4;
-  pdl_wait();
-  pdl_trigger();
+  constexpr int C4 = D / 4, CHUNKS = D / 32;
   const KVView& kv = a.kv;
   const int G = kv.Hq / kv.Hkv, gl = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, b = blockIdx.x;
-  const TreeItem x = tree_item<true>(a, 2 * b + 1, true);
-  const bool few = few_item(a, x.n, x.t);
-  if (x.n == 0 || (sizeof(T) == 4 && x.part != 2) || *a.part_ok == 0) return;
-  // the group's first token (its units of the shared keys count rows from there)
-  const int group0 = x.part == 2 ? max(0, a.cu_new[a.shared[b].x]) : 0;
-  const int rows = x.n << gl, blocks = (rows + 7) / 8;
-  const long long total = (long long)kv.Hkv * blocks * 8 * C4;
-  for (long long i = (long long)blockIdx.y * SJ_THREADS + threadIdx.x; i < total; i += (long long)gridDim.y * SJ_THREADS) {
-    const int in = (int)i & 7, c4 = (int)(i / 8 % C4), hr = (int)(i / (8 * C4)), kvh = hr / blocks, r = (hr - kvh * blocks) * 8 + in;
+  // as tree_item reads them (the launch before has flagged what does not fit)
+  const int4 mine = a.shared[b];
+  const int len = kv.seq_lens[b], lo = a.cu_new[b], hi = a.cu_new[b + 1];
+  if (blockIdx.x + blockIdx.y == 0) pdl_wait();  // (one waits whatever it has to do: this launch ends behind the one before)
+  if (lo < 0 || hi <= lo || hi > a.T || hi - lo > a.max_new) return;
+  const int t = max(0, min(len, kv.t_max)), n = hi - lo, head = max(0, min(mine.x, b));
+  const bool grouped = mine.x == head && !(mine.x == b && (mine.y <= 1 || mine.z == 0));
+  const int4 group = grouped ? a.shared[head] : make_int4(0, 0, 0, 0);
+  const int head_len = grouped ? kv.seq_lens[head] : 0, group0 = grouped ? max(0, a.cu_new[head]) : 0;
+  int keys = 0;  // that are shared
+  if (grouped) {
+    keys = kv.block_table != nullptr ? group.z / kv.block_size * kv.block_size : group.z;
+    if (group.x != head || b - head >= group.y || keys < 0 || keys > t || keys > head_len) keys = 0;
+  }
+  const bool few[2] = {false, sizeof(T) == 2 && few_item(a, n, t - keys)};  // whose are the states?
+  // all that was there before the launch in front; what it wrote from here on
+  pdl_wait();
+  pdl_trigger();
+  if (*a.part_ok == 0) return;
+  const int rows = n << gl, blocks = (rows + 7) / 8, lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.y * (SJ_THREADS / 32), total = (long long)kv.Hkv * blocks * CHUNKS;
+  for (long long i = (long long)blockIdx.y * (SJ_THREADS / 32) + threadIdx.x / 32; i < total; i += warps) {
+    const int chunk = (int)i % CHUNKS, hr = (int)(i / CHUNKS), kvh = hr / blocks, r = (hr - kvh * blocks) * 8 + (lane & 7);
     if (r >= rows) continue;
-    const int tok = x.c0 + (r >> gl), h = r & (G - 1);
+    const int tok = lo + (r >> gl), h = r & (G - 1), c4 = chunk * 8 + (lane >> 3) * 2;
     int2 at[2] = {make_int2(0, 1), make_int2(0, 1)};  // of the states against the shared and the other keys
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int k = 0; k < 2; k++)
-        if (k == 1 || x.part == 2) at[k] = __ldcg(a.where + part_row<T>(a, k + 1, tok, kvh, h, gl));
+        if (k == 1 || keys > 0) at[k] = __ldcg(a.where + part_row<T>(a, k + 1, tok, kvh, h, gl));
     }
-    if (x.part != 2 && at[1].y == 1) continue;  // its result stands
+    if (keys == 0 && (sizeof(T) == 4 || at[1].y <= 1)) continue;  // its result is written
     float M = -INFINITY, L = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 o) {  // (a state that holds NaN has it in its sum, whatever its maximum)
-      const float m = fmaxf(M, ml.x), w0 = tree_weight(M, m), w1 = tree_weight(ml.x, m);
-      L = fmaf(w1, ml.y, w0 * L);
-      y = make_float4(y.x * w0, y.y * w0, y.z * w0, y.w * w0);
-      tree_fma(y, w1, o);
-      M = m;
-    };
+    float4 y[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      if (k == 0 && x.part != 2) continue;
-      if (at[k].y == 1) {
-        add(__ldcg(a.part_ml + part_row<T>(a, k + 1, tok, kvh, h, gl)), __ldcg(part_at<T, D>(a, k + 1, tok, kvh, h, c4, gl)));
-        continue;
-      }
-      if constexpr (sizeof(T) == 2) {
-        // piece w: the first writer's second slot, the others' first ones; rows as their unit counts them
-        const bool warps = k == 1 && few;
-        const int writers = warps ? a.few_warps : ctas, unit = warps ? a.few_rows : 256;
-        const int first = max(0, min(at[k].x, writers - 1)), n = max(1, min(at[k].y, writers - first));
+      if (k == 0 && keys == 0) continue;
+      const float2* ml = a.part_ml + part_row<T>(a, k + 1, tok, kvh, h, gl);
+      const float4* o = part_at<T, D>(a, k + 1, tok, kvh, h, c4, gl);
+      long long ml_step = 0, o_step = 0, next = sizeof(T) == 4 ? 1 : (long long)a.T << gl;  // to the next piece, the next columns
+      int pieces = 1, first = 0;
+      if (sizeof(T) == 2 && at[k].y > 1) {
+        // a writer's second slot is of the unit that it begins, its first of one begun before
+        const int writers = few[k] ? a.few_warps : ctas, unit = few[k] ? a.few_rows : 256, stride = few[k] ? unit : rec.rows_max;
+        first = max(0, min(at[k].x, writers - 1));  // (whatever stands there after a launch that gave up)
+        pieces = min(at[k].y, writers - first);
         const int row = (k == 0 ? ((tok - group0) << gl) + h : r) & (unit - 1);
-        const float2* ml = warps ? reinterpret_cast<const float2*>(static_cast<const float4*>(a.few_states) +
-                                                                   (long long)2 * writers * C4 * unit)
-                                 : rec.ml;
-        const float4* o = warps ? static_cast<const float4*>(a.few_states) : rec.o;
-        const int stride = warps ? unit : rec.rows_max;
-#pragma unroll 4
-        for (int w = 0; w < n; w++) {
-          const long long slot = 2ll * (first + w) + (w == 0);
-          add(__ldcg(ml + slot * stride + row), __ldcg(o + (slot * C4 + c4) * stride + row));
+        const float4* states = static_cast<const float4*>(a.few_states);
+        ml = (few[k] ? reinterpret_cast<const float2*>(states + 2ll * a.few_warps * C4 * unit) : rec.ml) + row;
+        o = (few[k] ? states : rec.o) + (long long)c4 * stride + row;
+        ml_step = stride;
+        o_step = (long long)C4 * stride;
+        next = stride;
+      }
+      for (int p0 = 0; p0 < pieces; p0 += SJ_PIECES) {
+        float2 s[SJ_PIECES];
+        float4 x[SJ_PIECES][2];
+#pragma unroll
+        for (int p = 0; p < SJ_PIECES; p++) {
+          s[p] = make_float2(-INFINITY, 0.f);
+          x[p][0] = x[p][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p0 + p < pieces) {
+            const long long slot = 2ll * (first + p0 + p) + (p0 + p == 0);
+            s[p] = __ldcg(ml + slot * ml_step);
+            x[p][0] = __ldcg(o + slot * o_step);
+            x[p][1] = __ldcg(o + slot * o_step + next);
+          }
         }
+        float m = M;
+#pragma unroll
+        for (int p = 0; p < SJ_PIECES; p++) m = fmaxf(m, s[p].x);
+        const float keep = tree_weight(M, m);
+        L *= keep;
+#pragma unroll
+        for (int c = 0; c < 2; c++) y[c] = make_float4(y[c].x * keep, y[c].y * keep, y[c].z * keep, y[c].w * keep);
+#pragma unroll
+        for (int p = 0; p < SJ_PIECES; p++) {
+          const float w = tree_weight(s[p].x, m);
+          L = fmaf(w, s[p].y, L);  // (a state that holds NaN has it in its sum, whatever its maximum)
+          tree_fma(y[0], w, x[p][0]);
+          tree_fma(y[1], w, x[p][1]);
+        }
+        M = m;
       }
     }
     const float inv = tree_inv(L);
     const long long orow = (long long)tok * kv.Hq + (kvh << gl) + h;
-    tree_put(static_cast<T*>(a.out) + orow * D + c4 * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    T* out = static_cast<T*>(a.out) + orow * D + c4 * 4;
+#pragma unroll
+    for (int c = 0; c < 2; c++) tree_put(out + c * 4, make_float4(y[c].x * inv, y[c].y * inv, y[c].z * inv, y[c].w * inv));
     if (c4 == 0) a.lse[orow] = tree_lse(M, L);
   }
 }
 
 template <typename T, int D>
 static cudaError_t join_go(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
-  const long long rows = ((long long)a.max_new * (a.kv.Hq / a.kv.Hkv) + 7) / 8 * 8;
-  const long long y = (rows * a.kv.Hkv * D / 4 + SJ_THREADS - 1) / SJ_THREADS;
-  return launch_pdl(shared_join_kernel<T, D>, dim3(a.kv.B, (unsigned)(y < 256 ? y : 256)), dim3(SJ_THREADS), 0, st, true, a, rec, sms);
+  const long long blocks = ((long long)a.max_new * (a.kv.Hq / a.kv.Hkv) + 7) / 8;
+  const long long y = (blocks * a.kv.Hkv * (D / 32) + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
+  return launch_pdl(shared_join_kernel<T, D>, dim3(a.kv.B, (unsigned)(y < 1024 ? y : 1024)), dim3(SJ_THREADS), 0, st, true, a, rec,
+                    sms);
 }
 cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
   if (a.kv.dtype == PRHS_BF16)

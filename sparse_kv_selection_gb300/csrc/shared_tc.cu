@@ -10,10 +10,9 @@ void few_shape(TreeLaunch* a, int sms) {
   a->few_rows = (long long)a->max_new * (a->kv.Hq / a->kv.Hkv) <= 8 ? 8 : 16;
   a->few_warps = FEW_WARPS * sms;
 }
-size_t few_state_bytes(const KVView& kv, int max_new, int sms) {
+size_t few_state_bytes(const KVView& kv, int sms) {
   if (kv.dtype != PRHS_BF16) return 0;
-  const size_t rows = (long long)max_new * (kv.Hq / kv.Hkv) <= 8 ? 8 : 16;
-  return (size_t)2 * FEW_WARPS * sms * rows * (kv.d * sizeof(float) + sizeof(float2));
+  return (size_t)2 * FEW_WARPS * sms * 16 * (kv.d * sizeof(float) + sizeof(float2));
 }
 size_t shared_where_bytes(const KVView& kv, int T) {
   return kv.dtype != PRHS_BF16 ? 0 : (size_t)2 * T * kv.Hq * sizeof(int2);

@@ -86,15 +86,13 @@ struct TreeLaunch {
   int few_warps;     // warps that it may have
   void* few_states;  // [2 few_warps] states of units that several warps share, two a warp
 };
-// Whether a sequence's own t keys with its n tokens of G query heads a KV head go to
-// that part. Its units of few_rows rows read the keys each, at the cost of a step of 16
-// and five more to begin and end; a tile of 128 of the other part costs it about twice
-// as much as they take to read, and a unit as much as 45.
-constexpr int FEW_KEYS = 4096;
+// Whether a sequence's own t keys with its n tokens go to that part: at most two units
+// of few_rows query rows a KV head, which read the keys each, and few keys. (24 prompts of
+// 20 to 63 tokens, 4 heads a KV head, whose units are six and more: 158 us with those, 135
+// without.)
+constexpr int FEW_KEYS = 32768;
 __device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
-  if (a.few_rows == 0 || t + n > FEW_KEYS) return false;
-  const int blocks = (int)(((long long)n * (a.kv.Hq / a.kv.Hkv) + a.few_rows - 1) / a.few_rows), steps = (t + n + 15) / 16;
-  return (long long)blocks * (steps + 5) <= 2 * steps + 45;
+  return t + n <= FEW_KEYS && (long long)n * (a.kv.Hq / a.kv.Hkv) <= 2 * a.few_rows;
 }
 // fp32: two launches, the first counted by the callee; ws holds
 // tree_workspace(kv, max_new, sms) bytes.
@@ -111,7 +109,7 @@ struct TreeRecords;
 prhs_status launch_shared_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
 cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int ctas, cudaStream_t s);
 void few_shape(TreeLaunch* a, int sms);
-size_t few_state_bytes(const KVView& kv, int max_new, int sms);
+size_t few_state_bytes(const KVView& kv, int sms);
 size_t shared_where_bytes(const KVView& kv, int T);
 // The most tokens that a unit's rows may come from.
 inline int tree_most_new(const TreeLaunch& a) { return a.shared != nullptr ? a.T : a.max_new; }

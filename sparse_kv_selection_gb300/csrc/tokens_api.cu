@@ -204,7 +204,7 @@ SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   w.part_ml = w.part_o + up((size_t)2 * T * kv.Hq * kv.d * sizeof(float));
   w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
   w.states = w.part_ok + 256;
-  w.where = w.states + up(few_state_bytes(kv, max_new, sms));
+  w.where = w.states + up(few_state_bytes(kv, sms));
   w.total = w.where + up(shared_where_bytes(kv, T));
   return w;
 }

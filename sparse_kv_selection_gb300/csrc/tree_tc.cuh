@@ -127,6 +127,11 @@ struct TcSeq : TreeItem {  // one item's share of the list
   int tiles;         // tiles of one KV head
 };
 
+// What a tile of one and of two row tiles takes, in the few rows' steps: 9 and 12 are what
+// ends both parts at about the same time (8 and 10, 10 and 14: 8 groups of 16 sequences 100
+// and 98 us instead of 92).
+constexpr int TC_COST_1 = 9, TC_COST_2 = 12;
+
 struct TcBars {  // one mbarrier each
   uint64_t full[10], empty[10], qfull[2], qempty[2], sfull[2], pfull[2][2], ofull[2], done;
   uint64_t wfull[TC_WORKS], wempty[TC_WORKS];
@@ -146,6 +151,7 @@ struct TcAux {
   int begin, end;          // the run
   int wsum[TC_WARPS], wmax[TC_WARPS];
   int fsum[TC_WARPS];      // (shared keys) steps of the few rows' list
+  long long cost[TC_WARPS];  // what the tiles' list takes, in steps of the other
 };
 static_assert(sizeof(TcAux) <= TC_AUX, "aux region");
 
@@ -388,6 +394,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const int per_t = (items + TC_THREADS - 1) / TC_THREADS, e0 = tid * per_t;
   int mine = 0, most = 0;  // tiles of this thread's items, of their largest unit
   int steps = 0;           // of the few rows' list
+  long long cost = 0;
   bool back = false;       // offsets that step back: sequences would overlap, and counts pass 32 bits
   for (int e = e0; e < min(items, e0 + per_t); e++) {
     const TcSeq s = tc_seq<SHARED>(a, e, ul);
@@ -395,8 +402,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     mine += kv.Hkv * s.tiles;
     if (s.blocks > 0) most = max(most, tc_unit_tiles(s, s.blocks - 1, ul, a.mask == nullptr) + REST<SHARED>);
     if constexpr (SHARED) {
+      cost += (long long)kv.Hkv * s.tiles * ((s.n << gl) > TT ? TC_COST_2 : TC_COST_1);
       if (e & 1) {
-        const FewSeq f = few_seq<8 * NT1>(a, e >> 1, gl);
+        const FewSeq f = few_seq<8 * NT1>(a, tree_item<true>(a, e, true), gl);
         steps += kv.Hkv * f.blocks * f.steps;
       }
     }
@@ -413,8 +421,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(FULL_MASK, steps, o);
       if (lane >= o) steps += y;
+      cost += __shfl_xor_sync(FULL_MASK, cost, o);
     }
-    if (lane == 31) aux.fsum[warp] = steps;
+    if (lane == 31) {
+      aux.fsum[warp] = steps;
+      aux.cost[warp] = cost;
+    }
   }
   if (lane == 31) {
     aux.wsum[warp] = run;
@@ -432,16 +444,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     most = max(most, aux.wmax[w]);
   }
   before += run - mine;
-  int all_steps = 0;
+  // With shared keys the first CTAs take runs of the tiles and the others of the few rows' steps,
+  // as many as the two lists take: both begin at once. (Every CTA first one, then the other: 105 us
+  // instead of 92, the second list's latencies come behind the first's.)
+  int all_steps = 0, ctas = gridDim.x;
   if constexpr (SHARED) {
+    cost = 0;
 #pragma unroll
     for (int w = 0; w < TC_WARPS; w++) {
       const int x = aux.fsum[w];
       if (w < warp) steps += x;
       all_steps += x;
+      cost += aux.cost[w];
     }
+    if (all_steps > 0)
+      ctas = cost == 0 ? 0 : max(1, min(ctas - 1, (int)((ctas * cost + (cost + all_steps) / 2) / (cost + all_steps))));
   }
-  const int per = (total + gridDim.x - 1) / (int)gridDim.x;
+  const bool tile_cta = (int)blockIdx.x < ctas;
+  const int per = (total + max(ctas, 1) - 1) / max(ctas, 1);
   // Runs are [g0, g1), or, where cutting units costs more than it gives, they begin
   // at the unit that begins there or next. Joining takes about 4 us, a tile 0.8 or
   // (two row tiles) 1.6, so runs may be up to five tiles longer instead, on units so
@@ -485,9 +505,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = some ? aux.tmem : 0;
-  // With shared keys every CTA has a part of the few rows' list too, when its tiles are done:
-  // everyone meets, then hands its steps over in what held the softmax warps' states.
-  auto tiles_done = [&] {
+  // The tiles are done. A CTA with none of them has steps: everyone hands over how many its
+  // items have, where the softmax warps' states would be.
+  auto tiles_done = [&](auto between) {
     __syncthreads();
     if (warp == 9 && some) {
       tc_fence_after();
@@ -495,6 +515,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
     if constexpr (SHARED) {
       aux.few.steps_to[tid] = steps;
+      between();
       __syncthreads();
     }
   };
@@ -771,7 +792,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       __syncwarp();
     }
-    if constexpr (SHARED) tiles_done();
+    if constexpr (SHARED) {
+      // the sequences for the few rows' list, asked for before the barrier
+      constexpr int OTHERS = TC_THREADS - 2 * TT, PER = FEW_TABLE / OTHERS;
+      const bool noted = kv.B <= FEW_TABLE && !tile_cta;
+      TreeItem x[PER];
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (noted && tid - 2 * TT + i * OTHERS < kv.B) x[i] = tree_item<true>(a, 2 * (tid - 2 * TT + i * OTHERS) + 1, true);
+      tiles_done([&] {
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+          if (noted && tid - 2 * TT + i * OTHERS < kv.B)
+            few_note(reinterpret_cast<int*>(data + FEW_WARPS * few_warp_bytes(D)), tid - 2 * TT + i * OTHERS, x[i]);
+      });
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_REGS_SOFTMAX));
     // ------------------------------- softmax ------------------------------- //
@@ -1026,11 +1061,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     while (some && !softmax_meet(true)) {
     }
     if constexpr (SHARED) {
-      tiles_done();
-      few_role<D, NT1>(a, ktail, vtail, knmap, vnmap, tc_smem, aux.few, per_t, all_steps, (int)blockIdx.x, (int)gridDim.x, gl);
+      tiles_done([] {});
+      if (!tile_cta)
+        few_role<D, NT1>(a, ktail, vtail, knmap, vnmap, tc_smem, aux.few, per_t, all_steps, (int)blockIdx.x - ctas,
+                         (int)gridDim.x - ctas, gl);
     }
   }
-  if constexpr (!SHARED) tiles_done();
+  if constexpr (!SHARED) tiles_done([] {});
 }
 
 // -------------------------------------------------------------------------- //
