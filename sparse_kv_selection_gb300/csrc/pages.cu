@@ -15,10 +15,11 @@
 // before anything is written, and what shows later (a page outside the pool, no
 // room in the free list) takes the counts back.
 //
-// One cluster of CTAs. The entries of the table are tasks of 256 columns of a
-// row, a warp's tasks consecutive, so that a prefix over the warps' counts gives
-// every freed page its place. Bound: latency, a few dependent passes through L2
-// with a cluster barrier between two.
+// The entries of the table are tasks of 512 columns of a row, a warp's tasks
+// consecutive, so that a prefix over the warps' counts gives every freed page its
+// place. One cluster of CTAs, or for large tables all SMs (a cooperative launch).
+// Bound: latency, a few dependent passes through L2 with a barrier between two; atomics on
+// shared pages for large calls.
 #include <cooperative_groups.h>
 
 #include "pages.h"
@@ -27,11 +28,13 @@ namespace prhs {
 
 namespace cg = cooperative_groups;
 
-constexpr int PG_THREADS = 1024;
+constexpr int PG_THREADS = 512;          // (a lane holds a task's entries over the passes)
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_CLUSTER = 16;           // above 8 by opt-in
-constexpr int PG_COLS = 8;               // columns a lane
+constexpr int PG_GRID = 256;             // CTAs of a cooperative launch at most
+constexpr int PG_COLS = 16;              // columns a lane
 constexpr int PG_TASK = 32 * PG_COLS;    // columns of a task
+constexpr long long PG_ONE_CLUSTER = 1 << 16;  // entries up to which one cluster takes a call
 constexpr int PG_KEEP = 1024;            // kept positions a warp checks at a time
 
 // Exclusive prefix of x over the block's threads, the sum into *total.
@@ -45,7 +48,7 @@ __device__ __forceinline__ int block_scan(int x, int* wsum, int* total) {
   }
   if (lane == 31) wsum[warp] = y;
   __syncthreads();
-  int before = lane < warp ? wsum[lane] : 0, all = wsum[lane];
+  int before = lane < warp ? wsum[lane] : 0, all = lane < PG_WARPS ? wsum[lane] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     before += __shfl_xor_sync(FULL_MASK, before, o);
@@ -55,14 +58,35 @@ __device__ __forceinline__ int block_scan(int x, int* wsum, int* total) {
   return before + y - x;
 }
 
-template <bool FORK>
+// n numbers copied by nt threads, four 16-byte pieces of each in flight where the arrays allow.
+__device__ __forceinline__ void copy_ints(int32_t* dst, const int32_t* src, long long n, int t, int nt) {
+  long long i = 0;
+  if (((reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(src)) & 15) == 0) {
+    i = n / 4 * 4;
+    for (long long x0 = t; x0 < n / 4; x0 += 4ll * nt) {
+      int4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (x0 + (long long)k * nt < n / 4) v[k] = reinterpret_cast<const int4*>(src)[x0 + (long long)k * nt];
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (x0 + (long long)k * nt < n / 4) reinterpret_cast<int4*>(dst)[x0 + (long long)k * nt] = v[k];
+    }
+  }
+  for (i += t; i < n; i += nt) dst[i] = src[i];
+}
+
+template <bool FORK, bool GRID>
 __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant__ PagesLaunch a) {
   extern __shared__ int pg_smem[];
   __shared__ int wsum[PG_WARPS];
   __shared__ int sh_most, sh_base[PG_WARPS];
   __shared__ unsigned sh_bits;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int rank = blockIdx.x, ranks = gridDim.x;
+  auto meet = [] {
+    if constexpr (GRID) cg::this_grid().sync();
+    else cg::this_cluster().sync();
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gw = rank * PG_WARPS + warp, gws = ranks * PG_WARPS;      // the warp among the cluster's
   const int gt = rank * PG_THREADS + tid, gts = ranks * PG_THREADS;
@@ -80,12 +104,9 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
     sh_most = 0;
   }
   if (gt == 0) *late = 0;
-  if (a.shares_out != a.shares)
-    for (int i = gt; i < kv.num_blocks; i += gts) a.shares_out[i] = a.shares[i];
-  if (a.free_out != a.free_pages)
-    for (int i = gt; i < a.n_free; i += gts) a.free_out[i] = a.free_pages[i];
-  if (a.table_out != table)
-    for (long long i = gt; i < (long long)B * M; i += gts) a.table_out[i] = table[i];
+  if (a.shares_out != a.shares) copy_ints(a.shares_out, a.shares, kv.num_blocks, gt, gts);
+  if (a.free_out != a.free_pages) copy_ints(a.free_out, a.free_pages, a.n_free, gt, gts);
+  if (a.table_out != table) copy_ints(a.table_out, table, (long long)B * M, gt, gts);
   const int head = a.free_head[0];
 
   // ---- what every row becomes ----
@@ -122,7 +143,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
       bits = __reduce_or_sync(FULL_MASK, bits);
       if (lane == 0) a.part[x] = make_int2(same, (int)bits);
     }
-    cluster.sync();
+    meet();
   }
 
   auto plan_row = [&](int b, unsigned& bits) {
@@ -203,167 +224,203 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
   most = min(sh_most, M);
   if (bits == 0 && (head < 0 || head > a.n_free)) bits = PRHS_DEV_BAD_LEN;
   if (bits == 0 && taken > a.n_free - head) bits = PRHS_DEV_CAPACITY;
-  cluster.sync();
+  meet();
 
   const int chunks = (most + PG_TASK - 1) / PG_TASK;
   const long long tasks = (long long)B * chunks;
   const long long x0 = tasks * gw / gws, x1 = tasks * (gw + 1) / gws;
-  // A lane's released entries of a task (-2: none), and the number of its first entry.
-  auto released = [&](long long x, auto&& act) {
-    const int b = (int)(x / chunks), j0 = (int)(x % chunks) * PG_TASK + lane;
-    const PageRow r = a.rows[b];
-    int p[PG_COLS];
+  // A lane's share of a task: columns j0 + 32 k, and the entries released there (-2: none).
+  struct Task {
+    PageRow r;
+    int b, j0, p[PG_COLS];
+  };
+  auto ask = [&](long long x) {
+    Task t;
+    t.b = (int)(x / chunks);
+    t.j0 = (int)(x - (long long)t.b * chunks) * PG_TASK + lane;
+    t.r = a.rows[t.b];
 #pragma unroll
     for (int k = 0; k < PG_COLS; k++) {
-      const int j = j0 + 32 * k;
-      p[k] = j >= r.released && j < r.held && r.len >= 0 ? table[(long long)b * M + j] : -2;
+      const int j = t.j0 + 32 * k;
+      t.p[k] = j >= t.r.released && j < t.r.held && t.r.len >= 0 ? table[(long long)t.b * M + j] : -2;
     }
-    act(p, b * M + j0);
+    return t;
+  };
+  // The warp's tasks in order; the first one's entries stay in registers over the passes (most
+  // calls have no more), the next one's come in behind the one that is worked on.
+  Task own = {};
+  if (x0 < x1) own = ask(x0);
+  auto sweep = [&](auto&& act) {
+    Task t = own;
+    for (long long x = x0; x < x1; x++) {
+      Task next;
+      if (x + 1 < x1) next = ask(x + 1);
+      act(t);
+      t = next;
+    }
   };
   auto in_pool = [&](int p) { return (unsigned)p < (unsigned)kv.num_blocks; };
   // Entries joined (sign 1) or given up again (sign -1), and releases.
-  auto counts = [&](int sign, bool check) {
-    for (long long x = x0; x < x1; x++) {
-      unsigned bad = 0;
-      released(x, [&](int(&p)[PG_COLS], int) {
+  auto counts = [&](const Task& t, int sign) {
+    unsigned bad = 0;
+#pragma unroll
+    for (int k = 0; k < PG_COLS; k++) {
+      if (in_pool(t.p[k])) atomicAdd(&a.shares_out[t.p[k]], -sign);
+      else if (t.p[k] != -2) bad = PRHS_DEV_BAD_BLOCK;
+    }
+    if constexpr (FORK) {
+      const int n = count[t.b];
+      if (n > 0) {
+        const int whole = kv.seq_lens[t.b] / page;  // a last page in part is taken over below
+        int p[PG_COLS];
+#pragma unroll
+        for (int k = 0; k < PG_COLS; k++) p[k] = t.j0 + 32 * k < whole ? table[(long long)t.b * M + t.j0 + 32 * k] : -2;
 #pragma unroll
         for (int k = 0; k < PG_COLS; k++) {
-          if (in_pool(p[k])) atomicAdd(&a.shares_out[p[k]], -sign);
+          if (in_pool(p[k])) atomicAdd(&a.shares_out[p[k]], sign * n);
           else if (p[k] != -2) bad = PRHS_DEV_BAD_BLOCK;
         }
-      });
-      if constexpr (FORK) {
-        const int b = (int)(x / chunks), j0 = (int)(x % chunks) * PG_TASK + lane, n = count[b];
-        if (n > 0) {
-          const int whole = kv.seq_lens[b] / page;  // a last page in part is taken over below
-          int p[PG_COLS];
-#pragma unroll
-          for (int k = 0; k < PG_COLS; k++) p[k] = j0 + 32 * k < whole ? table[(long long)b * M + j0 + 32 * k] : -2;
-#pragma unroll
-          for (int k = 0; k < PG_COLS; k++) {
-            if (in_pool(p[k])) atomicAdd(&a.shares_out[p[k]], sign * n);
-            else if (p[k] != -2) bad = PRHS_DEV_BAD_BLOCK;
-          }
-        }
-        const PageRow r = a.rows[b];
-        if (r.len > 0 && r.len % page != 0 && r.keep == r.blocks && lane == 0 && x % chunks == 0)
-          atomicAdd(&a.shares_out[table[(long long)r.from * M + r.keep - 1]], sign);
       }
-      if (check && bad != 0) atomicOr(late, (int)bad);
+      if (t.r.len > 0 && t.r.len % page != 0 && t.r.keep == t.r.blocks && t.j0 == 0)
+        atomicAdd(&a.shares_out[table[(long long)t.r.from * M + t.r.keep - 1]], sign);
     }
+    return bad;
   };
-  // ---- counts; the new rows and the rows to copy, while the old table and the free list stand ----
-  const long long cells = (long long)B * a.cap;
+  // Columns that change, and the rows to copy, while the old table and the free list stand.
+  auto changes = [&](const Task& t, int k) {
+    const int j = t.j0 + 32 * k;
+    return t.r.len >= 0 && j >= t.r.released && j < max(t.r.held, t.r.blocks);
+  };
   auto copies = [&](bool refused) {
-    for (long long i = gt; i < cells; i += gts) {
-      const int b = (int)(i / a.cap), c = (int)(i - (long long)b * a.cap);
-      int from = -1, to = -1;
-      if (!refused) {
-        const PageRow r = a.rows[b];
+    const int per_row = (a.cap + PG_TASK - 1) / PG_TASK;
+    for (long long x = gw; x < (long long)B * per_row; x += gws) {
+      const int b = (int)(x / per_row), c0 = (int)(x - (long long)b * per_row) * PG_TASK + lane;
+      const PageRow r = a.rows[b];
+      int k[PG_COLS], from[PG_COLS], to[PG_COLS];
+#pragma unroll
+      for (int i = 0; i < PG_COLS; i++) {
+        const int c = c0 + 32 * i;
+        k[i] = -1;
+        if (refused) continue;
         if (FORK) {
-          if (r.last >= 0 && c < r.len % page) {
-            from = r.last * page + c;
-            to = a.free_pages[head + r.taken] * page + c;
-          }
+          if (r.last >= 0 && c < r.len % page) k[i] = c;
         } else if (c >= r.keep * page && c < r.len) {
-          const int k = a.keep[i];
-          from = table[(long long)b * M + k / page] * page + k % page;
-          to = a.free_pages[head + r.taken + c / page - r.keep] * page + c % page;
+          k[i] = a.keep[(long long)b * a.cap + c];
         }
       }
-      a.src[i] = from;
-      a.dst[i] = to;
+#pragma unroll
+      for (int i = 0; i < PG_COLS; i++) {
+        if (k[i] < 0) continue;
+        from[i] = FORK ? r.last : table[(long long)b * M + k[i] / page];
+        to[i] = a.free_pages[head + r.taken + (FORK ? 0 : (c0 + 32 * i) / page - r.keep)];
+      }
+#pragma unroll
+      for (int i = 0; i < PG_COLS; i++) {
+        const int c = c0 + 32 * i;
+        if (c >= a.cap) break;
+        a.src[(long long)b * a.cap + c] = k[i] < 0 ? -1 : from[i] * page + k[i] % page;
+        a.dst[(long long)b * a.cap + c] = k[i] < 0 ? -1 : to[i] * page + c % page;
+      }
     }
   };
   const bool early = bits != 0;  // refused before any count changed
   copies(early);
   int back = 0, before = 0, given = 0;  // pages that this warp, the warps before it, all warps give back
   if (!early) {
-    counts(1, true);
-    for (long long x = x0; x < x1; x++) {
-      const int b = (int)(x / chunks), j0 = (int)(x % chunks) * PG_TASK + lane;
-      const PageRow r = a.rows[b];
-      if (r.len < 0) continue;
-      const int end = max(r.held, r.blocks);
+    sweep([&](const Task& t) {
+      unsigned bad = counts(t, 1);
       int p[PG_COLS];
 #pragma unroll
       for (int k = 0; k < PG_COLS; k++) {
-        const int j = j0 + 32 * k;
+        const int j = t.j0 + 32 * k;
         p[k] = -1;
-        if (j < r.keep) p[k] = FORK ? table[(long long)r.from * M + j] : 0;
-        else if (j < r.blocks) p[k] = a.free_pages[head + r.taken + j - r.keep];
-        if (j >= r.keep && j < r.blocks && !in_pool(p[k])) atomicOr(late, PRHS_DEV_BAD_BLOCK);
+        if (!changes(t, k)) continue;
+        if (j < t.r.keep) p[k] = FORK ? table[(long long)t.r.from * M + j] : 0;
+        else if (j < t.r.blocks) p[k] = a.free_pages[head + t.r.taken + j - t.r.keep];
       }
 #pragma unroll
-      for (int k = 0; k < PG_COLS; k++)
-        if (j0 + 32 * k >= r.released && j0 + 32 * k < end) a.stage[(long long)b * M + j0 + 32 * k] = p[k];
-    }
-    cluster.sync();
+      for (int k = 0; k < PG_COLS; k++) {
+        const int j = t.j0 + 32 * k;
+        if (!changes(t, k)) continue;
+        if (j >= t.r.keep && j < t.r.blocks && !in_pool(p[k])) bad |= PRHS_DEV_BAD_BLOCK;
+        a.stage[(long long)t.b * M + j] = p[k];
+      }
+      if (bad != 0) atomicOr(late, (int)bad);
+    });
+    meet();
     bits = *(volatile unsigned*)late;
   }
 
   // ---- the pages that nobody holds now, each by its first release ----
   if (bits == 0) {
-    for (long long x = x0; x < x1; x++)
-      released(x, [&](int(&p)[PG_COLS], int id) {
-        int c[PG_COLS];
+    auto held_by = [&](const Task& t, int(&c)[PG_COLS]) {
 #pragma unroll
-        for (int k = 0; k < PG_COLS; k++) c[k] = p[k] >= 0 ? __ldcg(&a.shares_out[p[k]]) : 0;
-#pragma unroll
-        for (int k = 0; k < PG_COLS; k++)
-          if (c[k] < 0) atomicMin(&a.shares_out[p[k]], INT32_MIN + id + 32 * k);
-      });
-    cluster.sync();
-    // do(k, page) for the releases that free a page
-    auto freeing = [&](long long x, auto&& act) {
-      released(x, [&](int(&p)[PG_COLS], int id) {
-        int c[PG_COLS];
-#pragma unroll
-        for (int k = 0; k < PG_COLS; k++) c[k] = p[k] >= 0 ? __ldcg(&a.shares_out[p[k]]) : 0;
-#pragma unroll
-        for (int k = 0; k < PG_COLS; k++) act(c[k] == INT32_MIN + id + 32 * k, p[k]);
-      });
+      for (int k = 0; k < PG_COLS; k++) c[k] = t.p[k] >= 0 ? __ldcg(&a.shares_out[t.p[k]]) : 0;
     };
-    for (long long x = x0; x < x1; x++) freeing(x, [&](bool mine, int) { back += mine; });
+    auto frees = [&](const Task& t, int k, int count) { return count == INT32_MIN + t.b * M + t.j0 + 32 * k; };
+    sweep([&](const Task& t) {
+      int c[PG_COLS];
+      held_by(t, c);
+#pragma unroll
+      for (int k = 0; k < PG_COLS; k++)
+        if (c[k] < 0) atomicMin(&a.shares_out[t.p[k]], INT32_MIN + t.b * M + t.j0 + 32 * k);
+    });
+    meet();
+    sweep([&](const Task& t) {
+      int c[PG_COLS];
+      held_by(t, c);
+#pragma unroll
+      for (int k = 0; k < PG_COLS; k++) back += frees(t, k, c[k]);
+    });
     back = __reduce_add_sync(FULL_MASK, back);
     if (lane == 0) a.sums[gw] = back;
-    cluster.sync();
-    const int sum = block_scan(tid < gws ? __ldcg(&a.sums[tid]) : 0, wsum, &given);
-    if (tid / PG_WARPS == rank) sh_base[tid % PG_WARPS] = sum;
+    meet();
+    const int share = (gws + PG_THREADS - 1) / PG_THREADS, w0 = min(gws, tid * share), w1 = min(gws, w0 + share);
+    int sum = 0;
+    for (int w = w0; w < w1; w++) sum += __ldcg(&a.sums[w]);
+    sum = block_scan(sum, wsum, &given);
+    for (int w = w0; w < w1; w++) {
+      if (w / PG_WARPS == rank) sh_base[w % PG_WARPS] = sum;
+      sum += __ldcg(&a.sums[w]);
+    }
     __syncthreads();
     before = sh_base[warp];
     const int new_head = head + taken - given;
     if (new_head < 0) {  // no room in front of the free ones
       bits = PRHS_DEV_CAPACITY;
-      for (long long x = x0; x < x1; x++)
-        freeing(x, [&](bool mine, int p) {
-          if (mine) __stcg(&a.shares_out[p], -1);
-        });
-      cluster.sync();
+      sweep([&](const Task& t) {
+        int c[PG_COLS];
+        held_by(t, c);
+#pragma unroll
+        for (int k = 0; k < PG_COLS; k++)
+          if (frees(t, k, c[k])) __stcg(&a.shares_out[t.p[k]], -1);
+      });
+      meet();
     } else {
       int at = new_head + before;
-      for (long long x = x0; x < x1; x++) {
-        if (back > 0)
-          freeing(x, [&](bool mine, int p) {
-            const unsigned all = __ballot_sync(FULL_MASK, mine);
-            if (mine) {
-              a.free_out[at + __popc(all & ((1u << lane) - 1))] = p;
-              __stcg(&a.shares_out[p], 0);
-            }
-            at += __popc(all);
-          });
-        const int b = (int)(x / chunks), j0 = (int)(x % chunks) * PG_TASK + lane;
-        const PageRow r = a.rows[b];
-        if (r.len < 0) continue;
-        const int end = max(r.held, r.blocks);
+      sweep([&](const Task& t) {
         int p[PG_COLS];
 #pragma unroll
         for (int k = 0; k < PG_COLS; k++)
-          if (j0 + 32 * k >= r.released && j0 + 32 * k < end) p[k] = a.stage[(long long)b * M + j0 + 32 * k];
+          if (changes(t, k)) p[k] = a.stage[(long long)t.b * M + t.j0 + 32 * k];
+        if (back > 0) {
+          int c[PG_COLS];
+          held_by(t, c);
+#pragma unroll
+          for (int k = 0; k < PG_COLS; k++) {
+            const bool mine = frees(t, k, c[k]);
+            const unsigned all = __ballot_sync(FULL_MASK, mine);
+            if (mine) {
+              a.free_out[at + __popc(all & ((1u << lane) - 1))] = t.p[k];
+              __stcg(&a.shares_out[t.p[k]], 0);
+            }
+            at += __popc(all);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < PG_COLS; k++)
-          if (j0 + 32 * k >= r.released && j0 + 32 * k < end) a.table_out[(long long)b * M + j0 + 32 * k] = p[k];
-      }
+          if (changes(t, k)) a.table_out[(long long)t.b * M + t.j0 + 32 * k] = p[k];
+      });
       for (int b = gt; b < B; b += gts) {
         const PageRow r = a.rows[b];
         a.lens_out[b] = r.len < 0 ? kv.seq_lens[b] : r.len;
@@ -376,7 +433,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
 
   // ---- refused: everything as it was, nothing to copy ----
   if (!early) {
-    counts(-1, false);
+    sweep([&](const Task& t) { counts(t, -1); });
     copies(true);
   }
   for (int b = gt; b < B; b += gts) {
@@ -400,7 +457,7 @@ static size_t pages_bytes(const KVView& kv, size_t* at) {
   at[1] = at[0] + pages_up(B * sizeof(PageRow));
   at[2] = at[1] + pages_up(B * kv.max_blocks * sizeof(int32_t));
   at[3] = at[2] + pages_up(B * pages_chunks(kv) * sizeof(int2));
-  return at[3] + pages_up((PG_CLUSTER * PG_WARPS + 1) * sizeof(int));
+  return at[3] + pages_up((PG_GRID * PG_WARPS + 1) * sizeof(int));
 }
 size_t pages_workspace(const KVView& kv) {
   size_t at[4];
@@ -416,36 +473,46 @@ void pages_split(PagesLaunch* a, void* ws) {
   a->sums = reinterpret_cast<int*>(w + at[3]);
 }
 
-template <bool FORK>
-static cudaError_t pages_go(const PagesLaunch& a, cudaStream_t st) {
-  auto k = pages_kernel<FORK>;
+template <bool FORK, bool GRID>
+static cudaError_t pages_go(const PagesLaunch& a, int ctas, cudaStream_t st) {
+  auto k = pages_kernel<FORK, GRID>;
   const size_t smem = FORK ? (size_t)a.kv.B * 2 * sizeof(int) : 0;
   static int smem_set[SMEM_DEVICES];
   cudaError_t e = allow_smem(k, smem, smem_set);
   if (e != cudaSuccess) return e;
-  // a CTA while its warps have a few tasks each
-  const long long work = (long long)a.kv.B * a.kv.max_blocks + (long long)a.kv.B * a.cap;
-  int cl = 1;
-  while (cl < PG_CLUSTER && work > (long long)cl * PG_THREADS * PG_COLS) cl *= 2;
-  if (cl > 8 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+  if (!GRID && ctas > 8 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cl);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(PG_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cl;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  if (GRID) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  }
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.kv.pdl ? 2 : 1;
+  cfg.numAttrs = a.kv.pdl && !GRID ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t st) {
-  return a.parent != nullptr ? pages_go<true>(a, st) : pages_go<false>(a, st);
+cudaError_t launch_pages(const PagesLaunch& a, int sms, cudaStream_t st) {
+  // a CTA while its warps have a task each
+  const long long work = (long long)a.kv.B * a.kv.max_blocks + (long long)a.kv.B * a.cap;
+  int cl = 1;
+  while (cl < PG_CLUSTER && work > (long long)cl * PG_THREADS * PG_COLS) cl *= 2;
+  if (work <= PG_ONE_CLUSTER) return a.parent != nullptr ? pages_go<true, false>(a, cl, st) : pages_go<false, false>(a, cl, st);
+  const long long most = (work + PG_THREADS * PG_COLS - 1) / (PG_THREADS * PG_COLS);
+  int ctas = sms < PG_GRID ? sms : PG_GRID;
+  if (most < ctas) ctas = (int)most;
+  return a.parent != nullptr ? pages_go<true, true>(a, ctas, st) : pages_go<false, true>(a, ctas, st);
 }
 
 }  // namespace prhs

@@ -39,11 +39,11 @@ struct PagesLaunch {
   PageRow* rows;   // [B]
   int32_t* stage;  // [B][max_blocks]: the new rows of the table, until the old ones are read
   int2* part;      // [B][chunks of kept positions]: (positions kept in place, error bits)
-  int* sums;       // [warps of the cluster] pages given back, then one word of error bits
+  int* sums;       // [warps of the launch] pages given back, then one word of error bits
 };
 size_t pages_workspace(const KVView& kv);
 void pages_split(PagesLaunch* a, void* ws);
-cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t s);
+cudaError_t launch_pages(const PagesLaunch& a, int sms, cudaStream_t s);
 
 struct CopyLaunch {
   KVView to, from;

@@ -59,7 +59,7 @@ prhs_status pages_call(const prhs_kv* kv, const prhs_pages* now, const prhs_page
   a.free_out = next->free_pages;
   a.head_out = next->free_head;
   pages_split(&a, ws);
-  return launched(launch_pages(a, stream));
+  return launched(launch_pages(a, sms, stream));
 }
 
 }  // namespace
