@@ -15,7 +15,7 @@
 // before anything is written, and what shows later (a page outside the pool, no
 // room in the free list) takes the counts back.
 //
-// The entries of the table are tasks of 512 columns of a row, a warp's tasks
+// The entries of the table are tasks of 128 columns of a row, a warp's tasks
 // consecutive, so that a prefix over the warps' counts gives every freed page its
 // place. One cluster of CTAs, or for large tables all SMs (a cooperative launch).
 // Bound: latency, a few dependent passes through L2 with a barrier between two; atomics on
@@ -32,10 +32,10 @@ constexpr int PG_THREADS = 512;          // (a lane holds a task's entries over 
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_CLUSTER = 16;           // above 8 by opt-in
 constexpr int PG_GRID = 256;             // CTAs of a cooperative launch at most
-constexpr int PG_COLS = 16;              // columns a lane
+constexpr int PG_COLS = 4;               // columns a lane (16: a pass's code is fetched once and used once, 18.5 -> 28.7 us for 64 rows)
 constexpr int PG_TASK = 32 * PG_COLS;    // columns of a task
 constexpr long long PG_ONE_CLUSTER = 1 << 16;  // entries up to which one cluster takes a call
-constexpr int PG_KEEP = 1024;            // kept positions a warp checks at a time
+constexpr int PG_KEEP = 128;             // kept positions a warp checks at a time
 
 // Exclusive prefix of x over the block's threads, the sum into *total.
 __device__ __forceinline__ int block_scan(int x, int* wsum, int* total) {
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
       if (m < 0) return r;
       const int chunks = (min(a.cap, kv.t_max) + PG_KEEP - 1) / PG_KEEP;
       int same = 0;
+#pragma unroll 4
       for (int c = 0; c < chunks; c++) {
         const int2 x = a.part[(long long)b * chunks + c];
         same += x.x;

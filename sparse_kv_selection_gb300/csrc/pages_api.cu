@@ -22,8 +22,8 @@ prhs_status check_paged(const prhs_kv* kv) {
   if (kv->block_table == nullptr) return abi_fail(PRHS_EINVAL, "pages: the cache is not paged");
   if ((long long)kv->B * kv->max_blocks >= (1ll << 30))  // entries are numbered in 30 bits
     return abi_fail(PRHS_EUNSUPPORTED, "pages: B * max_blocks above 2^30 entries");
-  if ((long long)kv->B * kv->max_blocks * kv->block_size >= (1ll << 40))  // 1024 kept positions a task
-    return abi_fail(PRHS_EUNSUPPORTED, "pages: B * max_blocks * block_size above 2^40 positions");
+  if ((long long)kv->B * kv->max_blocks * kv->block_size >= (1ll << 36))  // 128 kept positions a task
+    return abi_fail(PRHS_EUNSUPPORTED, "pages: B * max_blocks * block_size above 2^36 positions");
   return PRHS_OK;
 }
 

@@ -7,7 +7,9 @@ the cache and the new tokens) and ``commit`` (accepted tokens join the cache).
 It serves prompt chunks (``rotate(..., append=True)``, then ``commit`` of all
 tokens), the verification of drafted trees, and plain decode with one token a
 sequence. Nothing synchronises with the host, so a step can be captured into a
-graph; the same cache can be decoded by ``SparseDecoder`` between steps.
+graph; the same cache can be decoded by ``SparseDecoder`` between steps. Where
+neighbouring sequences share pages (``PagePool.fork``), ``share_prefixes`` reads
+what they share once.
 """
 from __future__ import annotations
 
@@ -26,7 +28,8 @@ def _own_stream(stream, device):
 
 class TokenBatch:
     def __init__(self, kv: _b.KVCache, rope: _b.RopeTable, *, max_tokens: int, max_new: int,
-                 free_pages=None, n_pages=None, free_head=None, scale: float | None = None, stream=None):
+                 free_pages=None, n_pages=None, free_head=None, scale: float | None = None, stream=None,
+                 share_prefixes: bool = False, min_shared: int = 256):
         """max_tokens packed tokens at most (padding included), max_new of one
         sequence. A paged cache needs free_pages (int32, the pages that no
         sequence holds), n_pages (int32 [B], the pages each row of its block
@@ -35,7 +38,11 @@ class TokenBatch:
         batches on one cache share all three, TokenBatch(..., **other.pages). A
         sequence that ends gives its p pages back in front of the free ones
         (free_head -= p, then free_pages[free_head : free_head + p] = them) and has
-        its n_pages and its length set to 0."""
+        its n_pages and its length set to 0; PagePool does that, and keeps count of
+        pages that several sequences hold.
+        share_prefixes: plan also finds the prefixes of at least min_shared keys that
+        neighbouring sequences share, and attend reads each once (find_shared,
+        shared_attn)."""
         dev, B, d = kv.k.device, kv.B, kv.desc.d
         self.kv, self.rope, self.stream = kv, rope, stream
         self.max_new = int(max_new)
@@ -60,7 +67,12 @@ class TokenBatch:
             self.v = None
             self.out = torch.zeros(T, kv.Hq, d, device=dev, dtype=kv.k.dtype)
             self.lse = torch.zeros(T, kv.Hq, device=dev, dtype=torch.float32)
-            self.ws = _b.make_tree_workspace(kv, self.max_new)
+            self.min_shared, self.shared = int(min_shared), None
+            if share_prefixes:
+                self.shared = torch.zeros(B, 4, **i32)
+                self.ws = _b.make_shared_workspace(kv, T, self.max_new)
+            else:
+                self.ws = _b.make_tree_workspace(kv, self.max_new)
         self._in_cache = False
 
     def plan(self, n_new: torch.Tensor, parents: torch.Tensor | None = None) -> None:
@@ -70,6 +82,8 @@ class TokenBatch:
         self.v, self._in_cache = None, False     # rows of an earlier plan are not this one's
         _b.plan_tokens(self.kv, n_new, self.cu_new, self.positions, self.slots, parents=parents,
                        tree_mask=self.tree_mask, stream=self.stream, **self.pages)
+        if self.shared is not None:
+            _b.find_shared(self.kv, self.cu_new, self.shared, min_keys=self.min_shared, stream=self.stream)
 
     def rotate(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, append: bool = False) -> None:
         """Rotate q [max_tokens][Hq][d] and k [max_tokens][Hkv][d] at the planned
@@ -86,10 +100,14 @@ class TokenBatch:
     def attend(self, out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> None:
         """Attention of the new tokens into out and lse (the batch's own by default)."""
         tree = self.tree_mask is not None     # (planning refuses trees above TREE_MAX tokens)
-        _b.tree_attn(self.kv, self.q, self.k, self.v, self.scale, self.cu_new,
-                     min(self.max_new, _b.TREE_MAX) if tree else self.max_new,
-                     self.out if out is None else out, self.lse if lse is None else lse, self.ws,
-                     tree_mask=self.tree_mask, stream=self.stream)
+        max_new = min(self.max_new, _b.TREE_MAX) if tree else self.max_new
+        to = (self.out if out is None else out, self.lse if lse is None else lse, self.ws)
+        if self.shared is not None:
+            _b.shared_attn(self.kv, self.q, self.k, self.v, self.scale, self.cu_new, max_new, self.shared, *to,
+                           tree_mask=self.tree_mask, stream=self.stream)
+        else:
+            _b.tree_attn(self.kv, self.q, self.k, self.v, self.scale, self.cu_new, max_new, *to,
+                         tree_mask=self.tree_mask, stream=self.stream)
 
     def commit(self, accept_n: torch.Tensor, accept_idx: torch.Tensor | None = None) -> None:
         """Add accept_n[b] tokens (numbers accept_idx[b], or the first ones) to
