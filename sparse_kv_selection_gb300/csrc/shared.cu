@@ -15,8 +15,8 @@ namespace prhs {
 
 constexpr int SJ_THREADS = 128, SJ_PIECES = 4;  // (pieces in flight)
 
-template <typename T, int D>
-__global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ TreeLaunch a,
+template <typename T, int D, bool WAYS>
+__global__ void __launch_bounds__(SJ_THREADS, WAYS ? 5 : 8) shared_join_kernel(const __grid_constant__ TreeLaunch a,
                                                                  const __grid_constant__ TreeRecords rec, int ctas) {
   constexpr int C4 = D / 4, CHUNKS = D / 32;
   const KVView& kv = a.kv;
@@ -40,19 +40,23 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
   if (*a.part_ok == 0) return;
+  // eight lanes take the rows; of fewer rows (1, 2, 4) several take a part of the pieces each
   const int rows = n << gl, blocks = (rows + 7) / 8, lane = threadIdx.x & 31;
+  const int span = !WAYS || rows > 4 ? 8 : rows == 3 ? 4 : rows, ways = WAYS ? 8 / span : 1, way = WAYS ? (lane & 7) / span : 0;
   const long long warps = (long long)gridDim.y * (SJ_THREADS / 32), total = (long long)kv.Hkv * blocks * CHUNKS;
   for (long long i = (long long)blockIdx.y * (SJ_THREADS / 32) + threadIdx.x / 32; i < total; i += warps) {
-    const int chunk = (int)i % CHUNKS, hr = (int)(i / CHUNKS), kvh = hr / blocks, r = (hr - kvh * blocks) * 8 + (lane & 7);
-    if (r >= rows) continue;
-    const int tok = lo + (r >> gl), h = r & (G - 1), c4 = chunk * 8 + (lane >> 3) * 2;
+    const int chunk = (int)i % CHUNKS, hr = (int)(i / CHUNKS), kvh = hr / blocks, r = (hr - kvh * blocks) * 8 + (lane & 7) % span;
+    const bool out_of = r >= rows;
+    if (!WAYS && out_of) continue;
+    const int rr = min(r, rows - 1), tok = lo + (rr >> gl), h = rr & (G - 1), c4 = chunk * 8 + (lane >> 3) * 2;
     int2 at[2] = {make_int2(0, 1), make_int2(0, 1)};  // of the states against the shared and the other keys
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int k = 0; k < 2; k++)
         if (k == 1 || keys > 0) at[k] = __ldcg(a.where + part_row<T>(a, k + 1, tok, kvh, h, gl));
     }
-    if (keys == 0 && (sizeof(T) == 4 || at[1].y <= 1)) continue;  // its result is written
+    const bool stands = keys == 0 && (sizeof(T) == 4 || at[1].y <= 1);  // its result is written
+    if (WAYS ? __all_sync(FULL_MASK, stands || out_of) : stands) continue;
     float M = -INFINITY, L = 0.f;
     float4 y[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
         const int writers = few[k] ? a.few_warps : ctas, unit = few[k] ? a.few_rows : 256, stride = few[k] ? unit : rec.rows_max;
         first = max(0, min(at[k].x, writers - 1));  // (whatever stands there after a launch that gave up)
         pieces = min(at[k].y, writers - first);
-        const int row = (k == 0 ? ((tok - group0) << gl) + h : r) & (unit - 1);
+        const int row = (k == 0 ? ((tok - group0) << gl) + h : rr) & (unit - 1);
         const float4* states = static_cast<const float4*>(a.few_states);
         ml = (few[k] ? reinterpret_cast<const float2*>(states + 2ll * a.few_warps * C4 * unit) : rec.ml) + row;
         o = (few[k] ? states : rec.o) + (long long)c4 * stride + row;
@@ -75,15 +79,16 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
         o_step = (long long)C4 * stride;
         next = stride;
       }
-      for (int p0 = 0; p0 < pieces; p0 += SJ_PIECES) {
+      for (int p0 = 0; p0 < pieces; p0 += SJ_PIECES * ways) {
         float2 s[SJ_PIECES];
         float4 x[SJ_PIECES][2];
 #pragma unroll
         for (int p = 0; p < SJ_PIECES; p++) {
           s[p] = make_float2(-INFINITY, 0.f);
           x[p][0] = x[p][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (p0 + p < pieces) {
-            const long long slot = 2ll * (first + p0 + p) + (p0 + p == 0);
+          const int at_p = p0 + p * ways + way;
+          if (at_p < pieces) {
+            const long long slot = 2ll * (first + at_p) + (at_p == 0);
             s[p] = __ldcg(ml + slot * ml_step);
             x[p][0] = __ldcg(o + slot * o_step);
             x[p][1] = __ldcg(o + slot * o_step + next);
@@ -106,6 +111,21 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
         M = m;
       }
     }
+    if constexpr (WAYS) {
+      for (int d = span; d < 8; d <<= 1) {  // the ways' shares of a row meet
+        const float other = __shfl_xor_sync(FULL_MASK, M, d), m = fmaxf(M, other);
+        const float w0 = tree_weight(M, m), w1 = tree_weight(other, m);
+        L = fmaf(w1, __shfl_xor_sync(FULL_MASK, L, d), w0 * L);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          float* v = &y[c].x;
+#pragma unroll
+          for (int e = 0; e < 4; e++) v[e] = fmaf(w1, __shfl_xor_sync(FULL_MASK, v[e], d), w0 * v[e]);
+        }
+        M = m;
+      }
+      if (stands || out_of || way != 0) continue;
+    }
     const float inv = tree_inv(L);
     const long long orow = (long long)tok * kv.Hq + (kvh << gl) + h;
     T* out = static_cast<T*>(a.out) + orow * D + c4 * 4;
@@ -119,7 +139,8 @@ template <typename T, int D>
 static cudaError_t join_go(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
   const long long blocks = ((long long)a.max_new * (a.kv.Hq / a.kv.Hkv) + 7) / 8;
   const long long y = (blocks * a.kv.Hkv * (D / 32) + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
-  return launch_pdl(shared_join_kernel<T, D>, dim3(a.kv.B, (unsigned)(y < 1024 ? y : 1024)), dim3(SJ_THREADS), 0, st, true, a, rec,
+  auto* kernel = sizeof(T) == 2 && a.max_new * (a.kv.Hq / a.kv.Hkv) <= 4 ? shared_join_kernel<T, D, sizeof(T) == 2> : shared_join_kernel<T, D, false>;
+  return launch_pdl(kernel, dim3(a.kv.B, (unsigned)(y < 1024 ? y : 1024)), dim3(SJ_THREADS), 0, st, true, a, rec,
                     sms);
 }
 cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {

@@ -58,6 +58,8 @@ struct CommitLaunch {
 };
 cudaError_t launch_commit(const CommitLaunch& a, int sms, cudaStream_t s);
 
+// What a launch with shared keys takes of a batch: the groups' shared keys, the sequences' others, or both.
+enum : int { TREE_BOTH, TREE_GROUPS, TREE_OWN };
 struct TreeLaunch {
   KVView kv;
   const void* q;
@@ -76,6 +78,7 @@ struct TreeLaunch {
   // (fp32: [2][T * Hq][d] and [2][T * Hq]; bf16: [2][Hkv][d / 4][T * G] of four columns
   // and [2][Hkv][T * G])
   const int4* shared;
+  int items;        // (fp32) TREE_BOTH, ..
   float* part_o;    // against the state's maximum
   float2* part_ml;  // maximum (base 2) and sum
   int* part_ok;     // 0: the offsets step back, there are no states
@@ -94,10 +97,10 @@ constexpr int FEW_KEYS = 32768;
 __device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
   return t + n <= FEW_KEYS && (long long)n * (a.kv.Hq / a.kv.Hkv) <= 2 * a.few_rows;
 }
-// fp32: two launches, the first counted by the callee; ws holds
-// tree_workspace(kv, max_new, sms) bytes.
+// fp32: two launches (three with shared keys), all but the last counted by the callee; ws
+// holds tree_workspace(kv, max_new, shared, sms) bytes.
 cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t s);
-size_t tree_workspace(const KVView& kv, int max_new, int sms);  // (max_new: tree_most_new)
+size_t tree_workspace(const KVView& kv, int max_new, bool shared, int sms);  // (max_new: tree_most_new)
 // bf16: two launches, the first counted by the callee; *err is the launches'
 // result when the descriptors could be made. Workspace bytes of a call.
 prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);

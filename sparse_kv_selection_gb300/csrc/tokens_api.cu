@@ -26,8 +26,8 @@ prhs_status launched(cudaError_t e) {
   return abi_fail(PRHS_ECUDA, cudaGetErrorString(e));
 }
 
-size_t tree_ws_bytes(const KVView& kv, int max_new, int sms) {
-  return kv.dtype == PRHS_BF16 ? tree_tc_workspace(kv, max_new, sms) : tree_workspace(kv, max_new, sms);
+size_t tree_ws_bytes(const KVView& kv, int max_new, bool shared, int sms) {
+  return kv.dtype == PRHS_BF16 ? tree_tc_workspace(kv, max_new, sms) : tree_workspace(kv, max_new, shared, sms);
 }
 
 // Checks shared by every entry point: descriptor, device, token count.
@@ -185,7 +185,7 @@ size_t prhs_tree_workspace_size(const prhs_kv* kv, int max_new) {
   unsigned* err = nullptr;
   int sms = 0;
   if (abi_device(&err, &sms) != PRHS_OK) return 0;
-  return tree_ws_bytes(abi_view(*kv, err), max_new, sms);
+  return tree_ws_bytes(abi_view(*kv, err), max_new, false, sms);
 }
 
 }  // extern "C"
@@ -200,7 +200,7 @@ struct SharedWs {
 SharedWs shared_ws(const KVView& kv, int T, int max_new, int sms) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   SharedWs w;
-  w.part_o = up(tree_ws_bytes(kv, T, sms));
+  w.part_o = up(tree_ws_bytes(kv, T, true, sms));
   w.part_ml = w.part_o + up((size_t)2 * T * kv.Hq * kv.d * sizeof(float));
   w.part_ok = w.part_ml + up((size_t)2 * T * kv.Hq * sizeof(float2));
   w.states = w.part_ok + 256;
@@ -233,7 +233,7 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
     return abi_fail(PRHS_EUNSUPPORTED, "tree: too many key tiles for one call");
   if (!ws) return abi_fail(PRHS_EWORKSPACE, "workspace is null");
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return abi_fail(PRHS_EWORKSPACE, "workspace must be 256-byte aligned");
-  if (!shared && ws_bytes < tree_ws_bytes(a.kv, max_new, sms))
+  if (!shared && ws_bytes < tree_ws_bytes(a.kv, max_new, false, sms))
     return abi_fail(PRHS_EWORKSPACE, "workspace is smaller than prhs_tree_workspace_size()");
   if (T == 0) return PRHS_OK;
   a.q = q;

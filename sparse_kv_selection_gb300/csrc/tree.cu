@@ -108,7 +108,7 @@ template <bool SHARED>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeLaunch& a, int e, int ul) {
   TreeSeq s;
   const bool causal = a.mask == nullptr;
-  static_cast<TreeItem&>(s) = tree_item<SHARED>(a, e);
+  static_cast<TreeItem&>(s) = tree_item<SHARED>(a, !SHARED || a.items == TREE_BOTH ? e : 2 * e + (a.items == TREE_OWN));
   s.u = 1 << ul;
   s.blocks = (int)(((long long)s.n + s.u - 1) >> ul);
   s.cache_tiles = (int)(((long long)s.t + TK - 1) / TK);
@@ -140,15 +140,19 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   __shared__ uint32_t have_key[STEPS];      // those that exist
   __shared__ long long wsum[W];
 
-  pdl_wait();
+  // Own keys beside the groups' (TREE_OWN): nothing here needs that launch, but the next one
+  // needs both, so that this one's last CTA does nothing but wait for it.
+  const int ctas = gridDim.x - (SHARED && a.items == TREE_OWN ? 1 : 0), cta = (SHARED ? p.cta0 : 0) + blockIdx.x;
+  if (!SHARED || a.items != TREE_OWN || (int)blockIdx.x == ctas) pdl_wait();
   pdl_trigger();
+  if (SHARED && (int)blockIdx.x == ctas) return;
   const KVView& kv = a.kv;
   const bool causal = a.mask == nullptr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gl = p.group_log2, ul = S::TR_LOG2 - gl;  // log2 of the group and of a unit's tokens
 
   // ---- this CTA's run of the list of all tiles ----
-  const int items = SHARED ? 2 * kv.B : kv.B;
+  const int items = SHARED && a.items == TREE_BOTH ? 2 * kv.B : kv.B;
   const int per_t = (items + THREADS - 1) / THREADS, e0 = tid * per_t;
   long long mine = 0;
   bool back = false;  // offsets that step back: sequences would overlap, without bound
@@ -172,10 +176,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     if (w < warp) before += wsum[w];
     total += wsum[w];
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x, g0 = blockIdx.x * per;
+  const long long per = (total + ctas - 1) / ctas, g0 = blockIdx.x * per;
   const int count = (int)(min(total, g0 + per) - g0);  // negative: none are left
   if (count <= 0 || back) {
-    if (tid == 0) p.split[blockIdx.x] = TreeSplit{};
+    if (tid == 0) p.split[cta] = TreeSplit{};
     return;
   }
   if (g0 >= before && g0 < before + mine) {  // the run begins in this thread's items
@@ -211,7 +215,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   }
   __syncthreads();
 
-  // One thread: the step behind `x` (x.left > 0).
+  // The step behind `x` (x.left > 0): one thread; with shared keys a warp, since most items
+  // may then have no tiles: 32 are looked at together.
   auto advance = [&](TreeStep x) {
     x.left--;
     if (++x.tile == x.tiles) {
@@ -222,7 +227,26 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
         if (++x.kvh == kv.Hkv) {
           x.kvh = 0;
           TreeSeq s = {};
-          while (s.n == 0 && ++x.e < items) s = tree_seq<SHARED>(a, x.e, ul);
+          if constexpr (SHARED) {
+            unsigned some = 0;
+            int e = x.e + 1 + lane;
+            for (;; e += 32) {
+              if (e < items) s = tree_seq<SHARED>(a, e, ul); else s.n = 0;
+              some = __ballot_sync(FULL_MASK, s.n > 0);
+              if (some != 0 || e - lane + 32 >= items) break;
+            }
+            const int from = some != 0 ? __ffs(some) - 1 : 0;
+            x.e = e - lane + from;
+            s.b = __shfl_sync(FULL_MASK, s.b, from);
+            s.base = __shfl_sync(FULL_MASK, s.base, from);
+            s.part = __shfl_sync(FULL_MASK, s.part, from);
+            s.c0 = __shfl_sync(FULL_MASK, s.c0, from);
+            s.n = __shfl_sync(FULL_MASK, s.n, from);
+            s.t = __shfl_sync(FULL_MASK, s.t, from);
+            s.u = __shfl_sync(FULL_MASK, s.u, from);
+          } else {
+            while (s.n == 0 && ++x.e < items) s = tree_seq<SHARED>(a, x.e, ul);
+          }
           x.b = s.b;
           x.base = s.base;
           x.part = s.part;
@@ -288,8 +312,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
 
   constexpr int AHEAD = S::STAGES;  // tiles that have been looked up when the loop begins
   if (warp == W - 1) {
-    if (lane == 0)
-      for (int i = 1; i < min(AHEAD + 1, count); i++) steps[i] = advance(steps[i - 1]);
+    if (SHARED || lane == 0)
+      for (int i = 1; i < min(AHEAD + 1, count); i++) {
+        const TreeStep y = advance(steps[i - 1]);
+        if (lane == 0) steps[i] = y;
+        if (SHARED) __syncwarp();
+      }
     __syncwarp();
     long long row[AHEAD];
 #pragma unroll
@@ -340,7 +368,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     long long row = -1;
     if (warp == W - 1 && look < count) {
       row = find(steps[look & (STEPS - 1)]);
-      if (lane == 0 && look + 1 < count) steps[(look + 1) & (STEPS - 1)] = advance(steps[look & (STEPS - 1)]);
+      if ((SHARED || lane == 0) && look + 1 < count) {
+        const TreeStep y = advance(steps[look & (STEPS - 1)]);
+        if (lane == 0) steps[(look + 1) & (STEPS - 1)] = y;
+      }
     }
     const float* sk = tree_smem + stage * S::STAGE;
     const float* sv = sk + TK * LD;
@@ -468,13 +499,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
         y.rows = rows;
         y.kvh = x.kvh;
         y.tok = (int)(x.c0 + (long long)x.block * x.u);
-        y.first = (int)(start / per);
+        y.first = cta - (int)blockIdx.x + (int)(start / per);
         y.part = x.part;
-        y.n_rec = (int)((start + x.tiles - 1) / per) - y.first + 1;
+        y.n_rec = (int)((start + x.tiles - 1) / per) - (int)(start / per) + 1;
       }
-      p.split[blockIdx.x] = y;
+      p.split[cta] = y;
     }
-    const long long rec = (2ll * blockIdx.x + (x.tile0 == 0 ? 1 : 0)) * p.rows_max;
+    const long long rec = (2ll * cta + (x.tile0 == 0 ? 1 : 0)) * p.rows_max;
 #pragma unroll
     for (int i = 0; i < R; i++) {
       const int r = wrow + ty + TY * i;
@@ -543,18 +574,19 @@ static constexpr int tree_ctas_sm(int d, int rows) {
   return d == 128 ? (rows == 8 ? 3 : 2) : (rows == 8 ? 5 : rows == 32 ? 4 : 3);
 }
 static int tree_ctas(const KVView& kv, int rows, int sms) { return tree_ctas_sm(kv.d, rows) * sms; }
-size_t tree_workspace(const KVView& kv, int max_new, int sms) {
-  // (a call may take fewer rows than max_new names: the form for what its tokens leave)
+size_t tree_workspace(const KVView& kv, int max_new, bool shared, int sms) {
+  // (a call may take fewer rows than max_new names: the form for what its tokens leave;
+  // shared keys: with the CTAs of another form for the own keys)
   size_t need = 0;
   for (int rows = tree_rows(kv, max_new); rows >= 8; rows = rows == 64 ? 32 : rows == 32 ? 8 : 0) {
-    const size_t n = tree_record_bytes(kv.d, tree_ctas(kv, rows, sms), rows);
+    const size_t n = tree_record_bytes(kv.d, tree_ctas(kv, rows, sms) + (shared ? tree_ctas(kv, 8, sms) : 0), rows);
     need = n > need ? n : need;
   }
   return need;
 }
 
 template <int D, int TY, int R, int W, bool SHARED>
-static cudaError_t tree_go(const TreeLaunch& a, const TreeRecords& p, int sms, cudaStream_t st) {
+static cudaError_t tree_go(const TreeLaunch& a, const TreeRecords& p, int sms, cudaStream_t st, unsigned* ctas) {
   constexpr int CTAS = tree_ctas_sm(D, TY * R * W);
   using S = TreeShape<D, TY, R, W, CTAS>;
   auto k = tree_kernel<D, TY, R, W, CTAS, SHARED>;
@@ -562,28 +594,51 @@ static cudaError_t tree_go(const TreeLaunch& a, const TreeRecords& p, int sms, c
   cudaError_t e = allow_smem(k, S::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   // no more CTAs than tiles that the longest caches would give
-  const long long units = (((long long)tree_most_new(a) << p.group_log2) + S::TR - 1) / S::TR * a.kv.B * a.kv.Hkv;
+  const long long units = (((long long)(SHARED ? a.T : a.max_new) << p.group_log2) + S::TR - 1) / S::TR * a.kv.B * a.kv.Hkv;
   const long long tiles = (SHARED ? 2 : 1) * units * ((a.kv.t_max + TK - 1ll) / TK + (a.max_new + TK - 1ll) / TK);
-  const unsigned ctas = (unsigned)(tiles < CTAS * sms ? tiles : CTAS * sms);
-  if ((e = launch_pdl(k, dim3(ctas), dim3(S::THREADS), S::SMEM, st, a.kv.pdl, a, p)) != cudaSuccess) return e;
-  abi_count_launch();
-  return launch_tree_join<float, D, true>(a, p, ctas, st);
+  *ctas = (unsigned)(tiles < CTAS * sms ? tiles : CTAS * sms);
+  const bool own = SHARED && a.items == TREE_OWN;
+  e = launch_pdl(k, dim3(*ctas + own), dim3(S::THREADS), S::SMEM, st, own || a.kv.pdl, a, p);
+  if (e == cudaSuccess) abi_count_launch();
+  return e;
 }
 
 template <bool SHARED>
-static cudaError_t tree_form(const TreeLaunch& a, const TreeRecords& p, int rows, int sms, cudaStream_t st) {
+static cudaError_t tree_form(const TreeLaunch& a, const TreeRecords& p, int rows, int sms, cudaStream_t st, unsigned* ctas) {
   const bool wide = a.kv.d == 128;
-  if (rows == 8) return wide ? tree_go<128, 2, 2, 2, SHARED>(a, p, sms, st) : tree_go<64, 2, 2, 2, SHARED>(a, p, sms, st);
-  if (rows == 32) return wide ? tree_go<128, 2, 4, 4, SHARED>(a, p, sms, st) : tree_go<64, 2, 4, 4, SHARED>(a, p, sms, st);
-  return wide ? tree_go<128, 4, 4, 4, SHARED>(a, p, sms, st) : tree_go<64, 4, 4, 4, SHARED>(a, p, sms, st);
+  if (rows == 8)
+    return wide ? tree_go<128, 2, 2, 2, SHARED>(a, p, sms, st, ctas) : tree_go<64, 2, 2, 2, SHARED>(a, p, sms, st, ctas);
+  if (rows == 32)
+    return wide ? tree_go<128, 2, 4, 4, SHARED>(a, p, sms, st, ctas) : tree_go<64, 2, 4, 4, SHARED>(a, p, sms, st, ctas);
+  return wide ? tree_go<128, 4, 4, 4, SHARED>(a, p, sms, st, ctas) : tree_go<64, 4, 4, 4, SHARED>(a, p, sms, st, ctas);
 }
 
-cudaError_t launch_tree(const TreeLaunch& a, int sms, void* ws, cudaStream_t st) {
+cudaError_t launch_tree(const TreeLaunch& launch, int sms, void* ws, cudaStream_t st) {
+  TreeLaunch a = launch;
   const KVView& kv = a.kv;
-  const int G = kv.Hq / kv.Hkv, rows = tree_rows(kv, tree_most_new(a));
-  const TreeRecords p = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, tree_ctas(kv, rows, sms), rows);
-  if (a.shared != nullptr) return tree_form<true>(a, p, rows, sms, st);
-  return tree_form<false>(a, p, rows, sms, st);
+  const bool shared = a.shared != nullptr;
+  const int G = kv.Hq / kv.Hkv, own = tree_rows(kv, a.max_new);
+  // Groups may have many rows where their sequences have few: each in the form for its rows, in
+  // launches that run beside one another. (128 sequences of one token, 4 rows a KV head, in
+  // 8 groups of 3.7 to 5K keys: 733 us with the form of the few for all, 596 with the groups',
+  // 415; 32 questions on one prefix of 131072 keys 3.7, 1.8, 1.8 ms.) The second launch takes
+  // 6 to 25 us, so groups that are small whatever they share have the form of the few (14
+  // sequences, 8 rows a KV head, 2K keys: 45 us and 70; 16 samples of 4096 keys 92 and 107).
+  const long long most = (long long)a.T * G;  // rows of a group
+  const int rows = shared && most > 64 && most * kv.Hkv * kv.t_max > 1 << 20 ? tree_rows(kv, a.T) : own;
+  const int all = tree_ctas(kv, rows, sms) + (own != rows ? tree_ctas(kv, own, sms) : 0);
+  TreeRecords p = tree_records(ws, G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, all, rows);
+  unsigned ctas = 0, more = 0;
+  a.items = own == rows ? TREE_BOTH : TREE_GROUPS;
+  cudaError_t e = shared ? tree_form<true>(a, p, rows, sms, st, &ctas) : tree_form<false>(a, p, rows, sms, st, &ctas);
+  if (e == cudaSuccess && own != rows) {
+    a.items = TREE_OWN;
+    p.cta0 = ctas;
+    e = tree_form<true>(a, p, own, sms, st, &more);
+    ctas += more;
+  }
+  if (e != cudaSuccess) return e;
+  return kv.d == 128 ? launch_tree_join<float, 128, true>(a, p, ctas, st) : launch_tree_join<float, 64, true>(a, p, ctas, st);
 }
 
 }  // namespace prhs

@@ -18,6 +18,7 @@ struct __align__(16) TreeSplit {
 struct TreeRecords {
   int group_log2;    // log2 of the query heads of a KV head
   int rows_max;      // rows a record may hold
+  int cta0;          // the launch's first CTA
   TreeSplit* split;  // [CTAs]
   float2* ml;        // [2 CTAs][rows_max]
   float4* o;         // [2 CTAs][rows_max][D / 4] (ROW_MAJOR) or [2 CTAs][D / 4][rows_max]
@@ -159,6 +160,7 @@ inline TreeRecords tree_records(void* ws, int group_log2, size_t ctas, int rows_
   char* w = static_cast<char*>(ws);
   p.group_log2 = group_log2;
   p.rows_max = rows_max;
+  p.cta0 = 0;
   p.split = reinterpret_cast<TreeSplit*>(w);
   w += tree_up(ctas * sizeof(TreeSplit));
   p.ml = reinterpret_cast<float2*>(w);

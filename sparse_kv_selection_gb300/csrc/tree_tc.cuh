@@ -546,6 +546,37 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         off -= kv.Hkv * s.tiles;
         s = tc_seq<SHARED>(a, ++item, ul);
       }
+      // With shared keys most items may have no tiles here, and finding that out takes 0.6 us of
+      // dependent reads: 32 are looked at together, one a lane (640 single tokens in 19 small
+      // groups: 420 us one by one).
+      TcSeq ahead = {};
+      int ahead0 = 0, ahead_some = 0;  // item of lane 0; lanes whose items are still to come
+      auto next_item = [&]() {
+        if constexpr (SHARED) {
+          while (ahead_some == 0 && item + 1 < items) {
+            ahead0 = item + 1;
+            ahead.blocks = 0;
+            if (ahead0 + lane < items) ahead = tc_seq<SHARED>(a, ahead0 + lane, ul);
+            ahead_some = __ballot_sync(FULL_MASK, ahead.blocks > 0);
+            item = min(items, ahead0 + 32) - 1;
+          }
+          if (ahead_some == 0) return false;  // (there is one while tiles are left)
+          const int from = __ffs(ahead_some) - 1;
+          ahead_some &= ahead_some - 1;
+          s.b = __shfl_sync(FULL_MASK, ahead.b, from);
+          s.base = __shfl_sync(FULL_MASK, ahead.base, from);
+          s.t = __shfl_sync(FULL_MASK, ahead.t, from);
+          s.c0 = __shfl_sync(FULL_MASK, ahead.c0, from);
+          s.n = __shfl_sync(FULL_MASK, ahead.n, from);
+          s.part = __shfl_sync(FULL_MASK, ahead.part, from);
+          s.blocks = __shfl_sync(FULL_MASK, ahead.blocks, from);
+          s.cache_tiles = __shfl_sync(FULL_MASK, ahead.cache_tiles, from);
+        } else {
+          do s = tc_seq<SHARED>(a, ++item, ul);
+          while (s.blocks == 0);
+        }
+        return true;
+      };
       const int4 at = tc_unit_at<SHARED>(a, item, off, ul, false);
       int kvh = at.x, block = at.y;
       off = at.z;
@@ -616,8 +647,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           block = 0;
           if (++kvh == kv.Hkv) {
             kvh = 0;
-            do s = tc_seq<SHARED>(a, ++item, ul);
-            while (s.blocks == 0);
+            if (!next_item()) break;
           }
         }
       }
