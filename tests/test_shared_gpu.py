@@ -154,6 +154,17 @@ def test_largest_batch():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [(0, 1), (0, 6)])
+def test_small_groups_far_apart(dtype, n):
+    """More sequences than are kept at hand; few of them have a group, and few of the
+    batch's items have keys for the launch that looks for them."""
+    rng = np.random.default_rng(n[1])
+    families = [(int(rng.integers(1, 60)), int(rng.integers(0, 90)) if f % 3 == 0 else 0) for f in range(16)]
+    full(families, (0, 500), n, 8, 4, 64, dtype, 16, seed=n[1])
+    full([(1, 0)] * 150 + [(2, 64)] + [(1, 0)] * 150 + [(3, 256)] + [(1, 0)] * 150, (0, 300), n, 8, 4, 64, dtype, 0, seed=n[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_long_causal_chunks_share(dtype):
     """Chunks that fill tiles by themselves may share too."""
     full([(3, 500)], (0, 40), (200, 300), 4, 1, 64, dtype, 16, seed=6)
