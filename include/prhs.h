@@ -518,8 +518,10 @@ size_t prhs_shared_workspace_size(const prhs_kv* kv, int T, int max_new);
  * [0, P) of a group's rows are the same, so is the result, but for the order of sums.
  * shared[b] (int32 [B][4], 16-byte aligned) as prhs_find_shared fills it, or a caller
  * that knows its batch: every row of a group has the same (first row, rows, P, 0); a
- * row that is alone has (b, 1, 0, 0). Groups must not overlap. P counts whole pages (it
- * is rounded down to them; on a contiguous cache it is any number). A row whose entry
+ * row that is alone has (b, 1, 0, 0). Groups must not overlap (if they have more than T
+ * tokens together that is flagged, PRHS_DEV_BAD_INDEX, and no result has a meaning). P
+ * counts whole pages (it is rounded down to them; on a contiguous cache it is any number).
+ * A row whose entry
  * does not fit its group's first row, or with P above either row's length, is flagged
  * (PRHS_DEV_BAD_INDEX) and attends all its own keys. Everything else, errors too, as
  * prhs_tree_attn. */

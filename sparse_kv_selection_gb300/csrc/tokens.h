@@ -93,6 +93,7 @@ struct TreeLaunch {
 // of few_rows query rows a KV head, which read the keys each, and few keys. (24 prompts of
 // 20 to 63 tokens, 4 heads a KV head, whose units are six and more: 158 us with those, 135
 // without.)
+// (at most 16384 rows of KV heads: 2^26 steps)
 constexpr int FEW_KEYS = 32768;
 __device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
   return t + n <= FEW_KEYS && (long long)n * (a.kv.Hq / a.kv.Hkv) <= 2 * a.few_rows;
@@ -186,6 +187,13 @@ __device__ __forceinline__ int shared_keys(const KVView& kv, const int4* shared,
   if (ok) return keys;
   raise_error(kv.err, PRHS_DEV_BAD_INDEX);
   return 0;
+}
+
+// Groups are apart, so that all of them together have no more than T tokens. More are
+// flagged and nothing is attended: work and counts would be without bound.
+__device__ __forceinline__ bool groups_overlap(const TreeLaunch& a, long long tokens, int tid) {
+  if (tokens > a.T && tid == 0) raise_error(a.kv.err, PRHS_DEV_BAD_INDEX);
+  return tokens > a.T;
 }
 
 // What the rows of a launch attend, item by item: sequence b's tokens over its own

@@ -229,7 +229,7 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
   // 32-bit tile counts: units (256 rows of tokens times group) times their tiles
   const int G = kv->Hq / kv->Hkv;
   const long long units = ((long long)T * G / 256 + kv->B) * kv->Hkv * (shared ? 2 : 1);
-  if (units * (a.kv.t_max / 128 + (max_new < T ? max_new : T) / 128 + 2) >= (1ll << 31))
+  if (units * (a.kv.t_max / 128 + (max_new < T ? max_new : T) / 128 + (shared ? 4 : 2)) >= (1ll << 31))
     return abi_fail(PRHS_EUNSUPPORTED, "tree: too many key tiles for one call");
   if (!ws) return abi_fail(PRHS_EWORKSPACE, "workspace is null");
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return abi_fail(PRHS_EWORKSPACE, "workspace must be 256-byte aligned");

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   __shared__ TreeStep steps[STEPS];
   __shared__ long long key_row[STEPS][TK];  // a tile's keys: row of the cache, or the sequence's token; -1: none
   __shared__ uint32_t have_key[STEPS];      // those that exist
-  __shared__ long long wsum[W];
+  __shared__ long long wsum[W], wgrouped[SHARED ? W : 1];  // (tokens of all groups)
 
   // Own keys beside the groups' (TREE_OWN): nothing here needs that launch, but the next one
   // needs both, so that this one's last CTA does nothing but wait for it.
@@ -154,11 +154,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   // ---- this CTA's run of the list of all tiles ----
   const int items = SHARED && a.items == TREE_BOTH ? 2 * kv.B : kv.B;
   const int per_t = (items + THREADS - 1) / THREADS, e0 = tid * per_t;
-  long long mine = 0;
+  long long mine = 0, grouped = 0;
   bool back = false;  // offsets that step back: sequences would overlap, without bound
   for (int e = e0; e < min(items, e0 + per_t); e++) {
     const TreeSeq s = tree_seq<SHARED>(a, e, ul);
     mine += kv.Hkv * s.tiles;
+    if (SHARED && s.part == 1) grouped += s.n;
     back |= a.cu_new[s.b + 1] < a.cu_new[s.b];
   }
   long long run = mine;
@@ -167,9 +168,21 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
     const long long y = __shfl_up_sync(FULL_MASK, run, o);
     if (lane >= o) run += y;
   }
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) grouped += __shfl_xor_sync(FULL_MASK, grouped, o);
+    if (lane == 0) wgrouped[warp] = grouped;
+  }
   if (lane == 31) wsum[warp] = run;
   back = __syncthreads_or(back);  // (flagged by tree_seq)
-  if (SHARED && blockIdx.x == 0 && tid == 0) *a.part_ok = !back;
+  if constexpr (SHARED) {
+    grouped = 0;
+#pragma unroll
+    for (int w = 0; w < W; w++) grouped += wgrouped[w];
+    if (groups_overlap(a, grouped, tid)) back = true;
+    // (the groups' launch sees what there is to see)
+    if (a.items != TREE_OWN && blockIdx.x == 0 && tid == 0) *a.part_ok = !back;
+  }
   long long total = 0, before = run - mine;
 #pragma unroll
   for (int w = 0; w < W; w++) {

@@ -152,6 +152,7 @@ struct TcAux {
   int wsum[TC_WARPS], wmax[TC_WARPS];
   int fsum[TC_WARPS];      // (shared keys) steps of the few rows' list
   long long cost[TC_WARPS];  // what the tiles' list takes, in steps of the other
+  long long grouped[TC_WARPS];  // tokens of all groups
 };
 static_assert(sizeof(TcAux) <= TC_AUX, "aux region");
 
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const int per_t = (items + TC_THREADS - 1) / TC_THREADS, e0 = tid * per_t;
   int mine = 0, most = 0;  // tiles of this thread's items, of their largest unit
   int steps = 0;           // of the few rows' list
-  long long cost = 0;
+  long long cost = 0, grouped = 0;
   bool back = false;       // offsets that step back: sequences would overlap, and counts pass 32 bits
   for (int e = e0; e < min(items, e0 + per_t); e++) {
     const TcSeq s = tc_seq<SHARED>(a, e, ul);
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     mine += kv.Hkv * s.tiles;
     if (s.blocks > 0) most = max(most, tc_unit_tiles(s, s.blocks - 1, ul, a.mask == nullptr) + REST<SHARED>);
     if constexpr (SHARED) {
+      if (s.part == 1) grouped += s.n;
       cost += (long long)kv.Hkv * s.tiles * ((s.n << gl) > TT ? TC_COST_2 : TC_COST_1);
       if (e & 1) {
         const FewSeq f = few_seq<8 * NT1>(a, tree_item<true>(a, e, true), gl);
@@ -422,10 +424,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const int y = __shfl_up_sync(FULL_MASK, steps, o);
       if (lane >= o) steps += y;
       cost += __shfl_xor_sync(FULL_MASK, cost, o);
+      grouped += __shfl_xor_sync(FULL_MASK, grouped, o);
     }
     if (lane == 31) {
       aux.fsum[warp] = steps;
       aux.cost[warp] = cost;
+      aux.grouped[warp] = grouped;
     }
   }
   if (lane == 31) {
@@ -433,7 +437,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     aux.wmax[warp] = most;
   }
   back = __syncthreads_or(back);
-  if (SHARED && blockIdx.x == 0 && tid == 0) *a.part_ok = !back;
+  if constexpr (SHARED) {
+    grouped = 0;
+#pragma unroll
+    for (int w = 0; w < TC_WARPS; w++) grouped += aux.grouped[w];
+    if (groups_overlap(a, grouped, tid)) back = true;
+    if (blockIdx.x == 0 && tid == 0) *a.part_ok = !back;
+  }
   if (back) return;  // (flagged above)
   int total = 0, before = 0;
 #pragma unroll

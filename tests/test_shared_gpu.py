@@ -221,6 +221,19 @@ def test_entries_that_do_not_fit(dtype):
     b.check(out)
 
 
+@pytest.mark.parametrize("dtype,Hq", [(BF16, 2), (F32, 2), (F32, 16)])
+def test_overlapping_groups_refused(dtype, Hq):
+    """Every row the first of a group that reaches to the batch's end: more tokens than there are."""
+    import sparse_kv_selection_gb300 as S
+    from sparse_kv_selection_gb300.binding import DEV_BAD_INDEX
+    b = Batch([(64, 64)], (0, 20), (1, 1), Hq, 2, 64, dtype, 16, seed=9)
+    whole = b.run()
+    b.run(share=[[r, 64 - r, 64, 0] for r in range(64)])
+    assert S.last_error() == DEV_BAD_INDEX
+    again = b.run()
+    assert S.last_error() == 0 and torch.equal(whole[0], again[0]) and torch.equal(whole[1], again[1])
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_offsets_and_lengths_refused(dtype):
     import sparse_kv_selection_gb300 as S
