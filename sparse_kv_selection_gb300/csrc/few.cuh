@@ -102,13 +102,11 @@ __device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, const TreeItem& x
 struct FewTask {
   TreeItem x;
   int kvh, blk, s0, s1;    // KV head, unit, steps here
-  int taken;               // of the list
   int cached, fresh;       // steps over the cache, new tokens that the unit sees
   int first, cuts;         // the warp that begins the unit, the warps that have steps of it
   int window, page;        // pages of steps window .. window + 31, one a lane (not looked at before they are used)
   bool some;               // (none: the run is done)
 };
-
 
 struct FewAux {
   uint64_t full[FEW_WARPS][6];
@@ -199,15 +197,15 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     t.x = s.x;
     t.kvh = unit / s.blocks;
     t.blk = unit - t.kvh * s.blocks;
-    t.taken = min(s.steps - in, end - pos);
-    pos += t.taken;
+    const int taken = min(s.steps - in, end - pos);  // of the list
+    pos += taken;
     t.some = true;
     t.first = start / run;
     t.cuts = (start + s.steps - FEW_REST - 1) / run - t.first + 1;
     const int all = few_steps<RB>(a, t.x, gl, t.blk, &t.fresh);
     t.cached = (t.x.t + FEW_STEP - 1) / FEW_STEP;
     t.s0 = min(in, all);
-    t.s1 = min(in + t.taken, all);
+    t.s1 = min(in + taken, all);
     look_up(t, t.s0);
     // its Q rows, zeros behind its last
     __syncwarp();
@@ -274,175 +272,175 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
         for (int h = 0; h < 2; h++)
           q[t][j][h] = *reinterpret_cast<const uint32_t*>(next_q + (8 * t + g) * QS + (16 * j + 8 * h + 2 * c) * 2);
 
-  float m[NT][2], l[NT][2], o[NT][D / 16][4];  // rows 8 t + 2 c, + 1; O's columns 16 e + g, + 8
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-    m[t][0] = m[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 16; e++) o[t][e][0] = o[t][e][1] = o[t][e][2] = o[t][e][3] = 0.f;
-  }
-  // a lane's row of the four matrices of a product's operand: K's rows lane % 16, columns 8 (lane / 16) ..;
-  // V's the other way about (its matrices come in the order of d, then keys)
-  const int krow = lane & 15, kcol = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vcol = lane >> 3 & 1;
-  const uint32_t k_at = ring + krow * 128, v_at = ring + SEGS * SEG + vrow * 128;
-  for (int s = cur.s0;; s++) {
-    while (held < STAGES) {
-      if (!in_next && cursor >= cur.s1) {
-        if (!known || !nxt.some) break;
-        in_next = true;
-        cursor = nxt.s0;
-      }
-      if (in_next && cursor >= nxt.s1) break;
-      load(in_next ? nxt : cur, cursor++, fill);
-      fill = fill + 1 == STAGES ? 0 : fill + 1;
-      held++;
-    }
-    if (!known) {
-      nxt = fetch();
-      known = true;
-    }
-    if (s >= cur.s1) break;
-    dead = !__all_sync(FULL_MASK, mbar_wait(&full[warp][stage], phase, kv.err));
-    if (dead) break;
-    const int n = counts >> 5 * stage & 31;
-    float p[NT][4];  // keys g: rows 2 c, 2 c + 1; keys g + 8
-#pragma unroll
-    for (int t = 0; t < NT; t++) p[t][0] = p[t][1] = p[t][2] = p[t][3] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; j++) {
-      uint32_t k[4];
-      ldm4(k, k_at + stage * STAGE + j / 4 * SEG + (((j % 4 * 2 + kcol) ^ (krow & 7)) << 4));
-#pragma unroll
-      for (int t = 0; t < NT; t++) mma16(p[t], k[0], k[1], k[2], k[3], q[t][j][0], q[t][j][1]);
-    }
-    uint32_t pb[NT][2];
+    float m[NT][2], l[NT][2], o[NT][D / 16][4];  // rows 8 t + 2 c, + 1; O's columns 16 e + g, + 8
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const int key0 = (s - cached) * FEW_STEP;  // (new tokens)
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) p[t][i] *= sc;
-      if (s >= cached || n < FEW_STEP) {
+      for (int e = 0; e < D / 16; e++) o[t][e][0] = o[t][e][1] = o[t][e][2] = o[t][e][3] = 0.f;
+    }
+    // a lane's row of the four matrices of a product's operand: K's rows lane % 16, columns 8 (lane / 16) ..;
+    // V's the other way about (its matrices come in the order of d, then keys)
+    const int krow = lane & 15, kcol = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vcol = lane >> 3 & 1;
+    const uint32_t k_at = ring + krow * 128, v_at = ring + SEGS * SEG + vrow * 128;
+    for (int s = cur.s0;; s++) {
+      while (held < STAGES) {
+        if (!in_next && cursor >= cur.s1) {
+          if (!known || !nxt.some) break;
+          in_next = true;
+          cursor = nxt.s0;
+        }
+        if (in_next && cursor >= nxt.s1) break;
+        load(in_next ? nxt : cur, cursor++, fill);
+        fill = fill + 1 == STAGES ? 0 : fill + 1;
+        held++;
+      }
+      if (!known) {
+        nxt = fetch();
+        known = true;
+      }
+      if (s >= cur.s1) break;
+      dead = !__all_sync(FULL_MASK, mbar_wait(&full[warp][stage], phase, kv.err));
+      if (dead) break;
+      const int n = counts >> 5 * stage & 31;
+      float p[NT][4];  // keys g: rows 2 c, 2 c + 1; keys g + 8
+#pragma unroll
+      for (int t = 0; t < NT; t++) p[t][0] = p[t][1] = p[t][2] = p[t][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; j++) {
+        uint32_t k[4];
+        ldm4(k, k_at + stage * STAGE + j / 4 * SEG + (((j % 4 * 2 + kcol) ^ (krow & 7)) << 4));
+#pragma unroll
+        for (int t = 0; t < NT; t++) mma16(p[t], k[0], k[1], k[2], k[3], q[t][j][0], q[t][j][1]);
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        const int key0 = (s - cached) * FEW_STEP;  // (new tokens)
+#pragma unroll
+        for (int i = 0; i < 4; i++) p[t][i] *= sc;
+        if (s >= cached || n < FEW_STEP) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int key = g + 8 * (i >> 1);
+            bool see = key < n;
+            if (s >= cached && see) {
+              const int tok = min((blk * RB + 8 * t + 2 * c + (i & 1)) >> gl, x.n - 1);
+              see = causal ? key0 + key <= tok
+                           : (a.mask[(long long)(x.c0 + tok) * PRHS_TREE_WORDS + ((key0 + key) >> 5)] >> ((key0 + key) & 31)) & 1u;
+            }
+            if (!see) p[t][i] = -INFINITY;
+          }
+        }
+        float mx[2] = {fmaxf(p[t][0], p[t][2]), fmaxf(p[t][1], p[t][3])};
+        auto grows = [&](int r) { return mx[r] > m[t][r] + FEW_RESCALE || (m[t][r] == -INFINITY && mx[r] > -INFINITY); };
+        if (__any_sync(FULL_MASK, grows(0) || grows(1))) {
+#pragma unroll
+          for (int r = 0; r < 2; r++) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(FULL_MASK, mx[r], d));
+            const bool grow = grows(r);
+            const float corr = grow ? few_ex2(m[t][r] - mx[r]) : 1.f;
+            if (grow) m[t][r] = mx[r];
+            l[t][r] *= corr;
+#pragma unroll
+            for (int e = 0; e < D / 16; e++) {
+              o[t][e][r] *= corr;
+              o[t][e][2 + r] *= corr;
+            }
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int key = g + 8 * (i >> 1);
-          bool see = key < n;
-          if (s >= cached && see) {
-            const int tok = min((blk * RB + 8 * t + 2 * c + (i & 1)) >> gl, x.n - 1);
-            see = causal ? key0 + key <= tok
-                         : (a.mask[(long long)(x.c0 + tok) * PRHS_TREE_WORDS + ((key0 + key) >> 5)] >> ((key0 + key) & 31)) & 1u;
-          }
-          if (!see) p[t][i] = -INFINITY;
+          const float ref = m[t][i & 1] == -INFINITY ? 0.f : m[t][i & 1];
+          p[t][i] = few_ex2(p[t][i] - ref);
+          l[t][i & 1] += p[t][i];
         }
+        pb[t][0] = transpose8(few_pack(p[t][0], p[t][1]));
+        pb[t][1] = transpose8(few_pack(p[t][2], p[t][3]));
       }
-      float mx[2] = {fmaxf(p[t][0], p[t][2]), fmaxf(p[t][1], p[t][3])};
-      auto grows = [&](int r) { return mx[r] > m[t][r] + FEW_RESCALE || (m[t][r] == -INFINITY && mx[r] > -INFINITY); };
-      if (__any_sync(FULL_MASK, grows(0) || grows(1))) {
+      // rows of V that do not exist hold whatever was there, and 0 * inf is not 0
+      const uint32_t keep0 = (2 * c < n ? 0xffffu : 0u) | (2 * c + 1 < n ? 0xffff0000u : 0u);
+      const uint32_t keep1 = (2 * c + 8 < n ? 0xffffu : 0u) | (2 * c + 9 < n ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(FULL_MASK, mx[r], d));
-          const bool grow = grows(r);
-          const float corr = grow ? few_ex2(m[t][r] - mx[r]) : 1.f;
-          if (grow) m[t][r] = mx[r];
-          l[t][r] *= corr;
-#pragma unroll
-          for (int e = 0; e < D / 16; e++) {
-            o[t][e][r] *= corr;
-            o[t][e][2 + r] *= corr;
-          }
+      for (int e = 0; e < D / 16; e++) {
+        uint32_t v[4];  // columns 16 e + g, + 8: keys 2 c, + 1; then keys + 8
+        ldm4_trans(v, v_at + stage * STAGE + e / 4 * SEG + (((e % 4 * 2 + vcol) ^ (vrow & 7)) << 4));
+        if (n < FEW_STEP) {
+          v[0] &= keep0;
+          v[1] &= keep0;
+          v[2] &= keep1;
+          v[3] &= keep1;
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float ref = m[t][i & 1] == -INFINITY ? 0.f : m[t][i & 1];
-        p[t][i] = few_ex2(p[t][i] - ref);
-        l[t][i & 1] += p[t][i];
+        for (int t = 0; t < NT; t++) mma16(o[t][e], v[0], v[1], v[2], v[3], pb[t][0], pb[t][1]);
       }
-      pb[t][0] = transpose8(few_pack(p[t][0], p[t][1]));
-      pb[t][1] = transpose8(few_pack(p[t][2], p[t][3]));
-    }
-    // rows of V that do not exist hold whatever was there, and 0 * inf is not 0
-    const uint32_t keep0 = (2 * c < n ? 0xffffu : 0u) | (2 * c + 1 < n ? 0xffff0000u : 0u);
-    const uint32_t keep1 = (2 * c + 8 < n ? 0xffffu : 0u) | (2 * c + 9 < n ? 0xffff0000u : 0u);
-#pragma unroll
-    for (int e = 0; e < D / 16; e++) {
-      uint32_t v[4];  // columns 16 e + g, + 8: keys 2 c, + 1; then keys + 8
-      ldm4_trans(v, v_at + stage * STAGE + e / 4 * SEG + (((e % 4 * 2 + vcol) ^ (vrow & 7)) << 4));
-      if (n < FEW_STEP) {
-        v[0] &= keep0;
-        v[1] &= keep0;
-        v[2] &= keep1;
-        v[3] &= keep1;
+      __syncwarp();  // (the stage has been read)
+      held--;
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
       }
-#pragma unroll
-      for (int t = 0; t < NT; t++) mma16(o[t][e], v[0], v[1], v[2], v[3], pb[t][0], pb[t][1]);
     }
-    __syncwarp();  // (the stage has been read)
-    held--;
-    if (++stage == STAGES) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-  if (dead) break;
+    if (dead) break;
 
-  // ---- its state, four columns a lane: row lane % 8 of each eight, columns 4 (lane / 8 + 4 k) .. ----
-  const int sr = lane & 7, sq = lane >> 3;
-  float2 ml[NT];
-  float4 y[NT][C4 / 4];
+    // ---- its state, four columns a lane: row lane % 8 of each eight, columns 4 (lane / 8 + 4 k) .. ----
+    const int sr = lane & 7, sq = lane >> 3;
+    float2 ml[NT];
+    float4 y[NT][C4 / 4];
 #pragma unroll
-  for (int t = 0; t < NT; t++) {
-    __syncwarp();
+    for (int t = 0; t < NT; t++) {
+      __syncwarp();
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
+      for (int r = 0; r < 2; r++) {
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[t][r] += __shfl_xor_sync(FULL_MASK, l[t][r], d);
+        for (int d = 4; d < 32; d <<= 1) l[t][r] += __shfl_xor_sync(FULL_MASK, l[t][r], d);
 #pragma unroll
-      for (int e = 0; e < D / 16; e++)
+        for (int e = 0; e < D / 16; e++)
 #pragma unroll
-        for (int h = 0; h < 2; h++)
-          reinterpret_cast<float*>(staged + (4 * e + 2 * h + g / 4) * 8 + 2 * c + r)[g % 4] = o[t][e][2 * h + r];
+          for (int h = 0; h < 2; h++)
+            reinterpret_cast<float*>(staged + (4 * e + 2 * h + g / 4) * 8 + 2 * c + r)[g % 4] = o[t][e][2 * h + r];
+      }
+      __syncwarp();
+      // (row 8 t + 2 c + r is in lanes c of any g)
+      const float m0 = __shfl_sync(FULL_MASK, m[t][0], sr >> 1), m1 = __shfl_sync(FULL_MASK, m[t][1], sr >> 1);
+      const float l0 = __shfl_sync(FULL_MASK, l[t][0], sr >> 1), l1 = __shfl_sync(FULL_MASK, l[t][1], sr >> 1);
+      ml[t] = sr & 1 ? make_float2(m1, l1) : make_float2(m0, l0);
+#pragma unroll
+      for (int k = 0; k < C4 / 4; k++) y[t][k] = staged[(sq + 4 * k) * 8 + sr];
     }
-    __syncwarp();
-    // (row 8 t + 2 c + r is in lanes c of any g)
-    const float m0 = __shfl_sync(FULL_MASK, m[t][0], sr >> 1), m1 = __shfl_sync(FULL_MASK, m[t][1], sr >> 1);
-    const float l0 = __shfl_sync(FULL_MASK, l[t][0], sr >> 1), l1 = __shfl_sync(FULL_MASK, l[t][1], sr >> 1);
-    ml[t] = sr & 1 ? make_float2(m1, l1) : make_float2(m0, l0);
-#pragma unroll
-    for (int k = 0; k < C4 / 4; k++) y[t][k] = staged[(sq + 4 * k) * 8 + sr];
-  }
 
-  // a unit cut by the run's end, or with a state against shared keys, is for the join; nothing
-  // here waits for what it writes (or for the launch in front)
-  const bool cut = cur.cuts > 1, result = !cut && x.part == 0;
-  float4* states = static_cast<float4*>(a.few_states);  // [2 warps][C4][RB], then (maximum, sum) [2 warps][RB]
-  float2* sums = reinterpret_cast<float2*>(states + (long long)2 * a.few_warps * C4 * RB);
-  const long long slot = 2ll * gw + (cur.first == gw);
+    // a unit cut by the run's end, or with a state against shared keys, is for the join; nothing
+    // here waits for what it writes (or for the launch in front)
+    const bool cut = cur.cuts > 1, result = !cut && x.part == 0;
+    float4* states = static_cast<float4*>(a.few_states);  // [2 warps][C4][RB], then (maximum, sum) [2 warps][RB]
+    float2* sums = reinterpret_cast<float2*>(states + (long long)2 * a.few_warps * C4 * RB);
+    const long long slot = 2ll * gw + (cur.first == gw);
 #pragma unroll
-  for (int t = 0; t < NT; t++) {
-    const int r = blk * RB + 8 * t + sr, tok = x.c0 + (r >> gl), h = r & (G - 1);
-    if (8 * t + sr >= rows) continue;
-    const long long prow = part_row<__nv_bfloat16>(a, 2, tok, kvh, h, gl), orow = (long long)tok * kv.Hq + (kvh << gl) + h;
-    const float inv = tree_inv(ml[t].y);
+    for (int t = 0; t < NT; t++) {
+      const int r = blk * RB + 8 * t + sr, tok = x.c0 + (r >> gl), h = r & (G - 1);
+      if (8 * t + sr >= rows) continue;
+      const long long prow = part_row<__nv_bfloat16>(a, 2, tok, kvh, h, gl), orow = (long long)tok * kv.Hq + (kvh << gl) + h;
+      const float inv = tree_inv(ml[t].y);
 #pragma unroll
-    for (int k = 0; k < C4 / 4; k++) {
-      const int c4 = sq + 4 * k;
-      if (result)
-        tree_put(static_cast<__nv_bfloat16*>(a.out) + orow * D + c4 * 4,
-                 make_float4(y[t][k].x * inv, y[t][k].y * inv, y[t][k].z * inv, y[t][k].w * inv));
-      else if (cut)
-        __stcg(states + (slot * C4 + c4) * RB + 8 * t + sr, y[t][k]);
-      else
-        __stcg(part_at<__nv_bfloat16, D>(a, 2, tok, kvh, h, c4, gl), y[t][k]);
+      for (int k = 0; k < C4 / 4; k++) {
+        const int c4 = sq + 4 * k;
+        if (result)
+          tree_put(static_cast<__nv_bfloat16*>(a.out) + orow * D + c4 * 4,
+                   make_float4(y[t][k].x * inv, y[t][k].y * inv, y[t][k].z * inv, y[t][k].w * inv));
+        else if (cut)
+          __stcg(states + (slot * C4 + c4) * RB + 8 * t + sr, y[t][k]);
+        else
+          __stcg(part_at<__nv_bfloat16, D>(a, 2, tok, kvh, h, c4, gl), y[t][k]);
+      }
+      if (sq != 0) continue;
+      if (result) a.lse[orow] = tree_lse(ml[t].x, ml[t].y);
+      else if (cut) __stcg(sums + slot * RB + 8 * t + sr, ml[t]);
+      else __stcg(a.part_ml + prow, ml[t]);
+      // (warps that begin no step of a unit do not know its first)
+      if (cur.first == gw) a.where[prow] = make_int2(cur.first, cur.cuts);
     }
-    if (sq != 0) continue;
-    if (result) a.lse[orow] = tree_lse(ml[t].x, ml[t].y);
-    else if (cut) __stcg(sums + slot * RB + 8 * t + sr, ml[t]);
-    else __stcg(a.part_ml + prow, ml[t]);
-    // (warps that begin no step of a unit do not know its first)
-    if (cur.first == gw) a.where[prow] = make_int2(cur.first, cur.cuts);
-  }
   }
   if (dead)  // nothing may still be in flight when the CTA ends
     for (int i = 0; i < held; i++) {
