@@ -15,7 +15,10 @@
 // by the launch behind this one (shared.cu).
 //
 // Bound: HBM (the keys, once), and latency: lengths, page numbers, keys are dependent
-// reads before a warp's first product.
+// reads before a warp's first product. 32 sequences of up to 8 drafted tokens on 2048 shared
+// and up to 2K own keys, 32 heads, 606 MB: this launch 104 to 114 us, 5.4 to 5.8 TB/s; with
+// every unit as tiles 152. The same steps with the keys loaded into registers 120, by
+// 16-byte asynchronous copies 173.
 #pragma once
 
 #include "tree_join.cuh"

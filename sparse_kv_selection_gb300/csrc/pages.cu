@@ -18,8 +18,11 @@
 // The entries of the table are tasks of 128 columns of a row, a warp's tasks
 // consecutive, so that a prefix over the warps' counts gives every freed page its
 // place. One cluster of CTAs, or for large tables all SMs (a cooperative launch).
-// Bound: latency, a few dependent passes through L2 with a barrier between two; atomics on
-// shared pages for large calls.
+// Bound: latency, six or seven dependent passes through L2 with a barrier between two, 1 us
+// each for a cluster, 2 for the grid; for large calls atomics on shared pages too. 64 beams
+// of 3.7 to 7.9K keys on 16-key pages trade places in 15.5 us, 512 rows of up to 2173 pages in
+// 40 (a cluster alone: 178; bytes 1.4), one row of 4096 positions is compacted in 16 to 18, 117
+// rows of up to 19.6K in 31 (53 with one cluster).
 #include <cooperative_groups.h>
 
 #include "pages.h"

@@ -110,8 +110,8 @@ prhs_status prhs_copy_rows(const prhs_kv* kv, const prhs_kv* source, int n, cons
     return abi_fail(PRHS_EINVAL, "copy_rows: the caches differ in element type, KV heads or d");
   if (n < 0) return abi_fail(PRHS_EINVAL, "copy_rows: n must be >= 0");
   if (n > 0 && (!src || !dst)) return abi_fail(PRHS_EINVAL, "copy_rows: src and dst must be non-null");
-  // 32-bit counts of thread blocks: 2048 16-byte pieces each
-  if ((long long)n * 2 * kv->Hkv * kv->d * (kv->dtype == PRHS_BF16 ? 2 : 4) / 16 >= (1ll << 41))
+  // 32-bit counts of thread blocks: 1024 16-byte pieces each
+  if ((long long)n * 2 * kv->Hkv * kv->d * (kv->dtype == PRHS_BF16 ? 2 : 4) / 16 >= (1ll << 40))
     return abi_fail(PRHS_EUNSUPPORTED, "copy_rows: too many rows for one call");
   unsigned* err = nullptr;
   int sms = 0;

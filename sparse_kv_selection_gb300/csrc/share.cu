@@ -9,7 +9,9 @@
 //
 // One cluster of CTAs: a warp compares two rows, 512 entries at a time; then one
 // CTA forms the groups, a thread for each run of rows between two that share
-// nothing, and writes them. Bound: latency (the tables are read twice, from L2).
+// nothing, and writes them. Bound: latency (lengths, tables, the groups' chain; the tables
+// are read twice, from L2): 128 rows in 8 groups of up to 5072 keys on 16-key pages 8 to
+// 11 us, 8 rows 7.6.
 #include <cooperative_groups.h>
 
 #include "pages.h"
