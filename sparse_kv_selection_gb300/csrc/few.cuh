@@ -76,36 +76,24 @@ __device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// One sequence's share of the list of steps, KV head by KV head: units of RB query
-// rows, each of as many steps as the longest (causal ones that see fewer new tokens
-// leave the last empty).
+// One sequence's share of the list of steps: a unit for each KV head, of steps over the
+// cached keys, then the new tokens.
 struct FewSeq {
   TreeItem x;
-  int blocks, steps;  // units of a KV head, steps of a unit (FEW_REST with them)
+  int steps;  // of a unit (FEW_REST with them; 0: not here)
 };
-template <int RB>
-__device__ __forceinline__ int few_steps(const TreeLaunch& a, const TreeItem& x, int gl, int blk, int* fresh) {
-  const int end = min(x.n << gl, (blk + 1) * RB);  // (causal: new tokens up to the unit's last one)
-  *fresh = a.mask == nullptr ? ((end - 1) >> gl) + 1 : x.n;
-  return (x.t + FEW_STEP - 1) / FEW_STEP + (*fresh + FEW_STEP - 1) / FEW_STEP;
+__device__ __forceinline__ int few_steps(const TreeItem& x) {
+  return (x.t + FEW_STEP - 1) / FEW_STEP + (x.n + FEW_STEP - 1) / FEW_STEP;
 }
-template <int RB>
-__device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, const TreeItem& x, int gl) {
-  FewSeq s;
-  s.x = x;
-  s.blocks = s.steps = 0;
-  if (s.x.part == 1 || !few_item(a, s.x.n, s.x.t)) return s;
-  s.blocks = ((s.x.n << gl) + RB - 1) / RB;
-  int fresh;
-  if (s.blocks > 0) s.steps = few_steps<RB>(a, s.x, gl, s.blocks - 1, &fresh) + FEW_REST;
-  return s;
+__device__ __forceinline__ FewSeq few_seq(const TreeLaunch& a, const TreeItem& x) {
+  return {x, x.part == 1 || x.n == 0 || !few_item(a, x.n, x.t) ? 0 : few_steps(x) + FEW_REST};
 }
 
 // A unit's steps in a warp's run of the list.
 struct FewTask {
   TreeItem x;
-  int kvh, blk, s0, s1;    // KV head, unit, steps here
-  int cached, fresh;       // steps over the cache, new tokens that the unit sees
+  int kvh, s0, s1;         // KV head, steps here
+  int cached;              // steps over the cache
   int first, cuts;         // the warp that begins the unit, the warps that have steps of it
   int window, page;        // pages of steps window .. window + 31, one a lane (not looked at before they are used)
   bool some;               // (none: the run is done)
@@ -159,7 +147,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
   uint8_t* next_q = few_smem + warp * WARP_SMEM + few_q(D);
   const int* table = reinterpret_cast<const int*>(few_smem + FEW_WARPS * WARP_SMEM);
   auto seq_at = [&](int b) {
-    if (kv.B > FEW_TABLE) return few_seq<RB>(a, tree_item<true>(a, 2 * b + 1, true), gl);
+    if (kv.B > FEW_TABLE) return few_seq(a, tree_item<true>(a, 2 * b + 1, true));
     TreeItem x;
     x.b = b;
     x.base = table[b];
@@ -167,7 +155,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     x.c0 = table[2 * FEW_TABLE + b];
     x.n = table[3 * FEW_TABLE + b];
     x.part = table[4 * FEW_TABLE + b];
-    return few_seq<RB>(a, x, gl);
+    return few_seq(a, x);
   };
   auto look_up = [&](FewTask& t, int window) {
     t.window = window;
@@ -178,7 +166,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
   auto fetch = [&]() {  // at pos, which moves on
     FewTask t = {};
     FewSeq s = {};
-    int unit = 0, in = 0;
+    int kvh = 0, in = 0;
     for (;; pos += s.steps - in) {
       if (pos >= end) return t;
       int lo = 0, hi = 383;  // the first thread whose items end behind it
@@ -188,24 +176,23 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
       }
       int off = pos - (lo > 0 ? aux.steps_to[lo - 1] : 0), b = (lo * per_t) >> 1;  // (items 2 b + 1 have steps)
       s = seq_at(b);
-      for (int x; off >= (x = kv.Hkv * s.blocks * s.steps);) {
+      for (int x; off >= (x = kv.Hkv * s.steps);) {
         off -= x;
         s = seq_at(++b);
       }
-      unit = off / s.steps;
-      in = off - unit * s.steps;
+      kvh = off / s.steps;
+      in = off - kvh * s.steps;
       if (in < s.steps - FEW_REST) break;
     }
     const int start = pos - in;
     t.x = s.x;
-    t.kvh = unit / s.blocks;
-    t.blk = unit - t.kvh * s.blocks;
+    t.kvh = kvh;
     const int taken = min(s.steps - in, end - pos);  // of the list
     pos += taken;
     t.some = true;
     t.first = start / run;
     t.cuts = (start + s.steps - FEW_REST - 1) / run - t.first + 1;
-    const int all = few_steps<RB>(a, t.x, gl, t.blk, &t.fresh);
+    const int all = s.steps - FEW_REST;
     t.cached = (t.x.t + FEW_STEP - 1) / FEW_STEP;
     t.s0 = min(in, all);
     t.s1 = min(in + taken, all);
@@ -214,7 +201,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < RB * D / 8 / 32; i++) {
-      const int y = lane + 32 * i, r = t.blk * RB + y / (D / 8), piece = y % (D / 8);
+      const int y = lane + 32 * i, r = y / (D / 8), piece = y % (D / 8);
       const bool have = r < t.x.n << gl;
       const __nv_bfloat16* from =
           static_cast<const __nv_bfloat16*>(a.q) +
@@ -237,7 +224,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
       if (lane == 0) raise_error(kv.err, PRHS_DEV_BAD_BLOCK);
       row = -1;
     }
-    const int n = is_new ? min(FEW_STEP, t.fresh - j) : row < 0 ? 0 : min(FEW_STEP, t.x.t - s * FEW_STEP);
+    const int n = is_new ? min(FEW_STEP, t.x.n - j) : row < 0 ? 0 : min(FEW_STEP, t.x.t - s * FEW_STEP);
     counts = (counts & ~(31 << 5 * stage)) | n << 5 * stage;
     if (lane == 0) {
       mbar_arrive_expect_tx(&full[warp][stage], STAGE);
@@ -261,8 +248,8 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     in_next = false;
     bool known = false;
     const TreeItem x = cur.x;
-    const int blk = cur.blk, kvh = cur.kvh;
-    const int rows = min(RB, (x.n << gl) - blk * RB), cached = cur.cached;
+    const int kvh = cur.kvh;
+    const int rows = x.n << gl, cached = cur.cached;
     // Q as the products take it: rows g of each eight, columns 16 j + 2 c and 16 j + 8 + 2 c
     uint32_t q[NT][D / 16][2];
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -329,7 +316,7 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
             const int key = g + 8 * (i >> 1);
             bool see = key < n;
             if (s >= cached && see) {
-              const int tok = min((blk * RB + 8 * t + 2 * c + (i & 1)) >> gl, x.n - 1);
+              const int tok = min((8 * t + 2 * c + (i & 1)) >> gl, x.n - 1);
               see = causal ? key0 + key <= tok
                            : (a.mask[(long long)(x.c0 + tok) * PRHS_TREE_WORDS + ((key0 + key) >> 5)] >> ((key0 + key) & 31)) & 1u;
             }
@@ -422,8 +409,8 @@ __device__ __forceinline__ void few_role(const TreeLaunch& a, const CUtensorMap&
     const long long slot = 2ll * gw + (cur.first == gw);
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const int r = blk * RB + 8 * t + sr, tok = x.c0 + (r >> gl), h = r & (G - 1);
-      if (8 * t + sr >= rows) continue;
+      const int r = 8 * t + sr, tok = x.c0 + (r >> gl), h = r & (G - 1);
+      if (r >= rows) continue;
       const long long prow = part_row<__nv_bfloat16>(a, 2, tok, kvh, h, gl), orow = (long long)tok * kv.Hq + (kvh << gl) + h;
       const float inv = tree_inv(ml[t].y);
 #pragma unroll

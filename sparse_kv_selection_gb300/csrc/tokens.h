@@ -89,14 +89,16 @@ struct TreeLaunch {
   int few_warps;     // warps that it may have
   void* few_states;  // [2 few_warps] states of units that several warps share, two a warp
 };
-// Whether a sequence's own t keys with its n tokens go to that part: at most two units
-// of few_rows query rows a KV head, which read the keys each, and few keys. (24 prompts of
-// 20 to 63 tokens, 4 heads a KV head, whose units are six and more: 158 us with those, 135
-// without.)
-// (at most 16384 rows of KV heads: 2^26 steps)
+// Whether a sequence's own t keys with its n tokens go to that part: few keys, and one
+// unit of few_rows query rows a KV head. Two units read the keys twice: 386 sequences of 10
+// tokens, two heads a KV head, up to 1360 keys, take 201 us there and 123 as tiles, 16 of 17 to
+// 20 rows on up to 16K keys 679 and 351; only next to no own keys are better off (44 sequences
+// of 9 tokens that share all but 6 keys: 41 and 64), and a few such among longer ones hold the
+// others up (128 sequences of up to 3K keys 166 us, 187 to 221 with those below 256 there).
+// (At most 16384 rows of KV heads: 2^26 steps.)
 constexpr int FEW_KEYS = 32768;
 __device__ __forceinline__ bool few_item(const TreeLaunch& a, int n, int t) {
-  return t + n <= FEW_KEYS && (long long)n * (a.kv.Hq / a.kv.Hkv) <= 2 * a.few_rows;
+  return t + n <= FEW_KEYS && (long long)n * (a.kv.Hq / a.kv.Hkv) <= a.few_rows;
 }
 // fp32: two launches (three with shared keys), all but the last counted by the callee; ws
 // holds tree_workspace(kv, max_new, shared, sms) bytes.

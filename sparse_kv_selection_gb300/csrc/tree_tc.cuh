@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (s.part == 1) grouped += s.n;
       cost += (long long)kv.Hkv * s.tiles * ((s.n << gl) > TT ? TC_COST_2 : TC_COST_1);
       if (e & 1) {
-        const FewSeq f = few_seq<8 * NT1>(a, tree_item<true>(a, e, true), gl);
-        steps += kv.Hkv * f.blocks * f.steps;
+        const FewSeq f = few_seq(a, tree_item<true>(a, e, true));
+        steps += kv.Hkv * f.steps;
       }
     }
   }
