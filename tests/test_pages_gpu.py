@@ -213,6 +213,40 @@ def test_fork_refusals():
     refused(s, [1, 1, 0, 0] + [-1] * 4, DEV_CAPACITY)
 
 
+@pytest.mark.parametrize("what", ["fork_seqs", "compact_seqs"])
+def test_large_tables_from_a_graph(what):
+    """A table that all SMs take: captured once, replayed with other arguments on what it left."""
+    import sparse_kv_selection_gb300 as S
+    rng = np.random.default_rng(12)
+    s = make_state(rng, 8, (8, 8), (17000, 18000), (1, 90), 16)
+    assert len(s.lens) * s.table.shape[1] > 1 << 16
+    d, cap = Device(s), 16 if what == "fork_seqs" else 12000
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        src, dst = (torch.full((64, cap), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+        args = [i32(list(range(64)))] if what == "fork_seqs" else [torch.zeros(64, cap, dtype=torch.int32, device="cuda"), i32([-1] * 64)]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            getattr(S, what)(d.kv, *args, src, dst, d.ws, **d.pages)
+        for i in range(3):
+            if what == "fork_seqs":
+                new = [np.array(random_parents(rng, 64, 0.3, 0.1, within=8))]
+            else:
+                m = np.minimum(s.lens, rng.integers(0, cap, 64))
+                keep = np.zeros((64, cap), int)
+                for b in range(64):
+                    keep[b, :m[b]] = np.sort(rng.choice(s.lens[b], m[b], replace=False)) if s.lens[b] else []
+                new = [keep, m]
+            for x, y in zip(args, new):
+                x.copy_(i32(y))
+            g.replay()
+            stream.synchronize()
+            assert S.last_error() == 0
+            s, want_src, want_dst = fork_ref(s, *new) if what == "fork_seqs" else compact_ref(s, *new)
+            same_state(d.state(), s)
+            assert np.array_equal(src.cpu().numpy(), want_src) and np.array_equal(dst.cpu().numpy(), want_dst)
+
+
 def random_keep(rng, s, share, leave=0.1):
     """Kept positions: leading ones, some of the middle, the last ones."""
     m, rows = [], []

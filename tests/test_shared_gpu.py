@@ -221,6 +221,43 @@ def test_entries_that_do_not_fit(dtype):
     b.check(out)
 
 
+def test_batches_on_streams_of_their_own():
+    """Four batches at once, each with its own workspace, eager and from graphs."""
+    import sparse_kv_selection_gb300 as S
+    sizes = [([(16, 4096)], (0, 200), (1, 1), 8, 8, 128, BF16, 16), ([(40, 700), (3, 64)], (0, 900), (0, 6), 16, 4, 64, BF16, 64),
+             ([(60, 500)], (0, 900), (1, 1), 8, 2, 64, F32, 16), ([(4, 1000)] * 3, (0, 300), (30, 60), 8, 2, 128, F32, 48)]
+    batches = [Batch(*x, seed=20 + i) for i, x in enumerate(sizes)]
+    want = [b.run() for b in batches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    keep, graphs = [], []
+    for b, w, st in zip(batches, want, streams):
+        with torch.cuda.stream(st):
+            ws = S.make_shared_workspace(b.c.kv, b.T, max(b.n))
+            out = tuple(torch.full_like(x, 7.0) for x in w)
+            cu, share = i32(b.cu), i32(b.share)
+            call = lambda b=b, cu=cu, share=share, out=out, ws=ws: S.shared_attn(  # noqa: E731
+                b.c.kv, b.q, b.kn, b.vn, b.scale, cu, max(b.n), share, out[0], out[1], ws)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                call()
+        keep.append((out, call))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for how in ("eager", "graph"):
+        for out, _ in keep:
+            out[0].fill_(7.0), out[1].fill_(7.0)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for st, (_, call), g in zip(streams, keep, graphs):
+                with torch.cuda.stream(st):
+                    call() if how == "eager" else g.replay()
+        torch.cuda.synchronize()
+        assert S.last_error() == 0
+        for (out, _), w in zip(keep, want):
+            assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
+
+
 @pytest.mark.parametrize("dtype,Hq", [(BF16, 2), (F32, 2), (F32, 16)])
 def test_overlapping_groups_refused(dtype, Hq):
     """Every row the first of a group that reaches to the batch's end: more tokens than there are."""
