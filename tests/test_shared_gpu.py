@@ -258,6 +258,31 @@ def test_batches_on_streams_of_their_own():
             assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_behind_32_bits(dtype):
+    """The pages at the end of a pool of more than 2^31 elements; rows copied there and from there."""
+    import sparse_kv_selection_gb300 as S
+    b = Batch([(20, 300), (1, 0), (3, 64)], (0, 400), (1, 9), 4, 2, 64, dtype, 16, seed=30)
+    want, c = b.run(), b.c
+    pages, each = c.k.shape[0], c.k[0].numel()
+    behind = (1 << 31) // each + 5
+    k, v = (torch.empty(behind + pages, *c.k.shape[1:], dtype=dtype, device="cuda") for _ in range(2))
+    k[behind:], v[behind:] = c.k, c.v
+    table = torch.where(c.kv.block_table >= 0, c.kv.block_table + behind, -1)
+    b.c.kv = S.KVCache(k, v, c.kv.seq_lens, c.Hq, block_table=table)
+    got = b.run()
+    assert S.last_error() == 0 and torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    slots = torch.arange(pages * 16, dtype=torch.int32, device="cuda")
+    S.copy_rows(b.c.kv, slots + behind * 16, slots)
+    bits = lambda x: x.contiguous().view(torch.int16 if dtype == BF16 else torch.int32)  # noqa: E731  (rows behind the ends are NaN)
+    assert torch.equal(bits(k[:pages]), bits(c.k)) and torch.equal(bits(v[:pages]), bits(c.v))
+    back = torch.flip(slots, (0,)) + behind * 16
+    S.copy_rows(b.c.kv, slots, back)
+    assert S.last_error() == 0
+    flat = lambda x: bits(x.transpose(1, 2).reshape(pages * 16, -1))  # noqa: E731
+    assert torch.equal(flat(k[behind:]), flat(c.k).flip(0)) and torch.equal(flat(v[behind:]), flat(c.v).flip(0))
+
+
 @pytest.mark.parametrize("dtype,Hq", [(BF16, 2), (F32, 2), (F32, 16)])
 def test_overlapping_groups_refused(dtype, Hq):
     """Every row the first of a group that reaches to the batch's end: more tokens than there are."""
