@@ -1139,7 +1139,9 @@ static cudaError_t tc_go(const TcLaunch& p, const CUtensorMap* maps, int sms, cu
   static int smem_set[SMEM_DEVICES];
   cudaError_t e = allow_smem(k, S::SMEM, smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3(sms), dim3(TC_THREADS), S::SMEM, st, p.a.kv.pdl, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
+  // (with shared keys always early: calls back to back 127.7 -> 125.0 us for 913 prompt tokens, 115 -> 113.3
+  // for 131072 keys)
+  e = launch_pdl(k, dim3(sms), dim3(TC_THREADS), S::SMEM, st, NT > 0 || p.a.kv.pdl, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
                  maps[6], p);
   if (e == cudaSuccess) abi_count_launch();
   return e;
