@@ -225,13 +225,13 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Dynamic shared memory above the default 48 KB allowed for `kernel` on the
-// current device; `done` (one per kernel, zero at load) keeps the largest size
+// Dynamic shared memory beyond what a launch has unasked (48 KB less the kernel's static
+// arrays, of at most 24 KB) allowed for `kernel` on the current device; `done` (one per kernel, zero at load) keeps the largest size
 // set on each device, so that a call sets it once and not at every launch.
 constexpr int SMEM_DEVICES = 64;
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t smem, int (&done)[SMEM_DEVICES]) {
-  if (smem <= 48 * 1024) return cudaSuccess;
+  if (smem <= 24 * 1024) return cudaSuccess;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -326,6 +326,26 @@ def test_largest_batch():
     check(s, "compact_seqs", random_keep(rng, s, 0.6))
 
 
+@pytest.mark.parametrize("B", [3800, 4090, 4096, 6130, 6144, 6200])
+def test_batches_around_48_kb_of_shared_memory(B):
+    """Arrays of a number or three a row that just fit, or just do not, what a launch has unasked."""
+    import sparse_kv_selection_gb300 as S
+    rng = np.random.default_rng(B)
+    s = make_state(rng, B // 2, (2, 2), (16, 40), (0, 9), 16, extra=0)
+    d = Device(s)
+    parent = random_parents(rng, B, 0.5, 0.1, within=2)
+    want, src, dst = fork_ref(s, parent)
+    got, gs, gd, bits = call(d, "fork_seqs", [parent], 16, True)
+    assert bits == 0
+    same_state(got, want)
+    assert np.array_equal(gs, src) and np.array_equal(gd, dst)
+    shared = torch.full((B, 4), -9, dtype=torch.int32, device="cuda")
+    n = np.ones(B, int)
+    S.find_shared(d.kv, i32(np.arange(B + 1)), shared, min_keys=1)
+    assert S.last_error() == 0
+    assert np.array_equal(shared.cpu().numpy(), find_ref(want.table, want.lens, n, 16, 1, 1))
+
+
 # --------------------------------------------------------------------------- #
 # row copies
 # --------------------------------------------------------------------------- #
