@@ -20,9 +20,10 @@
 // place. One cluster of CTAs, or for large tables all SMs (a cooperative launch).
 // Bound: latency, six or seven dependent passes through L2 with a barrier between two, 1 us
 // each for a cluster, 2 for the grid; for large calls atomics on shared pages too. 64 beams
-// of 3.7 to 7.9K keys on 16-key pages trade places in 15.5 us, 512 rows of up to 2173 pages in
-// 40 (a cluster alone: 178; bytes 1.4), one row of 4096 positions is compacted in 16 to 18, 117
-// rows of up to 19.6K in 31 (53 with one cluster).
+// of 3.7 to 7.9K keys on 16-key pages trade places in 14.4 us (plans, sums and error bits through
+// L2 instead of the CTAs' shared memory, new columns read back: 15.6), 512 rows of up to 2173
+// pages in 41 (a cluster alone: 178; bytes 1.4), one row of 4096 positions is compacted in 14.5,
+// 117 rows of up to 19.6K in 29 (53 with one cluster).
 #include <cooperative_groups.h>
 
 #include "pages.h"
@@ -39,6 +40,7 @@ constexpr int PG_COLS = 4;               // columns a lane (16: a pass's code is
 constexpr int PG_TASK = 32 * PG_COLS;    // columns of a task
 constexpr long long PG_ONE_CLUSTER = 1 << 16;  // entries up to which one cluster takes a call
 constexpr int PG_KEEP = 128;             // kept positions a warp checks at a time
+constexpr int PG_LOCAL = PG_THREADS;     // rows up to which every CTA of a cluster keeps all plans itself
 
 // Exclusive prefix of x over the block's threads, the sum into *total.
 __device__ __forceinline__ int block_scan(int x, int* wsum, int* total) {
@@ -80,11 +82,15 @@ __device__ __forceinline__ void copy_ints(int32_t* dst, const int32_t* src, long
 }
 
 template <bool FORK, bool GRID>
-__global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant__ PagesLaunch a) {
+__global__ void __launch_bounds__(PG_THREADS, 1) pages_kernel(const __grid_constant__ PagesLaunch a) {
   extern __shared__ int pg_smem[];
   __shared__ int wsum[PG_WARPS];
   __shared__ int sh_most, sh_base[PG_WARPS];
   __shared__ unsigned sh_bits;
+  // A cluster's CTAs write these into each other's: what the others would read through L2, at 0.7 us
+  __shared__ __align__(16) PageRow sh_rows[GRID ? 1 : PG_LOCAL];
+  __shared__ int sh_sums[GRID ? 1 : PG_CLUSTER * PG_WARPS];
+  __shared__ unsigned sh_late;
   const int rank = blockIdx.x, ranks = gridDim.x;
   auto meet = [] {
     if constexpr (GRID) cg::this_grid().sync();
@@ -98,15 +104,17 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
   const int32_t* table = kv.block_table;
   int* first = pg_smem;     // fork, [B]: the first child of each row that takes a part of its last page
   int* count = first + B;   //       [B]: its children
-  int* late = a.sums + gws;
+  int* late = a.sums + gws;  // (all SMs)
+  const bool local = !GRID && B <= PG_LOCAL;
 
   pdl_wait();
   pdl_trigger();
   if (tid == 0) {
     sh_bits = 0;
+    sh_late = 0;
     sh_most = 0;
   }
-  if (gt == 0) *late = 0;
+  if (GRID && gt == 0) *late = 0;
   if (a.shares_out != a.shares) copy_ints(a.shares_out, a.shares, kv.num_blocks, gt, gts);
   if (a.free_out != a.free_pages) copy_ints(a.free_out, a.free_pages, a.n_free, gt, gts);
   if (a.table_out != table) copy_ints(a.table_out, table, (long long)B * M, gt, gts);
@@ -117,6 +125,12 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
     for (int b = tid; b < B; b += PG_THREADS) {
       first[b] = B;
       count[b] = 0;
+      // (a row's last page and its holders beside its parent, not behind it)
+      const int t = kv.seq_lens[b];
+      if (t > 0 && t <= kv.t_max) {
+        const int last = table[(long long)b * M + (t - 1) / page];
+        if ((unsigned)last < (unsigned)kv.num_blocks) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.shares + last));
+      }
     }
     __syncthreads();
     for (int b = tid; b < B; b += PG_THREADS) {
@@ -221,14 +235,23 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
     if (per > 1) r0 = plan_row(b, ignored);
     r0.taken = need;
     need += r0.blocks - r0.keep;
-    if (b % ranks == rank) a.rows[b] = r0;
+    if (local) sh_rows[b] = r0;
+    else if (b % ranks == rank) a.rows[b] = r0;
   }
   __syncthreads();
   bits = sh_bits;
   most = min(sh_most, M);
   if (bits == 0 && (head < 0 || head > a.n_free)) bits = PRHS_DEV_BAD_LEN;
   if (bits == 0 && taken > a.n_free - head) bits = PRHS_DEV_CAPACITY;
-  meet();
+  // Counts change when all CTAs have read what they plan by; with the plans at hand, what comes
+  // before that does not wait.
+  if constexpr (GRID) meet();
+  else asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  auto planned = [] {
+    if constexpr (!GRID) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  if (!local) planned();
+  auto row_of = [&](int b) -> PageRow { return local ? sh_rows[GRID ? 0 : b] : a.rows[b]; };
 
   const int chunks = (most + PG_TASK - 1) / PG_TASK;
   const long long tasks = (long long)B * chunks;
@@ -242,7 +265,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
     Task t;
     t.b = (int)(x / chunks);
     t.j0 = (int)(x - (long long)t.b * chunks) * PG_TASK + lane;
-    t.r = a.rows[t.b];
+    t.r = row_of(t.b);
 #pragma unroll
     for (int k = 0; k < PG_COLS; k++) {
       const int j = t.j0 + 32 * k;
@@ -259,7 +282,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
     for (long long x = x0; x < x1; x++) {
       Task next;
       if (x + 1 < x1) next = ask(x + 1);
-      act(t);
+      act(t, x == x0);
       t = next;
     }
   };
@@ -299,7 +322,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
     const int per_row = (a.cap + PG_TASK - 1) / PG_TASK;
     for (long long x = gw; x < (long long)B * per_row; x += gws) {
       const int b = (int)(x / per_row), c0 = (int)(x - (long long)b * per_row) * PG_TASK + lane;
-      const PageRow r = a.rows[b];
+      const PageRow r = row_of(b);
       int k[PG_COLS], from[PG_COLS], to[PG_COLS];
 #pragma unroll
       for (int i = 0; i < PG_COLS; i++) {
@@ -329,9 +352,12 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
   };
   const bool early = bits != 0;  // refused before any count changed
   copies(early);
+  if (local) planned();
+  int kept[PG_COLS] = {};  // the first task's new columns, of which it frees `freed`
+  unsigned freed = 0;
   int back = 0, before = 0, given = 0;  // pages that this warp, the warps before it, all warps give back
   if (!early) {
-    sweep([&](const Task& t) {
+    sweep([&](const Task& t, bool own_task) {
       unsigned bad = counts(t, 1);
       int p[PG_COLS];
 #pragma unroll
@@ -347,12 +373,17 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
         const int j = t.j0 + 32 * k;
         if (!changes(t, k)) continue;
         if (j >= t.r.keep && j < t.r.blocks && !in_pool(p[k])) bad |= PRHS_DEV_BAD_BLOCK;
-        a.stage[(long long)t.b * M + j] = p[k];
+        if (own_task) kept[k] = p[k];
+        else a.stage[(long long)t.b * M + j] = p[k];
       }
-      if (bad != 0) atomicOr(late, (int)bad);
+      if (bad != 0) {
+        if constexpr (GRID) atomicOr(late, (int)bad);
+        else
+          for (int r = 0; r < ranks; r++) atomicOr(cg::this_cluster().map_shared_rank(&sh_late, r), bad);
+      }
     });
     meet();
-    bits = *(volatile unsigned*)late;
+    bits = GRID ? *(volatile unsigned*)late : *(volatile unsigned*)&sh_late;
   }
 
   // ---- the pages that nobody holds now, each by its first release ----
@@ -362,7 +393,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
       for (int k = 0; k < PG_COLS; k++) c[k] = t.p[k] >= 0 ? __ldcg(&a.shares_out[t.p[k]]) : 0;
     };
     auto frees = [&](const Task& t, int k, int count) { return count == INT32_MIN + t.b * M + t.j0 + 32 * k; };
-    sweep([&](const Task& t) {
+    sweep([&](const Task& t, bool) {
       int c[PG_COLS];
       held_by(t, c);
 #pragma unroll
@@ -370,29 +401,38 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
         if (c[k] < 0) atomicMin(&a.shares_out[t.p[k]], INT32_MIN + t.b * M + t.j0 + 32 * k);
     });
     meet();
-    sweep([&](const Task& t) {
+    sweep([&](const Task& t, bool own_task) {
       int c[PG_COLS];
       held_by(t, c);
 #pragma unroll
-      for (int k = 0; k < PG_COLS; k++) back += frees(t, k, c[k]);
+      for (int k = 0; k < PG_COLS; k++) {
+        const bool mine = frees(t, k, c[k]);
+        back += mine;
+        if (own_task && mine) freed |= 1u << k;
+      }
     });
     back = __reduce_add_sync(FULL_MASK, back);
-    if (lane == 0) a.sums[gw] = back;
+    if constexpr (GRID) {
+      if (lane == 0) a.sums[gw] = back;
+    } else if (lane < ranks) {
+      cg::this_cluster().map_shared_rank(sh_sums, lane)[gw] = back;
+    }
     meet();
+    auto given_by = [&](int w) { return GRID ? __ldcg(&a.sums[w]) : sh_sums[GRID ? 0 : w]; };
     const int share = (gws + PG_THREADS - 1) / PG_THREADS, w0 = min(gws, tid * share), w1 = min(gws, w0 + share);
     int sum = 0;
-    for (int w = w0; w < w1; w++) sum += __ldcg(&a.sums[w]);
+    for (int w = w0; w < w1; w++) sum += given_by(w);
     sum = block_scan(sum, wsum, &given);
     for (int w = w0; w < w1; w++) {
       if (w / PG_WARPS == rank) sh_base[w % PG_WARPS] = sum;
-      sum += __ldcg(&a.sums[w]);
+      sum += given_by(w);
     }
     __syncthreads();
     before = sh_base[warp];
     const int new_head = head + taken - given;
     if (new_head < 0) {  // no room in front of the free ones
       bits = PRHS_DEV_CAPACITY;
-      sweep([&](const Task& t) {
+      sweep([&](const Task& t, bool) {
         int c[PG_COLS];
         held_by(t, c);
 #pragma unroll
@@ -402,17 +442,17 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
       meet();
     } else {
       int at = new_head + before;
-      sweep([&](const Task& t) {
+      sweep([&](const Task& t, bool own_task) {
         int p[PG_COLS];
 #pragma unroll
         for (int k = 0; k < PG_COLS; k++)
-          if (changes(t, k)) p[k] = a.stage[(long long)t.b * M + t.j0 + 32 * k];
+          if (changes(t, k)) p[k] = own_task ? kept[k] : a.stage[(long long)t.b * M + t.j0 + 32 * k];
         if (back > 0) {
           int c[PG_COLS];
-          held_by(t, c);
+          if (!own_task) held_by(t, c);
 #pragma unroll
           for (int k = 0; k < PG_COLS; k++) {
-            const bool mine = frees(t, k, c[k]);
+            const bool mine = own_task ? freed >> k & 1 : frees(t, k, c[k]);
             const unsigned all = __ballot_sync(FULL_MASK, mine);
             if (mine) {
               a.free_out[at + __popc(all & ((1u << lane) - 1))] = t.p[k];
@@ -426,7 +466,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
           if (changes(t, k)) a.table_out[(long long)t.b * M + t.j0 + 32 * k] = p[k];
       });
       for (int b = gt; b < B; b += gts) {
-        const PageRow r = a.rows[b];
+        const PageRow r = row_of(b);
         a.lens_out[b] = r.len < 0 ? kv.seq_lens[b] : r.len;
         a.n_pages_out[b] = r.len < 0 ? a.n_pages[b] : r.blocks;
       }
@@ -437,7 +477,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_kernel(const __grid_constant
 
   // ---- refused: everything as it was, nothing to copy ----
   if (!early) {
-    sweep([&](const Task& t) { counts(t, -1); });
+    sweep([&](const Task& t, bool) { counts(t, -1); });
     copies(true);
   }
   for (int b = gt; b < B; b += gts) {
