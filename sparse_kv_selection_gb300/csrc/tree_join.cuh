@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const __grid_co
     const int gl = p.group_log2;
     const float inv = tree_inv(L);
     const long long orow = (long long)(s.tok + (row >> gl)) * a.kv.Hq + (s.kvh << gl) + (row & ((1 << gl) - 1));
-    if (s.part != 0) {  // (fp32)
+    if (sizeof(T) == 4 && s.part != 0) {
       const int tok = s.tok + (row >> gl), g = row & ((1 << gl) - 1);
       *part_at<T, D>(a, s.part, tok, s.kvh, g, c, gl) = o;
       if (c == 0) a.part_ml[part_row<T>(a, s.part, tok, s.kvh, g, gl)] = make_float2(M, L);

@@ -615,9 +615,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           w.qtiles = qtiles;
           w.whole = nt == tiles;
           w.last = left == 0;
-          w.base = s.base;
-          w.part = s.part;
           if constexpr (SHARED) {
+            w.base = s.base;
+            w.part = s.part;
             w.first = nt == tiles ? (int)blockIdx.x : start / per;
             w.cuts = nt == tiles ? 1 : (start + tiles - 1) / per - w.first + 1;
           }
