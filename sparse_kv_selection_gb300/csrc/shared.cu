@@ -16,23 +16,24 @@
 
 namespace prhs {
 
-constexpr int SJ_THREADS = 128, SJ_PIECES = 4;  // (pieces in flight)
+constexpr int SJ_THREADS = 128, SJ_CTAS_SM = 8, SJ_PIECES = 4;  // (pieces in flight)
 
 template <typename T, int D, bool WAYS>
-__global__ void __launch_bounds__(SJ_THREADS, WAYS ? 5 : 8) shared_join_kernel(const __grid_constant__ TreeLaunch a,
+__global__ void __launch_bounds__(SJ_THREADS, WAYS ? 5 : SJ_CTAS_SM) shared_join_kernel(const __grid_constant__ TreeLaunch a,
                                                                  const __grid_constant__ TreeRecords rec, int ctas) {
   constexpr int C4 = D / 4, CHUNKS = D / 32;
   const KVView& kv = a.kv;
   const int G = kv.Hq / kv.Hkv, gl = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, b = blockIdx.x;
-  // as tree_item reads them (the launch before has flagged what does not fit)
-  const int4 mine = a.shared[b];
-  const int len = kv.seq_lens[b], lo = a.cu_new[b], hi = a.cu_new[b + 1];
+  // as tree_item reads them (the launch before has flagged what does not fit), through L2: what
+  // was there before that launch may stand in an L1 that this one's wait has not passed
+  const int4 mine = __ldcg(a.shared + b);
+  const int len = __ldcg(kv.seq_lens + b), lo = __ldcg(a.cu_new + b), hi = __ldcg(a.cu_new + b + 1);
   if (blockIdx.x + blockIdx.y == 0) pdl_wait();  // (one waits whatever it has to do: this launch ends behind the one before)
   if (lo < 0 || hi <= lo || hi > a.T || hi - lo > a.max_new) return;
   const int t = max(0, min(len, kv.t_max)), n = hi - lo, head = max(0, min(mine.x, b));
   const bool grouped = mine.x == head && !(mine.x == b && (mine.y <= 1 || mine.z == 0));
-  const int4 group = grouped ? a.shared[head] : make_int4(0, 0, 0, 0);
-  const int head_len = grouped ? kv.seq_lens[head] : 0, group0 = grouped ? max(0, a.cu_new[head]) : 0;
+  const int4 group = grouped ? __ldcg(a.shared + head) : make_int4(0, 0, 0, 0);
+  const int head_len = grouped ? __ldcg(kv.seq_lens + head) : 0, group0 = grouped ? max(0, __ldcg(a.cu_new + head)) : 0;
   int keys = 0;  // that are shared
   if (grouped) {
     keys = kv.block_table != nullptr ? group.z / kv.block_size * kv.block_size : group.z;
@@ -141,10 +142,12 @@ __global__ void __launch_bounds__(SJ_THREADS, WAYS ? 5 : 8) shared_join_kernel(c
 template <typename T, int D>
 static cudaError_t join_go(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
   const long long blocks = ((long long)a.max_new * (a.kv.Hq / a.kv.Hkv) + 7) / 8;
-  const long long y = (blocks * a.kv.Hkv * (D / 32) + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
+  long long y = (blocks * a.kv.Hkv * (D / 32) + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
+  // one wave, since each CTA looks its sequence up (24 prompts: two waves 127.5 us, one 128.6, half of one 143)
+  const long long most = ((long long)SJ_CTAS_SM * sms + a.kv.B - 1) / a.kv.B;
+  if (y > most) y = most;
   auto* kernel = sizeof(T) == 2 && a.max_new * (a.kv.Hq / a.kv.Hkv) <= 4 ? shared_join_kernel<T, D, sizeof(T) == 2> : shared_join_kernel<T, D, false>;
-  return launch_pdl(kernel, dim3(a.kv.B, (unsigned)(y < 1024 ? y : 1024)), dim3(SJ_THREADS), 0, st, true, a, rec,
-                    sms);
+  return launch_pdl(kernel, dim3(a.kv.B, (unsigned)y), dim3(SJ_THREADS), 0, st, true, a, rec, sms);
 }
 cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
   if (a.kv.dtype == PRHS_BF16)

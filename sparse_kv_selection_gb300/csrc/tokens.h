@@ -110,10 +110,10 @@ prhs_status launch_tree_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t 
 size_t tree_tc_workspace(const KVView& kv, int max_new, int sms);
 
 // With shared keys: fp32 launch_tree, then the join; bf16 one launch (counted) and the
-// join. rec: the partial states of the launch's `ctas` CTAs.
+// join. rec: (bf16) the partial states of the launch's CTAs, one an SM.
 struct TreeRecords;
 prhs_status launch_shared_tc(const TreeLaunch& a, int sms, void* ws, cudaStream_t s, cudaError_t* err);
-cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int ctas, cudaStream_t s);
+cudaError_t launch_shared_join(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t s);
 void few_shape(TreeLaunch* a, int sms);
 size_t few_state_bytes(const KVView& kv, int sms);
 size_t shared_where_bytes(const KVView& kv, int T);

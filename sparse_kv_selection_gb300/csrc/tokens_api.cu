@@ -267,7 +267,7 @@ prhs_status attend(const prhs_kv* kv, const void* q, const void* k_new, long lon
   e = launch_tree(a, sms, ws, stream);
   if (e != cudaSuccess || !shared) return launched(e);
   abi_count_launch();
-  return launched(launch_shared_join(a, TreeRecords{}, 0, stream));
+  return launched(launch_shared_join(a, TreeRecords{}, sms, stream));
 }
 
 }  // namespace

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) tree_kernel(const __grid_constan
   // needs both, so that this one's last CTA does nothing but wait for it.
   const int ctas = gridDim.x - (SHARED && a.items == TREE_OWN ? 1 : 0), cta = (SHARED ? p.cta0 : 0) + blockIdx.x;
   if (!SHARED || a.items != TREE_OWN || (int)blockIdx.x == ctas) pdl_wait();
+  else __threadfence();  // (that launch has waited for all that was before it; no L1 keeps older lengths or tables)
   pdl_trigger();
   if (SHARED && (int)blockIdx.x == ctas) return;
   const KVView& kv = a.kv;

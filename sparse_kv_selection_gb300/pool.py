@@ -65,7 +65,8 @@ class PagePool:
 
     def compact(self, keep: torch.Tensor, keep_n: torch.Tensor) -> None:
         """Row b keeps the positions keep[b][:keep_n[b]] (int32, ascending; keep_n[b] < 0:
-        all). Keys keep the rotation they were cached with."""
+        all). Keys keep the rotation they were cached with. The lists of rows to copy are kept
+        for each width of keep."""
         lists = self._lists(keep.shape[-1])
         _b.compact_seqs(self.kv, keep, keep_n, *lists, self.ws, page_shares=self.page_shares, stream=self.stream,
                         **self.pages)

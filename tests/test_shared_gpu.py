@@ -221,6 +221,46 @@ def test_entries_that_do_not_fit(dtype):
     b.check(out)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_lengths_and_groups_that_change_between_calls(dtype):
+    """Calls back to back on one cache, lengths, offsets and groups written by copies in between."""
+    import sparse_kv_selection_gb300 as S
+    B = 96
+    b = Batch([(24, 512)] * 4, (40, 400), (1, 1), 8, 4, 64, dtype, 16, pad=B, seed=40)
+    rng = np.random.default_rng(41)
+    full_lens = np.array(b.lens)
+    states = []
+    for i in range(8):
+        cut = 0 if i % 3 == 0 else int(rng.integers(0, 512))
+        n = rng.integers(0, 2 + i % 2, B)
+        share = [[f, r, cut // 16 * 16 if i % 2 else k // 32 * 16, 0] for f, r, k, _ in b.share]
+        share = [[j, 1, 0, 0] if not s[2] else s for j, s in enumerate(share)]
+        states.append([i32(full_lens - rng.integers(0, 40, B)), i32(np.concatenate([[0], np.cumsum(n)])), i32(share)])
+    lens, cu, share = (x.clone() for x in states[0])
+    kv = S.KVCache(b.c.k, b.c.v, lens, b.c.Hq, block_table=b.c.kv.block_table)
+    ws = S.make_shared_workspace(kv, b.T, 2)
+    out = (torch.empty(b.T, b.c.Hq, b.c.d, dtype=dtype, device="cuda"), torch.empty(b.T, b.c.Hq, device="cuda"))
+
+    def results(wait):
+        got = []
+        for s in states * 3:
+            for x, y in zip((lens, cu, share), s):
+                x.copy_(y)
+            for x in out:
+                x.fill_(7.0)
+            if wait:
+                torch.cuda.synchronize()
+            S.shared_attn(kv, b.q, b.kn, b.vn, b.scale, cu, 2, share, *out, ws)
+            if wait:
+                torch.cuda.synchronize()
+            got.append([x.clone() for x in out])
+        return got
+
+    for x, y in zip(results(True), results(False)):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert S.last_error() == 0
+
+
 def test_batches_on_streams_of_their_own():
     """Four batches at once, each with its own workspace, eager and from graphs."""
     import sparse_kv_selection_gb300 as S
