@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(FIND_THREADS) find_kernel(const __grid_constan
   int *row = find_smem, *same = row + B, *head = same + B;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  cluster_begin();
   pdl_wait();
   pdl_trigger();
 
@@ -62,7 +63,8 @@ __global__ void __launch_bounds__(FIND_THREADS) find_kernel(const __grid_constan
     if (tokens(b) > 0) row[at++] = b;
   __syncthreads();
 
-  // ---- shared pages of neighbours, into the first CTA ----
+  // ---- shared pages of neighbours, into the first CTA (once it has begun) ----
+  cluster_begun();
   int* to = cluster.map_shared_rank(same, 0);
   for (int k = rank * FIND_WARPS + warp; k < n; k += ranks * FIND_WARPS) {
     const int b = row[k];

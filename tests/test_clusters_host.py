@@ -1,0 +1,32 @@
+"""Shared memory of another CTA of a cluster may be touched only when that CTA has begun: in
+each kernel that does, a barrier of the whole cluster comes first. (Without one the result
+depends on when CTAs are started, which no run shows; so this reads the sources.)"""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_kv_selection_gb300", "csrc")
+REMOTE = re.compile(r"map_shared_rank|\bat_rank<|\brank_shared<|\bpush_hist_row\(")
+BARRIER = re.compile(r"\bcluster_begun\(\)|\bcluster\.sync\(\)|\bcluster_barrier<\w+>\(|\bhead_sync<\w+>\(|\bplanned\(\)")
+
+
+def kernels():
+    """Kernel names and their bodies, comments taken out."""
+    for name in sorted(os.listdir(CSRC)):
+        src = re.sub(r"//.*", "", open(os.path.join(CSRC, name)).read())
+        for m in re.finditer(r"__global__[^;{]*?\b(\w+_kernel)\s*\(", src):
+            at = src.index("{", m.end())
+            depth, end = 1, at + 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(src[end], 0)
+                end += 1
+            yield m.group(1), src[at:end]
+
+
+@pytest.mark.parametrize("name", ["find_kernel"])
+def test_a_barrier_before_another_ctas_memory(name):
+    body = dict(kernels())[name]
+    remote = REMOTE.search(body)
+    assert remote, "reaches no other CTA"
+    assert BARRIER.search(body, 0, remote.start()), body[:remote.end()][-300:]
