@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(ACL_THREADS, 2) attn_cluster_kernel(const Attn
     return;
   }
   const int mine = n > rank ? (n - rank + CL - 1) / CL : 0;  // positions rank + CL * i, i < mine
+  if (CL > 1) cluster_begin();
 
   const float qscale = a.scale * ACL_LOG2E;
   float qf[EL];
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(ACL_THREADS, 2) attn_cluster_kernel(const Attn
       for (int e = 0; e < EPC; e++) sm_o[warp][(cc * 8 + j) * EPC + e] = o[cc * EPC + e];
   }
   __syncthreads();
+  if (CL > 1) cluster_begun();  // CTA 0's table may be written
   if (tid < D) {
     float M = sm_m[0];
 #pragma unroll
