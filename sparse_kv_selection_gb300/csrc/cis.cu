@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(CIS_THREADS) cis_kernel(const CisLaunch a) {
   const int seg_hi = min(n, seg_lo + seg);  // this CTA's entries [seg_lo, seg_hi)
   int offset = 0, grand = 0;                // positions of the lower ranks' entries, of all
   if (CLU) {
+    cluster_begin();
     int local = 0;
     for (int base = seg_lo; base < seg_hi; base += CHUNK) {
       const int j0 = base + tid * CIS_PER;
@@ -376,6 +377,7 @@ __global__ void __launch_bounds__(CIS_THREADS) cis_kernel(const CisLaunch a) {
       local += chunk_intervals(y, prev, j0, seg_hi, t, w, ns, wlo, nullptr, start, cnt);
     }
     const int total = block_sum(local, warp_tot);
+    cluster_begun();
     if (tid < CL) cluster.map_shared_rank(seg_cnt, tid)[rank] = total;
     cluster.sync();  // every rank's count is in every rank
 #pragma unroll
