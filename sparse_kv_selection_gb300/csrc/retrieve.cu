@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(RT_THREADS, 2) retrieve_kernel(const SelectLau
   }
 
   // ---- round 1: logits of this CTA's slice, and its range to every rank ----
+  if (!ONE) cluster_begin();
   const int kvh = (qh % kv.Hq) / (kv.Hq / kv.Hkv);
   {
     float qf[EPC];
@@ -571,6 +572,7 @@ __global__ void __launch_bounds__(RT_THREADS, 2) retrieve_kernel(const SelectLau
       sh.red2[warp] = vmax;
     }
     __syncthreads();
+    if (!ONE) cluster_begun();
     if (tid < CL) {
       float m0 = INFINITY, m1 = -INFINITY;
 #pragma unroll

@@ -24,7 +24,7 @@ def kernels():
             yield m.group(1), src[at:end]
 
 
-@pytest.mark.parametrize("name", ["find_kernel", "attn_cluster_kernel", "cis_kernel"])
+@pytest.mark.parametrize("name", ["find_kernel", "attn_cluster_kernel", "cis_kernel", "retrieve_kernel"])
 def test_a_barrier_before_another_ctas_memory(name):
     body = dict(kernels())[name]
     remote = REMOTE.search(body)
