@@ -822,13 +822,16 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) score_select_kernel(const Sele
   cg::cluster_group cluster = cg::this_cluster();
   const int CL = ONE ? 1 : (int)cluster.num_blocks();
   const int rank = ONE ? 0 : (int)cluster.block_rank();
+  if (!ONE) cluster_begin();
   pdl_wait();
   pdl_trigger();
 
   const KVView& kv = a.kv;
   const int qh = blockIdx.x / CL;
   const int b = qh / kv.Hq;
-  if (a.head_skip != nullptr && a.head_skip[qh] != 0) return;  // uniform over the cluster
+  const bool skip = a.head_skip != nullptr && a.head_skip[qh] != 0;  // uniform over the cluster
+  if (!ONE) cluster_begun();  // CTA 0's row may be written
+  if (skip) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = seq_len(kv, b);
   int Nb = a.n_budget != nullptr ? a.n_budget[b] : a.N;

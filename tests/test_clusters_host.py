@@ -24,7 +24,14 @@ def kernels():
             yield m.group(1), src[at:end]
 
 
-@pytest.mark.parametrize("name", ["find_kernel", "attn_cluster_kernel", "cis_kernel", "retrieve_kernel"])
+NAMES = ["attn_cluster_kernel", "cis_kernel", "find_kernel", "pages_kernel", "retrieve_kernel", "score_select_kernel"]
+
+
+def test_every_such_kernel_is_named():
+    assert sorted(n for n, body in kernels() if REMOTE.search(body)) == NAMES
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_a_barrier_before_another_ctas_memory(name):
     body = dict(kernels())[name]
     remote = REMOTE.search(body)
