@@ -37,3 +37,11 @@ def test_a_barrier_before_another_ctas_memory(name):
     remote = REMOTE.search(body)
     assert remote, "reaches no other CTA"
     assert BARRIER.search(body, 0, remote.start()), body[:remote.end()][-300:]
+
+
+def test_an_anchors_age_changes_once_all_ranks_have_read_it():
+    """Ranks that read another age decide otherwise, and leave while the others still write to them."""
+    body = dict(kernels())["cis_kernel"]
+    read, write = body.index("= a.anchor_age !="), body.index("a.anchor_age[qh] = ")
+    begin, begun = body.index("cluster_begin()"), body.index("cluster_begun()")
+    assert read < begin < begun < write
