@@ -521,8 +521,8 @@ size_t prhs_shared_workspace_size(const prhs_kv* kv, int T, int max_new);
  * row that is alone has (b, 1, 0, 0). Groups must not overlap (if they have more than T
  * tokens together that is flagged, PRHS_DEV_BAD_INDEX, and no result has a meaning). P
  * counts whole pages (it is rounded down to them; on a contiguous cache it is any number).
- * A row whose entry
- * does not fit its group's first row, or with P above either row's length, is flagged
+ * A row whose entry is
+ * not its group's first row's, or with P above either row's length, is flagged
  * (PRHS_DEV_BAD_INDEX) and attends all its own keys. Everything else, errors too, as
  * prhs_tree_attn. */
 prhs_status prhs_shared_attn(const prhs_kv* kv, const void* q, const void* k_new, long long k_stride,

@@ -37,7 +37,8 @@ __global__ void __launch_bounds__(SJ_THREADS, WAYS ? 5 : SJ_CTAS_SM) shared_join
   int keys = 0;  // that are shared
   if (grouped) {
     keys = kv.block_table != nullptr ? group.z / kv.block_size * kv.block_size : group.z;
-    if (group.x != head || b - head >= group.y || keys < 0 || keys > t || keys > head_len) keys = 0;
+    const bool same = group.x == head && group.y == mine.y && group.z == mine.z;
+    if (!same || b - head >= group.y || keys < 0 || keys > t || keys > head_len) keys = 0;
   }
   const bool few[2] = {false, sizeof(T) == 2 && few_item(a, n, t - keys)};  // whose are the states?
   // all that was there before the launch in front; what it wrote from here on

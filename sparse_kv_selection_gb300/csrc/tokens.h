@@ -177,15 +177,15 @@ __device__ __forceinline__ int seq_tokens(const int32_t* cu_new, int b, int T, i
 }
 
 // Leading keys that sequence b, of t cached keys, shares with its group, 0 if it is
-// alone. An entry that does not fit (its group, a length below the shared keys) is
-// flagged and read as alone. Whole pages only.
+// alone. An entry that does not fit (other than its group's first row's, a length below
+// the shared keys) is flagged and read as alone. Whole pages only.
 __device__ __forceinline__ int shared_keys(const KVView& kv, const int4* shared, int b, int t) {
   const int4 s = shared[b];
   if (s.x == b && (s.y <= 1 || s.z == 0)) return 0;
   bool ok = s.x >= 0 && s.x <= b;
   const int4 g = ok ? shared[s.x] : s;
   const int keys = kv.block_table != nullptr ? g.z / kv.block_size * kv.block_size : g.z;
-  ok = ok && g.x == s.x && b - s.x < g.y && keys >= 0 && keys <= t && keys <= kv.seq_lens[s.x];
+  ok = ok && g.x == s.x && g.y == s.y && g.z == s.z && b - s.x < g.y && keys >= 0 && keys <= t && keys <= kv.seq_lens[s.x];
   if (ok) return keys;
   raise_error(kv.err, PRHS_DEV_BAD_INDEX);
   return 0;
