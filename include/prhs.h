@@ -443,6 +443,9 @@ prhs_status prhs_commit_planned(const prhs_kv* kv, int T, const int32_t* cu_new,
  * not at all: refused, it is flagged in the device error word, `next` is `now`,
  * and there is nothing to copy. Paged caches only. ws: prhs_pages_workspace_size()
  * bytes, 256-byte aligned, no initialisation.
+ * What a caller keeps by row or by position has to follow: the anchors of
+ * prhs_decode_step and its parts are positions of what the row was, so set anchor_n to 0
+ * for the heads of rows that change (parent[b] != b, keep_n[b] >= 0).
  * ------------------------------------------------------------------------- */
 typedef struct prhs_pages {
   int32_t* block_table;  /* [B][max_blocks]; now: null or the descriptor's, next: null for in place */

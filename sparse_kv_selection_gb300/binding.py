@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import weakref
 
 import torch
 
@@ -161,6 +162,7 @@ class KVCache:
         self.block_table = None if block_table is None else block_table.to(torch.int32).contiguous()
         self.device, self.dtype = self.k.device, self.k.dtype
         self.index = 0 if self.device.index is None else self.device.index
+        self.decoders = weakref.WeakSet()  # what keeps anchors of its rows
         self.desc = prhs_kv()
         d = self.desc
         d.dtype = PRHS_BF16 if k.dtype == torch.bfloat16 else PRHS_F32

@@ -49,11 +49,18 @@ class SparseDecoder:
         self.lse = torch.zeros(B, Hq, device=dev, dtype=torch.float32)
         self.ws = _b.make_workspace(kv, self.cap, stream)
         self.stream = stream
+        kv.decoders.add(self)
 
-    def reset(self) -> None:
-        """Forget every anchor: the next step retrieves for all heads."""
-        self.anchor_n.zero_()
-        self.anchor_age.zero_()
+    def reset(self, rows: torch.Tensor | None = None) -> None:
+        """Forget every anchor, or those of the rows flagged in rows (bool [B]): the next
+        step retrieves for their heads. Needed when a row becomes another sequence or its
+        positions change; ``PagePool`` does it for the decoders of its caches."""
+        if rows is None:
+            self.anchor_n.zero_()
+            self.anchor_age.zero_()
+            return
+        _b._array(rows, "rows", (self.kv.B,), torch.bool, self.kv.device)
+        self.anchor_n.masked_fill_(rows[:, None], 0)  # (a retrieval sets the age)
 
     def step(self, q: torch.Tensor, out=None, lse=None, delta=None, reuse=None, n_sel=None,
              gate=None) -> None:

@@ -7,6 +7,10 @@ places), end, or keep a part of their positions; the rows that have to move are
 copied in the cache of every layer. Nothing synchronises with the host, so the
 calls can be captured into a graph, and ``TokenBatch(kv, rope, ...,
 share_prefixes=True, **pool.pages)`` feeds tokens to the same sequences.
+
+A ``SparseDecoder`` on one of the caches loses its anchors of the rows that change (a
+captured call: those decoders that were there when it was captured, which the pool then
+keeps). Decoders on other ``KVCache`` objects of the same table need ``reset(rows)``.
 """
 from __future__ import annotations
 
@@ -37,7 +41,7 @@ class PagePool:
             self.page_shares = torch.zeros(kv.desc.num_blocks, **i32) if page_shares is None else page_shares
             self.ws = _b.make_pages_workspace(kv)
             self._rows = torch.arange(kv.B, **i32)
-        self._moves = {}
+        self._moves, self._captured = {}, []
 
     def _lists(self, cap):
         """The buffers of the row copies, kept for calls of the same size."""
@@ -50,12 +54,26 @@ class PagePool:
         for kv in self.layers:
             _b.copy_rows(kv, *lists, stream=self.stream)
 
+    def _forget(self, changed):
+        """No anchors of rows that are not what they were: changed() flags them. Those of
+        a refused call's rows too, which then retrieve once more."""
+        decoders = [x for kv in self.layers for x in kv.decoders]
+        if not decoders:
+            return
+        with torch.cuda.device(self.kv.index), torch.cuda.stream(_own_stream(self.stream, self.kv.device)):
+            rows = changed()
+            for x in decoders:
+                x.reset(rows)
+            if torch.cuda.is_current_stream_capturing():  # the graph writes to them
+                self._captured += [x for x in decoders if x not in self._captured]
+
     def fork(self, parent: torch.Tensor) -> None:
         """Row b becomes what row parent[b] (int32 [B]) is: b itself, another row, or -1:
         the sequence ends."""
         lists = self._lists(self.kv.desc.block_size)
         _b.fork_seqs(self.kv, parent, *lists, self.ws, page_shares=self.page_shares, stream=self.stream, **self.pages)
         self._copy(lists)
+        self._forget(lambda: parent != self._rows)
 
     def free(self, done: torch.Tensor) -> None:
         """The rows flagged in done (bool [B]) end."""
@@ -71,3 +89,4 @@ class PagePool:
         _b.compact_seqs(self.kv, keep, keep_n, *lists, self.ws, page_shares=self.page_shares, stream=self.stream,
                         **self.pages)
         self._copy(lists)
+        self._forget(lambda: keep_n >= 0)
