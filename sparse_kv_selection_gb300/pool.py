@@ -33,6 +33,10 @@ class PagePool:
         for x in layers:
             if x.block_table is None or x.block_table.data_ptr() != kv.block_table.data_ptr() or x.desc.block_size != kv.desc.block_size:
                 raise ValueError("the layers' caches must use the same block table and page size")
+            if x.seq_lens.data_ptr() != kv.seq_lens.data_ptr():
+                raise ValueError("the layers' caches must use the same seq_lens")
+            if x.block_table.shape != kv.block_table.shape or x.desc.num_blocks < kv.desc.num_blocks:
+                raise ValueError("the layers' caches must have the same rows and columns, and no fewer pages")
         self.kv, self.layers, self.stream = kv, (kv, *layers), stream
         i32 = dict(device=kv.device, dtype=torch.int32)
         with torch.cuda.stream(_own_stream(stream, kv.device)):
