@@ -45,14 +45,17 @@ class PagePool:
             self.page_shares = torch.zeros(kv.desc.num_blocks, **i32) if page_shares is None else page_shares
             self.ws = _b.make_pages_workspace(kv)
             self._rows = torch.arange(kv.B, **i32)
-        self._moves, self._captured = {}, []
+        self._moves, self._captured = [], []
 
     def _lists(self, cap):
-        """The buffers of the row copies, kept for calls of the same size."""
-        if cap not in self._moves:
+        """The lists of a call's row copies: the front of two buffers, which double when a call
+        needs more (the older ones stay, for the graphs that hold them)."""
+        n = self.kv.B * cap
+        if not self._moves or self._moves[-1][0].numel() < n:
+            most = max(n, 2 * self._moves[-1][0].numel()) if self._moves else n
             with torch.cuda.stream(_own_stream(self.stream, self.kv.device)):
-                self._moves[cap] = [torch.full((self.kv.B, cap), -1, device=self.kv.device, dtype=torch.int32) for _ in range(2)]
-        return self._moves[cap]
+                self._moves.append([torch.empty(most, device=self.kv.device, dtype=torch.int32) for _ in range(2)])
+        return [x[:n].view(self.kv.B, cap) for x in self._moves[-1]]
 
     def _copy(self, lists):
         for kv in self.layers:
@@ -87,8 +90,7 @@ class PagePool:
 
     def compact(self, keep: torch.Tensor, keep_n: torch.Tensor) -> None:
         """Row b keeps the positions keep[b][:keep_n[b]] (int32, ascending; keep_n[b] < 0:
-        all). Keys keep the rotation they were cached with. The lists of rows to copy are kept
-        for each width of keep."""
+        all). Keys keep the rotation they were cached with."""
         lists = self._lists(keep.shape[-1])
         _b.compact_seqs(self.kv, keep, keep_n, *lists, self.ws, page_shares=self.page_shares, stream=self.stream,
                         **self.pages)

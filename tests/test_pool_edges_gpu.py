@@ -34,3 +34,48 @@ def test_layers_that_do_not_fit_are_refused():
                 S.KVCache(k, k, lens[:2], 1, block_table=table[:2])):                   # fewer rows
         with pytest.raises(ValueError):
             S.PagePool(kv, layers=[bad], **pool_args())
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_row_lists_of_many_widths(order):
+    """Calls of many widths keep less than four times what the widest needs: buffers double, so the
+    last is below twice that, and those before it are no more together."""
+    import sparse_kv_selection_gb300 as S
+    (kv, _), _, lens = caches()
+    pool = S.PagePool(kv, **pool_args())
+    nothing = i32([-1] * 4)
+    widest = 20000
+    widths = [w for w in range(1, widest, 37)] + [widest]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for w in widths if order == "rising" else widths[::-1]:
+        pool.compact(torch.zeros(4, w, dtype=torch.int32, device="cuda"), nothing)
+    torch.cuda.synchronize()
+    assert S.last_error() == 0
+    assert torch.cuda.memory_allocated() - before <= 4 * (2 * 4 * widest * 4) + (1 << 16)
+
+
+def test_row_lists_of_a_graph_outlive_wider_calls():
+    import sparse_kv_selection_gb300 as S
+    (kv, _), table, lens = caches()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        pool = S.PagePool(kv, stream=stream, **pool_args())
+        keep, n = torch.zeros(4, 24, dtype=torch.int32, device="cuda"), i32([-1] * 4)
+        stream.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            pool.compact(keep, n)
+        wide = torch.zeros(4, 5000, dtype=torch.int32, device="cuda")
+        pool.compact(wide, n)
+        junk = [torch.full((4, 24), 7, dtype=torch.int32, device="cuda") for _ in range(64)]
+        want = kv.k[table[0, torch.arange(90, 100, device="cuda") // 16].long(), 0, torch.arange(90, 100, device="cuda") % 16].clone()
+        keep[0, :10] = torch.arange(90, 100, device="cuda")
+        n.copy_(i32([10, -1, -1, -1]))
+        g.replay()
+        pool.compact(wide, i32([-1] * 4))
+        stream.synchronize()
+        assert S.last_error() == 0
+        assert lens.tolist() == [10, 40, 0, 128]
+        assert torch.equal(kv.k[int(table[0, 0]), 0, :10], want)
+        assert all((x == 7).all() for x in junk)
