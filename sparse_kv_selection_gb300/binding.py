@@ -336,6 +336,12 @@ def _array(t, name, shape, dtype, device, optional=False):
     return _ptr(t)
 
 
+def _flags(t, name, kv):
+    """Checks a flag for each row of the batch, of any stride."""
+    if t.dtype is not torch.bool or t.shape != (kv.B,) or t.device != kv.device:
+        raise ValueError(f"{name} must be bool ({kv.B},) on {kv.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 def _rows(t, name, T, heads, d, dtype, device):
     """Pointer and token stride of [T][heads][d] rows that may be a view of a
     wider buffer (a fused projection's output): packed within a token."""

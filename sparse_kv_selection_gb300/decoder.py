@@ -59,7 +59,7 @@ class SparseDecoder:
             self.anchor_n.zero_()
             self.anchor_age.zero_()
             return
-        _b._array(rows, "rows", (self.kv.B,), torch.bool, self.kv.device)
+        _b._flags(rows, "rows", self.kv)
         self.anchor_n.masked_fill_(rows[:, None], 0)  # (a retrieval sets the age)
 
     def step(self, q: torch.Tensor, out=None, lse=None, delta=None, reuse=None, n_sel=None,

@@ -84,6 +84,7 @@ class PagePool:
 
     def free(self, done: torch.Tensor) -> None:
         """The rows flagged in done (bool [B]) end."""
+        _b._flags(done, "done", self.kv)
         with torch.cuda.stream(_own_stream(self.stream, self.kv.device)):
             parent = torch.where(done, -1, self._rows)
         self.fork(parent)

@@ -79,3 +79,18 @@ def test_row_lists_of_a_graph_outlive_wider_calls():
         assert lens.tolist() == [10, 40, 0, 128]
         assert torch.equal(kv.k[int(table[0, 0]), 0, :10], want)
         assert all((x == 7).all() for x in junk)
+
+
+def test_free_takes_one_flag_a_row():
+    import sparse_kv_selection_gb300 as S
+    (kv, _), _, lens = caches()
+    pool = S.PagePool(kv, **pool_args())
+    for bad in (torch.tensor([True], device="cuda"), torch.tensor(True, device="cuda"), i32([1, 0, 0, 0]),
+                torch.tensor([[True, False, False, False]], device="cuda"), torch.tensor([True, False, False, False])):
+        with pytest.raises(ValueError):
+            pool.free(bad)
+    assert lens.tolist() == [100, 40, 0, 128]
+    pool.free(torch.tensor([True, False, False, False], device="cuda"))
+    assert S.last_error() == 0 and lens.tolist() == [0, 40, 0, 128]
+    pool.free(torch.tensor([[False, True], [True, False]] * 2, device="cuda")[:, 0])    # (any stride)
+    assert S.last_error() == 0 and lens.tolist() == [0, 0, 0, 0]
