@@ -476,7 +476,7 @@ prhs_status prhs_fork_seqs(const prhs_kv* kv, const prhs_pages* now, const int32
                            const prhs_pages* next, int32_t* src, int32_t* dst, void* ws,
                            size_t ws_bytes, cudaStream_t stream);
 
-/* Row b keeps the positions keep[b][0 .. m) (int32 [B][cap], strictly ascending),
+/* Row b keeps the positions keep[b][0 .. m) (int32 [B][cap], strictly ascending, cap <= 2^30),
  * m = keep_n[b], which become its positions 0 .. m - 1; m < 0 leaves the row as it is.
  * The whole pages of the leading positions that keep their places stay, as does the
  * last page of a row that is only cut short and holds it alone. The others go to free

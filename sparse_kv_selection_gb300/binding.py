@@ -336,6 +336,14 @@ def _array(t, name, shape, dtype, device, optional=False):
     return _ptr(t)
 
 
+def _int32(x, name):
+    """A number that the C side takes in 32 bits (ctypes would cut it to them)."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _flags(t, name, kv):
     """Checks a flag for each row of the batch, of any stride."""
     if t.dtype is not torch.bool or t.shape != (kv.B,) or t.device != kv.device:
@@ -461,7 +469,7 @@ def rope_append(kv, rope, positions, q, k, v, q_out, *, slots=None, k_out=None, 
 
 def tree_workspace_size(kv: KVCache, max_new: int) -> int:
     with torch.cuda.device(kv.index):
-        n = load().prhs_tree_workspace_size(kv.ref(), int(max_new))
+        n = load().prhs_tree_workspace_size(kv.ref(), _int32(max_new, "max_new"))
     if n == 0:
         raise PrhsError(PRHS_EINVAL, "tree_workspace_size", load().prhs_last_message().decode())
     return n
@@ -481,7 +489,7 @@ def _attend(kv, where, fn, q, k_new, v_new, scale, cu_new, max_new, tree_mask, s
     if ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the cache on {dev}")
     _call(kv, where, fn, stream, kv.ref(), _array(q, "q", (T, Hq, d), dt, dev), kp, ks,
-          vp, vs, float(scale), T, _array(cu_new, "cu_new", (desc.B + 1,), torch.int32, dev), int(max_new),
+          vp, vs, float(scale), T, _array(cu_new, "cu_new", (desc.B + 1,), torch.int32, dev), _int32(max_new, "max_new"),
           _array(tree_mask, "tree_mask", (T, TREE_WORDS), torch.int32, dev, True), *shared,
           _array(out, "out", (T, Hq, d), dt, dev), _array(lse, "lse", (T, Hq), torch.float32, dev),
           _ptr(ws), ws.numel() * ws.element_size())
@@ -597,7 +605,7 @@ def compact_seqs(kv, keep, keep_n, src, dst, ws, *, n_pages, page_shares, free_p
 def copy_rows(kv, src, dst, *, source=None, stream=None) -> None:
     """Copy cache rows (K and V of every head) from slots src of `source` (another
     KVCache, or the same one) to slots dst of the cache; -1: none (prhs_copy_rows)."""
-    n = src.numel()
+    n = _int32(src.numel(), "the number of rows to copy")
     if source is not None and source.device != kv.device:
         raise ValueError(f"source is on {source.device}, the cache on {kv.device}")
     if dst.shape != src.shape:
@@ -611,12 +619,12 @@ def find_shared(kv, cu_new, shared, *, min_keys=256, stream=None) -> None:
     for shared_attn: (first row, rows, shared keys, 0) (prhs_find_shared)."""
     dev, i32, B = kv.device, torch.int32, kv.desc.B
     _call(kv, "find_shared", load().prhs_find_shared, stream, kv.ref(), _array(cu_new, "cu_new", (B + 1,), i32, dev),
-          int(min_keys), _array(shared, "shared", (B, 4), i32, dev))
+          _int32(min_keys, "min_keys"), _array(shared, "shared", (B, 4), i32, dev))
 
 
 def shared_workspace_size(kv: KVCache, T: int, max_new: int) -> int:
     with torch.cuda.device(kv.index):
-        n = load().prhs_shared_workspace_size(kv.ref(), int(T), int(max_new))
+        n = load().prhs_shared_workspace_size(kv.ref(), _int32(T, "T"), _int32(max_new, "max_new"))
     if n == 0:
         raise PrhsError(PRHS_EINVAL, "shared_workspace_size", load().prhs_last_message().decode())
     return n

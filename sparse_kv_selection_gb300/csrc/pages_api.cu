@@ -91,6 +91,7 @@ prhs_status prhs_compact_seqs(const prhs_kv* kv, const prhs_pages* now, const in
   if (s != PRHS_OK) return s;
   if (!keep || !keep_n) return abi_fail(PRHS_EINVAL, "compact: keep and keep_n must be non-null");
   if (cap <= 0) return abi_fail(PRHS_EINVAL, "compact: cap must be positive");
+  if (cap > 1 << 30) return abi_fail(PRHS_EUNSUPPORTED, "compact: cap above 2^30 positions");  // (a cache has fewer)
   PagesLaunch a = {};
   a.keep = keep;
   a.keep_n = keep_n;

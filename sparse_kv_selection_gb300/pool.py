@@ -50,7 +50,7 @@ class PagePool:
     def _lists(self, cap):
         """The lists of a call's row copies: the front of two buffers, which double when a call
         needs more (the older ones stay, for the graphs that hold them)."""
-        n = self.kv.B * cap
+        n = _b._int32(self.kv.B * cap, "the number of rows to copy")
         if not self._moves or self._moves[-1][0].numel() < n:
             most = max(n, 2 * self._moves[-1][0].numel()) if self._moves else n
             with torch.cuda.stream(_own_stream(self.stream, self.kv.device)):

@@ -46,6 +46,8 @@ class TokenBatch:
         dev, B, d = kv.k.device, kv.B, kv.desc.d
         self.kv, self.rope, self.stream = kv, rope, stream
         self.max_new = int(max_new)
+        if share_prefixes and not 0 <= min_shared < 2**31:
+            raise ValueError(f"min_shared must be in [0, 2**31), got {min_shared}")
         self.scale = scale if scale is not None else d ** -0.5
         # on the batch's own stream: it may run a step before this one gets to the fills
         with torch.cuda.stream(_own_stream(stream, dev)):
