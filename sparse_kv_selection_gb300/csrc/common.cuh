@@ -194,14 +194,24 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
 }
 
 // -------------------------------------------------------------------------- //
-// programmatic dependent launch: every kernel of the path waits for its
-// stream predecessor before touching memory the predecessor may write or
-// read, then lets its own successor start launching. The launch attribute is
-// set only when `pdl` is (caches of up to PDL_MAX_KEYS keys: short kernels
-// back to back, whose launch latency it hides); on longer caches the two
+// programmatic dependent launch: a kernel may start once all CTAs of its stream
+// predecessor have triggered (or ended), and its wait returns when that launch is done.
+// For this to order more than two launches, in every kernel of the path
+//   - a CTA triggers only behind its own wait (what a launch sees before it waits is
+//     then as the launch in front of its predecessor left it),
+//   - one CTA of every grid waits, whatever it has to do (a launch that ends is then
+//     behind all that came before it), and
+//   - nothing that the predecessor may read or write is touched before the wait.
+// Kernels that read or write earlier than that do so on what the predecessor leaves
+// alone, past an L1 that may hold older lines: shared_join_kernel (lengths, offsets and
+// groups, through L2; CTAs without rows do not wait), tree_kernel for the sequences' own
+// keys (behind a fence; its last CTA waits).
+// The launch attribute is set only when `pdl` is (caches of up to PDL_MAX_KEYS keys: short
+// kernels back to back, whose launch latency it hides); on longer caches the two
 // branches of a decode step overlap better without it (measured 4-6% faster
-// steps on 32K-131K-key caches). Without the attribute the wait and the
-// trigger are no-ops.
+// steps on 32K-131K-key caches). Joins behind their own main launch, and all launches of
+// shared_attn on bf16, have it always. Without the attribute the wait and the trigger are
+// no-ops.
 // -------------------------------------------------------------------------- //
 constexpr int PDL_MAX_KEYS = 8192;
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -226,8 +236,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 }
 
 // Dynamic shared memory beyond what a launch has unasked (48 KB less the kernel's static
-// arrays, of at most 24 KB) allowed for `kernel` on the current device; `done` (one per kernel, zero at load) keeps the largest size
-// set on each device, so that a call sets it once and not at every launch.
+// arrays, of at most 24 KB) allowed for `kernel` on the current device; `done` (one per
+// kernel, zero at load) keeps the largest size set on each device, so that a call sets it
+// once and not at every launch.
 constexpr int SMEM_DEVICES = 64;
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t smem, int (&done)[SMEM_DEVICES]) {

@@ -42,7 +42,9 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const __grid_constan
   to_heads = a.to.block_table != nullptr ? a.to.block_size : a.to.t_max;
   __syncthreads();
 
-  const float inv = 1.f / per_entry;  // (exact enough: y is below 2^16, half a piece from an entry's end)
+  // y / per_entry rounded down: y + 1/2 (below 2^20 + 1024, entries have at most 2^20 pieces) is half a
+  // piece or more from an entry's end, and two roundings move the quotient by less than (y + 1/2) 2^-22 of that
+  const float inv = 1.f / per_entry;
   const int half = per_entry / 2, last = (1 << ppr_log2) - 1;
   uint4 c[COPY_PER];
   uint4* dst[COPY_PER];

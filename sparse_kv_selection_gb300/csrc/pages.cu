@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_kernel(const __grid_const
   const int per = (B + PG_THREADS - 1) / PG_THREADS, b0 = min(B, tid * per), b1 = min(B, b0 + per);
   unsigned bits = 0;
   int need = 0, most = 0, taken = 0;
-  PageRow r0 = {};  // (the thread's only row of batches up to 1024)
+  PageRow r0 = {};  // (the thread's only row of batches up to PG_THREADS)
   for (int b = b0; b < b1; b++) {
     r0 = plan_row(b, bits);
     need += r0.blocks - r0.keep;

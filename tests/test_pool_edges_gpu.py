@@ -94,3 +94,67 @@ def test_free_takes_one_flag_a_row():
     assert S.last_error() == 0 and lens.tolist() == [0, 40, 0, 128]
     pool.free(torch.tensor([[False, True], [True, False]] * 2, device="cuda")[:, 0])    # (any stride)
     assert S.last_error() == 0 and lens.tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype,Hkv,d", [(torch.float32, 16384, 128), (torch.bfloat16, 5000, 64), (torch.bfloat16, 16383, 128)])
+def test_copies_of_rows_of_many_heads(dtype, Hkv, d):
+    """An entry of up to 2^20 pieces, begun in the middle of a thread block's share."""
+    import sparse_kv_selection_gb300 as S
+    k, v = (torch.randn(3, Hkv, 16, d, device="cuda").to(dtype) for _ in range(2))
+    kv = S.KVCache(k.clone(), v.clone(), i32([0]), Hkv, block_table=i32([[0, 1]]))
+    src, dst = [0, 17, -1, 31, 40], [33, 2, 5, 47, 16]
+    S.copy_rows(kv, i32(src), i32(dst))
+    assert S.last_error() == 0
+    for x, y in ((k, kv.k), (v, kv.v)):
+        want = x.clone()
+        for a, b in zip(src, dst):
+            if a >= 0:
+                want[b // 16, :, b % 16] = x[a // 16, :, a % 16]
+        assert torch.equal(want, y)
+
+
+FIRST = """
+import torch
+import sparse_kv_selection_gb300 as S
+z = dict(dtype=torch.int32, device="cuda")
+for dtype in (torch.bfloat16, torch.float32):
+    for B, wide in ((4, 8), (64, 2000)):            # a cluster's table, and one for all SMs
+        k, v = torch.randn(2, 300, 2, 16, 64, device="cuda").to(dtype)
+        table = torch.full((B, wide), -1, **z)
+        table[:2, :2] = torch.tensor([[0, 1], [2, 3]], **z)
+        lens, held = torch.zeros(B, **z), torch.zeros(B, **z)
+        lens[:2], held[:2] = torch.tensor([20, 32], **z), 2
+        kv = S.KVCache(k, v, lens, 4, block_table=table)
+        pool = S.PagePool(kv, free_pages=torch.arange(300, **z), free_head=torch.full((1,), 4, **z), n_pages=held)
+        batch = S.TokenBatch(kv, S.RopeTable(64), max_tokens=9, max_new=6, share_prefixes=True, min_shared=16, **pool.pages)
+        q, kn, vn = torch.randn(9, 4, 64, device="cuda").to(dtype), *torch.randn(2, 9, 2, 64, device="cuda").to(dtype)
+        n, parent = torch.zeros(B, **z), torch.arange(B, **z)
+        n[:4], parent[2:4] = torch.tensor([1, 2, 3, 1], **z), torch.tensor([0, 0], **z)
+        keep, m = torch.arange(24, **z).repeat(B, 1), torch.full((B,), -1, **z)
+        m[1] = 24
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pool.fork(parent)
+            pool.compact(keep, m)
+            batch.plan(n)
+            batch.rotate(q, kn, vn)
+            batch.attend()
+            batch.commit(n)
+        g.replay()
+        assert S.last_error() == 0
+        assert lens[:4].tolist() == [21, 26, 23, 21] and not lens[4:].any(), lens
+        assert pool.page_shares[0] == 2 and torch.isfinite(batch.out[:7]).all()
+"""
+
+
+def test_a_process_whose_first_call_is_captured(tmp_path):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    script = tmp_path / "first.py"
+    script.write_text(FIRST)
+    r = subprocess.run([sys.executable, str(script)], cwd=root, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": root})
+    assert r.returncode == 0, r.stdout + r.stderr

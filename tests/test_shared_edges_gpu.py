@@ -21,3 +21,13 @@ def test_an_entry_that_differs_from_its_groups_is_flagged(dtype, entry):
     out = b.run(share=share)
     assert S.last_error() == DEV_BAD_INDEX
     b.check(out)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (8, 1, 128)])
+def test_single_tokens_on_longer_own_keys_than_the_few_rows_part_takes(Hq, Hkv, d):
+    """Own keys around and above 32768: tiles and runs of steps in one launch."""
+    import sparse_kv_selection_gb300 as S
+    b = Batch([(3, 64), (2, 160), (1, 0)], [32760, 32767, 32768, 40000, 10, 33000], (1, 1), Hq, Hkv, d, BF16, 16, seed=51)
+    out = b.run()
+    assert S.last_error() == 0
+    b.check(out)
