@@ -10,6 +10,13 @@ sequence. Nothing synchronises with the host, so a step can be captured into a
 graph; the same cache can be decoded by ``SparseDecoder`` between steps. Where
 neighbouring sequences share pages (``PagePool.fork``), ``share_prefixes`` reads
 what they share once.
+
+Layers of a model whose caches have one block table and one ``seq_lens`` take a batch each,
+TokenBatch(kv_i, ..., **first.pages). Every layer plans (the pages that the first one took
+are there for the others, so all get the same slots) before any commits, and the lengths move
+once: chunks are appended by ``rotate`` in every layer and committed in the last; accepted
+tokens of trees are committed in the others by ``commit_tokens`` with a ``new_lens`` that
+nobody reads.
 """
 from __future__ import annotations
 
@@ -31,7 +38,8 @@ class TokenBatch:
                  free_pages=None, n_pages=None, free_head=None, scale: float | None = None, stream=None,
                  share_prefixes: bool = False, min_shared: int = 256):
         """max_tokens packed tokens at most (padding included), max_new of one
-        sequence. A paged cache needs free_pages (int32, the pages that no
+        sequence (the attention's form is chosen by it, so a batch for single tokens
+        is faster with 1 than one for chunks is at the same step). A paged cache needs free_pages (int32, the pages that no
         sequence holds), n_pages (int32 [B], the pages each row of its block
         table holds) and free_head (int32 [1], how many of free_pages have been
         taken; zero when left out). plan updates free_head and n_pages in place:
