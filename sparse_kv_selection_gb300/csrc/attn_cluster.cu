@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(ACL_THREADS, 2) attn_cluster_kernel(const Attn
   }
 
   // ---- this CTA's state: the 4 row groups of each warp, then the warps ----
+  if (CL > 1) cluster_begun();  // CTA 0's table may be written (below; nothing is waited for here)
 #pragma unroll
   for (int off = 8; off <= 16; off <<= 1) {
     const float m2 = __shfl_xor_sync(FULL_MASK, m, off);
@@ -224,7 +225,6 @@ __global__ void __launch_bounds__(ACL_THREADS, 2) attn_cluster_kernel(const Attn
       for (int e = 0; e < EPC; e++) sm_o[warp][(cc * 8 + j) * EPC + e] = o[cc * EPC + e];
   }
   __syncthreads();
-  if (CL > 1) cluster_begun();  // CTA 0's table may be written
   if (tid < D) {
     float M = sm_m[0];
 #pragma unroll

@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(CIS_THREADS) cis_kernel(const CisLaunch a) {
     for (int k = 0; k < CIS_PER; k++) x[k] = j0 + k < seg_cap_hi ? anc[j0 + k] : 0;
     prev0 = j0 > 0 && j0 - 1 < a.anchor_cap ? anc[j0 - 1] : -1;
   }
-  if (CLU) cluster_begin();  // (behind the age's read)
   if (warp == 0) {
     // the gated vectors in 16-byte pieces, one round trip: lanes below d / EPC
     // hold EPC elements each of g and of the anchor's copy
@@ -333,15 +332,26 @@ __global__ void __launch_bounds__(CIS_THREADS) cis_kernel(const CisLaunch a) {
       pass = den > 0.0 && dot / den >= a.tau;
     }
     // every rank takes the same decision; rank 0 records it
-    if (lane == 0) sh_reuse = n > 0 && pass && (a.max_run <= 0 || age < a.max_run - 1);
+    if (lane == 0) {
+      const bool run_over = a.max_run > 0 && age >= a.max_run - 1;
+      sh_reuse = n > 0 && pass ? (run_over ? -1 : 1) : 0;
+    }
   }
   __syncthreads();
-  if (CLU) cluster_begun();  // every rank has begun, and has read the age that now changes
-  if (rank == 0 && tid == 0) {
-    a.reuse[qh] = (uint8_t)sh_reuse;
-    if (a.anchor_age != nullptr) a.anchor_age[qh] = sh_reuse ? age + 1 : 0;
+  auto record = [&](int reuse) {
+    if (rank != 0 || tid != 0) return;
+    a.reuse[qh] = (uint8_t)reuse;
+    if (a.anchor_age != nullptr) a.anchor_age[qh] = reuse ? age + 1 : 0;
+  };
+  // The age changes once every rank has decided by it: ranks that decide otherwise would leave
+  // while the others still write into their shared memory.
+  const int reuse = sh_reuse;  // uniform over the cluster
+  if (reuse <= 0) {
+    if (CLU && reuse < 0) cluster.sync();  // (at 0 the age decides nothing)
+    record(0);
+    return;
   }
-  if (!sh_reuse) return;  // uniform over the cluster
+  if (!CLU) record(1);
 
   // ---- dilation of the anchor set: CIS_PER consecutive entries per thread ----
   if (n > a.anchor_cap) {
@@ -360,6 +370,7 @@ __global__ void __launch_bounds__(CIS_THREADS) cis_kernel(const CisLaunch a) {
   const int seg_hi = min(n, seg_lo + seg);  // this CTA's entries [seg_lo, seg_hi)
   int offset = 0, grand = 0;                // positions of the lower ranks' entries, of all
   if (CLU) {
+    cluster_begin();
     int local = 0;
     for (int base = seg_lo; base < seg_hi; base += CHUNK) {
       const int j0 = base + tid * CIS_PER;
@@ -376,8 +387,10 @@ __global__ void __launch_bounds__(CIS_THREADS) cis_kernel(const CisLaunch a) {
       local += chunk_intervals(y, prev, j0, seg_hi, t, w, ns, wlo, nullptr, start, cnt);
     }
     const int total = block_sum(local, warp_tot);
+    cluster_begun();
     if (tid < CL) cluster.map_shared_rank(seg_cnt, tid)[rank] = total;
     cluster.sync();  // every rank's count is in every rank
+    record(1);
 #pragma unroll
     for (int r = 0; r < CIS_CLUSTER_MAX; r++) {
       const int c = r < CL ? seg_cnt[r] : 0;

@@ -258,10 +258,12 @@ cudaError_t allow_smem(K kernel, size_t smem, int (&done)[SMEM_DEVICES]) {
 
 // -------------------------------------------------------------------------- //
 // a cluster's CTAs have all begun: shared memory of another CTA may be touched behind the
-// wait, not before. The arrive stands as far in front as it can, so that the wait costs
-// nothing; a path that leaves between the two waits as well. All threads of the block.
+// wait, not before. Nothing but that is ordered (an arrive that releases waits for what is in
+// flight: retrieval of 32 heads on 4096 keys 12.7 -> 13.3 us). The arrive stands as far in front
+// as it can, so that the wait costs nothing; a path that leaves between the two waits as well.
+// All threads of the block.
 // -------------------------------------------------------------------------- //
-__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // -------------------------------------------------------------------------- //

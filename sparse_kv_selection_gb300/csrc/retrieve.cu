@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(RT_THREADS, 2) retrieve_kernel(const SelectLau
         }
       }
     }
+    if (!ONE) cluster_begun();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       vmin = fminf(vmin, __shfl_xor_sync(FULL_MASK, vmin, o));
@@ -572,7 +573,6 @@ __global__ void __launch_bounds__(RT_THREADS, 2) retrieve_kernel(const SelectLau
       sh.red2[warp] = vmax;
     }
     __syncthreads();
-    if (!ONE) cluster_begun();
     if (tid < CL) {
       float m0 = INFINITY, m1 = -INFINITY;
 #pragma unroll

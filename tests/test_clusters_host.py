@@ -42,6 +42,9 @@ def test_a_barrier_before_another_ctas_memory(name):
 def test_an_anchors_age_changes_once_all_ranks_have_read_it():
     """Ranks that read another age decide otherwise, and leave while the others still write to them."""
     body = dict(kernels())["cis_kernel"]
-    read, write = body.index("= a.anchor_age !="), body.index("a.anchor_age[qh] = ")
-    begin, begun = body.index("cluster_begin()"), body.index("cluster_begun()")
-    assert read < begin < begun < write
+    assert body.index("= a.anchor_age !=") < body.index("a.anchor_age[qh] = ")
+    calls = [m.start() for m in re.finditer(r"\brecord\(\d\)", body)]
+    assert len(calls) == 3 and body.count("a.anchor_age[qh] = ") == 1
+    for at in calls:                    # behind a barrier of the cluster, or where there is none
+        before = body[:at].rstrip().splitlines()
+        assert any("cluster.sync()" in x for x in before[-2:]) or before[-1].strip() == "if (!CLU)"
