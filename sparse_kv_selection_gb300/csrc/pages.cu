@@ -19,7 +19,7 @@
 // consecutive, so that a prefix over the warps' counts gives every freed page its
 // place. One cluster of CTAs, or for large tables all SMs (a cooperative launch).
 // Bound: latency, six or seven dependent passes through L2 with a barrier between two, 1 us
-// each for a cluster, 2 for the grid; for large calls atomics on shared pages too. 64 beams
+// each for a cluster, 2 for the grid; for large calls atomics on shared pages too. From a graph, 64 beams
 // of 3.7 to 7.9K keys on 16-key pages trade places in 14.4 us (plans, sums and error bits through
 // L2 instead of the CTAs' shared memory, new columns read back: 15.6), 512 rows of up to 2173
 // pages in 41 (a cluster alone: 178; bytes 1.4), one row of 4096 positions is compacted in 14.5,

@@ -144,7 +144,9 @@ template <typename T, int D>
 static cudaError_t join_go(const TreeLaunch& a, const TreeRecords& rec, int sms, cudaStream_t st) {
   const long long blocks = ((long long)a.max_new * (a.kv.Hq / a.kv.Hkv) + 7) / 8;
   long long y = (blocks * a.kv.Hkv * (D / 32) + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
-  // one wave, since each CTA looks its sequence up (24 prompts: two waves 127.5 us, one 128.6, half of one 143)
+  // one wave, since each CTA looks its sequence up (24 prompts: two waves 127.5 us, one 128.6, half of one 143);
+  // with WAYS, of which an SM holds 5 CTAs, 1.6. A sequence's rows are its own CTAs' alone: one of many rows
+  // among many of few is joined by few CTAs
   const long long most = ((long long)SJ_CTAS_SM * sms + a.kv.B - 1) / a.kv.B;
   if (y > most) y = most;
   auto* kernel = sizeof(T) == 2 && a.max_new * (a.kv.Hq / a.kv.Hkv) <= 4 ? shared_join_kernel<T, D, sizeof(T) == 2> : shared_join_kernel<T, D, false>;
