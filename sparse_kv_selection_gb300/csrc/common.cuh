@@ -263,8 +263,14 @@ cudaError_t allow_smem(K kernel, size_t smem, int (&done)[SMEM_DEVICES]) {
 // as it can, so that the wait costs nothing; a path that leaves between the two waits as well.
 // All threads of the block.
 // -------------------------------------------------------------------------- //
-__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begin() {
+  __syncwarp();  // (aligned: a warp's threads together)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begun() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // -------------------------------------------------------------------------- //
 // small reductions
